@@ -9,6 +9,7 @@ Parity status: every public function is pinned by ``tests/test_oracle_pins.py``
 against an independent check (non-absorbed attention, closed forms, the
 split/merge identity, brute force, and torch's own float8 decoder).
 """
+from .chunk import cache_rows_at, mla_prefill_ref, seen_keys
 from .e4m3 import e4m3_decode_table, e4m3_encode, e4m3_to_f64
 from .kv_pack import kv_pack_ref
 from .sparse import mla_decode_sparse_ref
@@ -25,6 +26,7 @@ from .mla_oracle import (
 
 __all__ = [
     "attend",
+    "cache_rows_at",
     "e4m3_decode_table",
     "e4m3_encode",
     "e4m3_to_f64",
@@ -36,5 +38,7 @@ __all__ = [
     "mla_decode_ref",
     "mla_decode_ref_pieces",
     "mla_decode_sparse_ref",
+    "mla_prefill_ref",
+    "seen_keys",
     "visible_keys",
 ]

@@ -1,5 +1,6 @@
 """Paged MLA decode for GB300: Python binding of the C ABI in include/mla_decode.h,
-include/mla_kv_pack.h, include/mla_sparse.h and include/mla_cascade.h.
+include/mla_kv_pack.h, include/mla_sparse.h, include/mla_cascade.h and
+include/mla_prefill.h.
 
 The functions here only marshal arguments (torch tensors -> device
 pointers, shapes -> ``mla_dims``); every step of the decode runs in the
@@ -23,6 +24,7 @@ MLA_DEV_TIMEOUT = 4
 MLA_DEV_INTERNAL = 8
 MLA_DEV_BAD_INDEX = 16
 MLA_DEV_BAD_PREFIX = 32
+MLA_DEV_BAD_QUERY_RANGE = 64
 
 ENTRY_POINTS = (
     "mla_decode_workspace_size",
@@ -41,6 +43,10 @@ ENTRY_POINTS = (
     "mla_decode_cascade_workspace_size",
     "mla_decode_cascade",
     "mla_decode_cascade_query_status",
+    "mla_prefill_workspace_size",
+    "mla_prefill",
+    "mla_decode_window_workspace_size",
+    "mla_decode_window",
 )
 
 
@@ -67,6 +73,19 @@ class MlaKvPackDims(ctypes.Structure):
     _fields_ = [
         ("batch", ctypes.c_int32),
         ("num_new", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("page_table_stride", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+    ]
+
+
+class MlaPrefillDims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("total_q", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
         ("num_pages", ctypes.c_int32),
         ("max_pages_per_req", ctypes.c_int32),
         ("page_table_stride", ctypes.c_int32),
@@ -126,6 +145,16 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     lib.mla_decode_cascade.restype = ctypes.c_int
     lib.mla_decode_cascade_query_status.argtypes = [D, I32, P, P, ctypes.POINTER(I32)]
     lib.mla_decode_cascade_query_status.restype = ctypes.c_int
+    PD = ctypes.POINTER(MlaPrefillDims)
+    F = ctypes.c_float
+    lib.mla_prefill_workspace_size.argtypes = [PD, ctypes.c_int]
+    lib.mla_prefill_workspace_size.restype = SZ
+    lib.mla_prefill.argtypes = [PD, P, P, P, P, P, P, I32, I32, F, F, P, P, P, SZ, P]
+    lib.mla_prefill.restype = ctypes.c_int
+    lib.mla_decode_window_workspace_size.argtypes = [D, ctypes.c_int]
+    lib.mla_decode_window_workspace_size.restype = SZ
+    lib.mla_decode_window.argtypes = [D, P, P, P, P, P, I32, I32, F, F, P, P, P, SZ, P]
+    lib.mla_decode_window.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -440,6 +469,113 @@ def mla_decode_cascade_query_status(q_nope, kv_cache, page_table, prefix_pages: 
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_cascade_query_status")
     return st.value
+
+
+# ---- prompt chunks and windows (include/mla_prefill.h) ----
+
+def _check_current_device(t):
+    """The library runs on the current device; a tensor elsewhere would be
+    read through a pointer of another device."""
+    import torch
+
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device {torch.cuda.current_device()}, got {t.device}")
+
+
+def _int32_arg(name, v, low=0):
+    v = int(v)
+    if not low <= v <= 2**31 - 1:
+        raise ValueError(f"{name} must be between {low} and 2**31 - 1, got {v}")
+    return v
+
+
+def make_prefill_dims(q_nope, kv_cache, page_table, seq_lens) -> MlaPrefillDims:
+    T, H, _ = q_nope.shape
+    return MlaPrefillDims(
+        batch=int(seq_lens.shape[0]),
+        num_heads=H,
+        total_q=T,
+        page_size=int(kv_cache.shape[1]),
+        num_pages=int(kv_cache.shape[0]),
+        max_pages_per_req=int(page_table.shape[1]),
+        page_table_stride=int(page_table.stride(0)),
+        kv_dtype=kv_dtype_code(kv_cache),
+    )
+
+
+def mla_prefill_workspace_size(dims: MlaPrefillDims, device: int | None = None) -> int:
+    import torch
+
+    dev = torch.cuda.current_device() if device is None else device
+    n = load_library().mla_prefill_workspace_size(ctypes.byref(dims), dev)
+    if n == 0:
+        raise MlaError(-1, "mla_prefill_workspace_size")
+    return int(n)
+
+
+def _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace):
+    import torch
+
+    if q_nope.dim() != 3 or q_nope.shape[2] != 512:
+        raise ValueError(f"q_nope must be [total_q, H, 512], got {list(q_nope.shape)}")
+    T, H, _ = q_nope.shape
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _check_layout("q_nope", q_nope, (T, H, 512), (torch.bfloat16,))
+    _check_layout("q_pe", q_pe, (T, H, 64), (torch.bfloat16,))
+    _check_layout("out", out, (T, H, 512), (torch.bfloat16,))
+    _check_layout("lse", lse, (T, H), (torch.float32,))
+    _check_layout("cu_q_lens", cu_q_lens, (B + 1,), (torch.int32,))
+    _check_cache_and_table(kv_cache, page_table, seq_lens, B)
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    for t in (q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace):
+        if t.device != q_nope.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def mla_prefill(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, window, num_sinks, scale, kv_scale, out, lse,
+                workspace, stream=None) -> None:
+    """Enqueue the attention of chunks of new tokens over the paged cache (see
+    include/mla_prefill.h): q_nope [total_q, H, 512], cu_q_lens int32 [B + 1];
+    window 0 = none, else a sliding window plus num_sinks first tokens."""
+    _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+    _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+    _check_current_device(q_nope)
+    dims = make_prefill_dims(q_nope, kv_cache, page_table, seq_lens)
+    rc = load_library().mla_prefill(
+        ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens),
+        _ptr(cu_q_lens), _int32_arg("window", window), _int32_arg("num_sinks", num_sinks), float(scale),
+        float(kv_scale), _ptr(out), _ptr(lse), _ptr(workspace),
+        ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_prefill")
+
+
+def mla_decode_window_workspace_size(dims: MlaDims, device: int | None = None) -> int:
+    import torch
+
+    dev = torch.cuda.current_device() if device is None else device
+    n = load_library().mla_decode_window_workspace_size(ctypes.byref(dims), dev)
+    if n == 0:
+        raise MlaError(-1, "mla_decode_window_workspace_size")
+    return int(n)
+
+
+def mla_decode_window(q_nope, q_pe, kv_cache, page_table, seq_lens, window, num_sinks, scale, kv_scale, out, lse,
+                      workspace, stream=None) -> None:
+    """Enqueue a decode over a sliding window of `window` tokens and num_sinks
+    first tokens (see include/mla_prefill.h); tensors as for mla_decode."""
+    _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
+    _check_decode_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
+    _check_current_device(q_nope)
+    dims = make_dims(q_nope, kv_cache, page_table)
+    rc = load_library().mla_decode_window(
+        ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens),
+        _int32_arg("window", window, 1), _int32_arg("num_sinks", num_sinks), float(scale), float(kv_scale), _ptr(out),
+        _ptr(lse), _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
+        _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_window")
 
 
 @dataclass

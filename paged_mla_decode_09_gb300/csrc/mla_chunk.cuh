@@ -1,0 +1,1344 @@
+// Device code of the chunk attention behind mla_prefill and
+// mla_decode_window: schedule, split-KV attention, log-sum-exp combine.
+//
+// Row r of the flattened queries [T * H] belongs to token r / H, head r % H.
+// A request's rows are cut into blocks of kCg * 128 consecutive rows; a
+// block's keys are the pages that any of its rows sees: with a window the
+// sink pages, then the window's pages (a virtual page index v maps to the
+// real page v, or v + skip behind the sink pages).  Over those pages each
+// row computes, with one pass and a running maximum,
+//
+//     s_t = (q_nope . c_kv[t] + q_pe . k_pe[t]) * scale,  P = 2^(s log2e - R),
+//     O = sum P c_kv[t],  l = sum P,  out = O / l,  lse = (R + log2 l) ln 2.
+//
+// What bounds it: 2176 flops per (row, key) on the tensor pipe once a block
+// is full, the cache's bytes from HBM when a request has few rows.  How it is
+// laid out: an O accumulator of 128 rows x 512 fp32 fills an SM's tensor
+// memory, so scores and outputs live in different SMs.
+//   * S CTA: the block's queries in TMEM (A operand), pages K-major in shared
+//     memory (B), S = Q K^T of 64 keys at a time, softmax (one thread per
+//     row), P sent to its O CTA by st.async;
+//   * O CTA: O += P V, V = the same page through an MN-major descriptor.
+// kCg = 1: one S/O pair (cluster of 2) per 128 rows.  kCg = 2: two S CTAs and
+// two O CTAs (cluster of 4) per 256 rows, each pair running cta_group::2
+// MMAs of M = 256.  A pair's CTAs hold half of B each, so every SM copies in
+// and reads half the page bytes per MMA: at M = 128 the S CTA's page copies
+// and operand reads (72 KB each per 1152 tensor cycles) alone take the 128
+// bytes a cycle that shared memory has.
+//
+// An e4m3 cache: QK runs on the codes as they are (kind::f8f6f4), the queries
+// as two e4m3 terms hi + lo of q / 2^k.  A bf16 value has 8 significant bits
+// and hi + lo hold 4 + 4, so with a power-of-two row scale the split is exact
+// down to 2^-10 of the row's largest value and scores are as exact as with a
+// bf16 cache.  PV runs in bf16: four warps of the O CTA expand the codes
+// (exact in bf16) into the V ring, and P keeps bf16's range (P as e4m3 terms
+// loses the many small weights of a long row to subnormals).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "mla_decode.h"
+#include "mla_prefill.h"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace chunk {
+
+constexpr int kPage = 64;
+constexpr int kDL = 512;
+constexpr int kDR = 64;
+constexpr int kRows = 128;    // rows per CTA
+// warps: 0 TMA, 1 MMA, 2 TMEM alloc, 3 idle, 4-11 row warps
+constexpr int kThreads = 384;
+constexpr int kNS = 3;        // S buffers of 64 TMEM columns
+constexpr uint32_t kSCol0 = 320;  // queries use columns 0..287
+constexpr uint32_t kQLoCol = 144;  // e4m3: the lo terms' first column
+constexpr int kCtrlBytes = 640;
+constexpr int kMaxStages = 10;
+constexpr int kMaxP = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kMinusBig = -1.0e30f;  // running-maximum start (finite: no inf - inf)
+// O is rescaled only when a row's maximum grows by more than 2^8 (log2
+// units); P then stays below 2^8, which bf16 and the fp32 sums hold easily
+constexpr float kThreshold = 8.0f;
+constexpr int kMaxClusters = 96;       // the combine's lanes take 3 clusters each
+
+template <bool kF8, int kCg>
+struct Cfg {
+  // S CTA: kKeys rows of every page (all of B's N for kCg = 1, half for 2)
+  static constexpr int kKeys = kPage / kCg;
+  static constexpr int kSBoxes = kF8 ? 4 : 9;            // 128-byte columns of a row in the 3-D box
+  static constexpr int kSBoxBytes = kKeys * 128;
+  static constexpr int kPeBytes = kF8 ? kKeys * 64 : 0;  // e4m3 k_pe, 64-byte rows by a map of their own
+  static constexpr int kSlotS = kSBoxes * kSBoxBytes + kPeBytes;
+  static constexpr int kNStS = kF8 ? (kCg == 1 ? 6 : 10) : (kCg == 1 ? 3 : 6);
+  // ring entries of a block's bf16 query rows (1152 bytes each)
+  static constexpr int kQRows = kSlotS / 1152;
+  static constexpr int kQEntries = kRows / kQRows;
+  // O CTA: 512 / kCg latent dimensions of every page
+  static constexpr int kVDims = kDL / kCg;
+  static constexpr int kVBox = 8192;                     // 64 keys x 128 bytes
+  static constexpr int kVBoxes = kVDims / 64;
+  static constexpr int kSlotV = kVBoxes * kVBox;
+  static constexpr int kNV = kF8 ? (kCg == 1 ? 2 : 3) : (kCg == 1 ? 3 : 4);
+  static constexpr int kRawBoxes = kVDims / 128;         // e4m3: 64 keys x 128 codes
+  static constexpr int kSlotRaw = kRawBoxes * kVBox;
+  static constexpr int kNRaw = kF8 ? (kCg == 1 ? 2 : 3) : 0;
+  static constexpr int kNStO = kF8 ? kNRaw : kNV;        // slots that TMA fills
+  static constexpr int kSlotO = kF8 ? kSlotRaw : kSlotV;
+  static constexpr int kNP = kCg == 1 ? 2 : 4;           // P slots
+  static constexpr int kPBytes = kRows * kPage * 2;
+  // P: K-major without swizzle, core matrices of 8 rows x 16 bytes; the
+  // 16-byte chunk c of row r at (r / 8) * 1024 + c * 128 + (r % 8) * 16
+  static constexpr uint32_t kPLbo = 128, kPSbo = 1024;
+  static constexpr uint32_t kIdescQK = make_idesc(kF8, 128 * kCg, 64, false, false);
+  static constexpr uint32_t kIdescPV = make_idesc(false, 128 * kCg, 256, false, true);
+  // shared memory
+  static constexpr int kMlOff = kNStS * kSlotS;          // S: (m0, l0, m1, l1)[128]
+  static constexpr int kPubOff = kMlOff + kRows * 16;    // S: row references of the last 4 pages
+  static constexpr int kDataS = kPubOff + 4 * kRows * 8;
+  static constexpr int kVOff = kNP * kPBytes;            // O: P slots, V ring, raw ring, row factors, flags
+  static constexpr int kRawOff = kVOff + kNV * kSlotV;
+  static constexpr int kRefOff = kRawOff + kNRaw * kSlotRaw;
+  static constexpr int kFlagOff = kRefOff + kNP * kRows * 4;
+  static constexpr int kDataO = kFlagOff + kNP * 16;
+  static constexpr int kData = kDataS > kDataO ? kDataS : kDataO;
+  static constexpr int kSmem = 1024 + ((kData + 15) & ~15) + kCtrlBytes;
+  // bytes an S CTA sends per page: every row's P and O factor, a flag word per softmax warp
+  static constexpr uint32_t kPTx = kRows * (kPage * 2 + 4) + 4 * 4;
+  // O rows are corrected and stored by 8 warps (a half of the columns each),
+  // or by 4 where the other 4 expand the e4m3 pages
+  static constexpr int kCorrWarps = kF8 ? 4 : 8;
+  static_assert(kSmem <= 232448, "shared memory budget");
+  static_assert(kQEntries <= kNStS && kNStS <= kMaxStages && 2 * (kQEntries + 1) >= kNStS, "query entries");
+};
+
+struct __align__(8) Ctrl {
+  uint64_t kv_full[kMaxStages];
+  uint64_t kv_empty[kMaxStages];
+  uint64_t peer_kv[kMaxStages];  // S leader: the other S CTA's entry has landed
+  uint64_t q_bar[2];             // query rows of the unit landed (alternating units)
+  uint64_t s_full[kNS];
+  uint64_t s_empty[kNS];         // S leader: both CTAs read the S buffer
+  uint64_t q_full;               // S leader: queries in TMEM (both CTAs)
+  uint64_t p_full[kMaxP];
+  uint64_t p_empty[kMaxP];
+  uint64_t peer_pv[kMaxP];       // O leader: the other O CTA is ready for PV of the page
+  uint64_t v_full[4];            // e4m3: expanded pages
+  uint64_t v_empty[4];
+  uint64_t o_full;
+  uint64_t o_empty;
+  uint64_t resc_req;
+  uint64_t resc_done;
+  uint64_t ml_full;
+  uint64_t ml_empty;
+  uint64_t drain;
+  uint32_t tmem_base;
+  uint32_t resc_page;
+  int abort;
+};
+static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
+
+// One block of rows, as the schedule writes it.
+struct Block {
+  int32_t b;       // request
+  int32_t row0;    // first row of the flattened [T * H]
+  int32_t nrows;
+  int32_t sp;      // virtual pages before the skip
+  int32_t skip;    // real page = v + (v >= sp ? skip : 0)
+  int32_t pos0;    // position of the first row's token (< 0: sees nothing)
+  int32_t h0;      // head of the first row
+  int32_t len;     // the request's length, clamped to the table
+};
+static_assert(sizeof(Block) == 32, "two 16-byte loads");
+
+struct Params {
+  const uint8_t* q_nope;
+  const uint8_t* q_pe;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;      // [B + 1] first query token of each request; null: request b has tokens b*q_len ..
+  uint8_t* out;
+  float* lse;
+  float* o_part;            // [2C][128 kCg][512]
+  float* lse_part;          // [2C][128 kCg]
+  int32_t* status;          // [4]
+  int32_t* blkoff;          // [B + 1] first block of each request
+  Block* blk;               // [NB]
+  int32_t* prefix;          // [NB + 1] page prefix sums over blocks
+  int32_t* cinfo;           // [C][4] slice start, end, first block, last block
+  int32_t B, H, q_len, T, NB, C, BR;  // BR = rows per block
+  int32_t num_pages, max_pages, pt_stride;
+  int32_t window, sinks;    // window 0: everything up to the row's own position
+  int32_t unit_cost;        // schedule weight of starting a piece, in pages
+  float scale, kv_scale;
+  uint64_t timeout_ns;
+};
+
+// ---------------------------------------------------------------- schedule
+// One block of 1024 threads: the row blocks of every request, their page
+// counts, and each cluster's slice of all pages.  Slices are cut in a
+// weighted order (a piece of a block costs unit_cost pages to start), so that
+// clusters with many short blocks get fewer pages.
+constexpr int kSchedThreads = 1024;
+constexpr int kSchedSmemNB = 8192;  // prefix sums kept in shared memory for the searches
+
+__device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  // inclusive, all threads
+  const int tid = threadIdx.x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if ((tid & 31) >= o) v += t;
+  }
+  if ((tid & 31) == 31) warp_tot[tid >> 5] = v;
+  __syncthreads();
+  if (tid < 32) {
+    int w = warp_tot[tid];
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, w, o);
+      if (tid >= o) w += t;
+    }
+    warp_tot[tid] = w;
+  }
+  __syncthreads();
+  return v + ((tid >> 5) ? warp_tot[(tid >> 5) - 1] : 0) + carry;
+}
+
+__global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const __grid_constant__ Params p) {
+  __shared__ int warp_tot[32];
+  __shared__ int carry_s;
+  __shared__ int32_t sp[kSchedSmemNB + 1];
+  griddep_launch_dependents();
+  const int tid = threadIdx.x;
+  if (tid < 4) p.status[tid] = 0;
+  if (tid == 0) carry_s = 0;
+  __syncthreads();
+  // row blocks per request
+  for (int base = 0; base < p.B; base += kSchedThreads) {
+    const int b = base + tid;
+    int nblk = 0;
+    if (b < p.B) {
+      int64_t q0, q1;
+      if (p.cu_q) {
+        q0 = p.cu_q[b];
+        q1 = p.cu_q[b + 1];
+        if (q0 < 0 || q1 < q0 || q1 > p.T || (b == 0 && q0 != 0)) {
+          atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
+          q0 = q1 = 0;  // the request is left out
+        }
+      } else {
+        q0 = static_cast<int64_t>(b) * p.q_len;
+        q1 = q0 + p.q_len;
+      }
+      const int L = p.seq_lens[b];
+      if (q1 > q0 && (L < q1 - q0 || L > p.max_pages * kPage)) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
+      nblk = static_cast<int>(((q1 - q0) * p.H + p.BR - 1) / p.BR);
+    }
+    const int incl = block_scan(nblk, warp_tot, carry_s);
+    if (b < p.B) p.blkoff[b + 1] = incl < p.NB ? incl : p.NB;  // never beyond the arrays
+    __syncthreads();
+    if (tid == kSchedThreads - 1) carry_s = incl;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.blkoff[0] = 0;
+    if (carry_s > p.NB) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
+    carry_s = 0;
+  }
+  __syncthreads();
+  const int nblocks = p.blkoff[p.B];
+  const bool sp_ok = p.NB <= kSchedSmemNB;
+  // each block's rows and pages
+  for (int base = 0; base < p.NB; base += kSchedThreads) {
+    const int n = base + tid;
+    int np = 0;
+    if (n < nblocks) {
+      int lo = 0, hi = p.B - 1;  // last request with blkoff <= n
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.blkoff[mid] <= n) lo = mid; else hi = mid - 1;
+      }
+      const int b = lo;
+      const int q0 = p.cu_q ? p.cu_q[b] : b * p.q_len;
+      const int nq = (p.cu_q ? p.cu_q[b + 1] : q0 + p.q_len) - q0;
+      const int64_t r0 = static_cast<int64_t>(n - p.blkoff[b]) * p.BR;  // within the request
+      const int64_t left = static_cast<int64_t>(nq) * p.H - r0;
+      const int Lraw = p.seq_lens[b];
+      const int L = Lraw < 0 ? 0 : (Lraw > p.max_pages * kPage ? p.max_pages * kPage : Lraw);
+      Block k;
+      k.b = b;
+      k.row0 = static_cast<int32_t>(static_cast<int64_t>(q0) * p.H + r0);
+      k.nrows = static_cast<int32_t>(left < p.BR ? left : p.BR);
+      const int i0 = static_cast<int>(r0 / p.H);
+      k.h0 = static_cast<int32_t>(r0 % p.H);
+      k.pos0 = L - nq + i0;
+      const int pos1 = L - nq + static_cast<int>((r0 + k.nrows - 1) / p.H);
+      k.len = L;
+      const int last = (pos1 < 0 ? 0 : pos1) / kPage;  // at least one page, all of it masked if nothing is seen
+      k.sp = last + 1;
+      k.skip = 0;
+      if (p.window > 0) {
+        const int64_t wlo = static_cast<int64_t>(k.pos0) + 1 - p.window;  // first key of the first row's window
+        const int wp = wlo > 0 ? static_cast<int>(wlo / kPage) : 0;
+        const int ns = static_cast<int>((static_cast<int64_t>(p.sinks) + kPage - 1) / kPage);
+        if (wp > ns) {
+          k.sp = ns;
+          k.skip = wp - ns;
+        }
+      }
+      np = last + 1 - k.skip;
+      p.blk[n] = k;
+    }
+    const int incl = block_scan(np, warp_tot, carry_s);
+    if (n < p.NB) {
+      p.prefix[n + 1] = incl;
+      if (sp_ok) sp[n + 1] = incl;
+    }
+    __syncthreads();
+    if (tid == kSchedThreads - 1) carry_s = incl;
+    __syncthreads();
+  }
+  if (tid == 0) {
+    p.prefix[0] = 0;
+    sp[0] = 0;
+  }
+  __syncthreads();
+  const int32_t* pre = sp_ok ? sp : p.prefix;
+  if (nblocks == 0) {
+    for (int c = tid; c < p.C; c += kSchedThreads)
+      for (int k = 0; k < 4; ++k) p.cinfo[4 * c + k] = 0;
+    return;
+  }
+  // slices: weighted position of block n's first page is pre[n] + unit_cost * (n + 1)
+  const int64_t W = static_cast<int64_t>(pre[nblocks]) + static_cast<int64_t>(p.unit_cost) * nblocks;
+  auto page_at = [&](int64_t x) -> int {
+    int lo = 0, hi = nblocks - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] + static_cast<int64_t>(p.unit_cost) * mid <= x) lo = mid; else hi = mid - 1;
+    }
+    const int64_t np = pre[lo + 1] - pre[lo];
+    int64_t off = x - pre[lo] - static_cast<int64_t>(p.unit_cost) * (lo + 1);
+    off = off < 0 ? 0 : (off > np ? np : off);
+    return static_cast<int>(pre[lo] + off);
+  };
+  auto block_of = [&](int page) -> int {  // the block that holds the page
+    int lo = 0, hi = nblocks - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (pre[mid] <= page) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  };
+  for (int c = tid; c < p.C; c += kSchedThreads) {
+    const int s = c == 0 ? 0 : page_at(W * c / p.C);
+    const int e = c == p.C - 1 ? pre[nblocks] : page_at(W * (c + 1) / p.C);
+    p.cinfo[4 * c + 0] = s;
+    p.cinfo[4 * c + 1] = e;
+    p.cinfo[4 * c + 2] = s < e ? block_of(s) : 0;
+    p.cinfo[4 * c + 3] = s < e ? block_of(e - 1) : 0;
+  }
+}
+
+// One block's piece inside a cluster's slice.
+struct Unit {
+  int p0, p1, slot;  // virtual pages [p0, p1); slot < 0: the whole block
+  Block k;
+};
+
+struct UnitIter {
+  const Params* p;
+  int s, e, n, nfirst, nlast, cid;
+  __device__ void init(const Params& pp, int c) {
+    p = &pp;
+    cid = c;
+    s = pp.cinfo[4 * c + 0];
+    e = pp.cinfo[4 * c + 1];
+    nfirst = pp.cinfo[4 * c + 2];
+    nlast = pp.cinfo[4 * c + 3];
+    n = nfirst;
+  }
+  __device__ bool next(Unit& u) {
+    if (s >= e || n > nlast) return false;
+    const int pb0 = p->prefix[n], pb1 = p->prefix[n + 1];
+    u.p0 = (s > pb0 ? s : pb0) - pb0;
+    u.p1 = (e < pb1 ? e : pb1) - pb0;
+    const int4* src = reinterpret_cast<const int4*>(p->blk + n);
+    const int4 a = src[0], b = src[1];
+    u.k.b = a.x; u.k.row0 = a.y; u.k.nrows = a.z; u.k.sp = a.w;
+    u.k.skip = b.x; u.k.pos0 = b.y; u.k.h0 = b.z; u.k.len = b.w;
+    u.slot = (u.p0 > 0 || u.p1 < pb1 - pb0) ? 2 * cid + (n != nfirst ? 1 : 0) : -1;
+    ++n;
+    return true;
+  }
+};
+__device__ __forceinline__ int real_page(const Block& k, int v) { return v + (v >= k.sp ? k.skip : 0); }
+
+enum WaitTag : int {
+  kWaitProdS = 101, kWaitProdO, kWaitQFull, kWaitKvS, kWaitPeerKv, kWaitSFull, kWaitPEmpty, kWaitMlEmpty, kWaitPage,
+  kWaitRescDone, kWaitPeerPv, kWaitPvPrev, kWaitOFull, kWaitMlFull, kWaitSPrev, kWaitQEntry, kWaitPub, kWaitRaw,
+  kWaitVEmpty
+};
+
+template <int kCg>
+__device__ __forceinline__ void raise_timeout(const Params& p, Ctrl* ctrl, int tag, uint32_t j) {
+  if (atomicCAS(p.status + 1, 0, tag) == 0) {
+    p.status[2] = static_cast<int32_t>(j);
+    p.status[3] = static_cast<int32_t>((cluster_id_x() << 16) | (cluster_ctarank() << 8) | (threadIdx.x >> 5));
+  }
+  atomicOr(p.status, MLA_DEV_TIMEOUT);
+  for (uint32_t r = 0; r < 2 * kCg; ++r) st_cluster_u32(mapa(smem_u32(&ctrl->abort), r), 1u);
+}
+
+__device__ __forceinline__ int32_t read_page_id(const Params& p, int b, int pg) {
+  const int32_t pid = __ldg(p.page_table + static_cast<int64_t>(b) * p.pt_stride + pg);
+  if (pid < 0 || pid >= p.num_pages) {
+    atomicOr(p.status, MLA_DEV_BAD_PAGE_ID);
+    return 0;
+  }
+  return pid;
+}
+
+// Waits until every copy issued into the ring has landed (bounded).
+template <int kNSt>
+__device__ __forceinline__ void drain_ring(Ctrl* ctrl, uint32_t i, uint64_t timeout_ns) {
+  for (uint32_t q = 0; q < static_cast<uint32_t>(kNSt) && q < i; ++q) {
+    const uint32_t last = i - 1 - ((i - 1 - q) % kNSt);
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(&ctrl->kv_full[q]), (last / kNSt) & 1) && globaltimer_ns() - t0 < timeout_ns) {
+    }
+  }
+}
+
+// TMA producer of an S CTA: per unit its query rows (kQEntries ring entries,
+// completing on q_bar; the entries' own barriers complete by a plain arrival,
+// so that their phases keep in step), then kKeys rows of every page.
+template <bool kF8, int kCg>
+__device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUtensorMap* tm_s, const CUtensorMap* tm_pe,
+                          const CUtensorMap* tm_qn, const CUtensorMap* tm_qp, int cid, int pr) {
+  using C = Cfg<kF8, kCg>;
+  volatile int* abort = &ctrl->abort;
+  UnitIter it;
+  it.init(p, cid);
+  Unit u;
+  uint32_t i = 0, un = 0;
+  bool ok = true;
+  uint32_t bar = 0;
+  uint8_t* slot = nullptr;
+  auto acquire = [&]() -> bool {
+    const int st = static_cast<int>(i % C::kNStS);
+    if (!mbar_wait(smem_u32(&ctrl->kv_empty[st]), ((i / C::kNStS) & 1) ^ 1, abort, p.timeout_ns)) return false;
+    bar = smem_u32(&ctrl->kv_full[st]);
+    slot = ring + st * C::kSlotS;
+    return true;
+  };
+  uint32_t qloaded = 0;
+  while (ok && it.next(u)) {
+    const uint32_t qbar = smem_u32(&ctrl->q_bar[un & 1]);
+    for (int e = 0; e < C::kQEntries; ++e) {
+      if (!acquire()) {
+        ok = false;
+        break;
+      }
+      if (e == 0) {
+        mbar_expect_tx(qbar, static_cast<uint32_t>(kRows * 1152));
+        qloaded = un + 1;
+      }
+      mbar_arrive(bar);
+      const int row = u.k.row0 + pr * kRows + C::kQRows * e;
+      tma_load_3d(smem_u32(slot), tm_qn, 0, row, 0, qbar);
+      tma_load_2d(smem_u32(slot + C::kQRows * 128 * 8), tm_qp, 0, row, qbar);
+      ++i;
+    }
+    ++un;
+    for (int v = u.p0; v < u.p1 && ok; ++v) {
+      const int y = read_page_id(p, u.k.b, real_page(u.k, v)) * kPage + pr * C::kKeys;
+      if (!acquire()) {
+        ok = false;
+        break;
+      }
+      mbar_expect_tx(bar, static_cast<uint32_t>(C::kSlotS));
+      tma_load_3d(smem_u32(slot), tm_s, 0, y, 0, bar);
+      if constexpr (kF8) tma_load_2d(smem_u32(slot + C::kSBoxes * C::kSBoxBytes), tm_pe, kDL, y, bar);
+      ++i;
+    }
+  }
+  if (!ok) raise_timeout<kCg>(p, ctrl, kWaitProdS, i);
+  drain_ring<C::kNStS>(ctrl, i, p.timeout_ns);
+  // the last unit's query rows: a unit cut short by a timeout may not have
+  // armed all its bytes, so this wait is bounded too
+  if (qloaded) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(&ctrl->q_bar[(qloaded - 1) & 1]), ((qloaded - 1) >> 1) & 1) &&
+           globaltimer_ns() - t0 < p.timeout_ns) {
+    }
+  }
+}
+
+// TMA producer of an O CTA: its latent dimensions of every page.
+template <bool kF8, int kCg>
+__device__ void produce_o(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUtensorMap* tm_o, int cid, int pr) {
+  using C = Cfg<kF8, kCg>;
+  volatile int* abort = &ctrl->abort;
+  UnitIter it;
+  it.init(p, cid);
+  Unit u;
+  uint32_t i = 0;
+  bool ok = true;
+  while (ok && it.next(u)) {
+    for (int v = u.p0; v < u.p1; ++v) {
+      const int y = read_page_id(p, u.k.b, real_page(u.k, v)) * kPage;
+      const int st = static_cast<int>(i % C::kNStO);
+      if (!mbar_wait(smem_u32(&ctrl->kv_empty[st]), ((i / C::kNStO) & 1) ^ 1, abort, p.timeout_ns)) {
+        raise_timeout<kCg>(p, ctrl, kWaitProdO, i);
+        ok = false;
+        break;
+      }
+      const uint32_t bar = smem_u32(&ctrl->kv_full[st]);
+      mbar_expect_tx(bar, static_cast<uint32_t>(C::kSlotO));
+      tma_load_3d(smem_u32(ring + st * C::kSlotO), tm_o, 0, y, pr * (kF8 ? C::kRawBoxes : C::kVBoxes), bar);
+      ++i;
+    }
+  }
+  drain_ring<C::kNStO>(ctrl, i, p.timeout_ns);
+}
+
+// Query row r from the ring entries into TMEM lane r (bf16): chunks
+// [36 half, 36 half + 36) of 16 bytes; chunk c sits in box c / 8, piece c % 8
+// of the 128-byte-swizzled row.
+template <int kBoxBytes>
+__device__ __forceinline__ void q_row_bf16(const uint8_t* src, int rq, uint32_t taddr, int c0) {
+#pragma unroll
+  for (int c = 0; c < 36; c += 12) {
+    uint4 v[12];
+#pragma unroll
+    for (int k = 0; k < 12; ++k) {
+      const int cc = c0 + c + k;
+      v[k] = *reinterpret_cast<const uint4*>(src + (cc >> 3) * kBoxBytes + (((cc & 7) ^ (rq & 7)) << 4));
+    }
+#pragma unroll
+    for (int s4 = 0; s4 < 3; ++s4) {
+      const uint32_t w[16] = {v[4 * s4].x,     v[4 * s4].y,     v[4 * s4].z,     v[4 * s4].w,
+                              v[4 * s4 + 1].x, v[4 * s4 + 1].y, v[4 * s4 + 1].z, v[4 * s4 + 1].w,
+                              v[4 * s4 + 2].x, v[4 * s4 + 2].y, v[4 * s4 + 2].z, v[4 * s4 + 2].w,
+                              v[4 * s4 + 3].x, v[4 * s4 + 3].y, v[4 * s4 + 3].z, v[4 * s4 + 3].w};
+      tmem_st16(taddr + (c0 + c + 4 * s4) * 4, w);
+    }
+  }
+  tmem_wait_st();
+}
+
+// The same for an e4m3 cache: the row as hi + lo e4m3 terms of q / scale.
+// scale is the power of two that puts the row's largest |q| into [2^7, 2^8)
+// (2^-107 at least, so that its reciprocal stays finite); groups of 8 chunks
+// [g0, g1).  Returns scale (NaN for a row with an infinity or a NaN).
+template <int kBoxBytes>
+__device__ __forceinline__ float q_row_e4m3(const uint8_t* src, int rq, uint32_t taddr, int g0, int g1) {
+  uint32_t m = 0;  // largest |q| as bf16 bits (two lanes); bf16 bits order as integers
+#pragma unroll 6
+  for (int c = 0; c < 72; ++c) {
+    const uint4 v = *reinterpret_cast<const uint4*>(src + (c >> 3) * kBoxBytes + (((c & 7) ^ (rq & 7)) << 4));
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+  }
+  const uint32_t top = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
+  int e = static_cast<int>(top >> 7) - 127 - 7;  // exponent of the scale
+  e = e < -107 ? -107 : e;
+  const float scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll 1
+  for (int g = g0; g < g1; ++g) {
+    uint32_t hi[16], lo[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src + g * kBoxBytes + ((k ^ (rq & 7)) << 4));
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int h2 = 0; h2 < 2; ++h2) {
+        uint32_t h[2], l[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * h2 + q]));
+          x.x *= inv;
+          x.y *= inv;
+          const __nv_fp8x2_storage_t hh = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+          const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hh, __NV_E4M3);
+          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+          h[q] = hh;
+          l[q] = __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+        }
+        hi[2 * k + h2] = h[0] | (h[1] << 16);
+        lo[2 * k + h2] = l[0] | (l[1] << 16);
+      }
+    }
+    tmem_st16(taddr + g * 16, hi);
+    tmem_st16(taddr + kQLoCol + g * 16, lo);
+  }
+  tmem_wait_st();
+  return top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : scale;
+}
+
+// Writes TMEM columns [c0, c1) of one row: bf16 out and lse for a whole
+// block, fp32 partials (normalised O and its lse) for a piece.  Column c of
+// O is latent dimension c, or with kCg = 2 (each PV MMA's N = 256 is half
+// from each CTA of the pair) 256 ((c / 128) % 2) + 128 (c / 256) + c % 128.
+template <bool kF8, int kCg>
+__device__ __forceinline__ void store_row(const Params& p, const Unit& u, int br, int c0, int c1, uint32_t taddr,
+                                          float m_log2, float l) {
+  if (u.slot >= 2 * p.C) {  // cannot happen; a bad schedule never writes out of range
+    atomicOr(p.status, MLA_DEV_INTERNAL);
+    return;
+  }
+  const bool real = br < u.k.nrows;
+  const float inv_l = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays NaN
+  const float f = kF8 ? p.kv_scale * inv_l : inv_l;
+  const float lse_v = l > 0.f ? (m_log2 + __log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+  const int64_t orow = static_cast<int64_t>(u.k.row0) + br;
+  const int64_t prow = static_cast<int64_t>(u.slot) * p.BR + br;
+#pragma unroll 1
+  for (int c = c0; c < c1; c += 32) {
+    const int dim = kCg == 1 ? c : (((c >> 7) & 1) * 256 + (c >> 8) * 128 + (c & 127));
+    uint32_t v[2][16];
+    tmem_ld16(taddr + c, v[0]);
+    tmem_ld16(taddr + c + 16, v[1]);
+    tmem_wait_ld_tie(v[0]);
+    tmem_wait_ld_tie(v[1]);
+    if (!real) continue;
+    if (u.slot < 0) {
+      uint8_t* dst = p.out + (orow * kDL + dim) * 2;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const __nv_bfloat162 b2 =
+              __floats2bfloat162_rn(__uint_as_float(v[q][2 * k]) * f, __uint_as_float(v[q][2 * k + 1]) * f);
+          w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+        }
+        stg_v8(dst + 32 * q, w);
+      }
+    } else {
+      float* dst = p.o_part + prow * kDL + dim;
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(__uint_as_float(v[q][8 * k + e]) * f);
+          stg_v8(dst + 16 * q + 8 * k, w);
+        }
+    }
+  }
+  if (real && c0 == 0) {
+    if (u.slot < 0) p.lse[orow] = lse_v;
+    else p.lse_part[prow] = lse_v;
+  }
+}
+
+// --------------------------------------------------------------- attention
+template <bool kF8, int kCg>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_chunk_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_s,
+                     const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_pe,
+                     const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qp) {
+  using C = Cfg<kF8, kCg>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(data + ((C::kData + 15) & ~15));
+  // ranks 0 .. kCg - 1: S CTAs; kCg .. 2 kCg - 1: O CTAs; pr: place in the pair
+  const uint32_t rank = cluster_ctarank();
+  const bool role_s = rank < kCg;
+  const int pr = static_cast<int>(rank % kCg);
+  const bool leader = pr == 0;
+  const int cid = static_cast<int>(cluster_id_x());
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr uint16_t kMaskS = (1u << kCg) - 1u, kMaskO = kMaskS << kCg, kMaskAll = kMaskS | kMaskO;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMaxStages; ++i) {
+      mbar_init(smem_u32(&ctrl->kv_full[i]), 1);
+      mbar_init(smem_u32(&ctrl->kv_empty[i]), (!role_s && kF8) ? 4 : 1);  // e4m3 O CTA: the four expanding warps
+      mbar_init(smem_u32(&ctrl->peer_kv[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctrl->q_bar[i]), 1);
+    for (int i = 0; i < kNS; ++i) {
+      mbar_init(smem_u32(&ctrl->s_full[i]), 1);
+      mbar_init(smem_u32(&ctrl->s_empty[i]), 4 * kCg);
+    }
+    mbar_init(smem_u32(&ctrl->q_full), 8 * kCg);
+    for (int i = 0; i < kMaxP; ++i) {
+      mbar_init(smem_u32(&ctrl->p_full[i]), 1);
+      mbar_init(smem_u32(&ctrl->p_empty[i]), 1);
+      mbar_init(smem_u32(&ctrl->peer_pv[i]), 1);
+    }
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&ctrl->v_full[i]), 4);
+      mbar_init(smem_u32(&ctrl->v_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&ctrl->o_full), 1);
+    mbar_init(smem_u32(&ctrl->o_empty), C::kCorrWarps);
+    mbar_init(smem_u32(&ctrl->resc_req), 1);
+    mbar_init(smem_u32(&ctrl->resc_done), C::kCorrWarps);
+    mbar_init(smem_u32(&ctrl->ml_full), 8);
+    mbar_init(smem_u32(&ctrl->ml_empty), C::kCorrWarps);
+    mbar_init(smem_u32(&ctrl->drain), 1);
+    ctrl->abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(role_s ? &tm_s : &tm_o);
+    if (role_s) tma_prefetch_desc(&tm_qn);
+    if (role_s) tma_prefetch_desc(&tm_qp);
+    if (role_s && kF8) tma_prefetch_desc(&tm_pe);
+  }
+  if (role_s && threadIdx.x >= 128)  // page references: no page yet
+    for (int i = threadIdx.x - 128; i < 4 * kRows; i += kThreads - 128)
+      reinterpret_cast<uint64_t*>(data + C::kPubOff)[i] = 0ull;
+  __syncthreads();
+  cluster_sync();  // barriers initialised before any remote arrival; both CTAs of a pair here before the pair's alloc
+  if (warp == 2) {
+    tmem_alloc_cg<kCg>(smem_u32(&ctrl->tmem_base), 512);
+    tmem_relinquish_cg<kCg>();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's TMEM exists before the leader's first MMA writes it
+  tc_fence_after();
+  griddep_wait();
+  griddep_launch_dependents();
+  const uint32_t tmem = ctrl->tmem_base;
+  volatile int* abort = &ctrl->abort;
+
+  if (role_s) {
+    // =========================== S CTA ===========================
+    uint8_t* ring = data;
+    if (warp == 0) {
+      if (lane == 0) produce_s<kF8, kCg>(p, ctrl, ring, &tm_s, &tm_pe, &tm_qn, &tm_qp, cid, pr);
+    } else if (warp == 1) {
+      // The leader's warp issues QK for the pair (the whole warp runs the
+      // loop, one elected lane issues); the other CTA's warp passes on that
+      // its entries have landed.  Every entry's barriers are waited for, the
+      // query entries' too, so that no phase is ever missed.
+      UnitIter it;
+      it.init(p, cid);
+      Unit u;
+      uint32_t i = 0, j = 0, un = 0;
+      bool ok = true;
+      int why = 0;
+      auto landed = [&]() -> bool {  // entry i of this CTA and, for the leader, of the other
+        const int st = static_cast<int>(i % C::kNStS);
+        const uint32_t ph = (i / C::kNStS) & 1;
+        if (!mbar_wait_warp(smem_u32(&ctrl->kv_full[st]), ph, abort, p.timeout_ns)) {
+          why = kWaitKvS;
+          return false;
+        }
+        if (kCg == 2 && leader && !mbar_wait_warp(smem_u32(&ctrl->peer_kv[st]), ph, abort, p.timeout_ns)) {
+          why = kWaitPeerKv;
+          return false;
+        }
+        if (kCg == 2 && !leader && lane == 0) mbar_arrive_cluster(mapa(smem_u32(&ctrl->peer_kv[st]), 0));
+        return true;
+      };
+      while (ok && it.next(u)) {
+        for (int e = 0; e < C::kQEntries && ok; ++e, ++i) ok = landed();
+        if (!ok) break;
+        if (leader) {
+          if (!mbar_wait_warp(smem_u32(&ctrl->q_full), un & 1, abort, p.timeout_ns)) {
+            ok = false;
+            why = kWaitQFull;
+            break;
+          }
+          if (lane == 0)  // the query entries' slots go back to the producers
+            for (int e = C::kQEntries; e > 0; --e) {
+              const uint32_t bar = smem_u32(&ctrl->kv_empty[(i - e) % C::kNStS]);
+              mbar_arrive(bar);
+              if (kCg == 2) mbar_arrive_cluster(mapa(bar, 1));
+            }
+          __syncwarp();
+        }
+        ++un;
+        for (int v = u.p0; v < u.p1; ++v, ++j, ++i) {
+          const int sb = static_cast<int>(j % kNS);
+          if (leader && !mbar_wait_warp(smem_u32(&ctrl->s_empty[sb]), ((j / kNS) & 1) ^ 1, abort, p.timeout_ns)) {
+            ok = false;
+            why = kWaitSFull;
+            break;
+          }
+          if (!landed()) {
+            ok = false;
+            break;
+          }
+          if (!leader) continue;
+          tc_fence_after();
+          const int st = static_cast<int>(i % C::kNStS);
+          const uint32_t slot_addr = smem_u32(ring + st * C::kSlotS);
+          const uint64_t dlat = smem_desc(slot_addr, 16, 1024, kSwizzle128B);
+          const uint32_t dcol = tmem + kSCol0 + sb * 64;
+          if constexpr (!kF8) {
+#pragma unroll
+            for (int d = 0; d < 9; ++d)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts_cg<false, kCg>(dcol, tmem + d * 32 + k * 8,
+                                      dlat + static_cast<uint64_t>(d * (C::kSBoxBytes >> 4) + k * 2), C::kIdescQK,
+                                      (d | k) ? 1u : 0u);
+          } else {
+            const uint64_t dpe = smem_desc(slot_addr + C::kSBoxes * C::kSBoxBytes, 16, 512, kSwizzle64B);
+#pragma unroll
+            for (int term = 0; term < 2; ++term) {
+              const uint32_t qcol = tmem + (term ? kQLoCol : 0u);
+#pragma unroll
+              for (int d = 0; d < 4; ++d)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  mma_ts_cg<true, kCg>(dcol, qcol + d * 32 + k * 8,
+                                       dlat + static_cast<uint64_t>(d * (C::kSBoxBytes >> 4) + k * 2), C::kIdescQK,
+                                       (term | d | k) ? 1u : 0u);
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+                mma_ts_cg<true, kCg>(dcol, qcol + 128 + k * 8, dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
+            }
+          }
+          mma_commit_cg<kCg>(smem_u32(&ctrl->kv_empty[st]), kMaskS);
+          mma_commit_cg<kCg>(smem_u32(&ctrl->s_full[sb]), kMaskS);
+        }
+      }
+      if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
+      __syncwarp();
+      if (leader) {
+        mma_commit_cg<kCg>(smem_u32(&ctrl->drain), static_cast<uint16_t>(1u << rank));
+        if (lane == 0) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(smem_u32(&ctrl->drain), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+          }
+        }
+      }
+      __syncwarp();
+    } else if (warp >= 4) {
+      // ---- softmax: group gg (warps 4-7: 0, warps 8-11: 1) takes the pages
+      // j with j % 2 == gg, thread r row r of this CTA.  A page's reference
+      // is the previous page's, raised to the page's maximum where that
+      // exceeds it by more than the threshold, so references depend on the
+      // data alone; each group keeps its partial sum in its latest frame.
+      const int r = (warp & 3) * 32 + lane;
+      const int gg = (warp - 4) >> 2;
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t orank = kCg + pr;
+      const uint32_t p_remote = mapa(smem_u32(data), orank);
+      const uint32_t ref_remote = mapa(smem_u32(data + C::kRefOff), orank);
+      const uint32_t flag_remote = mapa(smem_u32(data + C::kFlagOff), orank);
+      const uint32_t mlfull_remote = mapa(smem_u32(&ctrl->ml_full), orank);
+      volatile uint64_t* pub = reinterpret_cast<volatile uint64_t*>(data + C::kPubOff);
+      const int br = pr * kRows + r;  // row in the block
+      UnitIter it;
+      it.init(p, cid);
+      Unit u;
+      uint32_t i = 0, j = 0, un = 0;
+      bool ok = true;
+      int why = 0;
+      while (ok && it.next(u)) {
+        // the unit's queries replace the previous unit's in TMEM once every
+        // QK of that unit is done: the S of its last page has landed
+        if (j > 0 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - 1) % kNS]), ((j - 1) / kNS) & 1, abort,
+                                                  p.timeout_ns)) {
+          ok = false;
+          why = kWaitSPrev;
+          break;
+        }
+        if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->q_bar[un & 1]), (un >> 1) & 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitQEntry;
+          break;
+        }
+        float qs = 1.f;
+        {
+          const int e = r / C::kQRows, rq = r % C::kQRows;
+          const uint8_t* src = ring + ((i + e) % C::kNStS) * C::kSlotS + rq * 128;
+          if constexpr (kF8) {
+            if (gg == 0) qs = q_row_e4m3<C::kQRows * 128>(src, rq, tmem + lane_base, 0, 5);
+            else qs = q_row_e4m3<C::kQRows * 128>(src, rq, tmem + lane_base, 5, 9);
+          } else {
+            q_row_bf16<C::kQRows * 128>(src, rq, tmem + lane_base, 36 * gg);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (kCg == 2) mbar_arrive_cluster(mapa(smem_u32(&ctrl->q_full), 0));
+          else mbar_arrive(smem_u32(&ctrl->q_full));
+        }
+        i += C::kQEntries + static_cast<uint32_t>(u.p1 - u.p0);
+        const float c2 = p.scale * kLog2e * (kF8 ? qs * p.kv_scale : 1.f);
+        const bool real = br < u.k.nrows;
+        // padding rows follow the block's last row (their results go nowhere)
+        const int pos = u.k.pos0 + (u.k.h0 + (real ? br : u.k.nrows - 1)) / p.H;
+        const int nvis = pos + 1;                                                     // sees t < nvis ...
+        const int lo = p.window > 0 && nvis > p.window ? nvis - p.window : 0;         // ... and t >= lo or t < sinks
+        float m_run = kMinusBig, l = 0.f;
+        for (int vp = u.p0; vp < u.p1; ++vp, ++j) {
+          if ((j & 1u) != static_cast<uint32_t>(gg)) continue;
+          const int sb = static_cast<int>(j % kNS);
+          if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (j / kNS) & 1, abort, p.timeout_ns)) {
+            ok = false;
+            why = kWaitSFull;
+            break;
+          }
+          tc_fence_after();
+          uint32_t v[4][16];
+          float red[4];
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+            tmem_ld16_max(tmem + lane_base + kSCol0 + sb * 64 + q4 * 16, v[q4], red[q4]);
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4) tmem_wait_ld_tie(v[q4], red[q4]);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) {
+            if (kCg == 2) mbar_arrive_cluster(mapa(smem_u32(&ctrl->s_empty[sb]), 0));
+            else mbar_arrive(smem_u32(&ctrl->s_empty[sb]));
+          }
+          const int t0 = real_page(u.k, vp) * kPage;
+          const bool full = t0 + kPage <= nvis && (t0 >= lo || t0 + kPage <= p.sinks);
+          // the page's keys [a, z) and [0, s) are seen
+          const int z = nvis - t0, a = lo - t0, s = p.sinks - t0;
+#define MLA_S(t) __uint_as_float(v[(t) >> 4][(t) & 15])
+          float m4[4] = {red[0], red[1], red[2], red[3]};
+          if (!full) {
+            // unseen keys become -inf here (their P is then exactly 0), so
+            // that whatever an unused slot holds, even NaN, never counts
+            m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
+#pragma unroll
+            for (int t = 0; t < 64; ++t) {
+              const float x = (t < z && (t >= a || t < s)) ? MLA_S(t) : -INFINITY;
+              v[t >> 4][t & 15] = __float_as_uint(x);
+              m4[t & 3] = fmaxf(m4[t & 3], x);
+            }
+          }
+          const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c2;
+          float m_ref = m_run;
+          float m_prev = kMinusBig;
+          if (vp != u.p0) {
+            volatile uint64_t* pe = pub + ((j - 1u) & 3u) * kRows + r;
+            uint64_t pv = *pe;
+            if (static_cast<uint32_t>(pv >> 32) != j) {
+              const uint64_t t_start = globaltimer_ns();
+              while (static_cast<uint32_t>((pv = *pe) >> 32) != j) {
+                if (*abort || globaltimer_ns() - t_start > p.timeout_ns) break;
+              }
+            }
+            if (__any_sync(0xffffffffu, static_cast<uint32_t>(pv >> 32) != j)) {
+              ok = false;
+              why = kWaitPub;
+              break;
+            }
+            m_prev = __uint_as_float(static_cast<uint32_t>(pv));
+            m_ref = fmaxf(m_ref, m_prev);
+          }
+          if (mx > m_ref + kThreshold) m_ref = mx;
+          pub[(j & 3u) * kRows + r] = (static_cast<uint64_t>(j + 1u) << 32) | __float_as_uint(m_ref);
+          const bool rose = vp != u.p0 && m_ref > m_prev;
+          const float o_scale = rose ? ex2_approx(m_prev - m_ref) : 1.f;
+          const uint32_t rose_mask = __ballot_sync(0xffffffffu, rose && real);
+          l *= ex2_approx(m_run - m_ref);
+          m_run = m_ref;
+          const int ps = static_cast<int>(j % C::kNP);
+          const uint32_t bar = mapa(smem_u32(&ctrl->p_full[ps]), orank);
+          const uint32_t prow = p_remote + ps * C::kPBytes + (r >> 3) * C::kPSbo + (r & 7) * 16;
+          float s4[4] = {0.f, 0.f, 0.f, 0.f};
+          uint4 pw[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float x = ex2_approx(fmaf(MLA_S(8 * c + 2 * k), c2, -m_ref));
+              const float y = ex2_approx(fmaf(MLA_S(8 * c + 2 * k + 1), c2, -m_ref));
+              s4[k] += x + y;  // the sum takes P before its bf16 rounding (half a step: 2^-8 relative, either sign)
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+              w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            pw[c] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+#undef MLA_S
+          if (!mbar_wait_warp<true, true>(smem_u32(&ctrl->p_empty[ps]), ((j / C::kNP) & 1) ^ 1, abort, p.timeout_ns)) {
+            ok = false;
+            why = kWaitPEmpty;
+            break;
+          }
+#pragma unroll
+          for (int c = 0; c < 8; ++c) st_async_v4(prow + c * C::kPLbo, pw[c], bar);
+          st_async_b32(ref_remote + (ps * kRows + r) * 4, __float_as_uint(o_scale), bar);
+          if (lane == 0) st_async_b32(flag_remote + (ps * 4 + (warp & 3)) * 4, rose_mask, bar);
+          l += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+        }
+        if (!ok) break;
+        if (!mbar_wait_warp<true, true>(smem_u32(&ctrl->ml_empty), (un & 1) ^ 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitMlEmpty;
+          break;
+        }
+        float* ml = reinterpret_cast<float*>(data + C::kMlOff);
+        ml[4 * r + 2 * gg] = m_run;
+        ml[4 * r + 2 * gg + 1] = l;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mlfull_remote);
+        ++un;
+      }
+      if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
+    }
+  } else {
+    // =========================== O CTA ===========================
+    uint8_t* vring = data + C::kVOff;
+    uint8_t* raw = data + C::kRawOff;
+    if (warp == 0) {
+      if (lane == 0) produce_o<kF8, kCg>(p, ctrl, kF8 ? raw : vring, &tm_o, cid, pr);
+    } else if (warp == 1) {
+      // ---- PV: each O CTA's warp waits until page j is ready here (V and P
+      // landed, O free on a unit's first page), has its rows of O rescaled
+      // where a reference rose, zeroes the slots past the sequence's end; the
+      // leader then waits for the other CTA and issues PV for both.
+      UnitIter it;
+      it.init(p, cid);
+      Unit u;
+      uint32_t j = 0, un = 0, nreq = 0;
+      bool ok = true;
+      int why = 0;
+      const volatile uint32_t* flags = reinterpret_cast<const volatile uint32_t*>(data + C::kFlagOff);
+      if (lane == 0)
+        for (int k = 0; k < C::kNP; ++k) mbar_expect_tx(smem_u32(&ctrl->p_full[k]), C::kPTx);
+      __syncwarp();
+      while (ok && it.next(u)) {
+        for (int vp = u.p0; vp < u.p1; ++vp, ++j) {
+          const int vs = static_cast<int>(j % C::kNV);
+          const int ps = static_cast<int>(j % C::kNP);
+          const bool first = vp == u.p0;
+          {
+            const uint32_t vbar = kF8 ? smem_u32(&ctrl->v_full[vs & 3]) : smem_u32(&ctrl->kv_full[vs]);
+            const uint32_t bars[4] = {first ? smem_u32(&ctrl->o_empty) : 0u, vbar, smem_u32(&ctrl->p_full[ps]), 0u};
+            const uint32_t pars[4] = {(un & 1) ^ 1, (j / C::kNV) & 1, (j / C::kNP) & 1, 0u};
+            if (!mbar_wait4_warp(bars, pars, abort, p.timeout_ns)) {
+              ok = false;
+              why = kWaitPage;
+              break;
+            }
+          }
+          const uint32_t fw = lane < 4 ? flags[ps * 4 + lane] : 0u;
+          if (__any_sync(0xffffffffu, fw != 0u)) {
+            if (lane == 0) {
+              ctrl->resc_page = j;
+              mbar_arrive(smem_u32(&ctrl->resc_req));
+            }
+            if (!mbar_wait_warp(smem_u32(&ctrl->resc_done), nreq & 1, abort, p.timeout_ns)) {
+              ok = false;
+              why = kWaitRescDone;
+              break;
+            }
+            ++nreq;
+          }
+          // this phase is done: arm the slot for page j + kNP, whose bytes
+          // come only after PV(j)
+          if (lane == 0) mbar_expect_tx(smem_u32(&ctrl->p_full[ps]), C::kPTx);
+          uint8_t* slot = vring + vs * C::kSlotV;
+          if constexpr (!kF8) {
+            const int valid = u.k.len - real_page(u.k, vp) * kPage;
+            if (valid < kPage) {
+              const int v0 = valid > 0 ? valid : 0;
+              for (int row = v0 + (lane >> 3); row < kPage; row += 4)
+#pragma unroll
+                for (int box = 0; box < C::kVBoxes; ++box)
+                  *reinterpret_cast<uint4*>(slot + box * C::kVBox + row * 128 + (lane & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+              __syncwarp();
+            }
+          }
+          fence_proxy_async_cta();
+          tc_fence_after();
+          if (kCg == 2 && !leader) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&ctrl->peer_pv[ps]), kCg));
+            continue;
+          }
+          if (kCg == 2) {
+            if (!mbar_wait_warp(smem_u32(&ctrl->peer_pv[ps]), (j / C::kNP) & 1, abort, p.timeout_ns)) {
+              ok = false;
+              why = kWaitPeerPv;
+              break;
+            }
+            tc_fence_after();
+          }
+          const uint64_t dv = smem_desc(smem_u32(slot), C::kVBox, 1024, kSwizzle128B);
+          const uint64_t dp = smem_desc(smem_u32(data + ps * C::kPBytes), C::kPLbo, C::kPSbo, kSwizzleNone);
+          // MMA h: N = 256 columns, each CTA's boxes (kVBoxes / 2) h ..
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss_cg<kCg>(tmem + h * 256, dp + static_cast<uint64_t>(k * (2 * C::kPLbo >> 4)),
+                             dv + static_cast<uint64_t>((h * (C::kVBoxes / 2) * C::kVBox + k * 2048) >> 4),
+                             C::kIdescPV, (first && k == 0) ? 0u : 1u);
+          mma_commit_cg<kCg>(kF8 ? smem_u32(&ctrl->v_empty[vs & 3]) : smem_u32(&ctrl->kv_empty[vs]), kMaskO);
+          mma_commit_cg<kCg>(smem_u32(&ctrl->p_empty[ps]), kMaskAll);
+          if (vp == u.p1 - 1) mma_commit_cg<kCg>(smem_u32(&ctrl->o_full), kMaskO);
+        }
+        ++un;
+      }
+      if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
+      __syncwarp();
+      if (leader) {
+        mma_commit_cg<kCg>(smem_u32(&ctrl->drain), static_cast<uint16_t>(1u << rank));
+        if (lane == 0) {
+          const uint64_t t0 = globaltimer_ns();
+          while (!mbar_try_wait(smem_u32(&ctrl->drain), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+          }
+        }
+      }
+      __syncwarp();
+    } else if (kF8 && warp >= 8) {
+      // ---- e4m3: four warps expand each page's codes to bf16 (exact), into
+      // the layout that PV reads.  A lane takes 16 codes (one 16-byte chunk)
+      // at a time; four lanes a row, eight rows a warp, so that the two
+      // 16-byte stores of eight neighbouring lanes meet all banks once.
+      if constexpr (kF8) {
+        UnitIter it;
+        it.init(p, cid);
+        Unit u;
+        uint32_t j = 0;
+        bool ok = true;
+        int why = 0;
+        const int w = warp - 8, c4 = lane & 3, r8 = lane >> 2;
+        while (ok && it.next(u)) {
+          for (int vp = u.p0; vp < u.p1; ++vp, ++j) {
+            const int rs = static_cast<int>(j % C::kNStO), vs = static_cast<int>(j % C::kNV);
+            if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->kv_full[rs]), (j / C::kNStO) & 1, abort, p.timeout_ns)) {
+              ok = false;
+              why = kWaitRaw;
+              break;
+            }
+            if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->v_empty[vs]), ((j / C::kNV) & 1) ^ 1, abort,
+                                             p.timeout_ns)) {
+              ok = false;
+              why = kWaitVEmpty;
+              break;
+            }
+            const uint8_t* src = raw + rs * C::kSlotRaw;
+            uint8_t* dst = vring + vs * C::kSlotV;
+            const int valid = u.k.len - real_page(u.k, vp) * kPage;
+#pragma unroll 2
+            for (int t = 0; t < C::kRawBoxes * 2 * 8 / 4; ++t) {
+              // warp w: item w + 4 t = (rows 8 ro .., half box hb)
+              const int item = w + 4 * t;
+              const int ro = item & 7, hb = item >> 3;
+              const int row = ro * 8 + r8;
+              const int chunk = (hb & 1) * 4 + c4;  // of the raw box's row
+              uint4 v = make_uint4(0, 0, 0, 0);  // slots past the sequence's end may hold anything
+              if (row < valid)
+                v = *reinterpret_cast<const uint4*>(src + (hb >> 1) * C::kVBox + row * 128 + ((chunk ^ (row & 7)) << 4));
+              const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+              uint32_t o[8];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int h2 = 0; h2 < 2; ++h2) {
+                  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                      static_cast<__nv_fp8x2_storage_t>(in[k] >> (16 * h2)), __NV_E4M3);
+                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x, f.y);
+                  o[2 * k + h2] = *reinterpret_cast<const uint32_t*>(&b2);
+                }
+              uint8_t* d = dst + hb * C::kVBox + row * 128;  // half a raw box = one box of 64 values
+              *reinterpret_cast<uint4*>(d + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+              *reinterpret_cast<uint4*>(d + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+            fence_proxy_async_cta();
+            __syncwarp();
+            if (lane == 0) {
+              mbar_arrive(smem_u32(&ctrl->kv_empty[rs]));
+              mbar_arrive(smem_u32(&ctrl->v_full[vs]));
+            }
+          }
+        }
+        if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
+      }
+    } else if (warp >= 4) {
+      // ---- lazy O rescale and epilogue: thread r owns columns [c0, c1) of row r
+      const int r = (warp & 3) * 32 + lane;
+      constexpr int kCols = C::kCorrWarps == 8 ? 256 : 512;
+      const int c0 = C::kCorrWarps == 8 ? ((warp - 4) >> 2) * 256 : 0;
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const float* factors = reinterpret_cast<const float*>(data + C::kRefOff);
+      const uint32_t ml_remote = mapa(smem_u32(data + C::kMlOff), static_cast<uint32_t>(pr));
+      const uint32_t mlempty_remote = mapa(smem_u32(&ctrl->ml_empty), static_cast<uint32_t>(pr));
+      const int br = pr * kRows + r;
+      UnitIter it;
+      it.init(p, cid);
+      Unit u;
+      uint32_t un = 0, nreq = 0, j = 0;
+      bool ok = true;
+      int why = 0;
+      while (ok && it.next(u)) {
+        const uint64_t t_unit = globaltimer_ns();
+        while (true) {
+          bool req = false, done = false;
+          while (true) {
+            req = mbar_try_wait(smem_u32(&ctrl->resc_req), nreq & 1);
+            done = !req && mbar_try_wait(smem_u32(&ctrl->o_full), un & 1);
+            if (__any_sync(0xffffffffu, req || done)) break;
+            if (__any_sync(0xffffffffu, *abort || globaltimer_ns() - t_unit > p.timeout_ns)) break;
+            __nanosleep(32);
+          }
+          req = __any_sync(0xffffffffu, req);
+          done = !req && __any_sync(0xffffffffu, done);
+          if (!req && !done) {
+            ok = false;
+            why = kWaitOFull;
+            break;
+          }
+          if (done) break;
+          const uint32_t jr = *reinterpret_cast<volatile uint32_t*>(&ctrl->resc_page);
+          const float a = br < u.k.nrows ? factors[(jr % C::kNP) * kRows + r] : 1.f;
+          if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->p_empty[(jr - 1) % C::kNP]), ((jr - 1) / C::kNP) & 1, abort,
+                                           p.timeout_ns)) {
+            ok = false;
+            why = kWaitPvPrev;
+            break;
+          }
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, a != 1.f)) {
+            for (int c = c0; c < c0 + kCols; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(tmem + lane_base + c, v);
+              tmem_wait_ld_tie(v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * a);
+              tmem_st16(tmem + lane_base + c, v);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctrl->resc_done));
+          ++nreq;
+        }
+        if (!ok) break;
+        j += static_cast<uint32_t>(u.p1 - u.p0);
+        if (!mbar_wait_warp<true, true>(smem_u32(&ctrl->ml_full), un & 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitMlFull;
+          break;
+        }
+        tc_fence_after();
+        const float m0 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r));
+        const float l0 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 4));
+        const float m1 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 8));
+        const float l1 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 12));
+        const float m_log2 = fmaxf(m0, m1);
+        const float l = l0 * ex2_approx(m0 - m_log2) + l1 * ex2_approx(m1 - m_log2);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mlempty_remote);
+        store_row<kF8, kCg>(p, u, br, c0, c0 + kCols, tmem + lane_base, m_log2, l);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->o_empty));
+        ++un;
+      }
+      if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the leaders' MMAs that read the other CTAs' memory are done
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc_cg<kCg>(tmem, 512);
+  cluster_sync();
+}
+
+// ----------------------------------------------------------------- combine
+// Merges the partials of every block that slice boundaries cut: column c
+// takes the block that starts in cluster c's slice (or exactly at its start)
+// and goes on behind it, if there is one.  A warp per row; lane l holds the
+// log-sum-exps of the pieces of clusters c + l, c + l + 32, c + l + 64, then
+// the warp walks the pieces in order, so that results never depend on timing.
+constexpr int kCombineWarps = 4;
+
+__global__ void __launch_bounds__(kCombineWarps * 32) mla_chunk_combine_kernel(const __grid_constant__ Params p) {
+  const int c = blockIdx.x;
+  griddep_wait();
+  const int s = p.cinfo[4 * c], e = p.cinfo[4 * c + 1];
+  if (s >= e) return;
+  const int n = p.cinfo[4 * c + 3];
+  const int pb0 = p.prefix[n], pb1 = p.prefix[n + 1];
+  if (pb1 <= e || pb0 < s) return;  // ends here, or started in an earlier slice
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Block k = p.blk[n];
+  const int br = blockIdx.y * kCombineWarps + warp;
+  if (br >= k.nrows) return;
+  int slot[3];
+  float ls[3];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const int cc = c + 32 * q + lane;
+    slot[q] = -1;
+    ls[q] = -INFINITY;
+    if (cc < p.C) {
+      const int cs = p.cinfo[4 * cc], ce = p.cinfo[4 * cc + 1];
+      if (cs < ce && cs < pb1) {
+        slot[q] = 2 * cc + (p.cinfo[4 * cc + 2] != n ? 1 : 0);
+        ls[q] = p.lse_part[static_cast<int64_t>(slot[q]) * p.BR + br];
+      }
+    }
+    mx = ls[q] > mx || ls[q] != ls[q] ? ls[q] : mx;  // a NaN stays
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float y = __shfl_xor_sync(0xffffffffu, mx, o);
+    mx = (y > mx || y != y) ? y : mx;
+  }
+  const float base = mx == -INFINITY ? 0.f : mx;
+  float w[3], z = 0.f;
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    w[q] = slot[q] >= 0 ? ex2_approx((ls[q] - base) * kLog2e) : 0.f;
+    z += w[q];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  float4 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const unsigned have = __ballot_sync(0xffffffffu, slot[q] >= 0);
+    for (unsigned m = have; m; m &= m - 1) {
+      const int src = __ffs(m) - 1;
+      const float wf = __shfl_sync(0xffffffffu, w[q], src) * inv;
+      const int sl = __shfl_sync(0xffffffffu, slot[q], src);
+      if (wf == 0.f) continue;
+      const float4* o = reinterpret_cast<const float4*>(p.o_part + (static_cast<int64_t>(sl) * p.BR + br) * kDL);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const float4 x = o[lane + 32 * g];
+        acc[g].x += wf * x.x; acc[g].y += wf * x.y; acc[g].z += wf * x.z; acc[g].w += wf * x.w;
+      }
+    }
+  }
+  const int64_t orow = static_cast<int64_t>(k.row0) + br;
+  uint2* dst = reinterpret_cast<uint2*>(p.out + orow * kDL * 2);
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[g].x, acc[g].y);
+    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[g].z, acc[g].w);
+    dst[lane + 32 * g] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+  if (lane == 0) p.lse[orow] = z == 0.f ? -INFINITY : base + __logf(z);
+}
+
+}  // namespace chunk
+}  // namespace mla

@@ -458,4 +458,77 @@ __device__ __forceinline__ float ex2_approx(float x) {
   return y;
 }
 
+// ------------------------------------------------- CTA-pair (kCg = 1 or 2)
+// The tcgen05 ops of a kernel that runs with kCg CTAs per MMA: kCg = 2 pairs
+// CTAs 2k and 2k + 1 of the cluster on one MMA of M = 256 rows (128 in each
+// CTA's TMEM), each CTA's shared memory holding half of B's N.  The leader
+// (even rank) issues; every op of one kernel uses the same kCg.
+template <int kCg>
+__device__ __forceinline__ void tmem_alloc_cg(uint32_t dst_smem, uint32_t ncols) {
+  if constexpr (kCg == 2)
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols)
+                 : "memory");
+  else
+    tmem_alloc(dst_smem, ncols);
+}
+template <int kCg>
+__device__ __forceinline__ void tmem_relinquish_cg() {
+  if constexpr (kCg == 2)
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  else
+    tmem_relinquish();
+}
+template <int kCg>
+__device__ __forceinline__ void tmem_dealloc_cg(uint32_t taddr, uint32_t ncols) {
+  if constexpr (kCg == 2)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+  else
+    tmem_dealloc(taddr, ncols);
+}
+template <bool kF8, int kCg>
+__device__ __forceinline__ void mma_ts_cg(uint32_t d, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  if constexpr (kCg == 1) {
+    mma_ts_e<kF8>(d, a_tmem, bdesc, idesc, acc);
+  } else if constexpr (kF8) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+// bf16 operands from shared memory
+template <int kCg>
+__device__ __forceinline__ void mma_ss_cg(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  if constexpr (kCg == 1) {
+    mma_ss_e<false>(d, adesc, bdesc, idesc, acc);
+  } else {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  }
+}
+// One arrival on the barrier at this offset in every CTA of `cta_mask` when
+// the MMAs issued so far by this warp's elected lane are done.
+template <int kCg>
+__device__ __forceinline__ void mma_commit_cg(uint32_t bar, uint16_t cta_mask) {
+  if constexpr (kCg == 1)
+    mma_commit_multicast_e(bar, cta_mask);
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(bar),
+        "h"(cta_mask)
+        : "memory");
+}
+
 }  // namespace mla
