@@ -24,14 +24,17 @@
 // MMAs of M = 256.  A pair's CTAs hold half of B each, so every SM copies in
 // and reads half the page bytes per MMA: at M = 128 the S CTA's page copies
 // and operand reads (72 KB each per 1152 tensor cycles) alone take the 128
-// bytes a cycle that shared memory has.
+// bytes a cycle that shared memory has.  A pair scores 128 keys at a time
+// (one page in each S CTA): an MMA of N = 64 lasts 32 cycles, no longer than
+// its issue takes, so that every wait of the issuing warp (~200 cycles each)
+// left the tensor pipe idle; at N = 128 the queue covers the waits.
 //
 // An e4m3 cache: QK runs on the codes as they are (kind::f8f6f4), the queries
 // as two e4m3 terms hi + lo of q / 2^k.  A bf16 value has 8 significant bits
 // and hi + lo hold 4 + 4, so with a power-of-two row scale the split is exact
 // down to 2^-10 of the row's largest value and scores are as exact as with a
-// bf16 cache.  PV runs in bf16: four warps of the O CTA expand the codes
-// (exact in bf16) into the V ring, and P keeps bf16's range (P as e4m3 terms
+// bf16 cache.  PV runs in f16: four warps of the O CTA expand the codes
+// (exact in f16) into the V ring, and P keeps f16's range (P as e4m3 terms
 // loses the many small weights of a long row to subnormals).
 #pragma once
 
@@ -53,32 +56,57 @@ constexpr int kDR = 64;
 constexpr int kRows = 128;    // rows per CTA
 // warps: 0 TMA, 1 MMA, 2 TMEM alloc, 3 idle, 4-11 row warps
 constexpr int kThreads = 384;
-constexpr int kNS = 3;        // S buffers of 64 TMEM columns
-constexpr uint32_t kSCol0 = 320;  // queries use columns 0..287
-constexpr uint32_t kQLoCol = 144;  // e4m3: the lo terms' first column
+constexpr int kMaxSB = 3;      // S buffers
 constexpr int kCtrlBytes = 640;
 constexpr int kMaxStages = 10;
 constexpr int kMaxP = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kMinusBig = -1.0e30f;  // running-maximum start (finite: no inf - inf)
-// O is rescaled only when a row's maximum grows by more than 2^8 (log2
-// units); P then stays below 2^8, which bf16 and the fp32 sums hold easily
-constexpr float kThreshold = 8.0f;
+// O is rescaled (a round trip through TMEM that stalls PV: ~1.3 us) only when
+// a row's maximum grows by more than 2^threshold over its reference.  P and
+// the fp32 sums then reach 2^threshold; a float's relative precision does not
+// depend on it.  bf16 P has fp32's range, so the threshold only has to keep
+// sums and outputs finite (2^40 N |v| stays far below 2^127).  f16 P (e4m3
+// cache) ends at 2^16.  A low first reference is common: a page of four sink
+// tokens comes first, and with a threshold of 8 a window of 2048 tokens
+// rescaled on 15 of its 34 pages.
+template <bool kF8>
+struct Rescale {
+  static constexpr float kThreshold = kF8 ? 14.0f : 40.0f;
+};
 constexpr int kMaxClusters = 96;       // the combine's lanes take 3 clusters each
+
+// PV: f16 operands with an e4m3 cache, else bf16 (format 0 and 1 of kind::f16)
+constexpr uint32_t make_idesc_pv(bool f16, uint32_t m) {
+  return make_idesc(false, m, 256, false, true) & ~(f16 ? (1u << 7) | (1u << 10) : 0u);
+}
 
 template <bool kF8, int kCg>
 struct Cfg {
-  // S CTA: kKeys rows of every page (all of B's N for kCg = 1, half for 2)
-  static constexpr int kKeys = kPage / kCg;
-  static constexpr int kSBoxes = kF8 ? 4 : 9;            // 128-byte columns of a row in the 3-D box
-  static constexpr int kSBoxBytes = kKeys * 128;
-  static constexpr int kPeBytes = kF8 ? kKeys * 64 : 0;  // e4m3 k_pe, 64-byte rows by a map of their own
-  static constexpr int kSlotS = kSBoxes * kSBoxBytes + kPeBytes;
-  static constexpr int kNStS = kF8 ? (kCg == 1 ? 6 : 10) : (kCg == 1 ? 3 : 6);
-  // ring entries of a block's bf16 query rows (1152 bytes each)
-  static constexpr int kQRows = kSlotS / 1152;
-  static constexpr int kQEntries = kRows / kQRows;
+  // S CTA: a score tile is kCg pages, one 64-key page of it in each S CTA of
+  // the pair (kCg = 2: one MMA covers N = 128 keys).  A page arrives in kParts
+  // ring slots of kPartBoxes 128-byte columns each.
+  static constexpr int kBox = 8192;                      // 64 rows x 128 bytes
+  static constexpr int kSBoxes = kF8 ? 4 : 9;            // columns of a page in the 3-D box
+  static constexpr int kPeBytes = kF8 ? 4096 : 0;        // e4m3 k_pe, 64-byte rows by a map of their own
+  static constexpr int kParts = (kCg == 2 && !kF8) ? 3 : 1;
+  static constexpr int kPartBoxes = kSBoxes / kParts;
+  static constexpr int kSlotS = kPartBoxes * kBox + kPeBytes;
+  static constexpr int kNStS = kF8 ? (kCg == 1 ? 6 : 4) : (kCg == 1 ? 3 : 7);
+  // TMEM columns: queries, then kNSB score buffers of a tile each.  A pair
+  // keeps the rope part of the queries in shared memory (A of its QK steps),
+  // which leaves 256 columns for two tiles of 128 keys.
+  static constexpr bool kPeSmem = kCg == 2;
+  static constexpr uint32_t kSCol0 = kCg == 1 ? 320 : 256;
+  static constexpr int kNSB = kCg == 1 ? 3 : 2;
+  static constexpr uint32_t kTileCols = 64 * kCg;
+  static constexpr uint32_t kQLoCol = kCg == 1 ? 144 : 128;  // e4m3: the lo terms' first column
+  // ring entries of a block's bf16 query rows.  bf16 pair: q_nope of 64 rows
+  // like a page (parts of 3, 3 and 2 boxes), q_pe straight into its tile;
+  // else kQRows rows with q_pe as a ninth box
+  static constexpr int kQRows = kParts == 3 ? 64 : kSlotS / 1152;
+  static constexpr int kQEntries = kParts * kRows / kQRows;
   // O CTA: 512 / kCg latent dimensions of every page
   static constexpr int kVDims = kDL / kCg;
   static constexpr int kVBox = 8192;                     // 64 keys x 128 bytes
@@ -95,10 +123,14 @@ struct Cfg {
   // P: K-major without swizzle, core matrices of 8 rows x 16 bytes; the
   // 16-byte chunk c of row r at (r / 8) * 1024 + c * 128 + (r % 8) * 16
   static constexpr uint32_t kPLbo = 128, kPSbo = 1024;
-  static constexpr uint32_t kIdescQK = make_idesc(kF8, 128 * kCg, 64, false, false);
-  static constexpr uint32_t kIdescPV = make_idesc(false, 128 * kCg, 256, false, true);
+  static constexpr uint32_t kIdescQK = make_idesc(kF8, 128 * kCg, 64 * kCg, false, false);
+  static constexpr uint32_t kIdescPV = make_idesc_pv(kF8, 128 * kCg);
   // shared memory
-  static constexpr int kMlOff = kNStS * kSlotS;          // S: (m0, l0, m1, l1)[128]
+  // S: the rope parts of the queries (bf16: two units' tiles of 128 rows x
+  // 128 bytes, swizzled by TMA; e4m3: hi and lo tiles of 128 rows x 64 codes)
+  static constexpr int kQPeOff = kNStS * kSlotS;
+  static constexpr int kQPeTile = kF8 ? 8192 : 16384;
+  static constexpr int kMlOff = kQPeOff + (kPeSmem ? 2 * kQPeTile : 0);  // S: (m0, l0, m1, l1)[128]
   static constexpr int kPubOff = kMlOff + kRows * 16;    // S: row references of the last 4 pages
   static constexpr int kDataS = kPubOff + 4 * kRows * 8;
   static constexpr int kVOff = kNP * kPBytes;            // O: P slots, V ring, raw ring, row factors, flags
@@ -114,7 +146,10 @@ struct Cfg {
   // or by 4 where the other 4 expand the e4m3 pages
   static constexpr int kCorrWarps = kF8 ? 4 : 8;
   static_assert(kSmem <= 232448, "shared memory budget");
-  static_assert(kQEntries <= kNStS && kNStS <= kMaxStages && 2 * (kQEntries + 1) >= kNStS, "query entries");
+  // a unit's query entries fit the ring, and two units' entries are more than
+  // the ring holds: what unit n + 2 overwrites, unit n + 1 has released
+  static_assert(kQEntries <= kNStS && kNStS <= kMaxStages && kQEntries + kParts >= kNStS / 2 + 1, "query entries");
+  static_assert(!kPeSmem || kQEntries + kParts >= kNStS, "a pair's rope tiles");
 };
 
 struct __align__(8) Ctrl {
@@ -122,8 +157,8 @@ struct __align__(8) Ctrl {
   uint64_t kv_empty[kMaxStages];
   uint64_t peer_kv[kMaxStages];  // S leader: the other S CTA's entry has landed
   uint64_t q_bar[2];             // query rows of the unit landed (alternating units)
-  uint64_t s_full[kNS];
-  uint64_t s_empty[kNS];         // S leader: both CTAs read the S buffer
+  uint64_t s_full[kMaxSB];
+  uint64_t s_empty[kMaxSB];         // S leader: both CTAs read the S buffer
   uint64_t q_full;               // S leader: queries in TMEM (both CTAs)
   uint64_t p_full[kMaxP];
   uint64_t p_empty[kMaxP];
@@ -415,7 +450,8 @@ __device__ __forceinline__ void drain_ring(Ctrl* ctrl, uint32_t i, uint64_t time
 
 // TMA producer of an S CTA: per unit its query rows (kQEntries ring entries,
 // completing on q_bar; the entries' own barriers complete by a plain arrival,
-// so that their phases keep in step), then kKeys rows of every page.
+// so that their phases keep in step), then its page of every tile (a unit's
+// odd last tile has none for the second CTA: its entries only arrive).
 template <bool kF8, int kCg>
 __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUtensorMap* tm_s, const CUtensorMap* tm_pe,
                           const CUtensorMap* tm_qn, const CUtensorMap* tm_qp, int cid, int pr) {
@@ -438,6 +474,7 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
   uint32_t qloaded = 0;
   while (ok && it.next(u)) {
     const uint32_t qbar = smem_u32(&ctrl->q_bar[un & 1]);
+    const int row0 = u.k.row0 + pr * kRows;
     for (int e = 0; e < C::kQEntries; ++e) {
       if (!acquire()) {
         ok = false;
@@ -446,24 +483,47 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
       if (e == 0) {
         mbar_expect_tx(qbar, static_cast<uint32_t>(kRows * 1152));
         qloaded = un + 1;
+        if constexpr (C::kParts == 3)
+          tma_load_2d(smem_u32(ring + C::kQPeOff + (un & 1) * C::kQPeTile), tm_qp, 0, row0, qbar);
       }
       mbar_arrive(bar);
-      const int row = u.k.row0 + pr * kRows + C::kQRows * e;
-      tma_load_3d(smem_u32(slot), tm_qn, 0, row, 0, qbar);
-      tma_load_2d(smem_u32(slot + C::kQRows * 128 * 8), tm_qp, 0, row, qbar);
+      if constexpr (C::kParts == 3) {
+        // boxes 3 (e % 3) .. of 64 rows; the third part's last box would be
+        // past the map's 8: it reads zeros, which count as copied bytes too,
+        // so its two boxes come one by one
+        const int row = row0 + 64 * (e / 3), part = e % 3;
+        if (part < 2) {
+          tma_load_3d(smem_u32(slot), tm_qn, 0, row, 3 * part, qbar);
+        } else {
+          tma_load_2d(smem_u32(slot), tm_pe, 64 * 6, row, qbar);
+          tma_load_2d(smem_u32(slot + C::kBox), tm_pe, 64 * 7, row, qbar);
+        }
+      } else {
+        const int row = row0 + C::kQRows * e;
+        tma_load_3d(smem_u32(slot), tm_qn, 0, row, 0, qbar);
+        tma_load_2d(smem_u32(slot + C::kQRows * 128 * 8), tm_qp, 0, row, qbar);
+      }
       ++i;
     }
     ++un;
-    for (int v = u.p0; v < u.p1 && ok; ++v) {
-      const int y = read_page_id(p, u.k.b, real_page(u.k, v)) * kPage + pr * C::kKeys;
-      if (!acquire()) {
-        ok = false;
-        break;
+    for (int vt = u.p0; vt < u.p1 && ok; vt += kCg) {
+      const int v = vt + pr;
+      const bool have = kCg == 1 || v < u.p1;
+      const int y = have ? read_page_id(p, u.k.b, real_page(u.k, v)) * kPage : 0;
+      for (int part = 0; part < C::kParts; ++part) {
+        if (!acquire()) {
+          ok = false;
+          break;
+        }
+        if (have) {
+          mbar_expect_tx(bar, static_cast<uint32_t>(C::kSlotS));
+          tma_load_3d(smem_u32(slot), tm_s, 0, y, part * C::kPartBoxes, bar);
+          if constexpr (kF8) tma_load_2d(smem_u32(slot + C::kSBoxes * C::kBox), tm_pe, kDL, y, bar);
+        } else {
+          mbar_arrive(bar);
+        }
+        ++i;
       }
-      mbar_expect_tx(bar, static_cast<uint32_t>(C::kSlotS));
-      tma_load_3d(smem_u32(slot), tm_s, 0, y, 0, bar);
-      if constexpr (kF8) tma_load_2d(smem_u32(slot + C::kSBoxes * C::kSBoxBytes), tm_pe, kDL, y, bar);
-      ++i;
     }
   }
   if (!ok) raise_timeout<kCg>(p, ctrl, kWaitProdS, i);
@@ -506,21 +566,28 @@ __device__ void produce_o(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
   drain_ring<C::kNStO>(ctrl, i, p.timeout_ns);
 }
 
-// Query row r from the ring entries into TMEM lane r (bf16): chunks
-// [36 half, 36 half + 36) of 16 bytes; chunk c sits in box c / 8, piece c % 8
-// of the 128-byte-swizzled row.
-template <int kBoxBytes>
-__device__ __forceinline__ void q_row_bf16(const uint8_t* src, int rq, uint32_t taddr, int c0) {
+// Where 16-byte chunk c of query row r of this CTA sits in the ring (c / 8:
+// box, c % 8: piece of the 128-byte-swizzled row), first entry i.
+template <bool kF8, int kCg>
+__device__ __forceinline__ const uint8_t* q_chunk(const uint8_t* ring, uint32_t i, int r, int c) {
+  using C = Cfg<kF8, kCg>;
+  const int e = r / C::kQRows, rq = r % C::kQRows, box = c >> 3;
+  const uint32_t entry = C::kParts == 3 ? i + 3 * e + box / 3 : i + e;
+  const int in_slot = C::kParts == 3 ? box % 3 : box;
+  return ring + (entry % C::kNStS) * C::kSlotS + in_slot * (C::kQRows * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4);
+}
+
+// Query row r into TMEM lane r (bf16): 16-byte chunks [c0, c0 + kN).
+template <int kCg, int kN>
+__device__ __forceinline__ void q_row_bf16(const uint8_t* ring, uint32_t i, int r, uint32_t taddr, int c0) {
+  constexpr int kStep = kN % 12 == 0 ? 12 : 8;
 #pragma unroll
-  for (int c = 0; c < 36; c += 12) {
-    uint4 v[12];
+  for (int c = 0; c < kN; c += kStep) {
+    uint4 v[kStep];
 #pragma unroll
-    for (int k = 0; k < 12; ++k) {
-      const int cc = c0 + c + k;
-      v[k] = *reinterpret_cast<const uint4*>(src + (cc >> 3) * kBoxBytes + (((cc & 7) ^ (rq & 7)) << 4));
-    }
+    for (int k = 0; k < kStep; ++k) v[k] = *reinterpret_cast<const uint4*>(q_chunk<false, kCg>(ring, i, r, c0 + c + k));
 #pragma unroll
-    for (int s4 = 0; s4 < 3; ++s4) {
+    for (int s4 = 0; s4 < kStep / 4; ++s4) {
       const uint32_t w[16] = {v[4 * s4].x,     v[4 * s4].y,     v[4 * s4].z,     v[4 * s4].w,
                               v[4 * s4 + 1].x, v[4 * s4 + 1].y, v[4 * s4 + 1].z, v[4 * s4 + 1].w,
                               v[4 * s4 + 2].x, v[4 * s4 + 2].y, v[4 * s4 + 2].z, v[4 * s4 + 2].w,
@@ -534,13 +601,18 @@ __device__ __forceinline__ void q_row_bf16(const uint8_t* src, int rq, uint32_t 
 // The same for an e4m3 cache: the row as hi + lo e4m3 terms of q / scale.
 // scale is the power of two that puts the row's largest |q| into [2^7, 2^8)
 // (2^-107 at least, so that its reciprocal stays finite); groups of 8 chunks
-// [g0, g1).  Returns scale (NaN for a row with an infinity or a NaN).
-template <int kBoxBytes>
-__device__ __forceinline__ float q_row_e4m3(const uint8_t* src, int rq, uint32_t taddr, int g0, int g1) {
+// [g0, g1), group 8 being the rope part, which a pair keeps in shared memory
+// (K-major core matrices: the 16-byte chunk c of row r at (r / 8) * 512 +
+// c * 128 + (r % 8) * 16).  Returns scale (NaN for a row with an infinity or
+// a NaN).
+template <int kCg>
+__device__ __forceinline__ float q_row_e4m3(const uint8_t* ring, uint32_t i, int r, uint32_t taddr, uint8_t* pe_tile,
+                                            int g0, int g1) {
+  using C = Cfg<true, kCg>;
   uint32_t m = 0;  // largest |q| as bf16 bits (two lanes); bf16 bits order as integers
 #pragma unroll 6
   for (int c = 0; c < 72; ++c) {
-    const uint4 v = *reinterpret_cast<const uint4*>(src + (c >> 3) * kBoxBytes + (((c & 7) ^ (rq & 7)) << 4));
+    const uint4 v = *reinterpret_cast<const uint4*>(q_chunk<true, kCg>(ring, i, r, c));
     m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
   }
   const uint32_t top = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
@@ -553,7 +625,7 @@ __device__ __forceinline__ float q_row_e4m3(const uint8_t* src, int rq, uint32_t
     uint32_t hi[16], lo[16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src + g * kBoxBytes + ((k ^ (rq & 7)) << 4));
+      const uint4 v = *reinterpret_cast<const uint4*>(q_chunk<true, kCg>(ring, i, r, 8 * g + k));
       const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int h2 = 0; h2 < 2; ++h2) {
@@ -573,10 +645,21 @@ __device__ __forceinline__ float q_row_e4m3(const uint8_t* src, int rq, uint32_t
         lo[2 * k + h2] = l[0] | (l[1] << 16);
       }
     }
-    tmem_st16(taddr + g * 16, hi);
-    tmem_st16(taddr + kQLoCol + g * 16, lo);
+    if (C::kPeSmem && g == 8) {
+      uint8_t* d = pe_tile + (r >> 3) * 512 + (r & 7) * 16;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        *reinterpret_cast<uint4*>(d + c * 128) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+        *reinterpret_cast<uint4*>(d + C::kQPeTile + c * 128) =
+            make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+      }
+    } else {
+      tmem_st16(taddr + g * 16, hi);
+      tmem_st16(taddr + C::kQLoCol + g * 16, lo);
+    }
   }
   tmem_wait_st();
+  if (C::kPeSmem) fence_proxy_async_cta();  // the rope tile is read by MMAs
   return top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : scale;
 }
 
@@ -665,9 +748,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctrl->peer_kv[i]), 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctrl->q_bar[i]), 1);
-    for (int i = 0; i < kNS; ++i) {
+    for (int i = 0; i < C::kNSB; ++i) {
       mbar_init(smem_u32(&ctrl->s_full[i]), 1);
-      mbar_init(smem_u32(&ctrl->s_empty[i]), 4 * kCg);
+      // the warps that read the tile: one group's four, or both groups' of both CTAs
+      mbar_init(smem_u32(&ctrl->s_empty[i]), kCg == 1 ? 4 : 16);
     }
     mbar_init(smem_u32(&ctrl->q_full), 8 * kCg);
     for (int i = 0; i < kMaxP; ++i) {
@@ -726,25 +810,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       UnitIter it;
       it.init(p, cid);
       Unit u;
-      uint32_t i = 0, j = 0, un = 0;
+      uint32_t i = 0, j = 0, un = 0;  // ring entries, tiles, units
       bool ok = true;
       int why = 0;
-      auto landed = [&]() -> bool {  // entry i of this CTA and, for the leader, of the other
+      // entry i of this CTA and, for the leader, of the other one have
+      // landed; `extra` is polled along with them (0: nothing)
+      auto landed = [&](uint32_t extra, uint32_t extra_parity) -> bool {
         const int st = static_cast<int>(i % C::kNStS);
         const uint32_t ph = (i / C::kNStS) & 1;
-        if (!mbar_wait_warp(smem_u32(&ctrl->kv_full[st]), ph, abort, p.timeout_ns)) {
+        if (!mbar_wait_all_warp(smem_u32(&ctrl->kv_full[st]), ph,
+                                kCg == 2 && leader ? smem_u32(&ctrl->peer_kv[st]) : 0u, ph, extra, extra_parity, 0u, 0u,
+                                abort, p.timeout_ns)) {
           why = kWaitKvS;
           return false;
         }
-        if (kCg == 2 && leader && !mbar_wait_warp(smem_u32(&ctrl->peer_kv[st]), ph, abort, p.timeout_ns)) {
-          why = kWaitPeerKv;
-          return false;
-        }
-        if (kCg == 2 && !leader && lane == 0) mbar_arrive_cluster(mapa(smem_u32(&ctrl->peer_kv[st]), 0));
+        if (kCg == 2 && !leader && lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctrl->peer_kv[st]), 0));
         return true;
       };
       while (ok && it.next(u)) {
-        for (int e = 0; e < C::kQEntries && ok; ++e, ++i) ok = landed();
+        for (int e = 0; e < C::kQEntries && ok; ++e, ++i) ok = landed(0u, 0u);
         if (!ok) break;
         if (leader) {
           if (!mbar_wait_warp(smem_u32(&ctrl->q_full), un & 1, abort, p.timeout_ns)) {
@@ -756,55 +840,65 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int e = C::kQEntries; e > 0; --e) {
               const uint32_t bar = smem_u32(&ctrl->kv_empty[(i - e) % C::kNStS]);
               mbar_arrive(bar);
-              if (kCg == 2) mbar_arrive_cluster(mapa(bar, 1));
+              if (kCg == 2) mbar_arrive_remote(mapa(bar, 1));
             }
           __syncwarp();
         }
+        const uint32_t qpe = smem_u32(ring + C::kQPeOff + (kF8 ? 0 : (un & 1) * C::kQPeTile));
         ++un;
-        for (int v = u.p0; v < u.p1; ++v, ++j, ++i) {
-          const int sb = static_cast<int>(j % kNS);
-          if (leader && !mbar_wait_warp(smem_u32(&ctrl->s_empty[sb]), ((j / kNS) & 1) ^ 1, abort, p.timeout_ns)) {
-            ok = false;
-            why = kWaitSFull;
-            break;
-          }
-          if (!landed()) {
-            ok = false;
-            break;
-          }
-          if (!leader) continue;
-          tc_fence_after();
-          const int st = static_cast<int>(i % C::kNStS);
-          const uint32_t slot_addr = smem_u32(ring + st * C::kSlotS);
-          const uint64_t dlat = smem_desc(slot_addr, 16, 1024, kSwizzle128B);
-          const uint32_t dcol = tmem + kSCol0 + sb * 64;
-          if constexpr (!kF8) {
+        for (int vt = u.p0; vt < u.p1 && ok; vt += kCg, ++j) {
+          const int sb = static_cast<int>(j % C::kNSB);
+          const uint32_t dcol = tmem + C::kSCol0 + sb * C::kTileCols;
 #pragma unroll
-            for (int d = 0; d < 9; ++d)
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                mma_ts_cg<false, kCg>(dcol, tmem + d * 32 + k * 8,
-                                      dlat + static_cast<uint64_t>(d * (C::kSBoxBytes >> 4) + k * 2), C::kIdescQK,
-                                      (d | k) ? 1u : 0u);
-          } else {
-            const uint64_t dpe = smem_desc(slot_addr + C::kSBoxes * C::kSBoxBytes, 16, 512, kSwizzle64B);
-#pragma unroll
-            for (int term = 0; term < 2; ++term) {
-              const uint32_t qcol = tmem + (term ? kQLoCol : 0u);
-#pragma unroll
-              for (int d = 0; d < 4; ++d)
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  mma_ts_cg<true, kCg>(dcol, qcol + d * 32 + k * 8,
-                                       dlat + static_cast<uint64_t>(d * (C::kSBoxBytes >> 4) + k * 2), C::kIdescQK,
-                                       (term | d | k) ? 1u : 0u);
-#pragma unroll
-              for (int k = 0; k < 2; ++k)
-                mma_ts_cg<true, kCg>(dcol, qcol + 128 + k * 8, dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
+          for (int part = 0; part < C::kParts; ++part, ++i) {
+            if (!landed(leader && part == 0 ? smem_u32(&ctrl->s_empty[sb]) : 0u, ((j / C::kNSB) & 1) ^ 1)) {
+              ok = false;
+              break;
             }
+            if (!leader) continue;
+            tc_fence_after();
+            const int st = static_cast<int>(i % C::kNStS);
+            const uint32_t slot_addr = smem_u32(ring + st * C::kSlotS);
+            const uint64_t dlat = smem_desc(slot_addr, 16, 1024, kSwizzle128B);
+            if constexpr (!kF8) {
+#pragma unroll
+              for (int d = 0; d < C::kPartBoxes; ++d)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const int box = part * C::kPartBoxes + d;
+                  const uint64_t db = dlat + static_cast<uint64_t>(d * (C::kBox >> 4) + k * 2);
+                  if (C::kPeSmem && box == 8)
+                    mma_ss_cg<kCg>(dcol, smem_desc(qpe, 16, 1024, kSwizzle128B) + static_cast<uint64_t>(k * 2), db,
+                                   C::kIdescQK, 1u);
+                  else
+                    mma_ts_cg<false, kCg>(dcol, tmem + box * 32 + k * 8, db, C::kIdescQK, (box | k) ? 1u : 0u);
+                }
+            } else {
+              const uint64_t dpe = smem_desc(slot_addr + C::kSBoxes * C::kBox, 16, 512, kSwizzle64B);
+#pragma unroll
+              for (int term = 0; term < 2; ++term) {
+                const uint32_t qcol = tmem + (term ? C::kQLoCol : 0u);
+#pragma unroll
+                for (int d = 0; d < 4; ++d)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    mma_ts_cg<true, kCg>(dcol, qcol + d * 32 + k * 8,
+                                         dlat + static_cast<uint64_t>(d * (C::kBox >> 4) + k * 2), C::kIdescQK,
+                                         (term | d | k) ? 1u : 0u);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  if constexpr (C::kPeSmem)
+                    mma_ss_f8_cg<kCg>(dcol, smem_desc(qpe + term * C::kQPeTile, 128, 512, kSwizzleNone) +
+                                                static_cast<uint64_t>(k * (256 >> 4)),
+                                      dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
+                  else
+                    mma_ts_cg<true, kCg>(dcol, qcol + 128 + k * 8, dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
+                }
+              }
+            }
+            mma_commit_cg<kCg>(smem_u32(&ctrl->kv_empty[st]), kMaskS);
           }
-          mma_commit_cg<kCg>(smem_u32(&ctrl->kv_empty[st]), kMaskS);
-          mma_commit_cg<kCg>(smem_u32(&ctrl->s_full[sb]), kMaskS);
+          if (ok && leader) mma_commit_cg<kCg>(smem_u32(&ctrl->s_full[sb]), kMaskS);
         }
       }
       if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
@@ -819,8 +913,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (warp >= 4) {
-      // ---- softmax: group gg (warps 4-7: 0, warps 8-11: 1) takes the pages
-      // j with j % 2 == gg, thread r row r of this CTA.  A page's reference
+      // ---- softmax: thread r of group gg (warps 4-7: 0, warps 8-11: 1) takes
+      // row r of this CTA, the groups alternate pages (tiles of one page, or
+      // one page each of a pair's tile of two).  A page's reference
       // is the previous page's, raised to the page's maximum where that
       // exceeds it by more than the threshold, so references depend on the
       // data alone; each group keeps its partial sum in its latest frame.
@@ -837,14 +932,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       UnitIter it;
       it.init(p, cid);
       Unit u;
-      uint32_t i = 0, j = 0, un = 0;
+      uint32_t i = 0, jt = 0, j0 = 0, un = 0;  // ring entries, tiles, pages of earlier units, units
+      uint32_t j = 0;                          // page
       bool ok = true;
       int why = 0;
       while (ok && it.next(u)) {
         // the unit's queries replace the previous unit's in TMEM once every
-        // QK of that unit is done: the S of its last page has landed
-        if (j > 0 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - 1) % kNS]), ((j - 1) / kNS) & 1, abort,
-                                                  p.timeout_ns)) {
+        // QK of that unit is done: the S of its last tile has landed
+        if (jt > 0 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(jt - 1) % C::kNSB]),
+                                                   ((jt - 1) / C::kNSB) & 1, abort, p.timeout_ns)) {
           ok = false;
           why = kWaitSPrev;
           break;
@@ -855,23 +951,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         float qs = 1.f;
-        {
-          const int e = r / C::kQRows, rq = r % C::kQRows;
-          const uint8_t* src = ring + ((i + e) % C::kNStS) * C::kSlotS + rq * 128;
-          if constexpr (kF8) {
-            if (gg == 0) qs = q_row_e4m3<C::kQRows * 128>(src, rq, tmem + lane_base, 0, 5);
-            else qs = q_row_e4m3<C::kQRows * 128>(src, rq, tmem + lane_base, 5, 9);
-          } else {
-            q_row_bf16<C::kQRows * 128>(src, rq, tmem + lane_base, 36 * gg);
-          }
+        if constexpr (kF8) {
+          uint8_t* pe_tile = data + C::kQPeOff;
+          qs = q_row_e4m3<kCg>(ring, i, r, tmem + lane_base, pe_tile, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9);
+        } else {
+          constexpr int kN = C::kPeSmem ? 32 : 36;
+          q_row_bf16<kCg, kN>(ring, i, r, tmem + lane_base, kN * gg);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          if (kCg == 2) mbar_arrive_cluster(mapa(smem_u32(&ctrl->q_full), 0));
+          if (kCg == 2) mbar_arrive_remote(mapa(smem_u32(&ctrl->q_full), 0));
           else mbar_arrive(smem_u32(&ctrl->q_full));
         }
-        i += C::kQEntries + static_cast<uint32_t>(u.p1 - u.p0);
+        i += C::kQEntries + C::kParts * static_cast<uint32_t>((u.p1 - u.p0 + kCg - 1) / kCg);
         const float c2 = p.scale * kLog2e * (kF8 ? qs * p.kv_scale : 1.f);
         const bool real = br < u.k.nrows;
         // padding rows follow the block's last row (their results go nowhere)
@@ -879,26 +972,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nvis = pos + 1;                                                     // sees t < nvis ...
         const int lo = p.window > 0 && nvis > p.window ? nvis - p.window : 0;         // ... and t >= lo or t < sinks
         float m_run = kMinusBig, l = 0.f;
-        for (int vp = u.p0; vp < u.p1; ++vp, ++j) {
-          if ((j & 1u) != static_cast<uint32_t>(gg)) continue;
-          const int sb = static_cast<int>(j % kNS);
-          if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (j / kNS) & 1, abort, p.timeout_ns)) {
+        for (int vt = u.p0; vt < u.p1; vt += kCg, ++jt) {
+          if (kCg == 1 && (jt & 1u) != static_cast<uint32_t>(gg)) continue;
+          const int vp = kCg == 1 ? vt : vt + gg;
+          j = j0 + static_cast<uint32_t>(vp - u.p0);
+          const int sb = static_cast<int>(jt % C::kNSB);
+          if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (jt / C::kNSB) & 1, abort, p.timeout_ns)) {
             ok = false;
             why = kWaitSFull;
             break;
+          }
+          if (kCg == 2 && vp >= u.p1) {  // an odd unit's last tile holds one page
+            if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctrl->s_empty[sb]), 0));
+            continue;
           }
           tc_fence_after();
           uint32_t v[4][16];
           float red[4];
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4)
-            tmem_ld16_max(tmem + lane_base + kSCol0 + sb * 64 + q4 * 16, v[q4], red[q4]);
+            tmem_ld16_max(tmem + lane_base + C::kSCol0 + sb * C::kTileCols + (kCg == 2 ? gg * 64 : 0) + q4 * 16, v[q4],
+                          red[q4]);
 #pragma unroll
           for (int q4 = 0; q4 < 4; ++q4) tmem_wait_ld_tie(v[q4], red[q4]);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) {
-            if (kCg == 2) mbar_arrive_cluster(mapa(smem_u32(&ctrl->s_empty[sb]), 0));
+            if (kCg == 2) mbar_arrive_remote(mapa(smem_u32(&ctrl->s_empty[sb]), 0));
             else mbar_arrive(smem_u32(&ctrl->s_empty[sb]));
           }
           const int t0 = real_page(u.k, vp) * kPage;
@@ -938,9 +1038,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             m_prev = __uint_as_float(static_cast<uint32_t>(pv));
             m_ref = fmaxf(m_ref, m_prev);
           }
-          if (mx > m_ref + kThreshold) m_ref = mx;
+          if (mx > m_ref + Rescale<kF8>::kThreshold) m_ref = mx;
           pub[(j & 3u) * kRows + r] = (static_cast<uint64_t>(j + 1u) << 32) | __float_as_uint(m_ref);
-          const bool rose = vp != u.p0 && m_ref > m_prev;
+          // a row that has seen nothing yet holds O = 0 in any frame
+          const bool rose = vp != u.p0 && m_ref > m_prev && m_prev > kMinusBig;
           const float o_scale = rose ? ex2_approx(m_prev - m_ref) : 1.f;
           const uint32_t rose_mask = __ballot_sync(0xffffffffu, rose && real);
           l *= ex2_approx(m_run - m_ref);
@@ -957,14 +1058,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 4; ++k) {
               const float x = ex2_approx(fmaf(MLA_S(8 * c + 2 * k), c2, -m_ref));
               const float y = ex2_approx(fmaf(MLA_S(8 * c + 2 * k + 1), c2, -m_ref));
-              s4[k] += x + y;  // the sum takes P before its bf16 rounding (half a step: 2^-8 relative, either sign)
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
-              w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+              s4[k] += x + y;  // the sum takes P before its rounding (bf16: half a step is 2^-8 relative, either sign)
+              if constexpr (kF8) {  // f16, as the expanded values: 2^-11 relative, 2^-25 absolute at least
+                const __half2 h2 = __floats2half2_rn(x, y);
+                w[k] = *reinterpret_cast<const uint32_t*>(&h2);
+              } else {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+                w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
             }
             pw[c] = make_uint4(w[0], w[1], w[2], w[3]);
           }
 #undef MLA_S
-          if (!mbar_wait_warp<true, true>(smem_u32(&ctrl->p_empty[ps]), ((j / C::kNP) & 1) ^ 1, abort, p.timeout_ns)) {
+          if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->p_empty[ps]), ((j / C::kNP) & 1) ^ 1, abort, p.timeout_ns)) {
             ok = false;
             why = kWaitPEmpty;
             break;
@@ -987,6 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mlfull_remote);
         ++un;
+        j0 += static_cast<uint32_t>(u.p1 - u.p0);
       }
       if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
     }
@@ -1007,7 +1114,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t j = 0, un = 0, nreq = 0;
       bool ok = true;
       int why = 0;
-      const volatile uint32_t* flags = reinterpret_cast<const volatile uint32_t*>(data + C::kFlagOff);
       if (lane == 0)
         for (int k = 0; k < C::kNP; ++k) mbar_expect_tx(smem_u32(&ctrl->p_full[k]), C::kPTx);
       __syncwarp();
@@ -1018,16 +1124,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool first = vp == u.p0;
           {
             const uint32_t vbar = kF8 ? smem_u32(&ctrl->v_full[vs & 3]) : smem_u32(&ctrl->kv_full[vs]);
-            const uint32_t bars[4] = {first ? smem_u32(&ctrl->o_empty) : 0u, vbar, smem_u32(&ctrl->p_full[ps]), 0u};
-            const uint32_t pars[4] = {(un & 1) ^ 1, (j / C::kNV) & 1, (j / C::kNP) & 1, 0u};
-            if (!mbar_wait4_warp(bars, pars, abort, p.timeout_ns)) {
+            const uint32_t pph = (j / C::kNP) & 1;
+            if (!mbar_wait_all_warp(vbar, (j / C::kNV) & 1, smem_u32(&ctrl->p_full[ps]), pph,
+                                    first ? smem_u32(&ctrl->o_empty) : 0u, (un & 1) ^ 1,
+                                    kCg == 2 && leader ? smem_u32(&ctrl->peer_pv[ps]) : 0u, pph, abort, p.timeout_ns)) {
               ok = false;
               why = kWaitPage;
               break;
             }
           }
-          const uint32_t fw = lane < 4 ? flags[ps * 4 + lane] : 0u;
-          if (__any_sync(0xffffffffu, fw != 0u)) {
+          // a row's reference rose: every lane reads the four flag words
+          const uint4 fw = *reinterpret_cast<const uint4*>(data + C::kFlagOff + ps * 16);
+          if ((fw.x | fw.y | fw.z | fw.w) != 0u) {
             if (lane == 0) {
               ctrl->resc_page = j;
               mbar_arrive(smem_u32(&ctrl->resc_req));
@@ -1060,16 +1168,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kCg == 2 && !leader) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(mapa(smem_u32(&ctrl->peer_pv[ps]), kCg));
+            if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctrl->peer_pv[ps]), kCg));
             continue;
-          }
-          if (kCg == 2) {
-            if (!mbar_wait_warp(smem_u32(&ctrl->peer_pv[ps]), (j / C::kNP) & 1, abort, p.timeout_ns)) {
-              ok = false;
-              why = kWaitPeerPv;
-              break;
-            }
-            tc_fence_after();
           }
           const uint64_t dv = smem_desc(smem_u32(slot), C::kVBox, 1024, kSwizzle128B);
           const uint64_t dp = smem_desc(smem_u32(data + ps * C::kPBytes), C::kPLbo, C::kPSbo, kSwizzleNone);
@@ -1099,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
     } else if (kF8 && warp >= 8) {
-      // ---- e4m3: four warps expand each page's codes to bf16 (exact), into
+      // ---- e4m3: four warps expand each page's codes to f16 (exact), into
       // the layout that PV reads.  A lane takes 16 codes (one 16-byte chunk)
       // at a time; four lanes a row, eight rows a warp, so that the two
       // 16-byte stores of eight neighbouring lanes meet all banks once.
@@ -1128,31 +1228,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint8_t* src = raw + rs * C::kSlotRaw;
             uint8_t* dst = vring + vs * C::kSlotV;
             const int valid = u.k.len - real_page(u.k, vp) * kPage;
-#pragma unroll 2
-            for (int t = 0; t < C::kRawBoxes * 2 * 8 / 4; ++t) {
-              // warp w: item w + 4 t = (rows 8 ro .., half box hb)
-              const int item = w + 4 * t;
-              const int ro = item & 7, hb = item >> 3;
-              const int row = ro * 8 + r8;
-              const int chunk = (hb & 1) * 4 + c4;  // of the raw box's row
-              uint4 v = make_uint4(0, 0, 0, 0);  // slots past the sequence's end may hold anything
-              if (row < valid)
-                v = *reinterpret_cast<const uint4*>(src + (hb >> 1) * C::kVBox + row * 128 + ((chunk ^ (row & 7)) << 4));
-              const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-              uint32_t o[8];
+#pragma unroll 1
+            for (int t = 0; t < C::kRawBoxes * 4; t += 4) {
+              // warp w: item w + 4 t = (rows 8 ro .., half box hb); four loads in flight
+              uint4 v[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
+              for (int q = 0; q < 4; ++q) {
+                const int item = w + 4 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
+                const int chunk = (hb & 1) * 4 + c4;  // of the raw box's row
+                v[q] = make_uint4(0, 0, 0, 0);  // slots past the sequence's end may hold anything
+                if (row < valid)
+                  v[q] = *reinterpret_cast<const uint4*>(src + (hb >> 1) * C::kVBox + row * 128 +
+                                                         ((chunk ^ (row & 7)) << 4));
+              }
 #pragma unroll
-                for (int h2 = 0; h2 < 2; ++h2) {
-                  const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-                      static_cast<__nv_fp8x2_storage_t>(in[k] >> (16 * h2)), __NV_E4M3);
-                  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
-                  const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x, f.y);
-                  o[2 * k + h2] = *reinterpret_cast<const uint32_t*>(&b2);
-                }
-              uint8_t* d = dst + hb * C::kVBox + row * 128;  // half a raw box = one box of 64 values
-              *reinterpret_cast<uint4*>(d + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-              *reinterpret_cast<uint4*>(d + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+              for (int q = 0; q < 4; ++q) {
+                const int item = w + 4 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
+                const uint32_t in[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                  for (int h2 = 0; h2 < 2; ++h2) {
+                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
+                        static_cast<__nv_fp8x2_storage_t>(in[k] >> (16 * h2)), __NV_E4M3);
+                    o[2 * k + h2] = static_cast<uint32_t>(hr.x) | (static_cast<uint32_t>(hr.y) << 16);
+                  }
+                uint8_t* d = dst + hb * C::kVBox + row * 128;  // half a raw box = one box of 64 values
+                *reinterpret_cast<uint4*>(d + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4*>(d + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+              }
             }
             fence_proxy_async_cta();
             __syncwarp();

@@ -99,6 +99,14 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t remote_bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
 }
 
+// The same without cluster-scoped release: for arrivals that publish no
+// ordinary memory writes (tensor-memory reads that are done, copies that have
+// landed).  The cluster-scoped release waits for the thread's earlier remote
+// stores: measured ~700 cycles behind a page's P stores.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t remote_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote_bar) : "memory");
+}
+
 __device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
@@ -184,6 +192,45 @@ __device__ __forceinline__ bool mbar_wait4_warp(const uint32_t (&bar)[4], const 
     }
   }
   return __all_sync(0xffffffffu, ok);
+}
+
+// Bounded warp-wide wait until up to four barrier phases have completed (a bar
+// of 0 is skipped).  Each poll is one block of four tests whose latencies
+// overlap (~65 cycles; mbar_wait4_warp, which consumes each result before the
+// next test, takes ~265 on phases that are all complete).  A completed phase
+// stays visible until the caller goes on, so all are tested again each time.
+__device__ __forceinline__ uint32_t mbar_test4(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2,
+                                               uint32_t p2, uint32_t b3, uint32_t p3) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred a, b, c, d;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 a, [%1], %2;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 b, [%3], %4;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 c, [%5], %6;\n\t"
+      "mbarrier.test_wait.parity.acquire.cta.shared::cta.b64 d, [%7], %8;\n\t"
+      "and.pred a, a, b;\n\tand.pred c, c, d;\n\tand.pred a, a, c;\n\t"
+      "selp.u32 %0, 1, 0, a;\n\t}"
+      : "=r"(ok)
+      : "r"(b0), "r"(p0), "r"(b1), "r"(p1), "r"(b2), "r"(p2), "r"(b3), "r"(p3)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ bool mbar_wait_all_warp(uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1, uint32_t b2,
+                                                   uint32_t p2, uint32_t b3, uint32_t p3, volatile int* abort,
+                                                   uint64_t limit_ns) {
+  // a skipped bar repeats the first one
+  if (!b1) { b1 = b0; p1 = p0; }
+  if (!b2) { b2 = b0; p2 = p0; }
+  if (!b3) { b3 = b0; p3 = p0; }
+  if (__all_sync(0xffffffffu, mbar_test4(b0, p0, b1, p1, b2, p2, b3, p3))) return true;
+  const uint64_t t0 = globaltimer_ns();
+#pragma unroll 1
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 16; ++i)
+      if (__all_sync(0xffffffffu, mbar_test4(b0, p0, b1, p1, b2, p2, b3, p3))) return true;
+    if (__any_sync(0xffffffffu, *abort || globaltimer_ns() - t0 > limit_ns)) return false;
+  }
 }
 
 // Warp-wide bounded wait: every lane waits, and the warp agrees on the
@@ -515,6 +562,18 @@ __device__ __forceinline__ void mma_ss_cg(uint32_t d, uint64_t adesc, uint64_t b
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
         : "memory");
   }
+}
+// e4m3 operands from shared memory
+template <int kCg>
+__device__ __forceinline__ void mma_ss_f8_cg(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+  if constexpr (kCg == 1)
+    mma_ss_e<true>(d, adesc, bdesc, idesc, acc);
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc)
+        : "memory");
 }
 // One arrival on the barrier at this offset in every CTA of `cta_mask` when
 // the MMAs issued so far by this warp's elected lane are done.
