@@ -11,6 +11,7 @@ split/merge identity, brute force, and torch's own float8 decoder).
 """
 from .chunk import cache_rows_at, mla_prefill_ref, seen_keys
 from .e4m3 import e4m3_decode_table, e4m3_encode, e4m3_to_f64
+from .evict import attn_mass_ref, evict_ref
 from .kv_pack import kv_pack_ref
 from .sparse import mla_decode_sparse_ref
 from .mla_oracle import (
@@ -26,11 +27,13 @@ from .mla_oracle import (
 
 __all__ = [
     "attend",
+    "attn_mass_ref",
     "cache_rows_at",
     "e4m3_decode_table",
     "e4m3_encode",
     "e4m3_to_f64",
     "bf16_bits_to_f64",
+    "evict_ref",
     "decode_cache_rows",
     "gather_rows",
     "kv_pack_ref",

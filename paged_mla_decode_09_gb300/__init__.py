@@ -1,6 +1,6 @@
 """Paged MLA decode for GB300: Python binding of the C ABI in include/mla_decode.h,
-include/mla_kv_pack.h, include/mla_sparse.h, include/mla_cascade.h and
-include/mla_prefill.h.
+include/mla_kv_pack.h, include/mla_sparse.h, include/mla_cascade.h,
+include/mla_prefill.h and include/mla_evict.h.
 
 The functions here only marshal arguments (torch tensors -> device
 pointers, shapes -> ``mla_dims``); every step of the decode runs in the
@@ -47,6 +47,10 @@ ENTRY_POINTS = (
     "mla_prefill",
     "mla_decode_window_workspace_size",
     "mla_decode_window",
+    "mla_attn_mass_workspace_size",
+    "mla_attn_mass",
+    "mla_evict_workspace_size",
+    "mla_evict",
 )
 
 
@@ -90,6 +94,20 @@ class MlaPrefillDims(ctypes.Structure):
         ("max_pages_per_req", ctypes.c_int32),
         ("page_table_stride", ctypes.c_int32),
         ("kv_dtype", ctypes.c_int32),
+    ]
+
+
+class MlaEvictDims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("mass_cols", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("page_table_stride", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("budget", ctypes.c_int32),
+        ("num_sinks", ctypes.c_int32),
+        ("num_recent", ctypes.c_int32),
     ]
 
 
@@ -155,6 +173,14 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     lib.mla_decode_window_workspace_size.restype = SZ
     lib.mla_decode_window.argtypes = [D, P, P, P, P, P, I32, I32, F, F, P, P, P, SZ, P]
     lib.mla_decode_window.restype = ctypes.c_int
+    lib.mla_attn_mass_workspace_size.argtypes = [D, ctypes.c_int]
+    lib.mla_attn_mass_workspace_size.restype = SZ
+    lib.mla_attn_mass.argtypes = [D, P, P, P, P, P, P, I32, F, F, P, P, I32, P, SZ, P]
+    lib.mla_attn_mass.restype = ctypes.c_int
+    lib.mla_evict_workspace_size.argtypes = [I32, I32]
+    lib.mla_evict_workspace_size.restype = SZ
+    lib.mla_evict.argtypes = [ctypes.POINTER(MlaEvictDims), P, P, P, P, P, P, P, P, P, P, SZ, P]
+    lib.mla_evict.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -576,6 +602,121 @@ def mla_decode_window(q_nope, q_pe, kv_cache, page_table, seq_lens, window, num_
         _stream_handle(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_window")
+
+
+# ---- attention mass and eviction (include/mla_evict.h) ----
+
+def _opt_ptr(t) -> ctypes.c_void_p:
+    return ctypes.c_void_p(None) if t is None else _ptr(t)
+
+
+def mla_attn_mass_workspace_size(dims: MlaDims, device: int | None = None) -> int:
+    import torch
+
+    dev = torch.cuda.current_device() if device is None else device
+    n = load_library().mla_attn_mass_workspace_size(ctypes.byref(dims), dev)
+    if n == 0:
+        raise MlaError(-1, "mla_attn_mass_workspace_size")
+    return int(n)
+
+
+def _check_mass_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace):
+    import torch
+
+    if q_nope.dim() != 4 or q_nope.shape[3] != 512:
+        raise ValueError(f"q_nope must be [B, q_len, H, 512], got {list(q_nope.shape)}")
+    B, Q, H, _ = q_nope.shape
+    _check_layout("q_nope", q_nope, (B, Q, H, 512), (torch.bfloat16,))
+    _check_layout("q_pe", q_pe, (B, Q, H, 64), (torch.bfloat16,))
+    _check_layout("lse", lse, (B, Q, H), (torch.float32,))
+    _check_cache_and_table(kv_cache, page_table, seq_lens, B)
+    if mass_out.dim() != 2:
+        raise ValueError("mass_out must be [B, mass_cols]")
+    _check_layout("mass_out", mass_out, (B, mass_out.shape[1]), (torch.float32,))
+    if mass is not None:
+        _check_layout("mass", mass, tuple(mass_out.shape), (torch.float32,))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    for t in (q_pe, kv_cache, page_table, seq_lens, lse, mass_out, workspace) + (() if mass is None else (mass,)):
+        if t.device != q_nope.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def mla_attn_mass(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, num_fresh, scale, kv_scale, mass, mass_out,
+                  workspace, stream=None) -> None:
+    """Enqueue the accumulation of the softmax weights that a step's queries
+    gave to every cached token (see include/mla_evict.h): mass (None: zeros)
+    and mass_out fp32 [B, mass_cols]; the last num_fresh tokens start at 0."""
+    _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass_out, workspace)
+    if mass is not None:
+        _check_cuda(mass)
+    _check_mass_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace)
+    _check_current_device(q_nope)
+    dims = make_dims(q_nope, kv_cache, page_table)
+    rc = load_library().mla_attn_mass(
+        ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(lse),
+        _int32_arg("num_fresh", num_fresh), float(scale), float(kv_scale), _opt_ptr(mass), _ptr(mass_out),
+        int(mass_out.shape[1]), _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
+        _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_attn_mass")
+
+
+def mla_evict_workspace_size(batch: int, budget: int) -> int:
+    n = load_library().mla_evict_workspace_size(_int32_arg("batch", batch), _int32_arg("budget", budget))
+    if n == 0:
+        raise MlaError(-1, "mla_evict_workspace_size")
+    return int(n)
+
+
+def _check_evict_tensors(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out,
+                         positions_out, workspace):
+    import torch
+
+    if mass.dim() != 2:
+        raise ValueError("mass must be [B, mass_cols]")
+    B, cols = mass.shape
+    _check_layout("mass", mass, (B, cols), (torch.float32,))
+    _check_layout("mass_out", mass_out, (B, cols), (torch.float32,))
+    if positions is not None:
+        if positions_out is None:
+            raise ValueError("positions_out is needed with positions")
+        _check_layout("positions", positions, (B, cols), (torch.int32,))
+        _check_layout("positions_out", positions_out, (B, cols), (torch.int32,))
+    _check_cache_and_table(kv_cache, page_table, seq_lens, B)
+    if kv_cache.shape[1] != 64:
+        raise ValueError("kv_cache must have pages of 64 tokens")
+    _check_layout("new_lens", new_lens, (B,), (torch.int32,))
+    _check_layout("kept", kept, (B, budget), (torch.int32,))
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    rest = (positions, positions_out) if positions is not None else ()
+    for t in (seq_lens, page_table, kv_cache, new_lens, kept, mass_out, workspace) + rest:
+        if t.device != mass.device:
+            raise ValueError("all tensors must be on one device")
+
+
+def mla_evict(mass, positions, seq_lens, page_table, kv_cache, budget, num_sinks, num_recent, new_lens, kept, mass_out,
+              positions_out, workspace, stream=None) -> None:
+    """Enqueue the eviction of every request's tokens beyond its budget (see
+    include/mla_evict.h).  positions and positions_out may be None."""
+    budget = _int32_arg("budget", budget, 1)
+    _check_cuda(mass, seq_lens, page_table, kv_cache, new_lens, kept, mass_out, workspace)
+    if positions is not None and positions_out is not None:
+        _check_cuda(positions, positions_out)
+    _check_evict_tensors(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out,
+                         positions_out, workspace)
+    _check_current_device(mass)
+    dims = MlaEvictDims(batch=int(mass.shape[0]), mass_cols=int(mass.shape[1]), num_pages=int(kv_cache.shape[0]),
+                        max_pages_per_req=int(page_table.shape[1]), page_table_stride=int(page_table.stride(0)),
+                        kv_dtype=kv_dtype_code(kv_cache), budget=budget,
+                        num_sinks=_int32_arg("num_sinks", num_sinks), num_recent=_int32_arg("num_recent", num_recent))
+    rc = load_library().mla_evict(
+        ctypes.byref(dims), _ptr(mass), _opt_ptr(positions), _ptr(seq_lens), _ptr(page_table), _ptr(kv_cache),
+        _ptr(new_lens), _ptr(kept), _ptr(mass_out), _opt_ptr(positions_out if positions is not None else None),
+        _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream_handle(stream))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_evict")
 
 
 @dataclass

@@ -3,9 +3,10 @@
 ``python -m paged_mla_decode_09_gb300.build`` compiles
 ``csrc/mla_decode.cu`` (the decode), ``csrc/mla_kv_pack.cu`` (the cache
 write), ``csrc/mla_sparse.cu`` (the top-k decode), ``csrc/mla_cascade.cu``
-(the shared-prefix cascade) and ``csrc/mla_chunk.cu`` (prompt chunks and
-windows) with nvcc into ``libmla_decode.so`` next to this file.  One
-``-gencode``; a few seconds.
+(the shared-prefix cascade), ``csrc/mla_chunk.cu`` (prompt chunks and
+windows), ``csrc/mla_mass.cu`` (attention mass) and ``csrc/mla_evict.cu``
+(eviction) with nvcc into ``libmla_decode.so`` next to this file.  One
+``-gencode``, the files in parallel; a few seconds.
 """
 from __future__ import annotations
 
@@ -21,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmla_decode.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "mla_kv_pack.cu", "mla_sparse.cu", "mla_cascade.cu",
-                                               "mla_chunk.cu")]
+                                               "mla_chunk.cu", "mla_mass.cu", "mla_evict.cu")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -53,7 +54,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [
         nvcc_path(), "-shared", "-Xcompiler", "-fPIC", *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17",
-        "-I", INCLUDE, "-I", CSRC, "-cudart", "shared", "-o", tmp, *SOURCES,
+        "-I", INCLUDE, "-I", CSRC, "-cudart", "shared", "--threads", "0", "-o", tmp, *SOURCES,
     ]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")

@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "mla_chunk.cuh"
+#include "mla_host.h"
 #include "mla_prefill.h"
 
 namespace {
@@ -19,8 +20,12 @@ using mla::chunk::Params;
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per pipeline wait
 
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using mla::host::align256;
+using mla::host::aligned;
+using mla::host::device_ok;
+using mla::host::encode_fn;
+using mla::host::map2;
+using mla::host::map3;
 
 // The dimensions both entry points come down to.
 struct Shape {
@@ -68,16 +73,6 @@ int check_shape(const Shape& s, int page_size, int kv_dtype) {
   if (s.num_pages * 64 > INT_MAX || s.max_pages * 64 > INT_MAX) return MLA_ERR_UNSUPPORTED;
   if ((s.T * s.H / 128 + s.B) * s.max_pages > INT_MAX) return MLA_ERR_UNSUPPORTED;  // the schedule's page sums
   return MLA_OK;
-}
-
-int device_ok(int device) {
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device) != cudaSuccess) {
-    cudaGetLastError();
-    return MLA_ERR_CUDA;
-  }
-  return major == 10 && minor == 3 ? MLA_OK : MLA_ERR_DEVICE;
 }
 
 template <bool kF8, int kCg>
@@ -139,47 +134,9 @@ int clusters_of(int device, bool f8, int cg, int* out) {
   return MLA_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
-  return fn;
-}
-
 struct Maps {
   CUtensorMap s, o, pe, qn, qp;
 };
-
-// A 3-D map over rows of `row_bytes`: (128 bytes of a row, rows, 128-byte
-// columns), read in boxes of 128 bytes x box_rows x box_cols that land as
-// [column][row][128 bytes] with the 128-byte swizzle.
-bool map3(CUtensorMap* m, const void* base, int64_t rows, int row_bytes, int esz, int cols, int box_rows, int box_cols) {
-  cuuint64_t gdim[3] = {static_cast<cuuint64_t>(128 / esz), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(cols)};
-  cuuint64_t gstr[2] = {static_cast<cuuint64_t>(row_bytes), 128};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / esz), static_cast<cuuint32_t>(box_rows),
-                       static_cast<cuuint32_t>(box_cols)};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return encode_fn()(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                     const_cast<void*>(base), gdim, gstr, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-bool map2(CUtensorMap* m, const void* base, int64_t rows, int width, int esz, int box_x, int box_rows,
-          CUtensorMapSwizzle swz) {
-  cuuint64_t gdim[2] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(rows)};
-  cuuint64_t gstr[1] = {static_cast<cuuint64_t>(width) * esz};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(box_x), static_cast<cuuint32_t>(box_rows)};
-  cuuint32_t estr[2] = {1, 1};
-  return encode_fn()(m, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                     const_cast<void*>(base), gdim, gstr, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
-                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // s: an S CTA's part of a page; o: an O CTA's dimensions of a page; pe: the
 // e4m3 k_pe rows, or (bf16 pair) single boxes of q_nope; qn, qp: query rows.

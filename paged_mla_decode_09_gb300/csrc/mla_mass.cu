@@ -1,0 +1,623 @@
+// mla_attn_mass (see include/mla_evict.h): the softmax weight that a step's
+// queries gave to every cached token.
+//
+//     mass_out[t] = mass[t] + sum_r 2^(s_rt c - lse_r log2e),
+//
+// r over the request's query rows (positions x heads).  The scores are
+// computed again (1152 flops per row and key, and every cache row read once),
+// which needs no store of the attention's weights.
+//
+// Work: the requests' pages in slices of equal weighted length, one per CTA;
+// a slice's piece of a request is taken kSub pages at a time through all of
+// the request's row blocks of 128 (decode steps have one), so that the pages
+// come from L2 for every block but the first.  Per page: S = Q K^T by tcgen05
+// with the queries in TMEM (lane = row), two groups of four warps take the
+// even and the odd pages: exp2, then each warp adds its 32 rows by halving
+// exchanges (62 shuffles leave every lane the sums of two keys) and 64 threads
+// add the four warps' sums to the keys' running values.  A key always meets
+// the same thread, its row blocks in order: no atomics, and results that do
+// not depend on how the pages were sliced.
+//
+// What bounds it: a decode step reads 72 KB per page and CTA, ~3100 cycles of
+// its share of HBM, against 1224 tensor cycles; many query rows are bound by
+// the tensor pipe (36 MMAs of 34 cycles per page).
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <mutex>
+
+#include "mla_evict.h"
+#include "mla_host.h"
+#include "mla_score.cuh"
+
+namespace mla {
+namespace mass {
+
+using chunk::kDL;
+using chunk::kLog2e;
+using chunk::kPage;
+using chunk::kRows;
+using chunk::kThreads;
+
+constexpr int kUnitCost = 4;  // pages' worth of starting a piece
+constexpr int kSub = 16;      // pages taken through all row blocks at a time
+
+template <bool kF8>
+struct Lay {
+  using C = chunk::Cfg<kF8, 1>;
+  static constexpr int kSums = C::kNStS * C::kSlotS;  // [group][2][4 warps][64] column sums
+  static constexpr int kData = kSums + 2 * 2 * 4 * 64 * 4;
+  static constexpr int kSmem = 1024 + kData + 512;
+  static_assert(kSmem <= 232448, "shared memory budget");
+};
+
+struct __align__(8) Ctrl {
+  uint64_t kv_full[chunk::kMaxStages];
+  uint64_t kv_empty[chunk::kMaxStages];
+  uint64_t q_bar[2];
+  uint64_t s_full[3];
+  uint64_t s_empty[3];
+  uint64_t q_full;
+  uint64_t sums[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int first;          // first request of this CTA's slice
+  long long start;    // its weighted start
+  long long total;    // weighted length of all requests
+};
+static_assert(sizeof(Ctrl) <= 512, "control block");
+
+struct Params {
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const float* lse;
+  const float* mass_in;
+  float* mass_out;
+  int32_t* status;
+  int32_t B, H, Q, R, G;
+  int32_t num_pages, max_pages, pt_stride, cols;
+  int32_t cap;        // longest length the table and the mass rows hold
+  int32_t num_fresh;
+  float scale, kv_scale;
+  uint64_t timeout_ns;
+};
+
+__global__ void mla_mass_clear_kernel(int32_t* status) {
+  griddep_launch_dependents();
+  if (threadIdx.x < 4) status[threadIdx.x] = 0;
+}
+
+__device__ __forceinline__ int length_of(const Params& p, int b) {
+  const int L = p.seq_lens[b];
+  return L < 0 ? 0 : (L > p.cap ? p.cap : L);
+}
+
+// The units of a CTA's slice, in order: for every piece of a request, kSub
+// pages at a time, every row block.
+struct Unit {
+  int b, L, p0, p1, g;
+};
+struct UnitIter {
+  const Params* p;
+  long long x0, x1, start;
+  int b, L, p1, a, g;
+  bool open;  // a piece is being walked: pages [a, p1), next block g
+  __device__ void init(const Params& pp, const Ctrl* c) {
+    p = &pp;
+    const long long W = c->total;
+    x0 = W * blockIdx.x / gridDim.x;
+    x1 = W * (blockIdx.x + 1) / gridDim.x;
+    start = c->start;
+    b = c->first;
+    open = false;
+  }
+  __device__ bool next(Unit& u) {
+    while (!open) {
+      if (b >= p->B || start >= x1) return false;
+      L = length_of(*p, b);
+      const int np = (L + kPage - 1) / kPage;
+      const long long lo = x0 - start - kUnitCost, hi = x1 - start - kUnitCost;
+      a = lo > 0 ? (lo < np ? static_cast<int>(lo) : np) : 0;
+      p1 = hi < np ? (hi > 0 ? static_cast<int>(hi) : 0) : np;
+      g = 0;
+      open = a < p1;
+      if (!open) {
+        start += kUnitCost + np;
+        ++b;
+      }
+    }
+    u.b = b;
+    u.L = L;
+    u.p0 = a;
+    u.p1 = p->G > 1 && p1 - a > kSub ? a + kSub : p1;
+    u.g = g;
+    if (++g == p->G) {
+      g = 0;
+      a = u.p1;
+      if (a >= p1) {
+        open = false;
+        start += kUnitCost + (L + kPage - 1) / kPage;
+        ++b;
+      }
+    }
+    return true;
+  }
+};
+
+enum WaitTag : int { kWaitEmpty = 201, kWaitLanded, kWaitQFull, kWaitSPrev, kWaitQ, kWaitS, kWaitSums };
+
+__device__ __forceinline__ void raise_timeout(const Params& p, Ctrl* ctrl, int tag, uint32_t j) {
+  if (atomicCAS(p.status + 1, 0, tag) == 0) {
+    p.status[2] = static_cast<int32_t>(j);
+    p.status[3] = static_cast<int32_t>((blockIdx.x << 16) | (threadIdx.x >> 5));
+  }
+  atomicOr(p.status, MLA_DEV_TIMEOUT);
+  *reinterpret_cast<volatile int*>(&ctrl->abort) = 1;
+}
+
+template <bool kF8>
+__device__ void produce(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUtensorMap* tm_s, const CUtensorMap* tm_pe,
+                        const CUtensorMap* tm_qn, const CUtensorMap* tm_qp) {
+  using C = chunk::Cfg<kF8, 1>;
+  volatile int* abort = &ctrl->abort;
+  UnitIter it;
+  it.init(p, ctrl);
+  Unit u;
+  uint32_t i = 0, un = 0, qloaded = 0;
+  bool ok = true;
+  auto acquire = [&]() -> bool {
+    const int st = static_cast<int>(i % C::kNStS);
+    return mbar_wait(smem_u32(&ctrl->kv_empty[st]), ((i / C::kNStS) & 1) ^ 1, abort, p.timeout_ns);
+  };
+  while (ok && it.next(u)) {
+    const uint32_t qbar = smem_u32(&ctrl->q_bar[un & 1]);
+    for (int e = 0; e < C::kQEntries; ++e, ++i) {
+      if (!acquire()) {
+        ok = false;
+        break;
+      }
+      const int st = static_cast<int>(i % C::kNStS);
+      if (e == 0) {
+        mbar_expect_tx(qbar, static_cast<uint32_t>(kRows * 1152));
+        qloaded = un + 1;
+      }
+      mbar_arrive(smem_u32(&ctrl->kv_full[st]));
+      const int row = u.b * p.R + u.g * kRows + C::kQRows * e;
+      const uint32_t slot = smem_u32(ring + st * C::kSlotS);
+      tma_load_3d(slot, tm_qn, 0, row, 0, qbar);
+      tma_load_2d(slot + C::kQRows * 128 * 8, tm_qp, 0, row, qbar);
+    }
+    ++un;
+    for (int pg = u.p0; pg < u.p1 && ok; ++pg) {
+      int32_t pid = __ldg(p.page_table + static_cast<int64_t>(u.b) * p.pt_stride + pg);
+      if (pid < 0 || pid >= p.num_pages) {
+        atomicOr(p.status, MLA_DEV_BAD_PAGE_ID);
+        pid = 0;
+      }
+      if (!acquire()) {
+        ok = false;
+        break;
+      }
+      const int st = static_cast<int>(i % C::kNStS);
+      const uint32_t bar = smem_u32(&ctrl->kv_full[st]), slot = smem_u32(ring + st * C::kSlotS);
+      mbar_expect_tx(bar, static_cast<uint32_t>(C::kSlotS));
+      tma_load_3d(slot, tm_s, 0, pid * kPage, 0, bar);
+      if constexpr (kF8) tma_load_2d(slot + C::kSBoxes * C::kBox, tm_pe, kDL, pid * kPage, bar);
+      ++i;
+    }
+  }
+  if (!ok) raise_timeout(p, ctrl, kWaitEmpty, i);
+  for (uint32_t q = 0; q < static_cast<uint32_t>(C::kNStS) && q < i; ++q) {  // every copy has landed before exit
+    const uint32_t last = i - 1 - ((i - 1 - q) % C::kNStS);
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(&ctrl->kv_full[q]), (last / C::kNStS) & 1) && globaltimer_ns() - t0 < p.timeout_ns) {
+    }
+  }
+  if (qloaded) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(smem_u32(&ctrl->q_bar[(qloaded - 1) & 1]), ((qloaded - 1) >> 1) & 1) &&
+           globaltimer_ns() - t0 < p.timeout_ns) {
+    }
+  }
+}
+
+template <bool kF8>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_mass_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_s,
+                    const __grid_constant__ CUtensorMap tm_pe, const __grid_constant__ CUtensorMap tm_qn,
+                    const __grid_constant__ CUtensorMap tm_qp) {
+  using C = chunk::Cfg<kF8, 1>;
+  using M = Lay<kF8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(data + M::kData);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < chunk::kMaxStages; ++i) {
+      mbar_init(smem_u32(&ctrl->kv_full[i]), 1);
+      mbar_init(smem_u32(&ctrl->kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctrl->q_bar[i]), 1);
+      mbar_init(smem_u32(&ctrl->sums[i]), 4);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_u32(&ctrl->s_full[i]), 1);
+      mbar_init(smem_u32(&ctrl->s_empty[i]), 4);
+    }
+    mbar_init(smem_u32(&ctrl->q_full), 8);
+    mbar_init(smem_u32(&ctrl->drain), 1);
+    ctrl->abort = 0;
+    ctrl->first = p.B;
+    ctrl->start = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_s);
+    tma_prefetch_desc(&tm_qn);
+    tma_prefetch_desc(&tm_qp);
+    if (kF8) tma_prefetch_desc(&tm_pe);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&ctrl->tmem_base), 512);
+    tmem_relinquish();
+  }
+  // The slice of this CTA.  A request occupies kUnitCost + pages of the
+  // weighted line; two passes over the lengths (inputs of the call, so before
+  // griddep_wait): the total, then the request that holds the slice's start.
+  bool bad = false;
+  {
+    __shared__ long long wsum[kThreads / 32];
+    __shared__ long long carry;
+    for (int pass = 0; pass < 2; ++pass) {
+      if (tid == 0) carry = 0;
+      __syncthreads();
+      const long long x0 = pass ? ctrl->total * blockIdx.x / gridDim.x : 0;
+      for (int base = 0; base < p.B; base += kThreads) {
+        const int b = base + tid;
+        long long v = 0;
+        if (b < p.B) {
+          const int L = p.seq_lens[b];
+          bad = bad || L < p.Q || L > p.cap;
+          v = kUnitCost + (length_of(p, b) + kPage - 1) / kPage;
+        }
+        const long long own = v;
+        for (int o = 1; o < 32; o <<= 1) {
+          const long long t = __shfl_up_sync(0xffffffffu, v, o);
+          if (lane >= o) v += t;
+        }
+        if (lane == 31) wsum[warp] = v;
+        __syncthreads();
+        long long before = carry;
+        for (int w = 0; w < warp; ++w) before += wsum[w];
+        const long long end = before + v;
+        if (pass && b < p.B && end > x0 && end - own <= x0) {  // exactly one request
+          ctrl->first = b;
+          ctrl->start = end - own;
+        }
+        __syncthreads();
+        if (tid == kThreads - 1) carry = end;
+        __syncthreads();
+      }
+      if (tid == 0 && !pass) ctrl->total = carry;
+      __syncthreads();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();  // the status words are cleared (and whatever the caller launched before has completed)
+  if (bad && blockIdx.x == 0) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
+  const uint32_t tmem = ctrl->tmem_base;
+  volatile int* abort = &ctrl->abort;
+  uint8_t* ring = data;
+
+  if (warp == 0) {
+    if (lane == 0) produce<kF8>(p, ctrl, ring, &tm_s, &tm_pe, &tm_qn, &tm_qp);
+  } else if (warp == 1) {
+    UnitIter it;
+    it.init(p, ctrl);
+    Unit u;
+    uint32_t i = 0, j = 0, un = 0;
+    bool ok = true;
+    int why = 0;
+    while (ok && it.next(u)) {
+      for (int e = 0; e < C::kQEntries && ok; ++e, ++i)  // no phase of an entry is ever skipped
+        ok = mbar_wait_warp(smem_u32(&ctrl->kv_full[i % C::kNStS]), (i / C::kNStS) & 1, abort, p.timeout_ns);
+      why = kWaitLanded;
+      if (!ok) break;
+      if (!mbar_wait_warp(smem_u32(&ctrl->q_full), un & 1, abort, p.timeout_ns)) {
+        ok = false;
+        why = kWaitQFull;
+        break;
+      }
+      if (lane == 0)
+        for (int e = C::kQEntries; e > 0; --e) mbar_arrive(smem_u32(&ctrl->kv_empty[(i - e) % C::kNStS]));
+      __syncwarp();
+      ++un;
+      for (int pg = u.p0; pg < u.p1; ++pg, ++j, ++i) {
+        const int st = static_cast<int>(i % C::kNStS), sb = static_cast<int>(j % 3);
+        if (!mbar_wait_all_warp(smem_u32(&ctrl->kv_full[st]), (i / C::kNStS) & 1, smem_u32(&ctrl->s_empty[sb]),
+                                ((j / 3) & 1) ^ 1, 0u, 0u, 0u, 0u, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitLanded;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t slot = smem_u32(ring + st * C::kSlotS);
+        const uint64_t dlat = smem_desc(slot, 16, 1024, kSwizzle128B);
+        const uint32_t dcol = tmem + C::kSCol0 + sb * 64;
+        if constexpr (!kF8) {
+#pragma unroll
+          for (int d = 0; d < 9; ++d)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ts_e<false>(dcol, tmem + d * 32 + k * 8, dlat + static_cast<uint64_t>(d * (C::kBox >> 4) + k * 2),
+                              C::kIdescQK, (d | k) ? 1u : 0u);
+        } else {
+          const uint64_t dpe = smem_desc(slot + C::kSBoxes * C::kBox, 16, 512, kSwizzle64B);
+#pragma unroll
+          for (int term = 0; term < 2; ++term) {
+            const uint32_t qcol = tmem + (term ? C::kQLoCol : 0u);
+#pragma unroll
+            for (int d = 0; d < 4; ++d)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                mma_ts_e<true>(dcol, qcol + d * 32 + k * 8, dlat + static_cast<uint64_t>(d * (C::kBox >> 4) + k * 2),
+                               C::kIdescQK, (term | d | k) ? 1u : 0u);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mma_ts_e<true>(dcol, qcol + 128 + k * 8, dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
+          }
+        }
+        mma_commit_e(smem_u32(&ctrl->kv_empty[st]));
+        mma_commit_e(smem_u32(&ctrl->s_full[sb]));
+      }
+    }
+    if (!ok && lane == 0) raise_timeout(p, ctrl, why, j);
+    __syncwarp();
+    mma_commit_e(smem_u32(&ctrl->drain));
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&ctrl->drain), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+      }
+    }
+    __syncwarp();
+  } else if (warp >= 4) {
+    const int r = (warp & 3) * 32 + lane;
+    const int gg = (warp - 4) >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    float* sums = reinterpret_cast<float*>(data + M::kSums) + gg * 2 * 4 * 64;
+    UnitIter it;
+    it.init(p, ctrl);
+    Unit u;
+    uint32_t i = 0, j = 0, un = 0, n = 0;  // n: pages of this group
+    bool ok = true;
+    int why = 0;
+    while (ok && it.next(u)) {
+      if (j > 0 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - 1) % 3]), ((j - 1) / 3) & 1, abort,
+                                                p.timeout_ns)) {
+        ok = false;
+        why = kWaitSPrev;
+        break;
+      }
+      if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->q_bar[un & 1]), (un >> 1) & 1, abort, p.timeout_ns)) {
+        ok = false;
+        why = kWaitQ;
+        break;
+      }
+      const int row = u.g * kRows + r;  // of the request's R rows
+      const bool real = row < p.R;
+      float nl = 0.f;  // -lse in log2 units
+      int nvis = 0;
+      if (real) {
+        const float l = p.lse[static_cast<int64_t>(u.b) * p.R + row];
+        nvis = l == -INFINITY ? 0 : u.L - p.Q + row / p.H + 1;
+        nl = -l * kLog2e;
+      }
+      float qs = 1.f;
+      if constexpr (kF8) qs = chunk::q_row_e4m3<1>(ring, i, r, tmem + lane_base, nullptr, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9);
+      else chunk::q_row_bf16<1, 36>(ring, i, r, tmem + lane_base, 36 * gg);
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl->q_full));
+      i += C::kQEntries + static_cast<uint32_t>(u.p1 - u.p0);
+      ++un;
+      const float c2 = p.scale * kLog2e * (kF8 ? qs * p.kv_scale : 1.f);
+      const float* in = p.mass_in ? p.mass_in + static_cast<int64_t>(u.b) * p.cols : nullptr;
+      float* out = p.mass_out + static_cast<int64_t>(u.b) * p.cols;
+      const int old = u.L - p.num_fresh;  // tokens below start from mass_in (num_fresh >= 0: no overflow below 0)
+      for (int pg = u.p0; pg < u.p1; ++pg, ++j) {
+        if ((pg & 1) != gg) continue;
+        const int sb = static_cast<int>(j % 3);
+        const int t0 = pg * kPage, t = t0 + r;
+        // the key's value so far: this thread's own store of the block before
+        float base = 0.f;
+        if (r < 64 && t < u.L) base = u.g > 0 ? out[t] : (in && t < old ? in[t] : 0.f);
+        if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (j / 3) & 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitS;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[4][16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld16(tmem + lane_base + C::kSCol0 + sb * 64 + q * 16, v[q]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_wait_ld_tie(v[q]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->s_empty[sb]));
+        float f[64];
+        const int z = nvis - t0;  // keys of the page that the row sees
+        if (__all_sync(0xffffffffu, z >= kPage)) {
+#pragma unroll
+          for (int k = 0; k < 64; ++k) f[k] = ex2_approx(fmaf(__uint_as_float(v[k >> 4][k & 15]), c2, nl));
+        } else {  // unseen keys, padding rows: exactly 0, whatever the slot holds
+#pragma unroll
+          for (int k = 0; k < 64; ++k) {
+            const float e = ex2_approx(fmaf(__uint_as_float(v[k >> 4][k & 15]), c2, nl));
+            f[k] = k < z ? e : 0.f;
+          }
+        }
+        // halving exchanges: lane l ends with the warp's sums of keys 2 l, 2 l + 1
+#pragma unroll
+        for (int o = 16, w = 32; w >= 2; o >>= 1, w >>= 1) {
+          const bool hi = (lane & o) != 0;
+#pragma unroll
+          for (int k = 0; k < w; ++k) {
+            const float keep = hi ? f[k + w] : f[k], send = hi ? f[k] : f[k + w];
+            f[k] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+          }
+        }
+        float* s4 = sums + (n & 1) * 256;
+        *reinterpret_cast<float2*>(s4 + (warp & 3) * 64 + 2 * lane) = make_float2(f[0], f[1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->sums[gg]));
+        // all four warps wait, so that none gets two pages ahead of another
+        if (!mbar_wait_warp(smem_u32(&ctrl->sums[gg]), n & 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitSums;
+          break;
+        }
+        ++n;
+        if (r < 64 && t < u.L) out[t] = base + ((s4[r] + s4[64 + r]) + (s4[128 + r] + s4[192 + r]));
+      }
+    }
+    if (!ok && lane == 0) raise_timeout(p, ctrl, why, j);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace mass
+}  // namespace mla
+
+namespace {
+
+using mla::chunk::Cfg;
+using mla::mass::Lay;
+using mla::mass::Params;
+using namespace mla::host;
+
+int check_mass_dims(const mla_dims* d) {
+  if (!d || d->batch < 1 || d->num_heads < 1 || d->q_len < 1 || d->num_pages < 1 || d->max_pages_per_req < 1 ||
+      d->page_table_stride < d->max_pages_per_req)
+    return MLA_ERR_INVALID_ARG;
+  if (d->page_size != 64) return MLA_ERR_UNSUPPORTED;
+  if (d->kv_dtype != MLA_KV_BF16 && d->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
+  const int64_t B = d->batch;
+  if (static_cast<int64_t>(d->num_pages) * 64 > INT_MAX || B * d->max_pages_per_req > INT_MAX / 64 ||
+      B * d->q_len > INT_MAX || B * d->q_len * d->num_heads > INT_MAX)
+    return MLA_ERR_UNSUPPORTED;
+  return MLA_OK;
+}
+
+template <bool kF8>
+cudaError_t launch_mass(const Params& p, const CUtensorMap& s, const CUtensorMap& pe, const CUtensorMap& qn,
+                        const CUtensorMap& qp, int ctas, int device, cudaStream_t stream) {
+  cudaError_t e = allow_smem<kF8>(mla::mass::mla_mass_kernel<kF8>, Lay<kF8>::kSmem, device);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, 1, 1);
+  cfg.blockDim = dim3(mla::chunk::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = Lay<kF8>::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mla::mass::mla_mass_kernel<kF8>, p, s, pe, qn, qp);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mla_attn_mass_workspace_size(const mla_dims* d, int device) {
+  (void)device;
+  return check_mass_dims(d) == MLA_OK ? 256 : 0;
+}
+
+int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const void* kv_cache,
+                  const int32_t* page_table, const int32_t* seq_lens, const float* lse, int32_t num_fresh, float scale,
+                  float kv_scale, const float* mass, float* mass_out, int32_t mass_cols, void* workspace,
+                  size_t workspace_bytes, void* stream_v) {
+  int rc = check_mass_dims(d);
+  if (rc != MLA_OK) return rc;
+  if (!q_nope || !q_pe || !kv_cache || !page_table || !seq_lens || !lse || !mass_out || !workspace || mass_cols < 1 ||
+      num_fresh < 0)
+    return MLA_ERR_INVALID_ARG;
+  const bool f8 = d->kv_dtype == MLA_KV_FP8_E4M3;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
+  if (f8 && (!(kv_scale > 0.f) || !std::isfinite(kv_scale))) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q_nope, 32) || !aligned(q_pe, 32) || !aligned(kv_cache, 16) || !aligned(page_table, 4) ||
+      !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(mass, 4) || !aligned(mass_out, 4) || !aligned(workspace, 256))
+    return MLA_ERR_ALIGNMENT;
+  if (workspace_bytes < 256) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  if ((rc = device_ok(dev)) != MLA_OK) return rc;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return MLA_ERR_CUDA;
+  if (!encode_fn()) return MLA_ERR_CUDA;
+  const int64_t R = static_cast<int64_t>(d->num_heads) * d->q_len;
+  const int64_t krows = static_cast<int64_t>(d->num_pages) * 64, qrows = d->batch * R;
+  CUtensorMap s, pe, qn, qp;
+  bool ok = true;
+  if (f8) {
+    using C = Cfg<true, 1>;
+    ok = map3(&s, kv_cache, krows, 576, 1, C::kSBoxes, 64, C::kPartBoxes) &&
+         map2(&pe, kv_cache, krows, 576, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B) &&
+         map3(&qn, q_nope, qrows, 1024, 2, 8, C::kQRows, 8) &&
+         map2(&qp, q_pe, qrows, 64, 2, 64, C::kQRows, CU_TENSOR_MAP_SWIZZLE_128B);
+  } else {
+    using C = Cfg<false, 1>;
+    ok = map3(&s, kv_cache, krows, 1152, 2, C::kSBoxes, 64, C::kPartBoxes) &&
+         map3(&qn, q_nope, qrows, 1024, 2, 8, C::kQRows, 8) &&
+         map2(&qp, q_pe, qrows, 64, 2, 64, C::kQRows, CU_TENSOR_MAP_SWIZZLE_128B);
+    pe = s;
+  }
+  if (!ok) return MLA_ERR_CUDA;
+  Params p;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.lse = lse;
+  p.mass_in = mass;
+  p.mass_out = mass_out;
+  p.status = static_cast<int32_t*>(workspace);
+  p.B = d->batch;
+  p.H = d->num_heads;
+  p.Q = d->q_len;
+  p.R = static_cast<int32_t>(R);
+  p.G = static_cast<int32_t>((R + mla::chunk::kRows - 1) / mla::chunk::kRows);
+  p.num_pages = d->num_pages;
+  p.max_pages = d->max_pages_per_req;
+  p.pt_stride = d->page_table_stride;
+  p.cols = mass_cols;
+  p.cap = d->max_pages_per_req * 64 < mass_cols ? d->max_pages_per_req * 64 : mass_cols;
+  p.num_fresh = num_fresh;
+  p.scale = scale;
+  p.kv_scale = f8 ? kv_scale : 1.f;
+  p.timeout_ns = 2000000000ull;
+  cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
+  mla::mass::mla_mass_clear_kernel<<<1, 32, 0, stream>>>(p.status);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess)
+    e = f8 ? launch_mass<true>(p, s, pe, qn, qp, sms, dev, stream)
+           : launch_mass<false>(p, s, pe, qn, qp, sms, dev, stream);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
+}
+
+}  // extern "C"
