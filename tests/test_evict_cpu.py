@@ -146,7 +146,7 @@ def test_evict_oracle_by_hand():
     assert kept[0].tolist() == [0, 1, 6, 7]
     pos = np.array([[0, 50, 51, 9, 8, 7, 6, 5, 99, 99]], dtype=np.int32)  # slots 1 and 2 are the latest
     n, kept, *_ = oracle.evict_ref(mass, pos, np.array([8]), table, cache, 4, 0, 2)
-    assert kept[0].tolist() == [3, 1, 2, 5]
+    assert kept[0].tolist() == [5, 1, 2, 3]
     # nothing to do within the budget
     n, kept, *_ = oracle.evict_ref(mass, None, np.array([3]), table, cache, 5, 0, 0)
     assert n.tolist() == [3] and kept[0].tolist() == [0, 1, 2, -1, -1]
