@@ -498,6 +498,24 @@ def mla_decode_cascade_query_status(q_nope, kv_cache, page_table, prefix_pages: 
 
 
 # ---- prompt chunks and windows (include/mla_prefill.h) ----
+#
+# Each call first runs one combined test of everything it passes on (it runs
+# on every call; a small step is bound by it); the functions below it name
+# what is wrong when that test fails.
+
+def _fits(t, shape, dtype, dev) -> bool:
+    return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
+
+
+def _cache_fits(kv_cache, page_table, seq_lens, B, dev) -> bool:
+    import torch
+
+    return (kv_cache.dim() == 3 and kv_cache.shape[2] == 576 and kv_cache.get_device() == dev
+            and kv_cache.dtype in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn) and kv_cache.is_contiguous()
+            and _fits(seq_lens, (B,), torch.int32, dev) and page_table.dtype is torch.int32
+            and page_table.dim() == 2 and page_table.shape[0] == B and page_table.get_device() == dev
+            and page_table.stride(1) == 1 and page_table.stride(0) >= page_table.shape[1])
+
 
 def _check_current_device(t):
     """The library runs on the current device; a tensor elsewhere would be
@@ -515,18 +533,16 @@ def _int32_arg(name, v, low=0):
     return v
 
 
+def _stream_int(stream):
+    import torch
+
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
 def make_prefill_dims(q_nope, kv_cache, page_table, seq_lens) -> MlaPrefillDims:
     T, H, _ = q_nope.shape
-    return MlaPrefillDims(
-        batch=int(seq_lens.shape[0]),
-        num_heads=H,
-        total_q=T,
-        page_size=int(kv_cache.shape[1]),
-        num_pages=int(kv_cache.shape[0]),
-        max_pages_per_req=int(page_table.shape[1]),
-        page_table_stride=int(page_table.stride(0)),
-        kv_dtype=kv_dtype_code(kv_cache),
-    )
+    return MlaPrefillDims(seq_lens.shape[0], H, T, kv_cache.shape[1], kv_cache.shape[0], page_table.shape[1],
+                          page_table.stride(0), kv_dtype_code(kv_cache))
 
 
 def mla_prefill_workspace_size(dims: MlaPrefillDims, device: int | None = None) -> int:
@@ -559,20 +575,34 @@ def _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_le
             raise ValueError("all tensors must be on one device")
 
 
+def _prefill_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace) -> bool:
+    import torch
+
+    bf16, s, dev = torch.bfloat16, q_nope.shape, q_nope.get_device()
+    if dev < 0 or len(s) != 3 or s[2] != 512 or seq_lens.dim() != 1:
+        return False
+    T, H, B = s[0], s[1], seq_lens.shape[0]
+    return (_fits(q_nope, s, bf16, dev) and _fits(q_pe, (T, H, 64), bf16, dev) and _fits(out, s, bf16, dev)
+            and _fits(lse, (T, H), torch.float32, dev) and _fits(cu_q_lens, (B + 1,), torch.int32, dev)
+            and _cache_fits(kv_cache, page_table, seq_lens, B, dev) and workspace.get_device() == dev
+            and workspace.is_contiguous())
+
+
 def mla_prefill(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, window, num_sinks, scale, kv_scale, out, lse,
                 workspace, stream=None) -> None:
     """Enqueue the attention of chunks of new tokens over the paged cache (see
     include/mla_prefill.h): q_nope [total_q, H, 512], cu_q_lens int32 [B + 1];
     window 0 = none, else a sliding window plus num_sinks first tokens."""
-    _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
-    _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+    if not _prefill_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace):
+        _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+        _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+        raise ValueError("prefill tensors do not have the shapes, types and layouts the library expects")
     _check_current_device(q_nope)
     dims = make_prefill_dims(q_nope, kv_cache, page_table, seq_lens)
     rc = load_library().mla_prefill(
-        ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens),
-        _ptr(cu_q_lens), _int32_arg("window", window), _int32_arg("num_sinks", num_sinks), float(scale),
-        float(kv_scale), _ptr(out), _ptr(lse), _ptr(workspace),
-        ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream_handle(stream))
+        ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), cu_q_lens.data_ptr(), _int32_arg("window", window), _int32_arg("num_sinks", num_sinks),
+        scale, kv_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_prefill")
 
@@ -591,24 +621,20 @@ def mla_decode_window(q_nope, q_pe, kv_cache, page_table, seq_lens, window, num_
                       workspace, stream=None) -> None:
     """Enqueue a decode over a sliding window of `window` tokens and num_sinks
     first tokens (see include/mla_prefill.h); tensors as for mla_decode."""
-    _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
+    if q_nope.get_device() < 0:
+        _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
     _check_decode_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
     _check_current_device(q_nope)
     dims = make_dims(q_nope, kv_cache, page_table)
     rc = load_library().mla_decode_window(
-        ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens),
-        _int32_arg("window", window, 1), _int32_arg("num_sinks", num_sinks), float(scale), float(kv_scale), _ptr(out),
-        _ptr(lse), _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
-        _stream_handle(stream))
+        ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), _int32_arg("window", window, 1), _int32_arg("num_sinks", num_sinks), scale, kv_scale,
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_window")
 
 
 # ---- attention mass and eviction (include/mla_evict.h) ----
-
-def _opt_ptr(t) -> ctypes.c_void_p:
-    return ctypes.c_void_p(None) if t is None else _ptr(t)
-
 
 def mla_attn_mass_workspace_size(dims: MlaDims, device: int | None = None) -> int:
     import torch
@@ -642,22 +668,37 @@ def _check_mass_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass,
             raise ValueError("all tensors must be on one device")
 
 
+def _mass_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace) -> bool:
+    import torch
+
+    bf16, f32, s, dev = torch.bfloat16, torch.float32, q_nope.shape, q_nope.get_device()
+    if dev < 0 or len(s) != 4 or s[3] != 512 or mass_out.dim() != 2 or mass_out.shape[0] != s[0]:
+        return False
+    B, Q, H, _ = s
+    return (_fits(q_nope, s, bf16, dev) and _fits(q_pe, (B, Q, H, 64), bf16, dev) and _fits(lse, (B, Q, H), f32, dev)
+            and _fits(mass_out, mass_out.shape, f32, dev) and (mass is None or _fits(mass, mass_out.shape, f32, dev))
+            and _cache_fits(kv_cache, page_table, seq_lens, B, dev) and workspace.get_device() == dev
+            and workspace.is_contiguous())
+
+
 def mla_attn_mass(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, num_fresh, scale, kv_scale, mass, mass_out,
                   workspace, stream=None) -> None:
     """Enqueue the accumulation of the softmax weights that a step's queries
     gave to every cached token (see include/mla_evict.h): mass (None: zeros)
     and mass_out fp32 [B, mass_cols]; the last num_fresh tokens start at 0."""
-    _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass_out, workspace)
-    if mass is not None:
-        _check_cuda(mass)
-    _check_mass_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace)
+    if not _mass_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace):
+        _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass_out, workspace)
+        if mass is not None:
+            _check_cuda(mass)
+        _check_mass_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace)
+        raise ValueError("mass tensors do not have the shapes, types and layouts the library expects")
     _check_current_device(q_nope)
     dims = make_dims(q_nope, kv_cache, page_table)
     rc = load_library().mla_attn_mass(
-        ctypes.byref(dims), _ptr(q_nope), _ptr(q_pe), _ptr(kv_cache), _ptr(page_table), _ptr(seq_lens), _ptr(lse),
-        _int32_arg("num_fresh", num_fresh), float(scale), float(kv_scale), _opt_ptr(mass), _ptr(mass_out),
-        int(mass_out.shape[1]), _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()),
-        _stream_handle(stream))
+        ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), lse.data_ptr(), _int32_arg("num_fresh", num_fresh), scale, kv_scale,
+        None if mass is None else mass.data_ptr(), mass_out.data_ptr(), mass_out.shape[1], workspace.data_ptr(),
+        workspace.nbytes, _stream_int(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_attn_mass")
 
@@ -696,25 +737,44 @@ def _check_evict_tensors(mass, positions, seq_lens, page_table, kv_cache, budget
             raise ValueError("all tensors must be on one device")
 
 
+def _evict_fits(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out, positions_out,
+                workspace) -> bool:
+    import torch
+
+    f32, i32, s, dev = torch.float32, torch.int32, mass.shape, mass.get_device()
+    if dev < 0 or len(s) != 2:
+        return False
+    if positions is not None:
+        if positions_out is None or not (_fits(positions, s, i32, dev) and _fits(positions_out, s, i32, dev)):
+            return False
+    return (_fits(mass, s, f32, dev) and _fits(mass_out, s, f32, dev) and _fits(new_lens, s[:1], i32, dev)
+            and _fits(kept, (s[0], budget), i32, dev) and _cache_fits(kv_cache, page_table, seq_lens, s[0], dev)
+            and kv_cache.shape[1] == 64 and workspace.get_device() == dev and workspace.is_contiguous())
+
+
 def mla_evict(mass, positions, seq_lens, page_table, kv_cache, budget, num_sinks, num_recent, new_lens, kept, mass_out,
               positions_out, workspace, stream=None) -> None:
     """Enqueue the eviction of every request's tokens beyond its budget (see
     include/mla_evict.h).  positions and positions_out may be None."""
     budget = _int32_arg("budget", budget, 1)
-    _check_cuda(mass, seq_lens, page_table, kv_cache, new_lens, kept, mass_out, workspace)
-    if positions is not None and positions_out is not None:
-        _check_cuda(positions, positions_out)
-    _check_evict_tensors(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out,
-                         positions_out, workspace)
+    if not _evict_fits(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out,
+                       positions_out, workspace):
+        _check_cuda(mass, seq_lens, page_table, kv_cache, new_lens, kept, mass_out, workspace)
+        if positions is not None and positions_out is not None:
+            _check_cuda(positions, positions_out)
+        _check_evict_tensors(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out,
+                             positions_out, workspace)
+        raise ValueError("eviction tensors do not have the shapes, types and layouts the library expects")
     _check_current_device(mass)
-    dims = MlaEvictDims(batch=int(mass.shape[0]), mass_cols=int(mass.shape[1]), num_pages=int(kv_cache.shape[0]),
-                        max_pages_per_req=int(page_table.shape[1]), page_table_stride=int(page_table.stride(0)),
-                        kv_dtype=kv_dtype_code(kv_cache), budget=budget,
-                        num_sinks=_int32_arg("num_sinks", num_sinks), num_recent=_int32_arg("num_recent", num_recent))
+    dims = MlaEvictDims(mass.shape[0], mass.shape[1], kv_cache.shape[0], page_table.shape[1], page_table.stride(0),
+                        kv_dtype_code(kv_cache), budget, _int32_arg("num_sinks", num_sinks),
+                        _int32_arg("num_recent", num_recent))
+    pos = None if positions is None else positions.data_ptr()
+    pos_out = None if positions is None else positions_out.data_ptr()
     rc = load_library().mla_evict(
-        ctypes.byref(dims), _ptr(mass), _opt_ptr(positions), _ptr(seq_lens), _ptr(page_table), _ptr(kv_cache),
-        _ptr(new_lens), _ptr(kept), _ptr(mass_out), _opt_ptr(positions_out if positions is not None else None),
-        _ptr(workspace), ctypes.c_size_t(workspace.numel() * workspace.element_size()), _stream_handle(stream))
+        ctypes.byref(dims), mass.data_ptr(), pos, seq_lens.data_ptr(), page_table.data_ptr(), kv_cache.data_ptr(),
+        new_lens.data_ptr(), kept.data_ptr(), mass_out.data_ptr(), pos_out, workspace.data_ptr(), workspace.nbytes,
+        _stream_int(stream))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_evict")
 

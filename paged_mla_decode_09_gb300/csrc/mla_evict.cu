@@ -1,12 +1,17 @@
 // mla_evict (see include/mla_evict.h): which tokens a request keeps, and the
 // rows that move.
 //
-// Selection (one block per request): the k-th greatest of L 32-bit keys by
-// radix selection (11 + 11 + 10 bits, a shared-memory histogram each), then
-// one ordered walk that ranks the ties by slot and lists the free slots below
-// k and the kept tokens behind.  Firm tokens have the greatest key, so one
-// rule covers them.  The keys live in shared memory where they fit (48K
-// tokens), else they are formed again from the inputs on every walk.
+// Selection (a cluster of 1 to 8 blocks per request, each with a contiguous
+// part of the slots): the k-th greatest of L 32-bit keys by radix selection
+// (four digits of 8 bits: every block counts its digits in shared memory and
+// adds up all blocks' counts over distributed shared memory, 256 words a
+// block and digit; with 2048 bins those reads took 4 us a digit), then one
+// walk that counts and one that ranks the ties by slot and lists the free
+// slots below k and the kept tokens behind.  Firm tokens have the greatest
+// key, so one rule covers them.  The keys live in shared memory where they fit
+// (20K tokens a block), else they are formed again from the inputs on every
+// walk.  512 threads, so that two blocks share an SM: clusters of 8 blocks of
+// 1024 threads did not all fit at once (16 requests ran in two waves).
 //
 // Moves: a kept token below k stays, so only the tokens kept behind k move,
 // each into a place that no kept token uses: sources and destinations are
@@ -14,8 +19,8 @@
 // in order instead would move nearly every row behind the first dropped one:
 // for 4096 of 4224 tokens about 4000 rows of a request instead of 125.)
 //
-// What bounds it: at a few hundred KB per request the latency of the walks
-// (a dozen barriers and the loads of L keys per 1024 threads), then the moved
+// What bounds it: the latency of about a dozen walks and barriers (a block per
+// request took 59 us for 16 requests of up to 32K tokens), then the moved
 // rows' bytes.
 #include <cuda_runtime.h>
 
@@ -30,10 +35,10 @@ namespace mla {
 namespace evict {
 
 constexpr int kPage = 64;
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBins = 2048;
-constexpr int kMaxSmemKeys = 48 * 1024;
+constexpr int kBins = 256;
+constexpr int kMaxSmemKeys = 20 * 1024;  // 8 bytes a token: key and position
 
 struct Params {
   const float* mass;
@@ -50,6 +55,7 @@ struct Params {
   int32_t* movers;   // [B][budget] old slots of the tokens that move
   int32_t* holes;    // [B][budget] the slots that receive them
   int32_t B, cols, cap, num_pages, pt_stride, budget, sinks, recent, smem_keys;
+  int32_t cluster;   // blocks per request
 };
 
 // Keys that order like the weights: a NaN lowest, -0 equal to 0.
@@ -59,31 +65,26 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Sum over the block's earlier warps of a per-warp value; total in *all.
-__device__ __forceinline__ int warps_before(int mine, int* buf, int* all) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  __syncthreads();
-  if (lane == 0) buf[warp] = mine;
-  __syncthreads();
-  const int v = buf[lane];  // 32 warps
-  int s = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += t;
-  }
-  *all = __shfl_sync(0xffffffffu, s, 31);
-  return __shfl_sync(0xffffffffu, s - v, warp);
+// Counts a digit per lane (digit < 0: none): one addition per distinct digit
+// of the warp.  Additions to one shared address queue up (1024 firm tokens, or
+// a tenth of the weights at zero, took 40 us that way).
+__device__ __forceinline__ void count_digit(int* hist, int digit) {
+  const unsigned peers = __match_any_sync(0xffffffffu, digit);
+  if (digit >= 0 && (threadIdx.x & 31) == static_cast<unsigned>(__ffs(peers) - 1)) atomicAdd(&hist[digit], __popc(peers));
 }
 
-__global__ void __launch_bounds__(kThreads) mla_evict_select_kernel(const __grid_constant__ Params p) {
-  extern __shared__ uint32_t keys[];
-  __shared__ int hist[kBins];
+__global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __grid_constant__ Params p) {
+  extern __shared__ uint32_t keys[];  // keys of the block's slots, then their positions
+  __shared__ int hist[4][kBins];
   __shared__ int buf[kWarps];
-  __shared__ int pick[2];  // the digit of the k-th key, keys above it
+  __shared__ int pick[2];          // the digit of the k-th key, keys above it
+  __shared__ int4 counts_w[kWarps];  // per warp, see below
+  __shared__ int4 share;           // the block's sums of them, and its greatest position: read by the other blocks
+  __shared__ int share_pos;
   griddep_launch_dependents();
-  const int b = blockIdx.x, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (b == 0 && tid < 4) p.status[tid] = 0;
+  const int cs = p.cluster, b = blockIdx.x / cs, rank = blockIdx.x % cs;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (blockIdx.x == 0 && tid < 4) p.status[tid] = 0;
   const int Lraw = p.seq_lens[b];
   const bool bad = Lraw < 0 || Lraw > p.cap;
   const int L = Lraw < 0 ? 0 : (Lraw > p.cap ? p.cap : Lraw);
@@ -96,96 +97,161 @@ __global__ void __launch_bounds__(kThreads) mla_evict_select_kernel(const __grid
   int32_t* movers = p.movers + static_cast<int64_t>(b) * p.budget;
   int32_t* holes = p.holes + static_cast<int64_t>(b) * p.budget;
   int moves = 0;
-  if (k < L) {
-    // the greatest position
-    int last = L - 1;
-    if (pos) {
+  const int step = cs * kThreads, first = rank * kThreads + tid;  // shares of the copies below
+  auto sync_ranks = [&]() {
+    if (cs > 1) cluster_sync();
+    else __syncthreads();
+  };
+  if (k < L) {  // the same in every block of the cluster
+    const int part = ((L + cs - 1) / cs + 31) & ~31;  // slots of a block
+    const int r0 = rank * part < L ? rank * part : L, r1 = r0 + part < L ? r0 + part : L;
+    const bool cached = part <= p.smem_keys;
+    int32_t* spos = reinterpret_cast<int32_t*>(keys) + p.smem_keys;
+    for (int i = tid; i < 4 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+    int last = L - 1;  // the greatest position
+    {
       int m = -1;
-      for (int t = tid; t < L; t += kThreads) m = max(m, pos[t]);
-      m = __reduce_max_sync(0xffffffffu, m);
-      if (lane == 0) buf[warp] = m;
-      __syncthreads();
-      last = __reduce_max_sync(0xffffffffu, buf[lane]);
-      __syncthreads();
+      for (int t = r0 + tid; t < r1; t += 4 * kThreads) {  // eight loads in flight
+        int q4[4];
+        float x4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const bool in = t + q * kThreads < r1;
+          q4[q] = pos && in ? pos[t + q * kThreads] : -1;
+          x4[q] = cached && in ? mass[t + q * kThreads] : 0.f;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          m = max(m, q4[q]);
+          const int at = t + q * kThreads - r0;
+          if (cached && t + q * kThreads < r1) {
+            keys[at] = weight_key(x4[q]);
+            if (pos) spos[at] = q4[q];
+          }
+        }
+      }
+      if (pos) {
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) buf[warp] = m;
+        __syncthreads();
+        m = __reduce_max_sync(0xffffffffu, buf[lane % kWarps]);
+        if (tid == 0) share_pos = m;
+        sync_ranks();
+        last = -1;
+        for (int r = 0; r < cs; ++r) last = max(last, static_cast<int>(ld_cluster_u32(mapa(smem_u32(&share_pos), r))));
+      } else {
+        __syncthreads();
+      }
     }
     const int64_t firm_from = static_cast<int64_t>(last) - p.recent + 1;
+    auto firm = [&](int q) { return q < p.sinks || q >= firm_from; };
+    // the key of slot t (0 past the block's slots); the first walk makes it
+    // final in shared memory
     auto form = [&](int t) -> uint32_t {
-      const int q = pos ? pos[t] : t;
-      return (q < p.sinks || q >= firm_from) ? 0xFFFFFFFFu : weight_key(mass[t]);
+      if (t >= r1) return 0u;
+      if (cached) return firm(pos ? spos[t - r0] : t) ? 0xFFFFFFFFu : keys[t - r0];
+      return firm(pos ? pos[t] : t) ? 0xFFFFFFFFu : weight_key(mass[t]);
     };
-    const bool cached = L <= p.smem_keys;
-    if (cached) {
-      for (int t = tid; t < L; t += kThreads) keys[t] = form(t);
-    }
-    auto key = [&](int t) -> uint32_t { return cached ? keys[t] : form(t); };
     // radix selection of the k-th greatest key
     uint32_t prefix = 0, mask = 0;
     int need = k;  // rank within the keys that share the prefix
 #pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
-      const int bins = pass == 2 ? 1024 : 2048;
-      for (int i = tid; i < bins; i += kThreads) hist[i] = 0;
-      __syncthreads();
-      for (int t = tid; t < L; t += kThreads) {
-        const uint32_t x = key(t);
-        if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & (bins - 1)], 1);
+    for (int pass = 0; pass < 4; ++pass) {
+      const int shift = 24 - 8 * pass;
+      for (int t = r0 + tid; t - lane < r1; t += kThreads) {
+        uint32_t x;
+        if (pass == 0 || !cached) {
+          x = form(t);
+          if (cached && t < r1) keys[t - r0] = x;
+        } else {
+          x = t < r1 ? keys[t - r0] : 0u;
+        }
+        const bool in = t < r1 && (x & mask) == prefix;
+        if (__any_sync(0xffffffffu, in)) count_digit(hist[pass], in ? static_cast<int>((x >> shift) & 255u) : -1);
       }
-      __syncthreads();
-      // from the greatest digit down: thread i has bins [lo, lo + per), the
-      // warps' sums in that order
-      const int per = bins / kThreads;
-      const int top = bins - 1 - tid * per;
-      int c[2];
-      c[0] = hist[top];
-      c[1] = per == 2 ? hist[top - 1] : 0;
-      int s = c[0] + c[1];
-      const int own = s;
+      sync_ranks();
+      // from the greatest digit down: thread i has bin 255 - i of all blocks
+      int own = 0;
+      if (tid < kBins) {
+        const uint32_t at = smem_u32(&hist[pass][kBins - 1 - tid]);
+        uint32_t c[8];
+#pragma unroll
+        for (int r = 0; r < 8; ++r) c[r] = r < cs ? ld_cluster_u32(mapa(at, r)) : 0u;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) own += static_cast<int>(c[r]);
+      }
+      int sum = own;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += t;
+        const int t = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += t;
       }
-      int all;
-      const int before = warps_before(__shfl_sync(0xffffffffu, s, 31), buf, &all) + s - own;
-      if (before < need && before + own >= need) {  // one thread
-        const bool second = before + c[0] < need;
-        pick[0] = second ? top - 1 : top;
-        pick[1] = before + (second ? c[0] : 0);
+      if (lane == 31) buf[warp] = sum;
+      __syncthreads();
+      int before = sum - own;
+      for (int w = 0; w < warp && w < kBins / 32; ++w) before += buf[w];
+      if (tid < kBins && before < need && before + own >= need) {  // one thread
+        pick[0] = kBins - 1 - tid;
+        pick[1] = before;
       }
       __syncthreads();
       prefix |= static_cast<uint32_t>(pick[0]) << shift;
-      mask |= static_cast<uint32_t>(bins - 1) << shift;
+      mask |= 255u << shift;
       need -= pick[1];
-      __syncthreads();
     }
-    // keys above prefix are kept, and of the keys equal to it the `need`
-    // lowest slots.  Each warp walks a contiguous range of slots.
-    const int per_warp = ((L + kWarps - 1) / kWarps + 31) & ~31;
-    const int t0 = warp * per_warp, t1 = min(L, t0 + per_warp);
-    int ties = 0;
-    for (int t = t0 + lane; t - lane < t1; t += 32)
-      ties += __popc(__ballot_sync(0xffffffffu, t < t1 && key(t) == prefix));
-    int all;
-    const int tie0 = warps_before(ties, buf, &all);
-    // free slots below k and movers behind it, counted, then written in order
-    int nh = 0, nm = 0, tie = tie0;
+    auto key = [&](int t) -> uint32_t { return cached ? (t < r1 ? keys[t - r0] : 0u) : form(t); };
+    // Keys above prefix are kept, and of the keys equal to it the `need`
+    // lowest slots.  Each warp walks a contiguous range of the block's slots
+    // and counts (x) ties below k, (y) ties from k on, (z) slots below k with a
+    // smaller key or a tie, (w) greater keys from k on; how many of its ties
+    // are kept follows from the ties before it, and with it its free slots
+    // below k and its movers.
+    const int per_warp = ((r1 - r0 + kWarps - 1) / kWarps + 31) & ~31;
+    const int t0 = min(r1, r0 + warp * per_warp), t1 = min(r1, t0 + per_warp);
+    int4 n = make_int4(0, 0, 0, 0);
     for (int t = t0 + lane; t - lane < t1; t += 32) {
       const bool in = t < t1;
       const uint32_t x = in ? key(t) : 0u;
-      const unsigned eq = __ballot_sync(0xffffffffu, in && x == prefix);
-      const bool keep = in && (x > prefix || (x == prefix && tie + __popc(eq & ((1u << lane) - 1u)) < need));
-      tie += __popc(eq);
-      nh += __popc(__ballot_sync(0xffffffffu, in && t < k && !keep));
-      nm += __popc(__ballot_sync(0xffffffffu, in && t >= k && keep));
+      n.x += __popc(__ballot_sync(0xffffffffu, in && t < k && x == prefix));
+      n.y += __popc(__ballot_sync(0xffffffffu, in && t >= k && x == prefix));
+      n.z += __popc(__ballot_sync(0xffffffffu, in && t < k && x <= prefix));
+      n.w += __popc(__ballot_sync(0xffffffffu, in && t >= k && x > prefix));
     }
-    int h = warps_before(nh, buf, &all);
-    int m = warps_before(nm, buf, &moves);
-    tie = tie0;
+    if (lane == 0) counts_w[warp] = n;
+    __syncthreads();
+    if (tid == 0) {
+      int4 a = make_int4(0, 0, 0, 0);
+      for (int w = 0; w < kWarps; ++w) {
+        a.x += counts_w[w].x; a.y += counts_w[w].y; a.z += counts_w[w].z; a.w += counts_w[w].w;
+      }
+      share = a;
+    }
+    sync_ranks();
+    // free slots and movers of the blocks and warps before this warp
+    int tie = 0, h = 0, m = 0;
+    auto add = [&](const int4& c) {
+      const int lo = min(max(need - tie, 0), c.x);            // kept ties below k
+      const int hi = min(max(need - tie - c.x, 0), c.y);      // and from k on
+      tie += c.x + c.y;
+      h += c.z - lo;
+      m += c.w + hi;
+    };
+    int tie_b = 0, h_b = 0, m_b = 0;
+    for (int r = 0; r < cs; ++r) {
+      if (r == rank) {
+        tie_b = tie; h_b = h; m_b = m;
+      }
+      const uint32_t at = mapa(smem_u32(&share), r);
+      add(make_int4(static_cast<int>(ld_cluster_u32(at)), static_cast<int>(ld_cluster_u32(at + 4)),
+                    static_cast<int>(ld_cluster_u32(at + 8)), static_cast<int>(ld_cluster_u32(at + 12))));
+    }
+    moves = m;
+    tie = tie_b; h = h_b; m = m_b;
+    for (int w = 0; w < warp; ++w) add(counts_w[w]);
+    const unsigned below = (1u << lane) - 1u;
     for (int t = t0 + lane; t - lane < t1; t += 32) {
       const bool in = t < t1;
       const uint32_t x = in ? key(t) : 0u;
-      const unsigned below = (1u << lane) - 1u;
       const unsigned eq = __ballot_sync(0xffffffffu, in && x == prefix);
       const bool keep = in && (x > prefix || (x == prefix && tie + __popc(eq & below) < need));
       tie += __popc(eq);
@@ -193,34 +259,32 @@ __global__ void __launch_bounds__(kThreads) mla_evict_select_kernel(const __grid
       const unsigned mb = __ballot_sync(0xffffffffu, in && t >= k && keep);
       if (in && t < k && !keep) holes[h + __popc(hb & below)] = t;
       if (in && t >= k && keep) movers[m + __popc(mb & below)] = t;
-      if (in && t < k && keep) kept[t] = t;
+      // outputs: only slots below k are written, and only slots that stay
+      // below k or movers from k on are read for them, so they may be the inputs
+      if (in && t < k && keep) {
+        kept[t] = t;
+        mass_out[t] = mass[t];
+        if (pos) pos_out[t] = pos[t];
+      }
       h += __popc(hb);
       m += __popc(mb);
     }
-    __syncthreads();
-    // outputs: only slots below k are written and only slots that stay below
-    // k or movers from k on are read, so outputs may be the inputs
-    for (int j = tid; j < moves; j += kThreads) {
+    sync_ranks();  // the lists are whole, every key has been read, and no block reads another's memory any more
+    for (int j = first; j < moves; j += step) {
       const int t = holes[j], o = movers[j];
       kept[t] = o;
       mass_out[t] = mass[o];
       if (pos) pos_out[t] = pos[o];
     }
-    __syncthreads();
-    for (int t = tid; t < k; t += kThreads) {
-      if (kept[t] != t) continue;
-      mass_out[t] = mass[t];
-      if (pos) pos_out[t] = pos[t];
-    }
   } else {
-    for (int t = tid; t < k; t += kThreads) {
+    for (int t = first; t < k; t += step) {
       kept[t] = t;
       mass_out[t] = mass[t];
       if (pos) pos_out[t] = pos[t];
     }
   }
-  for (int t = k + tid; t < p.budget; t += kThreads) kept[t] = -1;
-  if (tid == 0) {
+  for (int t = k + first; t < p.budget; t += step) kept[t] = -1;
+  if (rank == 0 && tid == 0) {
     p.new_lens[b] = k;
     p.counts[b] = bad ? -1 - moves : moves;
   }
@@ -340,13 +404,29 @@ int mla_evict(const mla_evict_dims* d, const float* mass, const int32_t* positio
   p.budget = d->budget;
   p.sinks = d->num_sinks;
   p.recent = d->num_recent;
-  p.smem_keys = p.cap < mla::evict::kMaxSmemKeys ? p.cap : mla::evict::kMaxSmemKeys;
-  const int smem = ((p.smem_keys * 4) + 15) & ~15;
+  // blocks per request: as many as fit one to an SM, each with 512 slots or
+  // more (a thread's worth each)
+  p.cluster = 1;
+  while (p.cluster < 8 && 2ll * p.cluster * d->batch <= sms && p.cap / (2 * p.cluster) >= mla::evict::kThreads)
+    p.cluster *= 2;
+  const int part = ((p.cap + p.cluster - 1) / p.cluster + 31) & ~31;
+  p.smem_keys = part < mla::evict::kMaxSmemKeys ? part : mla::evict::kMaxSmemKeys;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-  cudaError_t e = allow_smem<0>(mla::evict::mla_evict_select_kernel, mla::evict::kMaxSmemKeys * 4, dev);
+  cudaError_t e = allow_smem<0>(mla::evict::mla_evict_select_kernel, mla::evict::kMaxSmemKeys * 8, dev);
   if (e == cudaSuccess) {
-    mla::evict::mla_evict_select_kernel<<<d->batch, mla::evict::kThreads, smem, stream>>>(p);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(d->batch) * p.cluster, 1, 1);
+    cfg.blockDim = dim3(mla::evict::kThreads, 1, 1);
+    cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_keys) * 8;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, mla::evict::mla_evict_select_kernel, p);
   }
   if (e == cudaSuccess) {
     // about eight blocks per SM in all, each request's rows over its share

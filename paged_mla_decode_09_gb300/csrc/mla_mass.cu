@@ -7,20 +7,26 @@
 // computed again (1152 flops per row and key, and every cache row read once),
 // which needs no store of the attention's weights.
 //
-// Work: the requests' pages in slices of equal weighted length, one per CTA;
-// a slice's piece of a request is taken kSub pages at a time through all of
-// the request's row blocks of 128 (decode steps have one), so that the pages
-// come from L2 for every block but the first.  Per page: S = Q K^T by tcgen05
-// with the queries in TMEM (lane = row), two groups of four warps take the
-// even and the odd pages: exp2, then each warp adds its 32 rows by halving
-// exchanges (62 shuffles leave every lane the sums of two keys) and 64 threads
-// add the four warps' sums to the keys' running values.  A key always meets
-// the same thread, its row blocks in order: no atomics, and results that do
-// not depend on how the pages were sliced.
+// Two kernels, by which operand is the smaller one:
 //
-// What bounds it: a decode step reads 72 KB per page and CTA, ~3100 cycles of
-// its share of HBM, against 1224 tensor cycles; many query rows are bound by
-// the tensor pipe (36 MMAs of 34 cycles per page).
+//   * at most 128 query rows per request (decode steps): the queries stay in
+//     tensor memory and the pages stream by (lane = query row).  Each CTA takes
+//     a slice of all pages.  Per page two groups of four warps (even and odd
+//     pages) take exp2, each warp adds its 32 rows by halving exchanges (62
+//     shuffles leave every lane the sums of two keys) and 64 threads add the
+//     four warps' sums to the keys' values.  Bound by HBM: 72 KB per page and
+//     CTA are ~3100 cycles of its share, against 1224 tensor cycles.
+//   * more rows (a prompt's last tokens): 128 keys stay in tensor memory (an
+//     e4m3 cache's expanded to bf16, which is exact) and the query rows stream
+//     by, 64 at a time (lane = key), so that a key's sum is a thread's own
+//     running sum: no exchanges, every cache row read once, and the bf16
+//     queries need no splitting.  Bound by the tensor pipe: 36 MMAs of 34
+//     cycles per 128 keys x 64 rows.  (With the queries kept instead, every
+//     CTA moved and split all row blocks for the few pages of its slice: 503
+//     us for 32 tokens x 128 heads over 75K keys of four requests, e4m3.)
+//
+// No atomics: a key belongs to one CTA, which adds in a fixed order, so
+// results do not depend on timing or slicing.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -42,7 +48,6 @@ using chunk::kRows;
 using chunk::kThreads;
 
 constexpr int kUnitCost = 4;  // pages' worth of starting a piece
-constexpr int kSub = 16;      // pages taken through all row blocks at a time
 
 template <bool kF8>
 struct Lay {
@@ -77,7 +82,7 @@ struct Params {
   const float* mass_in;
   float* mass_out;
   int32_t* status;
-  int32_t B, H, Q, R, G;
+  int32_t B, H, Q, R;
   int32_t num_pages, max_pages, pt_stride, cols;
   int32_t cap;        // longest length the table and the mass rows hold
   int32_t num_fresh;
@@ -95,59 +100,38 @@ __device__ __forceinline__ int length_of(const Params& p, int b) {
   return L < 0 ? 0 : (L > p.cap ? p.cap : L);
 }
 
-// The units of a CTA's slice, in order: for every piece of a request, kSub
-// pages at a time, every row block.
+// The pieces of requests in a CTA's slice, in order.
 struct Unit {
-  int b, L, p0, p1, g;
+  int b, L, p0, p1;
 };
 struct UnitIter {
   const Params* p;
   long long x0, x1, start;
-  int b, L, p1, a, g;
-  bool open;  // a piece is being walked: pages [a, p1), next block g
+  int b;
   __device__ void init(const Params& pp, const Ctrl* c) {
     p = &pp;
-    const long long W = c->total;
-    x0 = W * blockIdx.x / gridDim.x;
-    x1 = W * (blockIdx.x + 1) / gridDim.x;
+    x0 = c->total * blockIdx.x / gridDim.x;
+    x1 = c->total * (blockIdx.x + 1) / gridDim.x;
     start = c->start;
     b = c->first;
-    open = false;
   }
   __device__ bool next(Unit& u) {
-    while (!open) {
-      if (b >= p->B || start >= x1) return false;
-      L = length_of(*p, b);
-      const int np = (L + kPage - 1) / kPage;
+    while (b < p->B && start < x1) {
+      u.b = b;
+      u.L = length_of(*p, b);
+      const int np = (u.L + kPage - 1) / kPage;
       const long long lo = x0 - start - kUnitCost, hi = x1 - start - kUnitCost;
-      a = lo > 0 ? (lo < np ? static_cast<int>(lo) : np) : 0;
-      p1 = hi < np ? (hi > 0 ? static_cast<int>(hi) : 0) : np;
-      g = 0;
-      open = a < p1;
-      if (!open) {
-        start += kUnitCost + np;
-        ++b;
-      }
+      u.p0 = lo > 0 ? (lo < np ? static_cast<int>(lo) : np) : 0;
+      u.p1 = hi < np ? (hi > 0 ? static_cast<int>(hi) : 0) : np;
+      start += kUnitCost + np;
+      ++b;
+      if (u.p0 < u.p1) return true;
     }
-    u.b = b;
-    u.L = L;
-    u.p0 = a;
-    u.p1 = p->G > 1 && p1 - a > kSub ? a + kSub : p1;
-    u.g = g;
-    if (++g == p->G) {
-      g = 0;
-      a = u.p1;
-      if (a >= p1) {
-        open = false;
-        start += kUnitCost + (L + kPage - 1) / kPage;
-        ++b;
-      }
-    }
-    return true;
+    return false;
   }
 };
 
-enum WaitTag : int { kWaitEmpty = 201, kWaitLanded, kWaitQFull, kWaitSPrev, kWaitQ, kWaitS, kWaitSums };
+enum WaitTag : int { kWaitEmpty = 201, kWaitOther, kWaitLanded, kWaitQFull, kWaitSPrev, kWaitQ, kWaitS, kWaitSums };
 
 __device__ __forceinline__ void raise_timeout(const Params& p, Ctrl* ctrl, int tag, uint32_t j) {
   if (atomicCAS(p.status + 1, 0, tag) == 0) {
@@ -156,6 +140,52 @@ __device__ __forceinline__ void raise_timeout(const Params& p, Ctrl* ctrl, int t
   }
   atomicOr(p.status, MLA_DEV_TIMEOUT);
   *reinterpret_cast<volatile int*>(&ctrl->abort) = 1;
+}
+
+// Where this CTA's slice of a line begins on which request b occupies
+// weight(length of b): two passes over the lengths (inputs of the call, so
+// before griddep_wait), first the total, then the request that holds the
+// slice's start.  All threads; returns whether this thread saw a bad length.
+template <typename Weight>
+__device__ __forceinline__ bool find_slice(const Params& p, Ctrl* ctrl, Weight weight) {
+  __shared__ long long wsum[kThreads / 32];
+  __shared__ long long carry;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  bool bad = false;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (tid == 0) carry = 0;
+    __syncthreads();
+    const long long x0 = pass ? ctrl->total * blockIdx.x / gridDim.x : 0;
+    for (int base = 0; base < p.B; base += kThreads) {
+      const int b = base + tid;
+      long long v = 0;
+      if (b < p.B) {
+        const int L = p.seq_lens[b];
+        bad = bad || L < p.Q || L > p.cap;
+        v = weight(length_of(p, b));
+      }
+      const long long own = v;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+      }
+      if (lane == 31) wsum[warp] = v;
+      __syncthreads();
+      long long before = carry;
+      for (int w = 0; w < warp; ++w) before += wsum[w];
+      const long long end = before + v;
+      if (pass && b < p.B && end > x0 && end - own <= x0) {  // exactly one request
+        ctrl->first = b;
+        ctrl->start = end - own;
+      }
+      __syncthreads();
+      if (tid == kThreads - 1) carry = end;
+      __syncthreads();
+    }
+    if (tid == 0 && !pass) ctrl->total = carry;
+    __syncthreads();
+  }
+  return bad;
 }
 
 template <bool kF8>
@@ -185,7 +215,7 @@ __device__ void produce(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUtens
         qloaded = un + 1;
       }
       mbar_arrive(smem_u32(&ctrl->kv_full[st]));
-      const int row = u.b * p.R + u.g * kRows + C::kQRows * e;
+      const int row = u.b * p.R + C::kQRows * e;
       const uint32_t slot = smem_u32(ring + st * C::kSlotS);
       tma_load_3d(slot, tm_qn, 0, row, 0, qbar);
       tma_load_2d(slot + C::kQRows * 128 * 8, tm_qp, 0, row, qbar);
@@ -264,47 +294,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(&ctrl->tmem_base), 512);
     tmem_relinquish();
   }
-  // The slice of this CTA.  A request occupies kUnitCost + pages of the
-  // weighted line; two passes over the lengths (inputs of the call, so before
-  // griddep_wait): the total, then the request that holds the slice's start.
-  bool bad = false;
-  {
-    __shared__ long long wsum[kThreads / 32];
-    __shared__ long long carry;
-    for (int pass = 0; pass < 2; ++pass) {
-      if (tid == 0) carry = 0;
-      __syncthreads();
-      const long long x0 = pass ? ctrl->total * blockIdx.x / gridDim.x : 0;
-      for (int base = 0; base < p.B; base += kThreads) {
-        const int b = base + tid;
-        long long v = 0;
-        if (b < p.B) {
-          const int L = p.seq_lens[b];
-          bad = bad || L < p.Q || L > p.cap;
-          v = kUnitCost + (length_of(p, b) + kPage - 1) / kPage;
-        }
-        const long long own = v;
-        for (int o = 1; o < 32; o <<= 1) {
-          const long long t = __shfl_up_sync(0xffffffffu, v, o);
-          if (lane >= o) v += t;
-        }
-        if (lane == 31) wsum[warp] = v;
-        __syncthreads();
-        long long before = carry;
-        for (int w = 0; w < warp; ++w) before += wsum[w];
-        const long long end = before + v;
-        if (pass && b < p.B && end > x0 && end - own <= x0) {  // exactly one request
-          ctrl->first = b;
-          ctrl->start = end - own;
-        }
-        __syncthreads();
-        if (tid == kThreads - 1) carry = end;
-        __syncthreads();
-      }
-      if (tid == 0 && !pass) ctrl->total = carry;
-      __syncthreads();
-    }
-  }
+  // A request occupies kUnitCost + pages of the weighted line.
+  const bool bad = find_slice(p, ctrl, [&](int L) { return kUnitCost + (L + kPage - 1) / kPage; });
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -408,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         why = kWaitQ;
         break;
       }
-      const int row = u.g * kRows + r;  // of the request's R rows
+      const int row = r;  // of the request's R <= 128 rows
       const bool real = row < p.R;
       float nl = 0.f;  // -lse in log2 units
       int nvis = 0;
@@ -428,14 +419,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float c2 = p.scale * kLog2e * (kF8 ? qs * p.kv_scale : 1.f);
       const float* in = p.mass_in ? p.mass_in + static_cast<int64_t>(u.b) * p.cols : nullptr;
       float* out = p.mass_out + static_cast<int64_t>(u.b) * p.cols;
-      const int old = u.L - p.num_fresh;  // tokens below start from mass_in (num_fresh >= 0: no overflow below 0)
+      const int old = u.L - p.num_fresh;  // tokens below start from mass_in
       for (int pg = u.p0; pg < u.p1; ++pg, ++j) {
         if ((pg & 1) != gg) continue;
         const int sb = static_cast<int>(j % 3);
         const int t0 = pg * kPage, t = t0 + r;
-        // the key's value so far: this thread's own store of the block before
         float base = 0.f;
-        if (r < 64 && t < u.L) base = u.g > 0 ? out[t] : (in && t < old ? in[t] : 0.f);
+        if (r < 64 && t < old && in) base = in[t];
         if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (j / 3) & 1, abort, p.timeout_ns)) {
           ok = false;
           why = kWaitS;
@@ -494,6 +484,382 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 2) tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------- many rows: the keys stay
+constexpr int kKeys = 128;   // keys of a tile (M of the MMAs)
+constexpr int kSlot = 73728;  // a page of the cache, or 64 query rows
+constexpr int kSlots = 3;
+constexpr int kNlOff = kSlots * kSlot;            // [3][64] -lse of a row tile, in log2 units
+constexpr int kPartOff = kNlOff + 3 * 64 * 4;     // [2][128] the second group's sums
+constexpr int kRowsData = kPartOff + 2 * kKeys * 4;
+constexpr int kRowsSmem = 1024 + kRowsData + 512;
+
+// The key tiles of a CTA's slice, in order.
+struct Tile {
+  int b, L, t0;  // keys t0 .. t0 + 127
+};
+struct TileIter {
+  const Params* p;
+  long long x, x1, start;
+  int b;
+  __device__ void init(const Params& pp, const Ctrl* c) {
+    p = &pp;
+    x = c->total * blockIdx.x / gridDim.x;
+    x1 = c->total * (blockIdx.x + 1) / gridDim.x;
+    start = c->start;
+    b = c->first;
+  }
+  __device__ bool next(Tile& u) {
+    while (x < x1 && b < p->B) {
+      u.L = length_of(*p, b);
+      const long long tiles = (u.L + kKeys - 1) / kKeys;
+      if (x >= start + tiles) {
+        start += tiles;
+        ++b;
+        continue;
+      }
+      u.b = b;
+      u.t0 = static_cast<int>(x - start) * kKeys;
+      ++x;
+      return true;
+    }
+    return false;
+  }
+};
+
+// 16 codes (a 16-byte chunk) as 16 bf16 values (exact).
+__device__ __forceinline__ void expand16(uint4 v, uint32_t* o) {
+  const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(in[k] >> (16 * h)), __NV_E4M3);
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x, f.y);
+      o[2 * k + h] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+}
+
+template <bool kF8>
+__global__ void __launch_bounds__(kThreads, 1)
+    mla_mass_rows_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_s,
+                         const __grid_constant__ CUtensorMap tm_pe, const __grid_constant__ CUtensorMap tm_qn,
+                         const __grid_constant__ CUtensorMap tm_qp) {
+  using C = chunk::Cfg<false, 1>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Ctrl* ctrl = reinterpret_cast<Ctrl*>(data + kRowsData);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&ctrl->kv_full[i]), 1);
+      mbar_init(smem_u32(&ctrl->kv_empty[i]), 1);
+      mbar_init(smem_u32(&ctrl->s_full[i]), 2);   // the tile's QK and its -lse (warp 3)
+      mbar_init(smem_u32(&ctrl->s_empty[i]), 4);  // the group that read it
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctrl->q_bar[i]), 1);
+      mbar_init(smem_u32(&ctrl->sums[i]), 4);
+    }
+    mbar_init(smem_u32(&ctrl->q_full), 8);
+    mbar_init(smem_u32(&ctrl->drain), 1);
+    ctrl->abort = 0;
+    ctrl->first = p.B;
+    ctrl->start = 0;
+    fence_barrier_init();
+    tma_prefetch_desc(&tm_s);
+    tma_prefetch_desc(&tm_qn);
+    tma_prefetch_desc(&tm_qp);
+    if (kF8) tma_prefetch_desc(&tm_pe);
+  }
+  if (warp == 2) {
+    tmem_alloc(smem_u32(&ctrl->tmem_base), 512);
+    tmem_relinquish();
+  }
+  const bool bad = find_slice(p, ctrl, [&](int L) { return (L + kKeys - 1) / kKeys; });
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  griddep_wait();
+  if (bad && blockIdx.x == 0) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
+  const uint32_t tmem = ctrl->tmem_base;
+  volatile int* abort = &ctrl->abort;
+  uint8_t* ring = data;
+  const int ntiles = (p.R + 63) / 64;  // row tiles
+  TileIter it;
+  it.init(p, ctrl);
+  Tile u;
+  uint32_t un = 0;
+  bool ok = true;
+  int why = 0;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // per key tile its pages (ring entries that complete on q_bar), then
+      // the request's row tiles
+      uint32_t i = 0;
+      auto acquire = [&]() -> bool {
+        return mbar_wait(smem_u32(&ctrl->kv_empty[i % kSlots]), ((i / kSlots) & 1) ^ 1, abort, p.timeout_ns);
+      };
+      while (ok && it.next(u)) {
+        const uint32_t qbar = smem_u32(&ctrl->q_bar[un & 1]);
+        const int pages = u.t0 + kPage < u.L ? 2 : 1;
+        for (int e = 0; e < 2; ++e, ++i) {
+          if (!acquire()) {
+            ok = false;
+            break;
+          }
+          const uint32_t slot = smem_u32(ring + (i % kSlots) * kSlot);
+          if (e == 0) mbar_expect_tx(qbar, static_cast<uint32_t>(pages * kPage * (kF8 ? 576 : 1152)));
+          mbar_arrive(smem_u32(&ctrl->kv_full[i % kSlots]));
+          if (e >= pages) continue;  // an odd last page: its lanes are not stored
+          int32_t pid = __ldg(p.page_table + static_cast<int64_t>(u.b) * p.pt_stride + u.t0 / kPage + e);
+          if (pid < 0 || pid >= p.num_pages) {
+            atomicOr(p.status, MLA_DEV_BAD_PAGE_ID);
+            pid = 0;
+          }
+          tma_load_3d(slot, &tm_s, 0, pid * kPage, 0, qbar);
+          if constexpr (kF8) tma_load_2d(slot + 4 * 8192, &tm_pe, kDL, pid * kPage, qbar);
+        }
+        ++un;
+        for (int n = 0; n < ntiles && ok; ++n, ++i) {
+          if (!acquire()) {
+            ok = false;
+            break;
+          }
+          const uint32_t slot = smem_u32(ring + (i % kSlots) * kSlot), bar = smem_u32(&ctrl->kv_full[i % kSlots]);
+          const int row = u.b * p.R + 64 * n;
+          mbar_expect_tx(bar, static_cast<uint32_t>(kSlot));
+          tma_load_3d(slot, &tm_qn, 0, row, 0, bar);
+          tma_load_2d(slot + 8 * 8192, &tm_qp, 0, row, bar);
+        }
+      }
+      if (!ok) raise_timeout(p, ctrl, kWaitEmpty, i);
+      for (uint32_t q = 0; q < static_cast<uint32_t>(kSlots) && q < i; ++q) {
+        const uint32_t last = i - 1 - ((i - 1 - q) % kSlots);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&ctrl->kv_full[q]), (last / kSlots) & 1) && globaltimer_ns() - t0 < p.timeout_ns) {
+        }
+      }
+      if (un) {
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(smem_u32(&ctrl->q_bar[(un - 1) & 1]), ((un - 1) >> 1) & 1) &&
+               globaltimer_ns() - t0 < p.timeout_ns) {
+        }
+      }
+    }
+  } else if (warp == 1) {
+    uint32_t i = 0, j = 0;
+    while (ok && it.next(u)) {
+      for (int e = 0; e < 2 && ok; ++e, ++i)
+        ok = mbar_wait_warp(smem_u32(&ctrl->kv_full[i % kSlots]), (i / kSlots) & 1, abort, p.timeout_ns);
+      why = kWaitLanded;
+      if (!ok) break;
+      if (!mbar_wait_warp(smem_u32(&ctrl->q_full), un & 1, abort, p.timeout_ns)) {
+        ok = false;
+        why = kWaitQFull;
+        break;
+      }
+      if (lane == 0) {
+        mbar_arrive(smem_u32(&ctrl->kv_empty[(i - 2) % kSlots]));
+        mbar_arrive(smem_u32(&ctrl->kv_empty[(i - 1) % kSlots]));
+      }
+      __syncwarp();
+      ++un;
+      for (int n = 0; n < ntiles; ++n, ++j, ++i) {
+        const int st = static_cast<int>(i % kSlots), sb = static_cast<int>(j % 3);
+        if (!mbar_wait_all_warp(smem_u32(&ctrl->kv_full[st]), (i / kSlots) & 1, smem_u32(&ctrl->s_empty[sb]),
+                                ((j / 3) & 1) ^ 1, 0u, 0u, 0u, 0u, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitLanded;
+          break;
+        }
+        tc_fence_after();
+        const uint64_t dq = smem_desc(smem_u32(ring + st * kSlot), 16, 1024, kSwizzle128B);
+        const uint32_t dcol = tmem + C::kSCol0 + sb * 64;
+#pragma unroll
+        for (int d = 0; d < 9; ++d)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ts_e<false>(dcol, tmem + d * 32 + k * 8, dq + static_cast<uint64_t>(d * (8192 >> 4) + k * 2),
+                            C::kIdescQK, (d | k) ? 1u : 0u);
+        mma_commit_e(smem_u32(&ctrl->kv_empty[st]));
+        mma_commit_e(smem_u32(&ctrl->s_full[sb]));
+      }
+    }
+    if (!ok && lane == 0) raise_timeout(p, ctrl, why, j);
+    __syncwarp();
+    mma_commit_e(smem_u32(&ctrl->drain));
+    if (lane == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(smem_u32(&ctrl->drain), 0) && globaltimer_ns() - t0 < p.timeout_ns) {
+      }
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // -lse of every row tile, in log2 units, beside the score buffer it
+    // belongs to; -inf (a weight of 0) for rows that saw nothing
+    uint32_t j = 0;
+    float* nl = reinterpret_cast<float*>(data + kNlOff);
+    while (ok && it.next(u)) {
+      const float* lse = p.lse + static_cast<int64_t>(u.b) * p.R;
+      for (int n = 0; n < ntiles; ++n, ++j) {
+        const int sb = static_cast<int>(j % 3);
+        float v[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int row = 64 * n + lane + 32 * q;
+          const float l = row < p.R ? lse[row] : INFINITY;
+          v[q] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        }
+        if (!mbar_wait_warp(smem_u32(&ctrl->s_empty[sb]), ((j / 3) & 1) ^ 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitOther;
+          break;
+        }
+        nl[sb * 64 + lane] = v[0];
+        nl[sb * 64 + 32 + lane] = v[1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->s_full[sb]));
+      }
+    }
+    if (!ok && lane == 0) raise_timeout(p, ctrl, why, j);
+  } else if (warp >= 4) {
+    const int r = (warp & 3) * 32 + lane;  // key of the tile
+    const int gg = (warp - 4) >> 2;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const float c2 = p.scale * kLog2e * (kF8 ? p.kv_scale : 1.f);
+    float* parts = reinterpret_cast<float*>(data + kPartOff);
+    uint32_t i = 0, j = 0;
+    while (ok && it.next(u)) {
+      // the tile's keys replace the earlier ones in TMEM once every QK with
+      // those is done
+      if (j > 0 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - 1) % 3]), ((j - 1) / 3) & 1, abort,
+                                                p.timeout_ns)) {
+        ok = false;
+        why = kWaitSPrev;
+        break;
+      }
+      if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->q_bar[un & 1]), (un >> 1) & 1, abort, p.timeout_ns)) {
+        ok = false;
+        why = kWaitQ;
+        break;
+      }
+      const uint8_t* src = ring + ((i + (r >> 6)) % kSlots) * kSlot;
+      const int row = r & 63;
+      if constexpr (kF8) {
+        // chunks of 16 codes: 32 of c_kv in four 128-byte columns, 4 of k_pe
+        // in 64-byte rows; group gg takes pairs [9 gg, 9 gg + 9)
+#pragma unroll 3
+        for (int q = 9 * gg; q < 9 * gg + 9; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * q + h;
+            const uint8_t* a = c < 32 ? src + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4)
+                                      : src + 4 * 8192 + row * 64 + (((c - 32) ^ ((row >> 1) & 3)) << 4);
+            expand16(*reinterpret_cast<const uint4*>(a), w + 8 * h);
+          }
+          tmem_st16(tmem + lane_base + 16 * q, w);
+        }
+      } else {
+#pragma unroll 3
+        for (int q = 9 * gg; q < 9 * gg + 9; ++q) {  // four chunks of 8 values
+          uint32_t w[16];
+#pragma unroll
+          for (int h = 0; h < 4; ++h) {
+            const int c = 4 * q + h;
+            const uint4 v = *reinterpret_cast<const uint4*>(src + (c >> 3) * 8192 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
+            w[4 * h] = v.x; w[4 * h + 1] = v.y; w[4 * h + 2] = v.z; w[4 * h + 3] = v.w;
+          }
+          tmem_st16(tmem + lane_base + 16 * q, w);
+        }
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctrl->q_full));
+      i += 2 + ntiles;
+      const int t = u.t0 + r;
+      // the first row that sees the key: rows of the positions from t on
+      const int64_t first_pos = static_cast<int64_t>(t) - (u.L - p.Q);
+      const int64_t rmin = t < u.L ? (first_pos > 0 ? first_pos * p.H : 0) : p.R;
+      float sum4[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < ntiles; ++n, ++j) {
+        if ((j & 1u) != static_cast<uint32_t>(gg)) continue;
+        const int sb = static_cast<int>(j % 3);
+        if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (j / 3) & 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitS;
+          break;
+        }
+        tc_fence_after();
+        uint32_t v[4][16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld16(tmem + lane_base + C::kSCol0 + sb * 64 + q * 16, v[q]);
+        float4 l[16];
+        const float4* nl = reinterpret_cast<const float4*>(data + kNlOff + sb * 256);
+#pragma unroll
+        for (int q = 0; q < 16; ++q) l[q] = nl[q];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_wait_ld_tie(v[q]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->s_empty[sb]));
+        // columns [a, z) of the tile count: from the first row that sees the
+        // key to the request's last row
+        const int64_t a64 = rmin - 64 * n;
+        const int a = a64 > 0 ? (a64 < 64 ? static_cast<int>(a64) : 64) : 0;
+        const int z = p.R - 64 * n < 64 ? p.R - 64 * n : 64;
+        if (__all_sync(0xffffffffu, a == 0) && z == 64) {
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            sum4[0] += ex2_approx(fmaf(__uint_as_float(v[q >> 2][(4 * q) & 15]), c2, l[q].x));
+            sum4[1] += ex2_approx(fmaf(__uint_as_float(v[q >> 2][(4 * q + 1) & 15]), c2, l[q].y));
+            sum4[2] += ex2_approx(fmaf(__uint_as_float(v[q >> 2][(4 * q + 2) & 15]), c2, l[q].z));
+            sum4[3] += ex2_approx(fmaf(__uint_as_float(v[q >> 2][(4 * q + 3) & 15]), c2, l[q].w));
+          }
+        } else {
+          const float* lf = reinterpret_cast<const float*>(l);
+#pragma unroll
+          for (int c = 0; c < 64; ++c) {
+            const float e = ex2_approx(fmaf(__uint_as_float(v[c >> 4][c & 15]), c2, lf[c]));
+            sum4[c & 3] += (c >= a && c < z) ? e : 0.f;
+          }
+        }
+      }
+      if (!ok) break;
+      const float sum = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+      // the second group hands its sums over; it writes the next ones into
+      // this buffer two tiles later, whose keys need the first group's q_full
+      float* part = parts + (un & 1) * kKeys;
+      if (gg == 1) {
+        part[r] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->sums[un & 1]));
+      } else {
+        if (!mbar_wait_warp(smem_u32(&ctrl->sums[un & 1]), (un >> 1) & 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitSums;
+          break;
+        }
+        if (t < u.L) {
+          const int64_t at = static_cast<int64_t>(u.b) * p.cols + t;
+          const float base = p.mass_in && t < u.L - p.num_fresh ? p.mass_in[at] : 0.f;
+          p.mass_out[at] = base + (sum + part[r]);
+        }
+      }
+      ++un;
+    }
+    if (!ok && lane == 0) raise_timeout(p, ctrl, why, j);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 2) tmem_dealloc(tmem, 512);
+}
+
 }  // namespace mass
 }  // namespace mla
 
@@ -517,22 +883,22 @@ int check_mass_dims(const mla_dims* d) {
   return MLA_OK;
 }
 
-template <bool kF8>
-cudaError_t launch_mass(const Params& p, const CUtensorMap& s, const CUtensorMap& pe, const CUtensorMap& qn,
-                        const CUtensorMap& qp, int ctas, int device, cudaStream_t stream) {
-  cudaError_t e = allow_smem<kF8>(mla::mass::mla_mass_kernel<kF8>, Lay<kF8>::kSmem, device);
+template <int kTag, typename Kernel>
+cudaError_t launch_mass(Kernel* kernel, int smem, const Params& p, const CUtensorMap& s, const CUtensorMap& pe,
+                        const CUtensorMap& qn, const CUtensorMap& qp, int ctas, int device, cudaStream_t stream) {
+  cudaError_t e = allow_smem<kTag>(kernel, smem, device);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(mla::chunk::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Lay<kF8>::kSmem;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mla::mass::mla_mass_kernel<kF8>, p, s, pe, qn, qp);
+  return cudaLaunchKernelEx(&cfg, kernel, p, s, pe, qn, qp);
 }
 
 }  // namespace
@@ -570,19 +936,22 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
   if (!encode_fn()) return MLA_ERR_CUDA;
   const int64_t R = static_cast<int64_t>(d->num_heads) * d->q_len;
   const int64_t krows = static_cast<int64_t>(d->num_pages) * 64, qrows = d->batch * R;
+  // more than 128 rows per request: the keys stay and the rows stream (64 at
+  // a time); measured at 5 tokens x 128 heads and 32 x 128
+  const bool rows = R > mla::chunk::kRows;
   CUtensorMap s, pe, qn, qp;
   bool ok = true;
   if (f8) {
     using C = Cfg<true, 1>;
     ok = map3(&s, kv_cache, krows, 576, 1, C::kSBoxes, 64, C::kPartBoxes) &&
          map2(&pe, kv_cache, krows, 576, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B) &&
-         map3(&qn, q_nope, qrows, 1024, 2, 8, C::kQRows, 8) &&
-         map2(&qp, q_pe, qrows, 64, 2, 64, C::kQRows, CU_TENSOR_MAP_SWIZZLE_128B);
+         map3(&qn, q_nope, qrows, 1024, 2, 8, rows ? 64 : C::kQRows, 8) &&
+         map2(&qp, q_pe, qrows, 64, 2, 64, rows ? 64 : C::kQRows, CU_TENSOR_MAP_SWIZZLE_128B);
   } else {
     using C = Cfg<false, 1>;
     ok = map3(&s, kv_cache, krows, 1152, 2, C::kSBoxes, 64, C::kPartBoxes) &&
-         map3(&qn, q_nope, qrows, 1024, 2, 8, C::kQRows, 8) &&
-         map2(&qp, q_pe, qrows, 64, 2, 64, C::kQRows, CU_TENSOR_MAP_SWIZZLE_128B);
+         map3(&qn, q_nope, qrows, 1024, 2, 8, rows ? 64 : C::kQRows, 8) &&
+         map2(&qp, q_pe, qrows, 64, 2, 64, rows ? 64 : C::kQRows, CU_TENSOR_MAP_SWIZZLE_128B);
     pe = s;
   }
   if (!ok) return MLA_ERR_CUDA;
@@ -597,7 +966,6 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
   p.H = d->num_heads;
   p.Q = d->q_len;
   p.R = static_cast<int32_t>(R);
-  p.G = static_cast<int32_t>((R + mla::chunk::kRows - 1) / mla::chunk::kRows);
   p.num_pages = d->num_pages;
   p.max_pages = d->max_pages_per_req;
   p.pt_stride = d->page_table_stride;
@@ -610,9 +978,13 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   mla::mass::mla_mass_clear_kernel<<<1, 32, 0, stream>>>(p.status);
   cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess)
-    e = f8 ? launch_mass<true>(p, s, pe, qn, qp, sms, dev, stream)
-           : launch_mass<false>(p, s, pe, qn, qp, sms, dev, stream);
+  if (e == cudaSuccess) {
+    using namespace mla::mass;
+    e = rows ? (f8 ? launch_mass<3>(mla_mass_rows_kernel<true>, kRowsSmem, p, s, pe, qn, qp, sms, dev, stream)
+                   : launch_mass<2>(mla_mass_rows_kernel<false>, kRowsSmem, p, s, pe, qn, qp, sms, dev, stream))
+             : (f8 ? launch_mass<1>(mla_mass_kernel<true>, Lay<true>::kSmem, p, s, pe, qn, qp, sms, dev, stream)
+                   : launch_mass<0>(mla_mass_kernel<false>, Lay<false>::kSmem, p, s, pe, qn, qp, sms, dev, stream));
+  }
   if (e != cudaSuccess) {
     cudaGetLastError();
     return MLA_ERR_CUDA;

@@ -91,6 +91,7 @@ def check_mass(m, fresh, mass=None):
 @pytest.mark.parametrize("B,Q,H,total", [
     (1, 1, 1, [1]), (1, 1, 16, [700]), (3, 1, 64, [64, 65, 1000]), (2, 1, 128, [129, 63]), (2, 3, 20, [300, 3]),
     (2, 5, 128, [700, 5]), (1, 32, 16, [2500]), (40, 1, 8, [1 + 37 * k for k in range(40)]), (1, 2, 200, [1200]),
+    (3, 3, 64, [200, 3, 129]), (2, 64, 3, [64, 257]), (1, 129, 1, [130]),
 ])
 def test_mass_parity(B, Q, H, total, kv_dtype):
     c = K.make([Q] * B, total, H, kv_dtype=kv_dtype, seed=B + Q + H)
@@ -245,6 +246,8 @@ EVICT = [
     dict(total=[5000, 1025, 1024, 1023], budget=1000, sinks=16, recent=500),
     dict(total=[3000], budget=2999, sinks=2, recent=7),
     dict(total=[300 + k for k in range(50)], budget=280, sinks=4, recent=30),
+    dict(total=[9000, 8191], budget=4000, sinks=4, recent=300),           # eight blocks a request
+    dict(total=[2100, 4100, 50, 3000, 1] * 8, budget=2000, sinks=1, recent=9),  # two
 ]
 
 
