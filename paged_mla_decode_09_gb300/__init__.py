@@ -503,27 +503,46 @@ def mla_decode_cascade_query_status(q_nope, kv_cache, page_table, prefix_pages: 
 # on every call; a small step is bound by it); the functions below it name
 # what is wrong when that test fails.
 
+class _Torch:
+    """What the tests below need of torch, looked up once (importing torch, or
+    its attributes, on every call costs microseconds)."""
+
+    torch = None
+
+    @classmethod
+    def load(cls):
+        import torch
+
+        cls.bf16, cls.f32, cls.i32 = torch.bfloat16, torch.float32, torch.int32
+        cls.cache_codes = {torch.bfloat16: MLA_KV_BF16, torch.uint8: MLA_KV_FP8_E4M3,
+                           torch.float8_e4m3fn: MLA_KV_FP8_E4M3}
+        cls.device, cls.raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        cls.torch = torch
+        return cls
+
+
+def _t():
+    return _Torch if _Torch.torch is not None else _Torch.load()
+
+
 def _fits(t, shape, dtype, dev) -> bool:
     return t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous()
 
 
-def _cache_fits(kv_cache, page_table, seq_lens, B, dev) -> bool:
-    import torch
-
-    return (kv_cache.dim() == 3 and kv_cache.shape[2] == 576 and kv_cache.get_device() == dev
-            and kv_cache.dtype in (torch.bfloat16, torch.uint8, torch.float8_e4m3fn) and kv_cache.is_contiguous()
-            and _fits(seq_lens, (B,), torch.int32, dev) and page_table.dtype is torch.int32
-            and page_table.dim() == 2 and page_table.shape[0] == B and page_table.get_device() == dev
-            and page_table.stride(1) == 1 and page_table.stride(0) >= page_table.shape[1])
+def _cache_fits(kv_cache, page_table, seq_lens, B, dev, T) -> bool:
+    c, p = kv_cache.shape, page_table.shape
+    return (len(c) == 3 and c[2] == 576 and kv_cache.get_device() == dev and kv_cache.dtype in T.cache_codes
+            and kv_cache.is_contiguous() and _fits(seq_lens, (B,), T.i32, dev) and page_table.dtype is T.i32
+            and len(p) == 2 and p[0] == B and page_table.get_device() == dev and page_table.stride(1) == 1
+            and page_table.stride(0) >= p[1])
 
 
-def _check_current_device(t):
+def _check_current_device(dev):
     """The library runs on the current device; a tensor elsewhere would be
     read through a pointer of another device."""
-    import torch
-
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device {torch.cuda.current_device()}, got {t.device}")
+    now = _t().device()
+    if dev != now:
+        raise ValueError(f"tensors must be on the current CUDA device {now}, got cuda:{dev}")
 
 
 def _int32_arg(name, v, low=0):
@@ -533,16 +552,22 @@ def _int32_arg(name, v, low=0):
     return v
 
 
-def _stream_int(stream):
-    import torch
-
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _stream_int(stream, dev):
+    return _t().raw_stream(dev) if stream is None else stream.cuda_stream
 
 
 def make_prefill_dims(q_nope, kv_cache, page_table, seq_lens) -> MlaPrefillDims:
     T, H, _ = q_nope.shape
-    return MlaPrefillDims(seq_lens.shape[0], H, T, kv_cache.shape[1], kv_cache.shape[0], page_table.shape[1],
-                          page_table.stride(0), kv_dtype_code(kv_cache))
+    c = kv_cache.shape
+    return MlaPrefillDims(seq_lens.shape[0], H, T, c[1], c[0], page_table.shape[1], page_table.stride(0),
+                          kv_dtype_code(kv_cache))
+
+
+def _decode_dims(s, kv_cache, page_table, T) -> MlaDims:
+    """make_dims for tensors that passed their tests (s: q_nope's shape)."""
+    c = kv_cache.shape
+    return MlaDims(s[0], s[2], s[1], c[1], c[0], page_table.shape[1], page_table.stride(0),
+                   T.cache_codes[kv_cache.dtype])
 
 
 def mla_prefill_workspace_size(dims: MlaPrefillDims, device: int | None = None) -> int:
@@ -576,15 +601,14 @@ def _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_le
 
 
 def _prefill_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace) -> bool:
-    import torch
-
-    bf16, s, dev = torch.bfloat16, q_nope.shape, q_nope.get_device()
+    t = _t()
+    s, dev = q_nope.shape, q_nope.get_device()
     if dev < 0 or len(s) != 3 or s[2] != 512 or seq_lens.dim() != 1:
         return False
     T, H, B = s[0], s[1], seq_lens.shape[0]
-    return (_fits(q_nope, s, bf16, dev) and _fits(q_pe, (T, H, 64), bf16, dev) and _fits(out, s, bf16, dev)
-            and _fits(lse, (T, H), torch.float32, dev) and _fits(cu_q_lens, (B + 1,), torch.int32, dev)
-            and _cache_fits(kv_cache, page_table, seq_lens, B, dev) and workspace.get_device() == dev
+    return (_fits(q_nope, s, t.bf16, dev) and _fits(q_pe, (T, H, 64), t.bf16, dev) and _fits(out, s, t.bf16, dev)
+            and _fits(lse, (T, H), t.f32, dev) and _fits(cu_q_lens, (B + 1,), t.i32, dev)
+            and _cache_fits(kv_cache, page_table, seq_lens, B, dev, t) and workspace.get_device() == dev
             and workspace.is_contiguous())
 
 
@@ -597,12 +621,14 @@ def mla_prefill(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, window,
         _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
         _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
         raise ValueError("prefill tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(q_nope)
+    dev = q_nope.get_device()
+    _check_current_device(dev)
     dims = make_prefill_dims(q_nope, kv_cache, page_table, seq_lens)
     rc = load_library().mla_prefill(
         ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
         seq_lens.data_ptr(), cu_q_lens.data_ptr(), _int32_arg("window", window), _int32_arg("num_sinks", num_sinks),
-        scale, kv_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream))
+        scale, kv_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_prefill")
 
@@ -621,15 +647,20 @@ def mla_decode_window(q_nope, q_pe, kv_cache, page_table, seq_lens, window, num_
                       workspace, stream=None) -> None:
     """Enqueue a decode over a sliding window of `window` tokens and num_sinks
     first tokens (see include/mla_prefill.h); tensors as for mla_decode."""
-    if q_nope.get_device() < 0:
+    t = _t()
+    s, dev = q_nope.shape, q_nope.get_device()
+    if not (dev >= 0 and len(s) == 4 and s[3] == 512 and _fits(q_nope, s, t.bf16, dev)
+            and _fits(q_pe, (s[0], s[1], s[2], 64), t.bf16, dev) and _fits(out, s, t.bf16, dev)
+            and _fits(lse, s[:3], t.f32, dev) and _cache_fits(kv_cache, page_table, seq_lens, s[0], dev, t)
+            and workspace.get_device() == dev and workspace.is_contiguous()):
         _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
-    _check_decode_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
-    _check_current_device(q_nope)
-    dims = make_dims(q_nope, kv_cache, page_table)
+        _check_decode_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, out, lse, workspace)
+    _check_current_device(dev)
+    dims = _decode_dims(s, kv_cache, page_table, t)
     rc = load_library().mla_decode_window(
         ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
         seq_lens.data_ptr(), _int32_arg("window", window, 1), _int32_arg("num_sinks", num_sinks), scale, kv_scale,
-        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream))
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_window")
 
@@ -669,15 +700,14 @@ def _check_mass_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass,
 
 
 def _mass_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace) -> bool:
-    import torch
-
-    bf16, f32, s, dev = torch.bfloat16, torch.float32, q_nope.shape, q_nope.get_device()
-    if dev < 0 or len(s) != 4 or s[3] != 512 or mass_out.dim() != 2 or mass_out.shape[0] != s[0]:
+    t = _t()
+    s, o, dev = q_nope.shape, mass_out.shape, q_nope.get_device()
+    if dev < 0 or len(s) != 4 or s[3] != 512 or len(o) != 2 or o[0] != s[0]:
         return False
-    B, Q, H, _ = s
-    return (_fits(q_nope, s, bf16, dev) and _fits(q_pe, (B, Q, H, 64), bf16, dev) and _fits(lse, (B, Q, H), f32, dev)
-            and _fits(mass_out, mass_out.shape, f32, dev) and (mass is None or _fits(mass, mass_out.shape, f32, dev))
-            and _cache_fits(kv_cache, page_table, seq_lens, B, dev) and workspace.get_device() == dev
+    return (_fits(q_nope, s, t.bf16, dev) and _fits(q_pe, (s[0], s[1], s[2], 64), t.bf16, dev)
+            and _fits(lse, s[:3], t.f32, dev) and _fits(mass_out, o, t.f32, dev)
+            and (mass is None or _fits(mass, o, t.f32, dev))
+            and _cache_fits(kv_cache, page_table, seq_lens, s[0], dev, t) and workspace.get_device() == dev
             and workspace.is_contiguous())
 
 
@@ -692,13 +722,14 @@ def mla_attn_mass(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, num_fresh, 
             _check_cuda(mass)
         _check_mass_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, mass, mass_out, workspace)
         raise ValueError("mass tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(q_nope)
-    dims = make_dims(q_nope, kv_cache, page_table)
+    dev = q_nope.get_device()
+    _check_current_device(dev)
+    dims = _decode_dims(q_nope.shape, kv_cache, page_table, _t())
     rc = load_library().mla_attn_mass(
         ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
         seq_lens.data_ptr(), lse.data_ptr(), _int32_arg("num_fresh", num_fresh), scale, kv_scale,
         None if mass is None else mass.data_ptr(), mass_out.data_ptr(), mass_out.shape[1], workspace.data_ptr(),
-        workspace.nbytes, _stream_int(stream))
+        workspace.nbytes, _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_attn_mass")
 
@@ -739,16 +770,15 @@ def _check_evict_tensors(mass, positions, seq_lens, page_table, kv_cache, budget
 
 def _evict_fits(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out, positions_out,
                 workspace) -> bool:
-    import torch
-
-    f32, i32, s, dev = torch.float32, torch.int32, mass.shape, mass.get_device()
+    t = _t()
+    s, dev = mass.shape, mass.get_device()
     if dev < 0 or len(s) != 2:
         return False
     if positions is not None:
-        if positions_out is None or not (_fits(positions, s, i32, dev) and _fits(positions_out, s, i32, dev)):
+        if positions_out is None or not (_fits(positions, s, t.i32, dev) and _fits(positions_out, s, t.i32, dev)):
             return False
-    return (_fits(mass, s, f32, dev) and _fits(mass_out, s, f32, dev) and _fits(new_lens, s[:1], i32, dev)
-            and _fits(kept, (s[0], budget), i32, dev) and _cache_fits(kv_cache, page_table, seq_lens, s[0], dev)
+    return (_fits(mass, s, t.f32, dev) and _fits(mass_out, s, t.f32, dev) and _fits(new_lens, s[:1], t.i32, dev)
+            and _fits(kept, (s[0], budget), t.i32, dev) and _cache_fits(kv_cache, page_table, seq_lens, s[0], dev, t)
             and kv_cache.shape[1] == 64 and workspace.get_device() == dev and workspace.is_contiguous())
 
 
@@ -765,16 +795,17 @@ def mla_evict(mass, positions, seq_lens, page_table, kv_cache, budget, num_sinks
         _check_evict_tensors(mass, positions, seq_lens, page_table, kv_cache, budget, new_lens, kept, mass_out,
                              positions_out, workspace)
         raise ValueError("eviction tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(mass)
+    dev = mass.get_device()
+    _check_current_device(dev)
     dims = MlaEvictDims(mass.shape[0], mass.shape[1], kv_cache.shape[0], page_table.shape[1], page_table.stride(0),
-                        kv_dtype_code(kv_cache), budget, _int32_arg("num_sinks", num_sinks),
+                        _t().cache_codes[kv_cache.dtype], budget, _int32_arg("num_sinks", num_sinks),
                         _int32_arg("num_recent", num_recent))
     pos = None if positions is None else positions.data_ptr()
     pos_out = None if positions is None else positions_out.data_ptr()
     rc = load_library().mla_evict(
         ctypes.byref(dims), mass.data_ptr(), pos, seq_lens.data_ptr(), page_table.data_ptr(), kv_cache.data_ptr(),
         new_lens.data_ptr(), kept.data_ptr(), mass_out.data_ptr(), pos_out, workspace.data_ptr(), workspace.nbytes,
-        _stream_int(stream))
+        _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_evict")
 
