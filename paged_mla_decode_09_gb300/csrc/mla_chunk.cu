@@ -45,9 +45,9 @@ struct Shape {
 // against 91.
 int Shape::cg() const { return T * H > 128 * B ? 2 : 1; }
 
-// [status | blkoff | blocks | prefix | cinfo | partial outputs | partial lse]
+// [status | blkoff | blocks | prefix | cinfo | cut blocks | partial outputs | partial lse]
 struct Layout {
-  size_t status, blkoff, blk, prefix, cinfo, o_part, lse_part, total;
+  size_t status, blkoff, blk, prefix, cinfo, cuts, o_part, lse_part, total;
 };
 
 Layout layout_of(const Shape& s, int C) {
@@ -58,7 +58,8 @@ Layout layout_of(const Shape& s, int C) {
   l.blk = l.blkoff + align256(static_cast<size_t>(s.B + 1) * 4);
   l.prefix = l.blk + align256(nb * sizeof(Block));
   l.cinfo = l.prefix + align256((nb + 1) * 4);
-  l.o_part = l.cinfo + align256(static_cast<size_t>(C) * 16);
+  l.cuts = l.cinfo + align256(static_cast<size_t>(C) * 16);
+  l.o_part = l.cuts + align256(static_cast<size_t>(C + 1) * 32);
   l.lse_part = l.o_part + align256(2 * static_cast<size_t>(C) * rows * mla::chunk::kDL * 4);
   l.total = l.lse_part + align256(2 * static_cast<size_t>(C) * rows * 4);
   return l;
@@ -222,6 +223,7 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   p.blk = reinterpret_cast<Block*>(ws + lay.blk);
   p.prefix = reinterpret_cast<int32_t*>(ws + lay.prefix);
   p.cinfo = reinterpret_cast<int32_t*>(ws + lay.cinfo);
+  p.cuts = reinterpret_cast<int32_t*>(ws + lay.cuts);
   p.B = static_cast<int32_t>(s.B);
   p.H = static_cast<int32_t>(s.H);
   p.q_len = s.q_len;
@@ -240,13 +242,21 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   p.timeout_ns = kTimeoutNs;
 
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-  mla::chunk::mla_chunk_schedule_kernel<<<1, mla::chunk::kSchedThreads, 0, stream>>>(p);
+  mla::chunk::mla_chunk_schedule_kernel<<<1, s.B <= 256 && p.NB <= 256 && C <= 256 ? 256 : mla::chunk::kSchedThreads, 0,
+                                         stream>>>(p);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   cudaError_t e = s.f8 ? (cg == 2 ? launch_attention<true, 2>(p, m, stream) : launch_attention<true, 1>(p, m, stream))
                        : (cg == 2 ? launch_attention<false, 2>(p, m, stream) : launch_attention<false, 1>(p, m, stream));
   if (e == cudaSuccess) {
+    // a column per block that may be cut, at most one per slice boundary; a
+    // warp per row, or four where that still fits the SMs about once
+    const int64_t cuts = s.blocks() < C ? s.blocks() : C;
+    const int64_t rows = s.T * s.H < p.BR ? s.T * s.H : p.BR;
+    const bool four = cuts * rows * 4 <= 152 * 32;
+    const int64_t items = rows * (four ? 4 : 1);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C, p.BR / mla::chunk::kCombineWarps, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(cuts),
+                       static_cast<unsigned>((items + mla::chunk::kCombineWarps - 1) / mla::chunk::kCombineWarps), 1);
     cfg.blockDim = dim3(mla::chunk::kCombineWarps * 32, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -254,7 +264,8 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mla::chunk::mla_chunk_combine_kernel, p);
+    e = four ? cudaLaunchKernelEx(&cfg, mla::chunk::mla_chunk_combine_kernel<4>, p)
+             : cudaLaunchKernelEx(&cfg, mla::chunk::mla_chunk_combine_kernel<1>, p);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

@@ -119,6 +119,8 @@ struct Params {
   Block* blk;               // [NB]
   int32_t* prefix;          // [NB + 1] page prefix sums over blocks
   int32_t* cinfo;           // [C][4] slice start, end, first block, last block
+  int32_t* cuts;            // [8] count, then [min(NB, C)][8] per block cut into pieces (any order): block, first
+                            // cluster, last cluster, partial slot of the first piece, first row, rows
   int32_t B, H, q_len, T, NB, C, BR;  // BR = rows per block
   int32_t num_pages, max_pages, pt_stride;
   int32_t window, sinks;    // window 0: everything up to the row's own position
@@ -132,7 +134,7 @@ struct Params {
 // counts, and each cluster's slice of all pages.  Slices are cut in a
 // weighted order (a piece of a block costs unit_cost pages to start), so that
 // clusters with many short blocks get fewer pages.
-constexpr int kSchedThreads = 1024;
+constexpr int kSchedThreads = 1024;  // or 256 for small batches (fewer warps at each barrier)
 constexpr int kSchedSmemNB = 8192;  // prefix sums kept in shared memory for the searches
 
 __device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  // inclusive, all threads
@@ -144,7 +146,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  //
   if ((tid & 31) == 31) warp_tot[tid >> 5] = v;
   __syncthreads();
   if (tid < 32) {
-    int w = warp_tot[tid];
+    int w = tid < static_cast<int>(blockDim.x >> 5) ? warp_tot[tid] : 0;
     for (int o = 1; o < 32; o <<= 1) {
       const int t = __shfl_up_sync(0xffffffffu, w, o);
       if (tid >= o) w += t;
@@ -158,14 +160,16 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  //
 __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const __grid_constant__ Params p) {
   __shared__ int warp_tot[32];
   __shared__ int carry_s;
+  __shared__ int ncuts;
+  __shared__ int cb[kMaxClusters + 1];  // where the slices begin
   __shared__ int32_t sp[kSchedSmemNB + 1];
   griddep_launch_dependents();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, nt = static_cast<int>(blockDim.x);
   if (tid < 4) p.status[tid] = 0;
-  if (tid == 0) carry_s = 0;
+  if (tid == 0) carry_s = ncuts = 0;
   __syncthreads();
   // row blocks per request
-  for (int base = 0; base < p.B; base += kSchedThreads) {
+  for (int base = 0; base < p.B; base += nt) {
     const int b = base + tid;
     int nblk = 0;
     if (b < p.B) {
@@ -188,7 +192,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
     const int incl = block_scan(nblk, warp_tot, carry_s);
     if (b < p.B) p.blkoff[b + 1] = incl < p.NB ? incl : p.NB;  // never beyond the arrays
     __syncthreads();
-    if (tid == kSchedThreads - 1) carry_s = incl;
+    if (tid == nt - 1) carry_s = incl;
     __syncthreads();
   }
   if (tid == 0) {
@@ -200,7 +204,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
   const int nblocks = p.blkoff[p.B];
   const bool sp_ok = p.NB <= kSchedSmemNB;
   // each block's rows and pages
-  for (int base = 0; base < p.NB; base += kSchedThreads) {
+  for (int base = 0; base < p.NB; base += nt) {
     const int n = base + tid;
     int np = 0;
     if (n < nblocks) {
@@ -246,7 +250,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
       if (sp_ok) sp[n + 1] = incl;
     }
     __syncthreads();
-    if (tid == kSchedThreads - 1) carry_s = incl;
+    if (tid == nt - 1) carry_s = incl;
     __syncthreads();
   }
   if (tid == 0) {
@@ -256,8 +260,9 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
   __syncthreads();
   const int32_t* pre = sp_ok ? sp : p.prefix;
   if (nblocks == 0) {
-    for (int c = tid; c < p.C; c += kSchedThreads)
+    for (int c = tid; c < p.C; c += nt)
       for (int k = 0; k < 4; ++k) p.cinfo[4 * c + k] = 0;
+    if (tid == 0) p.cuts[0] = 0;
     return;
   }
   // slices: weighted position of block n's first page is pre[n] + unit_cost * (n + 1)
@@ -281,14 +286,28 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
     }
     return lo;
   };
-  for (int c = tid; c < p.C; c += kSchedThreads) {
-    const int s = c == 0 ? 0 : page_at(W * c / p.C);
-    const int e = c == p.C - 1 ? pre[nblocks] : page_at(W * (c + 1) / p.C);
-    p.cinfo[4 * c + 0] = s;
-    p.cinfo[4 * c + 1] = e;
-    p.cinfo[4 * c + 2] = s < e ? block_of(s) : 0;
-    p.cinfo[4 * c + 3] = s < e ? block_of(e - 1) : 0;
+  for (int c = tid; c <= p.C; c += nt) cb[c] = c == 0 ? 0 : (c == p.C ? pre[nblocks] : page_at(W * c / p.C));
+  __syncthreads();
+  for (int c = tid; c < p.C; c += nt) {
+    const int s = cb[c], e = cb[c + 1];
+    const int first = s < e ? block_of(s) : 0, last = s < e ? block_of(e - 1) : 0;
+    *reinterpret_cast<int4*>(p.cinfo + 4 * c) = make_int4(s, e, first, last);
+    // the block that starts in this slice (or exactly with it) and goes on
+    // behind it, if there is one: an entry of the combine's list
+    if (s < e && pre[last + 1] > e && pre[last] >= s) {
+      int lo = c, hi = p.C - 1;  // last cluster whose slice begins before the block's end
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cb[mid] < pre[last + 1]) lo = mid; else hi = mid - 1;
+      }
+      const Block k = p.blk[last];
+      int4* dst = reinterpret_cast<int4*>(p.cuts + 8 * (1 + atomicAdd(&ncuts, 1)));
+      dst[0] = make_int4(last, c, lo, 2 * c + (first != last ? 1 : 0));
+      dst[1] = make_int4(k.row0, k.nrows, 0, 0);
+    }
   }
+  __syncthreads();
+  if (tid == 0) p.cuts[0] = ncuts;
 }
 
 // One block's piece inside a cluster's slice.
@@ -385,16 +404,24 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
     return true;
   };
   uint32_t qloaded = 0;
+  // the next unit's query rows are pulled into L2 a few pages ahead
+  UnitIter ahead;
+  ahead.init(p, cid);
+  Unit nx;
+  bool have_next = ahead.next(nx);
   while (ok && it.next(u)) {
     const uint32_t qbar = smem_u32(&ctrl->q_bar[un & 1]);
     const int row0 = u.k.row0 + pr * kRows;
-    for (int e = 0; e < C::kQEntries; ++e) {
+    const int qe = C::q_entries(u.k.nrows);
+    have_next = have_next && ahead.next(nx);
+    const int pf = u.p1 - 4 * kCg > u.p0 ? u.p0 + (u.p1 - 4 * kCg - u.p0) / kCg * kCg : u.p0;
+    for (int e = 0; e < qe; ++e) {
       if (!acquire()) {
         ok = false;
         break;
       }
       if (e == 0) {
-        mbar_expect_tx(qbar, static_cast<uint32_t>(kRows * 1152));
+        mbar_expect_tx(qbar, static_cast<uint32_t>(C::kParts == 3 ? kRows * 1152 : qe * C::kQRows * 1152));
         qloaded = un + 1;
         if constexpr (C::kParts == 3)
           tma_load_2d(smem_u32(ring + C::kQPeOff + (un & 1) * C::kQPeTile), tm_qp, 0, row0, qbar);
@@ -420,6 +447,14 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
     }
     ++un;
     for (int vt = u.p0; vt < u.p1 && ok; vt += kCg) {
+      if (have_next && vt == pf) {
+        const int64_t r0 = static_cast<int64_t>(nx.k.row0) + pr * kRows;
+        const int left = nx.k.nrows - pr * kRows, n = left < kRows ? left : kRows;
+        if (n > 0) {
+          prefetch_l2_bulk(p.q_nope + r0 * kDL * 2, static_cast<uint32_t>(n) * kDL * 2);
+          prefetch_l2_bulk(p.q_pe + r0 * kDR * 2, static_cast<uint32_t>(n) * kDR * 2);
+        }
+      }
       const int v = vt + pr;
       const bool have = kCg == 1 || v < u.p1;
       const int y = have ? read_page_id(p, u.k.b, real_page(u.k, v)) * kPage : 0;
@@ -479,6 +514,15 @@ __device__ void produce_o(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
   drain_ring<C::kNStO>(ctrl, i, p.timeout_ns);
 }
 
+// Two e4m3 codes, in the low bytes of the halves, as f16 values times 2^-8:
+// moving exponent and mantissa to f16's place (exponent bias 15 instead of 7)
+// scales every finite code by exactly 2^-8, subnormals included; the outputs'
+// scale puts it back.  (b & 127) << 7 | (b & 128) << 8 = (b + (b & 128)) * 128,
+// half of it on the multiply pipe; the conversion instruction took twice as
+// long.  A NaN code becomes 1.875: its key's scores, from the codes as they
+// are, are NaN already.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) { return b * 128u + (b & 0x00800080u) * 128u; }
+
 // Writes TMEM columns [c0, c1) of one row: bf16 out and lse for a whole
 // block, fp32 partials (normalised O and its lse) for a piece.  Column c of
 // O is latent dimension c, or with kCg = 2 (each PV MMA's N = 256 is half
@@ -492,7 +536,7 @@ __device__ __forceinline__ void store_row(const Params& p, const Unit& u, int br
   }
   const bool real = br < u.k.nrows;
   const float inv_l = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays NaN
-  const float f = kF8 ? p.kv_scale * inv_l : inv_l;
+  const float f = kF8 ? p.kv_scale * 256.f * inv_l : inv_l;  // e4m3 values are in f16 as value / 256
   const float lse_v = l > 0.f ? (m_log2 + __log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
   const int64_t orow = static_cast<int64_t>(u.k.row0) + br;
   const int64_t prow = static_cast<int64_t>(u.slot) * p.BR + br;
@@ -644,7 +688,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return true;
       };
       while (ok && it.next(u)) {
-        for (int e = 0; e < C::kQEntries && ok; ++e, ++i) ok = landed(0u, 0u);
+        const int qe = C::q_entries(u.k.nrows);
+        for (int e = 0; e < qe && ok; ++e, ++i) ok = landed(0u, 0u);
         if (!ok) break;
         if (leader) {
           if (!mbar_wait_warp(smem_u32(&ctrl->q_full), un & 1, abort, p.timeout_ns)) {
@@ -653,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           if (lane == 0)  // the query entries' slots go back to the producers
-            for (int e = C::kQEntries; e > 0; --e) {
+            for (int e = qe; e > 0; --e) {
               const uint32_t bar = smem_u32(&ctrl->kv_empty[(i - e) % C::kNStS]);
               mbar_arrive(bar);
               if (kCg == 2) mbar_arrive_remote(mapa(bar, 1));
@@ -767,7 +812,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         float qs = 1.f;
-        if constexpr (kF8) {
+        const int qe = C::q_entries(u.k.nrows);
+        // (rows past the block's entries keep what TMEM holds: their results go nowhere)
+        const bool loads = (warp & 3) * 32 < qe / C::kParts * C::kQRows;  // one answer per warp
+        if (!loads) {
+        } else if constexpr (kF8) {
           uint8_t* pe_tile = data + C::kQPeOff;
           qs = q_row_e4m3<kCg>(ring, i, r, tmem + lane_base, pe_tile, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9);
         } else {
@@ -780,7 +829,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kCg == 2) mbar_arrive_remote(mapa(smem_u32(&ctrl->q_full), 0));
           else mbar_arrive(smem_u32(&ctrl->q_full));
         }
-        i += C::kQEntries + C::kParts * static_cast<uint32_t>((u.p1 - u.p0 + kCg - 1) / kCg);
+        i += qe + C::kParts * static_cast<uint32_t>((u.p1 - u.p0 + kCg - 1) / kCg);
         const float c2 = p.scale * kLog2e * (kF8 ? qs * p.kv_scale : 1.f);
         const bool real = br < u.k.nrows;
         // padding rows follow the block's last row (their results go nowhere)
@@ -1045,11 +1094,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* dst = vring + vs * C::kSlotV;
             const int valid = u.k.len - real_page(u.k, vp) * kPage;
 #pragma unroll 1
-            for (int t = 0; t < C::kRawBoxes * 4; t += 4) {
-              // warp w: item w + 4 t = (rows 8 ro .., half box hb); four loads in flight
-              uint4 v[4];
+            for (int t = 0; t < C::kRawBoxes * 4; t += 8) {
+              // warp w: item w + 4 t = (rows 8 ro .., half box hb); eight loads in flight
+              uint4 v[8];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 8; ++q) {
                 const int item = w + 4 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
                 const int chunk = (hb & 1) * 4 + c4;  // of the raw box's row
                 v[q] = make_uint4(0, 0, 0, 0);  // slots past the sequence's end may hold anything
@@ -1058,18 +1107,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                          ((chunk ^ (row & 7)) << 4));
               }
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 8; ++q) {
                 const int item = w + 4 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
                 const uint32_t in[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
                 uint32_t o[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                  for (int h2 = 0; h2 < 2; ++h2) {
-                    const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(
-                        static_cast<__nv_fp8x2_storage_t>(in[k] >> (16 * h2)), __NV_E4M3);
-                    o[2 * k + h2] = static_cast<uint32_t>(hr.x) | (static_cast<uint32_t>(hr.y) << 16);
-                  }
+                for (int k = 0; k < 4; ++k) {
+                  o[2 * k] = e4m3x2_to_f16x2(__byte_perm(in[k], 0u, 0x4140));
+                  o[2 * k + 1] = e4m3x2_to_f16x2(__byte_perm(in[k], 0u, 0x4342));
+                }
                 uint8_t* d = dst + hb * C::kVBox + row * 128;  // half a raw box = one box of 64 values
                 *reinterpret_cast<uint4*>(d + (((2 * c4) ^ (row & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
                 *reinterpret_cast<uint4*>(d + (((2 * c4 + 1) ^ (row & 7)) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
@@ -1180,40 +1226,50 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ----------------------------------------------------------------- combine
-// Merges the partials of every block that slice boundaries cut: column c
-// takes the block that starts in cluster c's slice (or exactly at its start)
-// and goes on behind it, if there is one.  A warp per row; lane l holds the
-// log-sum-exps of the pieces of clusters c + l, c + l + 32, c + l + 64, then
-// the warp walks the pieces in order, so that results never depend on timing.
+// Merges the partials of every block that slice boundaries cut (the schedule's
+// list).  kParts warps share a row, each 512 / kParts of its columns: a call
+// with few cut blocks gets more warps, each with more partial rows in flight.
+// Lane l holds the log-sum-exps of the pieces of clusters c + l, c + l + 32,
+// c + l + 64, then the warp walks the pieces in order, so that results never
+// depend on timing.  The list is the schedule's, complete before the attention
+// kernel began, so it is read before waiting for the latter.
 constexpr int kCombineWarps = 4;
 
+template <int kParts>
 __global__ void __launch_bounds__(kCombineWarps * 32) mla_chunk_combine_kernel(const __grid_constant__ Params p) {
-  const int c = blockIdx.x;
-  griddep_wait();
-  const int s = p.cinfo[4 * c], e = p.cinfo[4 * c + 1];
-  if (s >= e) return;
-  const int n = p.cinfo[4 * c + 3];
-  const int pb0 = p.prefix[n], pb1 = p.prefix[n + 1];
-  if (pb1 <= e || pb0 < s) return;  // ends here, or started in an earlier slice
+  constexpr int kV = 4 / kParts;      // float4s of a row per lane
+  constexpr int kFly = 2 * kParts;    // partial rows in flight
+  const bool block0 = blockIdx.x == 0 && blockIdx.y == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Block k = p.blk[n];
-  const int br = blockIdx.y * kCombineWarps + warp;
-  if (br >= k.nrows) return;
+  const int item = blockIdx.y * kCombineWarps + warp, br = item / kParts, col = (item % kParts) * 32 * kV + lane;
+  // an earlier call's list may sit in this SM's L1: read through L2
+  const bool any = static_cast<int>(blockIdx.x) < __ldcg(p.cuts);
+  int4 a = make_int4(0, 0, 0, 0), b = a;
+  if (any) {
+    const int4* src = reinterpret_cast<const int4*>(p.cuts + 8 * (1 + static_cast<int>(blockIdx.x)));
+    a = __ldcg(src);
+    b = __ldcg(src + 1);
+  }
+  if (!any || br >= b.y) {
+    if (block0) griddep_wait();  // so that this grid completes after every earlier kernel of the call
+    return;
+  }
   int slot[3];
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    const int cc = a.y + 32 * q + lane;
+    slot[q] = -1;
+    if (cc <= a.z) {
+      const int4 ci = __ldcg(reinterpret_cast<const int4*>(p.cinfo + 4 * cc));
+      if (ci.x < ci.y) slot[q] = cc == a.y ? a.w : 2 * cc;  // an empty slice holds no piece
+    }
+  }
+  griddep_wait();
   float ls[3];
   float mx = -INFINITY;
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    const int cc = c + 32 * q + lane;
-    slot[q] = -1;
-    ls[q] = -INFINITY;
-    if (cc < p.C) {
-      const int cs = p.cinfo[4 * cc], ce = p.cinfo[4 * cc + 1];
-      if (cs < ce && cs < pb1) {
-        slot[q] = 2 * cc + (p.cinfo[4 * cc + 2] != n ? 1 : 0);
-        ls[q] = p.lse_part[static_cast<int64_t>(slot[q]) * p.BR + br];
-      }
-    }
+    ls[q] = slot[q] >= 0 ? p.lse_part[static_cast<int64_t>(slot[q]) * p.BR + br] : -INFINITY;
     mx = ls[q] > mx || ls[q] != ls[q] ? ls[q] : mx;  // a NaN stays
   }
 #pragma unroll
@@ -1231,34 +1287,47 @@ __global__ void __launch_bounds__(kCombineWarps * 32) mla_chunk_combine_kernel(c
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
   const float inv = z == 0.f ? 0.f : 1.f / z;
-  float4 acc[4];
+  float4 acc[kV];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int q = 0; q < kV; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
-    const unsigned have = __ballot_sync(0xffffffffu, slot[q] >= 0);
-    for (unsigned m = have; m; m &= m - 1) {
-      const int src = __ffs(m) - 1;
-      const float wf = __shfl_sync(0xffffffffu, w[q], src) * inv;
-      const int sl = __shfl_sync(0xffffffffu, slot[q], src);
-      if (wf == 0.f) continue;
-      const float4* o = reinterpret_cast<const float4*>(p.o_part + (static_cast<int64_t>(sl) * p.BR + br) * kDL);
+    unsigned have = __ballot_sync(0xffffffffu, slot[q] >= 0);
+    while (have) {
+      float wf[kFly];
+      float4 v[kFly][kV];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float4 x = o[lane + 32 * g];
-        acc[g].x += wf * x.x; acc[g].y += wf * x.y; acc[g].z += wf * x.z; acc[g].w += wf * x.w;
+      for (int f = 0; f < kFly; ++f) {
+        wf[f] = 0.f;
+        if (have == 0) continue;
+        const int src = __ffs(have) - 1;
+        have &= have - 1;
+        wf[f] = __shfl_sync(0xffffffffu, w[q], src) * inv;
+        const int sl = __shfl_sync(0xffffffffu, slot[q], src);
+        const float4* o = reinterpret_cast<const float4*>(p.o_part + (static_cast<int64_t>(sl) * p.BR + br) * kDL);
+#pragma unroll
+        for (int g = 0; g < kV; ++g) v[f][g] = o[col + 32 * g];
+      }
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) {
+        if (wf[f] == 0.f) continue;
+#pragma unroll
+        for (int g = 0; g < kV; ++g) {
+          acc[g].x += wf[f] * v[f][g].x; acc[g].y += wf[f] * v[f][g].y;
+          acc[g].z += wf[f] * v[f][g].z; acc[g].w += wf[f] * v[f][g].w;
+        }
       }
     }
   }
-  const int64_t orow = static_cast<int64_t>(k.row0) + br;
+  const int64_t orow = static_cast<int64_t>(b.x) + br;
   uint2* dst = reinterpret_cast<uint2*>(p.out + orow * kDL * 2);
 #pragma unroll
-  for (int g = 0; g < 4; ++g) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(acc[g].x, acc[g].y);
-    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[g].z, acc[g].w);
-    dst[lane + 32 * g] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  for (int g = 0; g < kV; ++g) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[g].x, acc[g].y);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[g].z, acc[g].w);
+    dst[col + 32 * g] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
-  if (lane == 0) p.lse[orow] = z == 0.f ? -INFINITY : base + __logf(z);
+  if (item % kParts == 0 && lane == 0) p.lse[orow] = z == 0.f ? -INFINITY : base + __logf(z);
 }
 
 }  // namespace chunk

@@ -95,10 +95,18 @@ struct Cfg {
   // or by 4 where the other 4 expand the e4m3 pages
   static constexpr int kCorrWarps = kF8 ? 4 : 8;
   static_assert(kSmem <= 232448, "shared memory budget");
-  // a unit's query entries fit the ring, and two units' entries are more than
-  // the ring holds: what unit n + 2 overwrites, unit n + 1 has released
-  static_assert(kQEntries <= kNStS && kNStS <= kMaxStages && kQEntries + kParts >= kNStS / 2 + 1, "query entries");
-  static_assert(!kPeSmem || kQEntries + kParts >= kNStS, "a pair's rope tiles");
+  // Ring entries of a block with `rows` rows in the first CTA (the pair's CTAs
+  // keep in step): as many as hold them.  Two units' entries are at least what
+  // the ring holds, so that what unit n + 2 arms, unit n has released; a bf16
+  // pair's rope tiles need one unit's entries to be that many.
+  static constexpr int kMinQEntries = kParts == 3 ? kQEntries : (kNStS + 1) / 2 - kParts > 1 ? (kNStS + 1) / 2 - kParts : 1;
+  static __device__ __forceinline__ int q_entries(int rows) {
+    if (kParts == 3) return kQEntries;
+    const int n = ((rows < kRows ? rows : kRows) + kQRows - 1) / kQRows;
+    return n < kMinQEntries ? kMinQEntries : n;
+  }
+  static_assert(kQEntries <= kNStS && kNStS <= kMaxStages && 2 * (kMinQEntries + kParts) >= kNStS, "query entries");
+  static_assert(kParts != 3 || kQEntries + kParts >= kNStS, "a pair's rope tiles");
 };
 
 // Where 16-byte chunk c of query row r of this CTA sits in the ring (c / 8:
