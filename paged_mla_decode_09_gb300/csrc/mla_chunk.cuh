@@ -33,7 +33,7 @@
 // as two e4m3 terms hi + lo of q / 2^k.  A bf16 value has 8 significant bits
 // and hi + lo hold 4 + 4, so with a power-of-two row scale the split is exact
 // down to 2^-10 of the row's largest value and scores are as exact as with a
-// bf16 cache.  PV runs in f16: four warps of the O CTA expand the codes
+// bf16 cache.  PV runs in f16: the O CTA's row warps expand the codes
 // (exact in f16) into the V ring, and P keeps f16's range (P as e4m3 terms
 // loses the many small weights of a long row to subnormals).
 #pragma once
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(smem_u32(&ctrl->kv_full[i]), 1);
-      mbar_init(smem_u32(&ctrl->kv_empty[i]), (!role_s && kF8) ? 4 : 1);  // e4m3 O CTA: the four expanding warps
+      mbar_init(smem_u32(&ctrl->kv_empty[i]), (!role_s && kF8) ? 8 : 1);  // e4m3 O CTA: the eight expanding warps
       mbar_init(smem_u32(&ctrl->peer_kv[i]), 1);
     }
     for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctrl->q_bar[i]), 1);
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctrl->peer_pv[i]), 1);
     }
     for (int i = 0; i < 4; ++i) {
-      mbar_init(smem_u32(&ctrl->v_full[i]), 4);
+      mbar_init(smem_u32(&ctrl->v_full[i]), 8);
       mbar_init(smem_u32(&ctrl->v_empty[i]), 1);
     }
     mbar_init(smem_u32(&ctrl->o_full), 1);
@@ -1063,43 +1063,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-    } else if (kF8 && warp >= 8) {
-      // ---- e4m3: four warps expand each page's codes to f16 (exact), into
-      // the layout that PV reads.  A lane takes 16 codes (one 16-byte chunk)
-      // at a time; four lanes a row, eight rows a warp, so that the two
-      // 16-byte stores of eight neighbouring lanes meet all banks once.
-      if constexpr (kF8) {
-        UnitIter it;
-        it.init(p, cid);
-        Unit u;
-        uint32_t j = 0;
-        bool ok = true;
-        int why = 0;
-        const int w = warp - 8, c4 = lane & 3, r8 = lane >> 2;
-        while (ok && it.next(u)) {
+    } else if (warp >= 4) {
+      // ---- lazy O rescale and epilogue: thread r of half h (warps 4-7: 0,
+      // warps 8-11: 1) owns columns [256 h, 256 h + 256) of row r.  With an
+      // e4m3 cache the eight warps also expand each page's codes to f16
+      // (exact), into the layout that PV reads, serving rescale requests while
+      // they wait for a page or a free slot.
+      const int r = (warp & 3) * 32 + lane;
+      constexpr int kCols = 256;
+      const int c0 = ((warp - 4) >> 2) * kCols;
+      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const float* factors = reinterpret_cast<const float*>(data + C::kRefOff);
+      const uint32_t ml_remote = mapa(smem_u32(data + C::kMlOff), static_cast<uint32_t>(pr));
+      const uint32_t mlempty_remote = mapa(smem_u32(&ctrl->ml_empty), static_cast<uint32_t>(pr));
+      const int br = pr * kRows + r;
+      UnitIter it;
+      it.init(p, cid);
+      Unit u;
+      uint32_t un = 0, nreq = 0, j = 0;
+      bool ok = true;
+      int why = 0;
+      // Waits until the phases of both barriers have completed, serving
+      // rescale requests meanwhile (a pending request holds back a PV of the
+      // unit, so its o_full cannot complete while one is pending).
+      auto wait_serving = [&](uint32_t b0, uint32_t p0, uint32_t b1, uint32_t p1) -> bool {
+        uint64_t t0 = globaltimer_ns();
+        while (true) {
+          const bool req = __any_sync(0xffffffffu, mbar_try_wait(smem_u32(&ctrl->resc_req), nreq & 1));
+          if (!req) {
+            if (__all_sync(0xffffffffu, mbar_test4(b0, p0, b1, p1, b0, p0, b1, p1))) return true;
+            if (__any_sync(0xffffffffu, *abort || globaltimer_ns() - t0 > p.timeout_ns)) {
+              why = kWaitOFull;
+              return false;
+            }
+            if (!kF8) __nanosleep(32);
+            continue;
+          }
+          const uint32_t jr = *reinterpret_cast<volatile uint32_t*>(&ctrl->resc_page);
+          const float a = br < u.k.nrows ? factors[(jr % C::kNP) * kRows + r] : 1.f;
+          if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->p_empty[(jr - 1) % C::kNP]), ((jr - 1) / C::kNP) & 1, abort,
+                                           p.timeout_ns)) {
+            why = kWaitPvPrev;
+            return false;
+          }
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, a != 1.f)) {
+            for (int c = c0; c < c0 + kCols; c += 16) {
+              uint32_t v[16];
+              tmem_ld16(tmem + lane_base + c, v);
+              tmem_wait_ld_tie(v);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * a);
+              tmem_st16(tmem + lane_base + c, v);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctrl->resc_done));
+          ++nreq;
+          t0 = globaltimer_ns();
+        }
+      };
+      while (ok && it.next(u)) {
+        if constexpr (kF8) {
+          // A lane takes 16 codes (one 16-byte chunk) at a time; four lanes a
+          // row, eight rows a warp, so that the two 16-byte stores of eight
+          // neighbouring lanes meet all banks once.
+          const int w = warp - 4, c4 = lane & 3, r8 = lane >> 2;
           for (int vp = u.p0; vp < u.p1; ++vp, ++j) {
             const int rs = static_cast<int>(j % C::kNStO), vs = static_cast<int>(j % C::kNV);
-            if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->kv_full[rs]), (j / C::kNStO) & 1, abort, p.timeout_ns)) {
+            if (!wait_serving(smem_u32(&ctrl->kv_full[rs]), (j / C::kNStO) & 1, smem_u32(&ctrl->v_empty[vs]),
+                              ((j / C::kNV) & 1) ^ 1)) {
               ok = false;
-              why = kWaitRaw;
-              break;
-            }
-            if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->v_empty[vs]), ((j / C::kNV) & 1) ^ 1, abort,
-                                             p.timeout_ns)) {
-              ok = false;
-              why = kWaitVEmpty;
               break;
             }
             const uint8_t* src = raw + rs * C::kSlotRaw;
             uint8_t* dst = vring + vs * C::kSlotV;
             const int valid = u.k.len - real_page(u.k, vp) * kPage;
+            constexpr int kItems = C::kRawBoxes * 2;  // per warp: (rows 8 ro .., half box hb), four loads in flight
 #pragma unroll 1
-            for (int t = 0; t < C::kRawBoxes * 4; t += 8) {
-              // warp w: item w + 4 t = (rows 8 ro .., half box hb); eight loads in flight
-              uint4 v[8];
+            for (int t = 0; t < kItems; t += 4) {
+              uint4 v[4];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const int item = w + 4 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
+              for (int q = 0; q < 4; ++q) {
+                const int item = w + 8 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
                 const int chunk = (hb & 1) * 4 + c4;  // of the raw box's row
                 v[q] = make_uint4(0, 0, 0, 0);  // slots past the sequence's end may hold anything
                 if (row < valid)
@@ -1107,8 +1155,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                          ((chunk ^ (row & 7)) << 4));
               }
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const int item = w + 4 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
+              for (int q = 0; q < 4; ++q) {
+                const int item = w + 8 * (t + q), ro = item & 7, hb = item >> 3, row = ro * 8 + r8;
                 const uint32_t in[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
                 uint32_t o[8];
 #pragma unroll
@@ -1128,72 +1176,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               mbar_arrive(smem_u32(&ctrl->v_full[vs]));
             }
           }
+          if (!ok) break;
         }
-        if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
-      }
-    } else if (warp >= 4) {
-      // ---- lazy O rescale and epilogue: thread r owns columns [c0, c1) of row r
-      const int r = (warp & 3) * 32 + lane;
-      constexpr int kCols = C::kCorrWarps == 8 ? 256 : 512;
-      const int c0 = C::kCorrWarps == 8 ? ((warp - 4) >> 2) * 256 : 0;
-      const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const float* factors = reinterpret_cast<const float*>(data + C::kRefOff);
-      const uint32_t ml_remote = mapa(smem_u32(data + C::kMlOff), static_cast<uint32_t>(pr));
-      const uint32_t mlempty_remote = mapa(smem_u32(&ctrl->ml_empty), static_cast<uint32_t>(pr));
-      const int br = pr * kRows + r;
-      UnitIter it;
-      it.init(p, cid);
-      Unit u;
-      uint32_t un = 0, nreq = 0, j = 0;
-      bool ok = true;
-      int why = 0;
-      while (ok && it.next(u)) {
-        const uint64_t t_unit = globaltimer_ns();
-        while (true) {
-          bool req = false, done = false;
-          while (true) {
-            req = mbar_try_wait(smem_u32(&ctrl->resc_req), nreq & 1);
-            done = !req && mbar_try_wait(smem_u32(&ctrl->o_full), un & 1);
-            if (__any_sync(0xffffffffu, req || done)) break;
-            if (__any_sync(0xffffffffu, *abort || globaltimer_ns() - t_unit > p.timeout_ns)) break;
-            __nanosleep(32);
-          }
-          req = __any_sync(0xffffffffu, req);
-          done = !req && __any_sync(0xffffffffu, done);
-          if (!req && !done) {
-            ok = false;
-            why = kWaitOFull;
-            break;
-          }
-          if (done) break;
-          const uint32_t jr = *reinterpret_cast<volatile uint32_t*>(&ctrl->resc_page);
-          const float a = br < u.k.nrows ? factors[(jr % C::kNP) * kRows + r] : 1.f;
-          if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->p_empty[(jr - 1) % C::kNP]), ((jr - 1) / C::kNP) & 1, abort,
-                                           p.timeout_ns)) {
-            ok = false;
-            why = kWaitPvPrev;
-            break;
-          }
-          tc_fence_after();
-          if (__any_sync(0xffffffffu, a != 1.f)) {
-            for (int c = c0; c < c0 + kCols; c += 16) {
-              uint32_t v[16];
-              tmem_ld16(tmem + lane_base + c, v);
-              tmem_wait_ld_tie(v);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * a);
-              tmem_st16(tmem + lane_base + c, v);
-            }
-            tmem_wait_st();
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctrl->resc_done));
-          ++nreq;
+        const uint32_t of = smem_u32(&ctrl->o_full), mf = smem_u32(&ctrl->ml_full);
+        if (!wait_serving(of, un & 1, of, un & 1)) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
-        j += static_cast<uint32_t>(u.p1 - u.p0);
-        if (!mbar_wait_warp<true, true>(smem_u32(&ctrl->ml_full), un & 1, abort, p.timeout_ns)) {
+        if (!mbar_wait_warp<true, true>(mf, un & 1, abort, p.timeout_ns)) {
           ok = false;
           why = kWaitMlFull;
           break;

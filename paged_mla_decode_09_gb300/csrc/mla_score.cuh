@@ -91,9 +91,7 @@ struct Cfg {
   static constexpr int kSmem = 1024 + ((kData + 15) & ~15) + kCtrlBytes;
   // bytes an S CTA sends per page: every row's P and O factor, a flag word per softmax warp
   static constexpr uint32_t kPTx = kRows * (kPage * 2 + 4) + 4 * 4;
-  // O rows are corrected and stored by 8 warps (a half of the columns each),
-  // or by 4 where the other 4 expand the e4m3 pages
-  static constexpr int kCorrWarps = kF8 ? 4 : 8;
+  static constexpr int kCorrWarps = 8;  // O rows are corrected and stored by 8 warps, a half of the columns each
   static_assert(kSmem <= 232448, "shared memory budget");
   // Ring entries of a block with `rows` rows in the first CTA (the pair's CTAs
   // keep in step): as many as hold them.  Two units' entries are at least what
