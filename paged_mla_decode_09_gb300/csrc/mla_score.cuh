@@ -42,7 +42,7 @@ struct Cfg {
   static constexpr int kParts = (kCg == 2 && !kF8) ? 3 : 1;
   static constexpr int kPartBoxes = kSBoxes / kParts;
   static constexpr int kSlotS = kPartBoxes * kBox + kPeBytes;
-  static constexpr int kNStS = kF8 ? (kCg == 1 ? 6 : 4) : (kCg == 1 ? 3 : 7);
+  static constexpr int kNStS = kF8 ? (kCg == 1 ? 6 : 5) : (kCg == 1 ? 3 : 7);
   // TMEM columns: queries, then kNSB score buffers of a tile each.  A pair
   // keeps the rope part of the queries in shared memory (A of its QK steps),
   // which leaves 256 columns for two tiles of 128 keys.
