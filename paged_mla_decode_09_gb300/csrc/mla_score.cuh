@@ -150,17 +150,25 @@ template <int kCg>
 __device__ __forceinline__ float q_row_e4m3(const uint8_t* ring, uint32_t i, int r, uint32_t taddr, uint8_t* pe_tile,
                                             int g0, int g1) {
   using C = Cfg<true, kCg>;
-  uint32_t m = 0;  // largest |q| as bf16 bits (two lanes); bf16 bits order as integers
+  // the largest |q| (a NaN stays), two lanes in each of four chains
+  __nv_bfloat162 m4[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) m4[e] = __floats2bfloat162_rn(0.f, 0.f);
 #pragma unroll 6
   for (int c = 0; c < 72; ++c) {
     const uint4 v = *reinterpret_cast<const uint4*>(q_chunk<true, kCg>(ring, i, r, c));
-    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu)));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m4[e] = __hmax2_nan(m4[e], __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[e])));
   }
-  const uint32_t top = (m & 0xFFFFu) > (m >> 16) ? (m & 0xFFFFu) : (m >> 16);
+  const __nv_bfloat162 m2 = __hmax2_nan(__hmax2_nan(m4[0], m4[1]), __hmax2_nan(m4[2], m4[3]));
+  const uint32_t top = __bfloat16_as_ushort(__hmax_nan(m2.x, m2.y));
   int e = static_cast<int>(top >> 7) - 127 - 7;  // exponent of the scale
   e = e < -107 ? -107 : e;
   const float scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+  const uint32_t inv_bits = static_cast<uint32_t>(127 - e) << 7;  // 1 / scale, a power of two in bf16 too
+  const uint32_t inv_pair = inv_bits | (inv_bits << 16);
+  const __nv_bfloat162 inv2 = *reinterpret_cast<const __nv_bfloat162*>(&inv_pair);
 #pragma unroll 1
   for (int g = g0; g < g1; ++g) {
     uint32_t hi[16], lo[16];
@@ -173,14 +181,16 @@ __device__ __forceinline__ float q_row_e4m3(const uint8_t* ring, uint32_t i, int
         uint32_t h[2], l[2];
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-          float2 x = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * h2 + q]));
-          x.x *= inv;
-          x.y *= inv;
-          const __nv_fp8x2_storage_t hh = __nv_cvt_float2_to_fp8x2(x, __NV_SATFINITE, __NV_E4M3);
+          // q / scale is exact in bf16 and, from 2^-14 on, in f16 (8 bits, at
+          // most 2^8); so is the residual of its e4m3 rounding
+          const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * h2 + q]), inv2);
+          const __half2 x = __float22half2_rn(__bfloat1622float2(y));
+          const __nv_fp8x2_storage_t hh =
+              __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3);
           const __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(hh, __NV_E4M3);
-          const float2 hf = __half22float2(*reinterpret_cast<const __half2*>(&hr));
+          const __half2 res = __hsub2(x, *reinterpret_cast<const __half2*>(&hr));
           h[q] = hh;
-          l[q] = __nv_cvt_float2_to_fp8x2(make_float2(x.x - hf.x, x.y - hf.y), __NV_SATFINITE, __NV_E4M3);
+          l[q] = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&res), __NV_SATFINITE, __NV_E4M3);
         }
         hi[2 * k + h2] = h[0] | (h[1] << 16);
         lo[2 * k + h2] = l[0] | (l[1] << 16);
