@@ -24,6 +24,7 @@ using mla::host::align256;
 using mla::host::aligned;
 using mla::host::device_ok;
 using mla::host::encode_fn;
+using mla::host::launch_pdl;
 using mla::host::map2;
 using mla::host::map3;
 
@@ -159,21 +160,8 @@ bool make_maps(const void* q_nope, const void* q_pe, const void* kv, const Shape
 
 template <bool kF8, int kCg>
 cudaError_t launch_attention(const Params& p, const Maps& m, cudaStream_t stream) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * kCg * p.C, 1, 1);
-  cfg.blockDim = dim3(mla::chunk::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Cfg<kF8, kCg>::kSmem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2 * kCg;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, mla::chunk::mla_chunk_kernel<kF8, kCg>, p, m.s, m.o, m.pe, m.qn, m.qp);
+  return launch_pdl(mla::chunk::mla_chunk_kernel<kF8, kCg>, dim3(2 * kCg * p.C), dim3(mla::chunk::kThreads),
+                    Cfg<kF8, kCg>::kSmem, stream, 2 * kCg, p, m.s, m.o, m.pe, m.qn, m.qp);
 }
 
 int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, const void* q_pe, const void* kv_cache,
@@ -236,17 +224,20 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   p.pt_stride = static_cast<int32_t>(s.stride);
   p.window = window;
   p.sinks = sinks;
-  p.unit_cost = 6;
+  // a piece's start in pages' time: swept 3 to 22 on GB300; flat for bf16, an
+  // e4m3 pair splits its 256 query rows for ~5 us (ragged chunks 1540 us at 6,
+  // 1445 at 15; two drafts over windows 148 and 144)
+  p.unit_cost = s.f8 && cg == 2 ? 15 : 6;
   p.scale = scale;
   p.kv_scale = s.f8 ? kv_scale : 1.f;
   p.timeout_ns = kTimeoutNs;
 
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-  mla::chunk::mla_chunk_schedule_kernel<<<1, s.B <= 256 && p.NB <= 256 && C <= 256 ? 256 : mla::chunk::kSchedThreads, 0,
-                                         stream>>>(p);
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  cudaError_t e = s.f8 ? (cg == 2 ? launch_attention<true, 2>(p, m, stream) : launch_attention<true, 1>(p, m, stream))
-                       : (cg == 2 ? launch_attention<false, 2>(p, m, stream) : launch_attention<false, 1>(p, m, stream));
+  const int nt = s.B <= 256 && p.NB <= 256 && C <= 256 ? 256 : mla::chunk::kSchedThreads;
+  cudaError_t e = launch_pdl(mla::chunk::mla_chunk_schedule_kernel, dim3(1), dim3(nt), 0, stream, 0, p);
+  if (e == cudaSuccess)
+    e = s.f8 ? (cg == 2 ? launch_attention<true, 2>(p, m, stream) : launch_attention<true, 1>(p, m, stream))
+             : (cg == 2 ? launch_attention<false, 2>(p, m, stream) : launch_attention<false, 1>(p, m, stream));
   if (e == cudaSuccess) {
     // a column per block that may be cut, at most one per slice boundary; a
     // warp per row, or four where that still fits the SMs about once
@@ -254,18 +245,11 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
     const int64_t rows = s.T * s.H < p.BR ? s.T * s.H : p.BR;
     const bool four = cuts * rows * 4 <= 152 * 32;
     const int64_t items = rows * (four ? 4 : 1);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(cuts),
-                       static_cast<unsigned>((items + mla::chunk::kCombineWarps - 1) / mla::chunk::kCombineWarps), 1);
-    cfg.blockDim = dim3(mla::chunk::kCombineWarps * 32, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = four ? cudaLaunchKernelEx(&cfg, mla::chunk::mla_chunk_combine_kernel<4>, p)
-             : cudaLaunchKernelEx(&cfg, mla::chunk::mla_chunk_combine_kernel<1>, p);
+    const dim3 grid(static_cast<unsigned>(cuts),
+                    static_cast<unsigned>((items + mla::chunk::kCombineWarps - 1) / mla::chunk::kCombineWarps));
+    const dim3 block(mla::chunk::kCombineWarps * 32);
+    e = four ? launch_pdl(mla::chunk::mla_chunk_combine_kernel<4>, grid, block, 0, stream, 0, p)
+             : launch_pdl(mla::chunk::mla_chunk_combine_kernel<1>, grid, block, 0, stream, 0, p);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

@@ -163,6 +163,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
   __shared__ int ncuts;
   __shared__ int cb[kMaxClusters + 1];  // where the slices begin
   __shared__ int32_t sp[kSchedSmemNB + 1];
+  griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, nt = static_cast<int>(blockDim.x);
   if (tid < 4) p.status[tid] = 0;
@@ -1229,6 +1230,7 @@ template <int kParts>
 __global__ void __launch_bounds__(kCombineWarps * 32) mla_chunk_combine_kernel(const __grid_constant__ Params p) {
   constexpr int kV = 4 / kParts;      // float4s of a row per lane
   constexpr int kFly = 2 * kParts;    // partial rows in flight
+  griddep_launch_dependents();
   const bool block0 = blockIdx.x == 0 && blockIdx.y == 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.y * kCombineWarps + warp, br = item / kParts, col = (item % kParts) * 32 * kV + lane;

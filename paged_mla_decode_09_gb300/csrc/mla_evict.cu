@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
   __shared__ int4 counts_w[kWarps];  // per warp, see below
   __shared__ int4 share;           // the block's sums of them, and its greatest position: read by the other blocks
   __shared__ int share_pos;
+  griddep_wait();
   griddep_launch_dependents();
   const int cs = p.cluster, b = blockIdx.x / cs, rank = blockIdx.x % cs;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -299,6 +300,7 @@ __global__ void __launch_bounds__(kMoveWarps * 32) mla_evict_move_kernel(const _
   constexpr int kChunks = kRowBytes / 16;
   constexpr int kPer = (kChunks + 31) / 32;
   griddep_wait();
+  griddep_launch_dependents();
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int n0 = p.counts[b];
   const int n = n0 < 0 ? -1 - n0 : n0;
@@ -414,19 +416,8 @@ int mla_evict(const mla_evict_dims* d, const float* mass, const int32_t* positio
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   cudaError_t e = allow_smem<0>(mla::evict::mla_evict_select_kernel, mla::evict::kMaxSmemKeys * 8, dev);
   if (e == cudaSuccess) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(d->batch) * p.cluster, 1, 1);
-    cfg.blockDim = dim3(mla::evict::kThreads, 1, 1);
-    cfg.dynamicSmemBytes = static_cast<size_t>(p.smem_keys) * 8;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, mla::evict::mla_evict_select_kernel, p);
+    e = launch_pdl(mla::evict::mla_evict_select_kernel, dim3(static_cast<unsigned>(d->batch) * p.cluster),
+                   dim3(mla::evict::kThreads), static_cast<size_t>(p.smem_keys) * 8, stream, p.cluster, p);
   }
   if (e == cudaSuccess) {
     // about eight blocks per SM in all, each request's rows over its share
@@ -434,17 +425,9 @@ int mla_evict(const mla_evict_dims* d, const float* mass, const int32_t* positio
     const int64_t most = (static_cast<int64_t>(d->budget) + rows - 1) / rows;
     int64_t gx = (8ll * sms + d->batch - 1) / d->batch;
     if (gx > most) gx = most;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(gx), static_cast<unsigned>(d->batch), 1);
-    cfg.blockDim = dim3(mla::evict::kMoveWarps * 32, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    e = d->kv_dtype == MLA_KV_FP8_E4M3 ? cudaLaunchKernelEx(&cfg, mla::evict::mla_evict_move_kernel<576>, p)
-                                       : cudaLaunchKernelEx(&cfg, mla::evict::mla_evict_move_kernel<1152>, p);
+    const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(d->batch)), block(mla::evict::kMoveWarps * 32);
+    e = d->kv_dtype == MLA_KV_FP8_E4M3 ? launch_pdl(mla::evict::mla_evict_move_kernel<576>, grid, block, 0, stream, 0, p)
+                                       : launch_pdl(mla::evict::mla_evict_move_kernel<1152>, grid, block, 0, stream, 0, p);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();

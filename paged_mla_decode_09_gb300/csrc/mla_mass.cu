@@ -91,6 +91,7 @@ struct Params {
 };
 
 __global__ void mla_mass_clear_kernel(int32_t* status) {
+  griddep_wait();  // before the kernel behind it may read its inputs
   griddep_launch_dependents();
   if (threadIdx.x < 4) status[threadIdx.x] = 0;
 }
@@ -160,9 +161,10 @@ __device__ __forceinline__ bool find_slice(const Params& p, Ctrl* ctrl, Weight w
       const int b = base + tid;
       long long v = 0;
       if (b < p.B) {
-        const int L = p.seq_lens[b];
+        // through L2: a line of an earlier call may sit in this SM's L1 until griddep_wait
+        const int L = __ldcg(p.seq_lens + b);
         bad = bad || L < p.Q || L > p.cap;
-        v = weight(length_of(p, b));
+        v = weight(L < 0 ? 0 : (L > p.cap ? p.cap : L));
       }
       const long long own = v;
       for (int o = 1; o < 32; o <<= 1) {
@@ -299,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  griddep_wait();  // the status words are cleared (and whatever the caller launched before has completed)
+  griddep_wait();  // the status words are cleared
+  griddep_launch_dependents();
   if (bad && blockIdx.x == 0) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
   const uint32_t tmem = ctrl->tmem_base;
   volatile int* abort = &ctrl->abort;
@@ -582,6 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   griddep_wait();
+  griddep_launch_dependents();
   if (bad && blockIdx.x == 0) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
   const uint32_t tmem = ctrl->tmem_base;
   volatile int* abort = &ctrl->abort;
@@ -888,17 +892,7 @@ cudaError_t launch_mass(Kernel* kernel, int smem, const Params& p, const CUtenso
                         const CUtensorMap& qn, const CUtensorMap& qp, int ctas, int device, cudaStream_t stream) {
   cudaError_t e = allow_smem<kTag>(kernel, smem, device);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, 1, 1);
-  cfg.blockDim = dim3(mla::chunk::kThreads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p, s, pe, qn, qp);
+  return launch_pdl(kernel, dim3(ctas), dim3(mla::chunk::kThreads), smem, stream, 0, p, s, pe, qn, qp);
 }
 
 }  // namespace
@@ -976,8 +970,7 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
   p.kv_scale = f8 ? kv_scale : 1.f;
   p.timeout_ns = 2000000000ull;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-  mla::mass::mla_mass_clear_kernel<<<1, 32, 0, stream>>>(p.status);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_pdl(mla::mass::mla_mass_clear_kernel, dim3(1), dim3(32), 0, stream, 0, p.status);
   if (e == cudaSuccess) {
     using namespace mla::mass;
     e = rows ? (f8 ? launch_mass<3>(mla_mass_rows_kernel<true>, kRowsSmem, p, s, pe, qn, qp, sms, dev, stream)
