@@ -135,7 +135,14 @@ struct Params {
 // weighted order (a piece of a block costs unit_cost pages to start), so that
 // clusters with many short blocks get fewer pages.
 constexpr int kSchedThreads = 1024;  // or 256 for small batches (fewer warps at each barrier)
-constexpr int kSchedSmemNB = 8192;  // prefix sums kept in shared memory for the searches
+constexpr int kSchedSmemNB = 8192;  // blocks and requests whose sums are kept in shared memory for the searches
+constexpr int kSchedSmemB = 2048;
+
+// The page of the last key that the block's last row sees.
+__device__ __forceinline__ int last_page(const Block& k, int H) {
+  const int pos1 = k.pos0 + (k.h0 + k.nrows - 1) / H;
+  return (pos1 < 0 ? 0 : pos1) / kPage;
+}
 
 __device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  // inclusive, all threads
   const int tid = threadIdx.x;
@@ -159,90 +166,103 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  //
 
 __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const __grid_constant__ Params p) {
   __shared__ int warp_tot[32];
-  __shared__ int carry_s;
-  __shared__ int ncuts;
-  __shared__ int cb[kMaxClusters + 1];  // where the slices begin
-  __shared__ int32_t sp[kSchedSmemNB + 1];
+  __shared__ int carry_s, ncuts;
+  __shared__ int32_t sp[kSchedSmemNB + 1];    // page prefix sums, first block of each request: copies for the
+  __shared__ int32_t sb[kSchedSmemB + 1];     // searches (a search through global memory waits ~0.7 us a step)
+  __shared__ int cb[kMaxClusters + 1];        // where the slices begin
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x, nt = static_cast<int>(blockDim.x);
   if (tid < 4) p.status[tid] = 0;
   if (tid == 0) carry_s = ncuts = 0;
   __syncthreads();
+  const bool sb_ok = p.B <= kSchedSmemB, sp_ok = p.NB <= kSchedSmemNB;
+  // request b's query tokens [q0, q1); an invalid range is left out
+  auto range = [&](int b, int& q0, int& q1) -> bool {
+    if (!p.cu_q) {
+      q0 = b * p.q_len;
+      q1 = q0 + p.q_len;
+      return true;
+    }
+    q0 = p.cu_q[b];
+    q1 = p.cu_q[b + 1];
+    if (q0 >= 0 && q1 >= q0 && q1 <= p.T && (b > 0 || q0 == 0)) return true;
+    q0 = q1 = 0;
+    return false;
+  };
   // row blocks per request
   for (int base = 0; base < p.B; base += nt) {
     const int b = base + tid;
     int nblk = 0;
     if (b < p.B) {
-      int64_t q0, q1;
-      if (p.cu_q) {
-        q0 = p.cu_q[b];
-        q1 = p.cu_q[b + 1];
-        if (q0 < 0 || q1 < q0 || q1 > p.T || (b == 0 && q0 != 0)) {
-          atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
-          q0 = q1 = 0;  // the request is left out
-        }
-      } else {
-        q0 = static_cast<int64_t>(b) * p.q_len;
-        q1 = q0 + p.q_len;
-      }
+      int q0, q1;
+      if (!range(b, q0, q1)) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
       const int L = p.seq_lens[b];
       if (q1 > q0 && (L < q1 - q0 || L > p.max_pages * kPage)) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
-      nblk = static_cast<int>(((q1 - q0) * p.H + p.BR - 1) / p.BR);
+      nblk = static_cast<int>((static_cast<int64_t>(q1 - q0) * p.H + p.BR - 1) / p.BR);
     }
     const int incl = block_scan(nblk, warp_tot, carry_s);
-    if (b < p.B) p.blkoff[b + 1] = incl < p.NB ? incl : p.NB;  // never beyond the arrays
+    if (b < p.B) {
+      const int v = incl < p.NB ? incl : p.NB;  // never beyond the arrays
+      p.blkoff[b + 1] = v;
+      if (sb_ok) sb[b + 1] = v;
+    }
     __syncthreads();
     if (tid == nt - 1) carry_s = incl;
     __syncthreads();
   }
   if (tid == 0) {
     p.blkoff[0] = 0;
+    sb[0] = 0;
     if (carry_s > p.NB) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
     carry_s = 0;
   }
   __syncthreads();
-  const int nblocks = p.blkoff[p.B];
-  const bool sp_ok = p.NB <= kSchedSmemNB;
+  const int32_t* off = sb_ok ? sb : p.blkoff;
+  const int nblocks = off[p.B];
+  auto block_at = [&](int n) -> Block {
+    int lo = 0, hi = p.B - 1;  // last request with off <= n
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (off[mid] <= n) lo = mid; else hi = mid - 1;
+    }
+    int q0, q1;
+    range(lo, q0, q1);
+    const int nq = q1 - q0;
+    const int64_t r0 = static_cast<int64_t>(n - off[lo]) * p.BR;  // within the request
+    const int64_t left = static_cast<int64_t>(nq) * p.H - r0;
+    const int Lraw = p.seq_lens[lo];
+    const int L = Lraw < 0 ? 0 : (Lraw > p.max_pages * kPage ? p.max_pages * kPage : Lraw);
+    Block k;
+    k.b = lo;
+    k.row0 = static_cast<int32_t>(static_cast<int64_t>(q0) * p.H + r0);
+    k.nrows = static_cast<int32_t>(left < p.BR ? left : p.BR);
+    // rows of a request fit in 32 bits (total_q * H does)
+    const uint32_t i0 = static_cast<uint32_t>(r0) / static_cast<uint32_t>(p.H);
+    k.h0 = static_cast<int32_t>(static_cast<uint32_t>(r0) - i0 * static_cast<uint32_t>(p.H));
+    k.pos0 = L - nq + static_cast<int>(i0);
+    k.len = L;
+    const int last = last_page(k, p.H);  // at least one page, all of it masked if nothing is seen
+    k.sp = last + 1;
+    k.skip = 0;
+    if (p.window > 0) {
+      const int64_t wlo = static_cast<int64_t>(k.pos0) + 1 - p.window;  // first key of the first row's window
+      const int wp = wlo > 0 ? static_cast<int>(wlo / kPage) : 0;
+      const int ns = static_cast<int>((static_cast<int64_t>(p.sinks) + kPage - 1) / kPage);
+      if (wp > ns) {
+        k.sp = ns;
+        k.skip = wp - ns;
+      }
+    }
+    return k;
+  };
   // each block's rows and pages
   for (int base = 0; base < p.NB; base += nt) {
     const int n = base + tid;
     int np = 0;
     if (n < nblocks) {
-      int lo = 0, hi = p.B - 1;  // last request with blkoff <= n
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (p.blkoff[mid] <= n) lo = mid; else hi = mid - 1;
-      }
-      const int b = lo;
-      const int q0 = p.cu_q ? p.cu_q[b] : b * p.q_len;
-      const int nq = (p.cu_q ? p.cu_q[b + 1] : q0 + p.q_len) - q0;
-      const int64_t r0 = static_cast<int64_t>(n - p.blkoff[b]) * p.BR;  // within the request
-      const int64_t left = static_cast<int64_t>(nq) * p.H - r0;
-      const int Lraw = p.seq_lens[b];
-      const int L = Lraw < 0 ? 0 : (Lraw > p.max_pages * kPage ? p.max_pages * kPage : Lraw);
-      Block k;
-      k.b = b;
-      k.row0 = static_cast<int32_t>(static_cast<int64_t>(q0) * p.H + r0);
-      k.nrows = static_cast<int32_t>(left < p.BR ? left : p.BR);
-      const int i0 = static_cast<int>(r0 / p.H);
-      k.h0 = static_cast<int32_t>(r0 % p.H);
-      k.pos0 = L - nq + i0;
-      const int pos1 = L - nq + static_cast<int>((r0 + k.nrows - 1) / p.H);
-      k.len = L;
-      const int last = (pos1 < 0 ? 0 : pos1) / kPage;  // at least one page, all of it masked if nothing is seen
-      k.sp = last + 1;
-      k.skip = 0;
-      if (p.window > 0) {
-        const int64_t wlo = static_cast<int64_t>(k.pos0) + 1 - p.window;  // first key of the first row's window
-        const int wp = wlo > 0 ? static_cast<int>(wlo / kPage) : 0;
-        const int ns = static_cast<int>((static_cast<int64_t>(p.sinks) + kPage - 1) / kPage);
-        if (wp > ns) {
-          k.sp = ns;
-          k.skip = wp - ns;
-        }
-      }
-      np = last + 1 - k.skip;
+      const Block k = block_at(n);
+      np = last_page(k, p.H) + 1 - k.skip;
       p.blk[n] = k;
     }
     const int incl = block_scan(np, warp_tot, carry_s);
@@ -275,9 +295,9 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
       if (pre[mid] + static_cast<int64_t>(p.unit_cost) * mid <= x) lo = mid; else hi = mid - 1;
     }
     const int64_t np = pre[lo + 1] - pre[lo];
-    int64_t off = x - pre[lo] - static_cast<int64_t>(p.unit_cost) * (lo + 1);
-    off = off < 0 ? 0 : (off > np ? np : off);
-    return static_cast<int>(pre[lo] + off);
+    int64_t off_p = x - pre[lo] - static_cast<int64_t>(p.unit_cost) * (lo + 1);
+    off_p = off_p < 0 ? 0 : (off_p > np ? np : off_p);
+    return static_cast<int>(pre[lo] + off_p);
   };
   auto block_of = [&](int page) -> int {  // the block that holds the page
     int lo = 0, hi = nblocks - 1;
@@ -287,7 +307,13 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
     }
     return lo;
   };
-  for (int c = tid; c <= p.C; c += nt) cb[c] = c == 0 ? 0 : (c == p.C ? pre[nblocks] : page_at(W * c / p.C));
+  const bool cut32 = W * p.C < (static_cast<int64_t>(1) << 31);  // a 32-bit division where it fits
+  for (int c = tid; c <= p.C; c += nt) {
+    const int64_t x = cut32 ? static_cast<int64_t>(static_cast<uint32_t>(W) * static_cast<uint32_t>(c) /
+                                                   static_cast<uint32_t>(p.C))
+                            : W * c / p.C;
+    cb[c] = c == 0 ? 0 : (c == p.C ? pre[nblocks] : page_at(x));
+  }
   __syncthreads();
   for (int c = tid; c < p.C; c += nt) {
     const int s = cb[c], e = cb[c + 1];
@@ -301,7 +327,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
         const int mid = (lo + hi + 1) >> 1;
         if (cb[mid] < pre[last + 1]) lo = mid; else hi = mid - 1;
       }
-      const Block k = p.blk[last];
+      const Block k = block_at(last);
       int4* dst = reinterpret_cast<int4*>(p.cuts + 8 * (1 + atomicAdd(&ncuts, 1)));
       dst[0] = make_int4(last, c, lo, 2 * c + (first != last ? 1 : 0));
       dst[1] = make_int4(k.row0, k.nrows, 0, 0);
