@@ -228,7 +228,7 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   // e4m3 pair splits its 256 query rows for ~5 us (ragged chunks 1540 us at 6,
   // 1445 at 15; two drafts over windows 148 and 144)
   p.unit_cost = s.f8 && cg == 2 ? 15 : 6;
-  p.scale = scale;
+  p.c2 = mla::host::log2_scale(scale, s.f8 ? kv_scale : 1.f);
   p.kv_scale = s.f8 ? kv_scale : 1.f;
   p.timeout_ns = kTimeoutNs;
 

@@ -125,7 +125,8 @@ struct Params {
   int32_t num_pages, max_pages, pt_stride;
   int32_t window, sinks;    // window 0: everything up to the row's own position
   int32_t unit_cost;        // schedule weight of starting a piece, in pages
-  float scale, kv_scale;
+  float c2;                 // scale log2(e) (kv_scale), rounded once: scores in log2 units per product
+  float kv_scale;
   uint64_t timeout_ns;
 };
 
@@ -857,7 +858,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           else mbar_arrive(smem_u32(&ctrl->q_full));
         }
         i += qe + C::kParts * static_cast<uint32_t>((u.p1 - u.p0 + kCg - 1) / kCg);
-        const float c2 = p.scale * kLog2e * (kF8 ? qs * p.kv_scale : 1.f);
+        const float c2 = kF8 ? p.c2 * qs : p.c2;  // qs is a power of two
         const bool real = br < u.k.nrows;
         // padding rows follow the block's last row (their results go nowhere)
         const int pos = u.k.pos0 + (u.k.h0 + (real ? br : u.k.nrows - 1)) / p.H;

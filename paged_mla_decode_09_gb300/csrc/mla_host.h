@@ -67,6 +67,12 @@ inline bool map2(CUtensorMap* m, const void* base, int64_t rows, int width, int 
                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// scale * log2(e) * kv_scale rounded to fp32 once: the factor of every score,
+// so that its error (2^-24 relative) is that of one rounding.
+inline float log2_scale(float scale, float kv_scale) {
+  return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074 * static_cast<double>(kv_scale));
+}
+
 // Launches a kernel with programmatic stream serialization: it may begin while
 // the kernel before it in the stream ends, and waits for that one's results
 // (griddep_wait) before it touches any.  Kernels that begin a call do so at

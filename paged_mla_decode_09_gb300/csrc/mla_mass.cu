@@ -24,6 +24,8 @@
 //     cycles per 128 keys x 64 rows.  (With the queries kept instead, every
 //     CTA moved and split all row blocks for the few pages of its slice: 503
 //     us for 32 tokens x 128 heads over 75K keys of four requests, e4m3.)
+//     Where a call has few key tiles, a cluster of 2 to 8 CTAs shares one,
+//     every CTA some of the row tiles, and the first adds up their sums.
 //
 // No atomics: a key belongs to one CTA, which adds in a fixed order, so
 // results do not depend on timing or slicing.
@@ -86,7 +88,8 @@ struct Params {
   int32_t num_pages, max_pages, pt_stride, cols;
   int32_t cap;        // longest length the table and the mass rows hold
   int32_t num_fresh;
-  float scale, kv_scale;
+  int32_t cluster;    // CTAs that share a key tile (the first kernel: 1)
+  float c2;           // scale log2(e) (kv_scale), rounded once
   uint64_t timeout_ns;
 };
 
@@ -156,7 +159,7 @@ __device__ __forceinline__ bool find_slice(const Params& p, Ctrl* ctrl, Weight w
   for (int pass = 0; pass < 2; ++pass) {
     if (tid == 0) carry = 0;
     __syncthreads();
-    const long long x0 = pass ? ctrl->total * blockIdx.x / gridDim.x : 0;
+    const long long x0 = pass ? ctrl->total * (blockIdx.x / p.cluster) / (gridDim.x / p.cluster) : 0;
     for (int base = 0; base < p.B; base += kThreads) {
       const int b = base + tid;
       long long v = 0;
@@ -419,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&ctrl->q_full));
       i += C::kQEntries + static_cast<uint32_t>(u.p1 - u.p0);
       ++un;
-      const float c2 = p.scale * kLog2e * (kF8 ? qs * p.kv_scale : 1.f);
+      const float c2 = kF8 ? p.c2 * qs : p.c2;  // qs is a power of two
       const float* in = p.mass_in ? p.mass_in + static_cast<int64_t>(u.b) * p.cols : nullptr;
       float* out = p.mass_out + static_cast<int64_t>(u.b) * p.cols;
       const int old = u.L - p.num_fresh;  // tokens below start from mass_in
@@ -493,7 +496,8 @@ constexpr int kSlot = 73728;  // a page of the cache, or 64 query rows
 constexpr int kSlots = 3;
 constexpr int kNlOff = kSlots * kSlot;            // [3][64] -lse of a row tile, in log2 units
 constexpr int kPartOff = kNlOff + 3 * 64 * 4;     // [2][128] the second group's sums
-constexpr int kRowsData = kPartOff + 2 * kKeys * 4;
+constexpr int kClusOff = kPartOff + 2 * kKeys * 4;  // [8][128] the sums of the cluster's CTAs (in its first)
+constexpr int kRowsData = kClusOff + 8 * kKeys * 4;
 constexpr int kRowsSmem = 1024 + kRowsData + 512;
 
 // The key tiles of a CTA's slice, in order.
@@ -506,8 +510,9 @@ struct TileIter {
   int b;
   __device__ void init(const Params& pp, const Ctrl* c) {
     p = &pp;
-    x = c->total * blockIdx.x / gridDim.x;
-    x1 = c->total * (blockIdx.x + 1) / gridDim.x;
+    const int n = gridDim.x / pp.cluster, i = blockIdx.x / pp.cluster;
+    x = c->total * i / n;
+    x1 = c->total * (i + 1) / n;
     start = c->start;
     b = c->first;
   }
@@ -590,7 +595,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = ctrl->tmem_base;
   volatile int* abort = &ctrl->abort;
   uint8_t* ring = data;
-  const int ntiles = (p.R + 63) / 64;  // row tiles
+  // row tiles first, first + step .. of the request are this CTA's
+  const int all_tiles = (p.R + 63) / 64, step = p.cluster, first = static_cast<int>(blockIdx.x) % p.cluster;
   TileIter it;
   it.init(p, ctrl);
   Tile u;
@@ -627,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kF8) tma_load_2d(slot + 4 * 8192, &tm_pe, kDL, pid * kPage, qbar);
         }
         ++un;
-        for (int n = 0; n < ntiles && ok; ++n, ++i) {
+        for (int n = first; n < all_tiles && ok; n += step, ++i) {
           if (!acquire()) {
             ok = false;
             break;
@@ -671,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       ++un;
-      for (int n = 0; n < ntiles; ++n, ++j, ++i) {
+      for (int n = first; n < all_tiles; n += step, ++j, ++i) {
         const int st = static_cast<int>(i % kSlots), sb = static_cast<int>(j % 3);
         if (!mbar_wait_all_warp(smem_u32(&ctrl->kv_full[st]), (i / kSlots) & 1, smem_u32(&ctrl->s_empty[sb]),
                                 ((j / 3) & 1) ^ 1, 0u, 0u, 0u, 0u, abort, p.timeout_ns)) {
@@ -708,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* nl = reinterpret_cast<float*>(data + kNlOff);
     while (ok && it.next(u)) {
       const float* lse = p.lse + static_cast<int64_t>(u.b) * p.R;
-      for (int n = 0; n < ntiles; ++n, ++j) {
+      for (int n = first; n < all_tiles; n += step, ++j) {
         const int sb = static_cast<int>(j % 3);
         float v[2];
 #pragma unroll
@@ -733,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = (warp & 3) * 32 + lane;  // key of the tile
     const int gg = (warp - 4) >> 2;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const float c2 = p.scale * kLog2e * (kF8 ? p.kv_scale : 1.f);
+    const float c2 = p.c2;
     float* parts = reinterpret_cast<float*>(data + kPartOff);
     uint32_t i = 0, j = 0;
     while (ok && it.next(u)) {
@@ -784,13 +790,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl->q_full));
-      i += 2 + ntiles;
+      i += 2 + (all_tiles - first + step - 1) / step;
       const int t = u.t0 + r;
       // the first row that sees the key: rows of the positions from t on
       const int64_t first_pos = static_cast<int64_t>(t) - (u.L - p.Q);
       const int64_t rmin = t < u.L ? (first_pos > 0 ? first_pos * p.H : 0) : p.R;
       float sum4[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int n = 0; n < ntiles; ++n, ++j) {
+      for (int n = first; n < all_tiles; n += step, ++j) {
         if ((j & 1u) != static_cast<uint32_t>(gg)) continue;
         const int sb = static_cast<int>(j % 3);
         if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (j / 3) & 1, abort, p.timeout_ns)) {
@@ -848,7 +854,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           why = kWaitSums;
           break;
         }
-        if (t < u.L) {
+        if (step > 1) {  // added up below
+          st_cluster_u32(mapa(smem_u32(data + kClusOff) + (first * kKeys + r) * 4, 0), __float_as_uint(sum + part[r]));
+        } else if (t < u.L) {
           const int64_t at = static_cast<int64_t>(u.b) * p.cols + t;
           const float base = p.mass_in && t < u.L - p.num_fresh ? p.mass_in[at] : 0.f;
           p.mass_out[at] = base + (sum + part[r]);
@@ -862,6 +870,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, 512);
+  if (step > 1) {  // a cluster has one key tile at most
+    __syncwarp();
+    cluster_sync();
+    TileIter last;
+    last.init(p, ctrl);
+    const int r = tid;
+    if (first == 0 && r < kKeys && last.next(u) && u.t0 + r < u.L && !*abort) {
+      const int t = u.t0 + r;
+      const int64_t at = static_cast<int64_t>(u.b) * p.cols + t;
+      float sum = p.mass_in && t < u.L - p.num_fresh ? p.mass_in[at] : 0.f;
+      const float* parts = reinterpret_cast<const float*>(data + kClusOff);
+      float add = 0.f;
+      for (int q = 0; q < step; ++q) add += parts[q * kKeys + r];
+      p.mass_out[at] = sum + add;
+    }
+  }
 }
 
 }  // namespace mass
@@ -889,10 +913,11 @@ int check_mass_dims(const mla_dims* d) {
 
 template <int kTag, typename Kernel>
 cudaError_t launch_mass(Kernel* kernel, int smem, const Params& p, const CUtensorMap& s, const CUtensorMap& pe,
-                        const CUtensorMap& qn, const CUtensorMap& qp, int ctas, int device, cudaStream_t stream) {
+                        const CUtensorMap& qn, const CUtensorMap& qp, int ctas, unsigned cluster, int device,
+                        cudaStream_t stream) {
   cudaError_t e = allow_smem<kTag>(kernel, smem, device);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(ctas), dim3(mla::chunk::kThreads), smem, stream, 0, p, s, pe, qn, qp);
+  return launch_pdl(kernel, dim3(ctas), dim3(mla::chunk::kThreads), smem, stream, cluster, p, s, pe, qn, qp);
 }
 
 }  // namespace
@@ -966,17 +991,25 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
   p.cols = mass_cols;
   p.cap = d->max_pages_per_req * 64 < mass_cols ? d->max_pages_per_req * 64 : mass_cols;
   p.num_fresh = num_fresh;
-  p.scale = scale;
-  p.kv_scale = f8 ? kv_scale : 1.f;
+  // CTAs per key tile: while every tile that the lengths allow can have twice
+  // as many (128 CTAs in clusters of 8 fit at once), and row tiles for each
+  p.cluster = 1;
+  if (rows) {
+    const int64_t tiles = static_cast<int64_t>(d->batch) * ((p.cap + mla::mass::kKeys - 1) / mla::mass::kKeys);
+    while (p.cluster < 8 && 2 * p.cluster * tiles <= 128 && 2 * p.cluster * 64 <= R) p.cluster *= 2;
+  }
+  p.c2 = log2_scale(scale, f8 ? kv_scale : 1.f);
   p.timeout_ns = 2000000000ull;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   cudaError_t e = launch_pdl(mla::mass::mla_mass_clear_kernel, dim3(1), dim3(32), 0, stream, 0, p.status);
   if (e == cudaSuccess) {
     using namespace mla::mass;
-    e = rows ? (f8 ? launch_mass<3>(mla_mass_rows_kernel<true>, kRowsSmem, p, s, pe, qn, qp, sms, dev, stream)
-                   : launch_mass<2>(mla_mass_rows_kernel<false>, kRowsSmem, p, s, pe, qn, qp, sms, dev, stream))
-             : (f8 ? launch_mass<1>(mla_mass_kernel<true>, Lay<true>::kSmem, p, s, pe, qn, qp, sms, dev, stream)
-                   : launch_mass<0>(mla_mass_kernel<false>, Lay<false>::kSmem, p, s, pe, qn, qp, sms, dev, stream));
+    const unsigned cl = p.cluster > 1 ? p.cluster : 0;
+    const int ctas = sms / p.cluster * p.cluster;
+    e = rows ? (f8 ? launch_mass<3>(mla_mass_rows_kernel<true>, kRowsSmem, p, s, pe, qn, qp, ctas, cl, dev, stream)
+                   : launch_mass<2>(mla_mass_rows_kernel<false>, kRowsSmem, p, s, pe, qn, qp, ctas, cl, dev, stream))
+             : (f8 ? launch_mass<1>(mla_mass_kernel<true>, Lay<true>::kSmem, p, s, pe, qn, qp, ctas, cl, dev, stream)
+                   : launch_mass<0>(mla_mass_kernel<false>, Lay<false>::kSmem, p, s, pe, qn, qp, ctas, cl, dev, stream));
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
