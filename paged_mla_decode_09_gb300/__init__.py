@@ -627,7 +627,7 @@ def mla_prefill(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, window,
     rc = load_library().mla_prefill(
         ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
         seq_lens.data_ptr(), cu_q_lens.data_ptr(), _int32_arg("window", window), _int32_arg("num_sinks", num_sinks),
-        scale, kv_scale, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        float(scale), float(kv_scale), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes,
         _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_prefill")
@@ -659,7 +659,8 @@ def mla_decode_window(q_nope, q_pe, kv_cache, page_table, seq_lens, window, num_
     dims = _decode_dims(s, kv_cache, page_table, t)
     rc = load_library().mla_decode_window(
         ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
-        seq_lens.data_ptr(), _int32_arg("window", window, 1), _int32_arg("num_sinks", num_sinks), scale, kv_scale,
+        seq_lens.data_ptr(), _int32_arg("window", window, 1), _int32_arg("num_sinks", num_sinks), float(scale),
+        float(kv_scale),
         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_window")
@@ -727,7 +728,8 @@ def mla_attn_mass(q_nope, q_pe, kv_cache, page_table, seq_lens, lse, num_fresh, 
     dims = _decode_dims(q_nope.shape, kv_cache, page_table, _t())
     rc = load_library().mla_attn_mass(
         ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
-        seq_lens.data_ptr(), lse.data_ptr(), _int32_arg("num_fresh", num_fresh), scale, kv_scale,
+        seq_lens.data_ptr(), lse.data_ptr(), _int32_arg("num_fresh", num_fresh), float(scale),
+        float(kv_scale),
         None if mass is None else mass.data_ptr(), mass_out.data_ptr(), mass_out.shape[1], workspace.data_ptr(),
         workspace.nbytes, _stream_int(stream, dev))
     if rc != MLA_OK:

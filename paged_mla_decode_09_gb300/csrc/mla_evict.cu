@@ -65,14 +65,6 @@ __device__ __forceinline__ uint32_t weight_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Counts a digit per lane (digit < 0: none): one addition per distinct digit
-// of the warp.  Additions to one shared address queue up (1024 firm tokens, or
-// a tenth of the weights at zero, took 40 us that way).
-__device__ __forceinline__ void count_digit(int* hist, int digit) {
-  const unsigned peers = __match_any_sync(0xffffffffu, digit);
-  if (digit >= 0 && (threadIdx.x & 31) == static_cast<unsigned>(__ffs(peers) - 1)) atomicAdd(&hist[digit], __popc(peers));
-}
-
 __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __grid_constant__ Params p) {
   extern __shared__ uint32_t keys[];  // keys of the block's slots, then their positions
   __shared__ int hist[4][kBins];
@@ -168,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
           x = t < r1 ? keys[t - r0] : 0u;
         }
         const bool in = t < r1 && (x & mask) == prefix;
-        if (__any_sync(0xffffffffu, in)) count_digit(hist[pass], in ? static_cast<int>((x >> shift) & 255u) : -1);
+        if (in) atomicAdd(&hist[pass][(x >> shift) & 255u], 1);
       }
       sync_ranks();
       // from the greatest digit down: thread i has bin 255 - i of all blocks

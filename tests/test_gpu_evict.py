@@ -276,8 +276,10 @@ def test_evict_all_equal_and_special_weights():
     assert r.kept[0].cpu().tolist() == list(range(150))
 
 
-def test_evict_longer_than_shared_memory():
-    r = Evict(evict_case([60000, 49153], 2048, 4, 100, kv_dtype="fp8_e4m3", seed=2))
+@pytest.mark.parametrize("positions", [True, False])
+def test_evict_longer_than_shared_memory(positions):
+    """More tokens than a cluster of eight blocks keeps keys of (8 x 20K)."""
+    r = Evict(evict_case([170000], 3000, 4, 100, kv_dtype="fp8_e4m3", seed=2, positions=positions))
     r.launch()
     assert r.status() == 0
     check_evict(r)

@@ -252,3 +252,24 @@ def test_two_streams_with_their_own_workspaces():
     for r, (o, l) in zip(rs, want):
         r.result()
         assert torch.equal(r.out, o) and torch.equal(r.lse, l)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 4)])
+def test_many_blocks_per_cluster(window, sinks, kv_dtype):
+    """More row blocks than clusters, so that clusters walk from one to the
+    next: sampled tokens of chunks of 300 and 129 tokens, 128 heads."""
+    c = K.make([300, 129], [3500, 129], 128, window=window, sinks=sinks, kv_dtype=kv_dtype, seed=41)
+    r = Run(c)
+    r.launch()
+    out, lse, status = r.result()
+    assert status == 0 and np.all(np.isfinite(out)) and np.all(np.isfinite(lse))
+    for b, tokens in ((0, (0, 1, 63, 150, 298, 299)), (1, (0, 5, 64, 128))):
+        for i in tokens:
+            t = int(c.cu[b]) + i
+            keys = oracle.seen_keys(int(c.seq_lens[b] - (c.cu[b + 1] - c.cu[b])) + i, window, sinks)
+            rows = oracle.cache_rows_at(c.kv_cache, c.page_table[b], keys, kv_dtype, c.kv_scale)
+            q = np.concatenate([oracle.bf16_bits_to_f64(c.q_nope[t]), oracle.bf16_bits_to_f64(c.q_pe[t])], axis=-1)
+            ro, rl = oracle.attend(q, rows, rows.shape[0], c.scale)
+            to, tl = K.error_bounds(c, b, i)
+            assert np.all(np.abs(out[t] - ro) <= to) and np.all(np.abs(lse[t] - rl) <= tl), (b, i)
