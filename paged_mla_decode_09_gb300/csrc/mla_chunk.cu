@@ -137,13 +137,14 @@ int clusters_of(int device, bool f8, int cg, int* out) {
 }
 
 struct Maps {
-  CUtensorMap s, o, pe, qn, qp;
+  CUtensorMap s, o, pe, qn, qp, out, part;
 };
 
 // s: an S CTA's part of a page; o: an O CTA's dimensions of a page; pe: the
-// e4m3 k_pe rows, or (bf16 pair) single boxes of q_nope; qn, qp: query rows.
+// e4m3 k_pe rows, or (bf16 pair) single boxes of q_nope; qn, qp: query rows;
+// out, part (bf16 pair): where the outputs and the partial ones go.
 template <bool kF8, int kCg>
-bool make_maps(const void* q_nope, const void* q_pe, const void* kv, const Shape& s, Maps* m) {
+bool make_maps(const void* q_nope, const void* q_pe, const void* kv, const Shape& s, const Params& p, Maps* m) {
   using C = Cfg<kF8, kCg>;
   const int64_t krows = s.num_pages * 64, qrows = s.T * s.H;
   const int row_bytes = kF8 ? 576 : 1152, esz = kF8 ? 1 : 2;
@@ -155,13 +156,17 @@ bool make_maps(const void* q_nope, const void* q_pe, const void* kv, const Shape
   m->pe = m->s;
   if (ok && kF8) ok = map2(&m->pe, kv, krows, 576, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B);
   if (ok && kPair16) ok = map2(&m->pe, q_nope, qrows, 512, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
+  m->out = m->part = m->s;
+  if (ok && kPair16)
+    ok = map2(&m->out, p.out, qrows, 512, 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
+         map2(&m->part, p.o_part, 2ll * p.C * p.BR, 512, 4, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   return ok;
 }
 
 template <bool kF8, int kCg>
 cudaError_t launch_attention(const Params& p, const Maps& m, cudaStream_t stream) {
   return launch_pdl(mla::chunk::mla_chunk_kernel<kF8, kCg>, dim3(2 * kCg * p.C), dim3(mla::chunk::kThreads),
-                    Cfg<kF8, kCg>::kSmem, stream, 2 * kCg, p, m.s, m.o, m.pe, m.qn, m.qp);
+                    Cfg<kF8, kCg>::kSmem, stream, 2 * kCg, p, m.s, m.o, m.pe, m.qn, m.qp, m.out, m.part);
 }
 
 int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, const void* q_pe, const void* kv_cache,
@@ -189,12 +194,6 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   const Layout lay = layout_of(s, C);
   if (ws_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
   if (!encode_fn()) return MLA_ERR_CUDA;
-  Maps m;
-  const bool ok = s.f8 ? (cg == 2 ? make_maps<true, 2>(q_nope, q_pe, kv_cache, s, &m)
-                                  : make_maps<true, 1>(q_nope, q_pe, kv_cache, s, &m))
-                       : (cg == 2 ? make_maps<false, 2>(q_nope, q_pe, kv_cache, s, &m)
-                                  : make_maps<false, 1>(q_nope, q_pe, kv_cache, s, &m));
-  if (!ok) return MLA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Params p;
   p.q_nope = static_cast<const uint8_t*>(q_nope);
@@ -232,6 +231,12 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   p.kv_scale = s.f8 ? kv_scale : 1.f;
   p.timeout_ns = kTimeoutNs;
 
+  Maps m;
+  const bool ok = s.f8 ? (cg == 2 ? make_maps<true, 2>(q_nope, q_pe, kv_cache, s, p, &m)
+                                  : make_maps<true, 1>(q_nope, q_pe, kv_cache, s, p, &m))
+                       : (cg == 2 ? make_maps<false, 2>(q_nope, q_pe, kv_cache, s, p, &m)
+                                  : make_maps<false, 1>(q_nope, q_pe, kv_cache, s, p, &m));
+  if (!ok) return MLA_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
   const int nt = s.B <= 256 && p.NB <= 256 && C <= 256 ? 256 : mla::chunk::kSchedThreads;
   cudaError_t e = launch_pdl(mla::chunk::mla_chunk_schedule_kernel, dim3(1), dim3(nt), 0, stream, 0, p);

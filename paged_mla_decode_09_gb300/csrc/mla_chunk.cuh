@@ -73,6 +73,7 @@ struct __align__(8) Ctrl {
   uint64_t s_full[kMaxSB];
   uint64_t s_empty[kMaxSB];         // S leader: both CTAs read the S buffer
   uint64_t q_full;               // S leader: queries in TMEM (both CTAs)
+  uint64_t q_part[3];            // bf16 pair: a part of the queries has been read
   uint64_t p_full[kMaxP];
   uint64_t p_empty[kMaxP];
   uint64_t peer_pv[kMaxP];       // O leader: the other O CTA is ready for PV of the page
@@ -87,6 +88,7 @@ struct __align__(8) Ctrl {
   uint64_t drain;
   uint32_t tmem_base;
   uint32_t resc_page;
+  uint32_t held[8];              // bf16 pair: what the S ring's slots hold (the producer's)
   int abort;
 };
 static_assert(sizeof(Ctrl) <= kCtrlBytes, "control block");
@@ -367,6 +369,10 @@ struct UnitIter {
     u.k.skip = b.x; u.k.pos0 = b.y; u.k.h0 = b.z; u.k.len = b.w;
     u.slot = (u.p0 > 0 || u.p1 < pb1 - pb0) ? 2 * cid + (n != nfirst ? 1 : 0) : -1;
     ++n;
+    if (n <= nlast) {  // the next unit's lines into L1, for the CTA's other warps too
+      prefetch_l1(p->blk + n);
+      prefetch_l1(p->prefix + n + 1);
+    }
     return true;
   }
 };
@@ -397,7 +403,7 @@ __device__ __forceinline__ int32_t read_page_id(const Params& p, int b, int pg) 
   return pid;
 }
 
-// Waits until every copy issued into the ring has landed (bounded).
+// Waits until the copies behind i phases of a ring's barriers have landed (bounded).
 template <int kNSt>
 __device__ __forceinline__ void drain_ring(Ctrl* ctrl, uint32_t i, uint64_t timeout_ns) {
   for (uint32_t q = 0; q < static_cast<uint32_t>(kNSt) && q < i; ++q) {
@@ -409,9 +415,16 @@ __device__ __forceinline__ void drain_ring(Ctrl* ctrl, uint32_t i, uint64_t time
 }
 
 // TMA producer of an S CTA: per unit its query rows (kQEntries ring entries,
-// completing on q_bar; the entries' own barriers complete by a plain arrival,
-// so that their phases keep in step), then its page of every tile (a unit's
-// odd last tile has none for the second CTA: its entries only arrive).
+// completing on q_bar), then its page of every tile (a unit's odd last tile
+// has none for the second CTA: its barrier only gets an arrival).
+//
+// Where a page is one ring entry, every entry has its barriers (a query
+// entry's complete by plain arrivals, so that the phases keep in step).  A
+// bf16 pair's page is three entries, but has one barrier and frees its slots
+// with its score tile: a commit and a wait per part kept the issuing warp
+// busy for ~940 cycles per 768 cycles of MMAs (2815 a tile instead of 2304).
+// So the slot of an entry is free once the tile of the page that it held is
+// scored (s_full), or once the query part that it held is in TMEM (q_part).
 template <bool kF8, int kCg>
 __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUtensorMap* tm_s, const CUtensorMap* tm_pe,
                           const CUtensorMap* tm_qn, const CUtensorMap* tm_qp, int cid, int pr) {
@@ -422,14 +435,32 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
   Unit u;
   uint32_t i = 0, un = 0;
   bool ok = true;
-  uint32_t bar = 0;
+  uint32_t bar = 0, jt = 0;  // jt: tiles
+  uint32_t scored = 0;       // tiles known to be scored
   uint8_t* slot = nullptr;
-  auto acquire = [&]() -> bool {
+  // a free slot for entry i; `held`: what the entry will be, 4 unit + part of
+  // the queries or 4 tile + 3 (waiting for a tile only until it is known to be
+  // scored also keeps the parity right: two tiles later it would be wrong)
+  auto acquire = [&](uint32_t held) -> bool {
     const int st = static_cast<int>(i % C::kNStS);
-    if (!mbar_wait(smem_u32(&ctrl->kv_empty[st]), ((i / C::kNStS) & 1) ^ 1, abort, p.timeout_ns)) return false;
-    bar = smem_u32(&ctrl->kv_full[st]);
     slot = ring + st * C::kSlotS;
-    return true;
+    if constexpr (C::kParts == 3) {
+      if (i >= static_cast<uint32_t>(C::kNStS)) {
+        const uint32_t was = ctrl->held[st], k = was >> 2;
+        if ((was & 3u) == 3u) {
+          if (k >= scored && !mbar_wait(smem_u32(&ctrl->s_full[k % C::kNSB]), (k / C::kNSB) & 1, abort, p.timeout_ns))
+            return false;
+          scored = k >= scored ? k + 1 : scored;
+        } else if (!mbar_wait(smem_u32(&ctrl->q_part[was & 3u]), k & 1, abort, p.timeout_ns)) {
+          return false;
+        }
+      }
+      ctrl->held[st] = held;
+      return true;
+    } else {
+      bar = smem_u32(&ctrl->kv_full[st]);
+      return mbar_wait(smem_u32(&ctrl->kv_empty[st]), ((i / C::kNStS) & 1) ^ 1, abort, p.timeout_ns);
+    }
   };
   uint32_t qloaded = 0;
   // the next unit's query rows are pulled into L2 a few pages ahead
@@ -444,7 +475,7 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
     have_next = have_next && ahead.next(nx);
     const int pf = u.p1 - 4 * kCg > u.p0 ? u.p0 + (u.p1 - 4 * kCg - u.p0) / kCg * kCg : u.p0;
     for (int e = 0; e < qe; ++e) {
-      if (!acquire()) {
+      if (!acquire(4 * un + static_cast<uint32_t>(e) / 2)) {
         ok = false;
         break;
       }
@@ -454,12 +485,12 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
         if constexpr (C::kParts == 3)
           tma_load_2d(smem_u32(ring + C::kQPeOff + (un & 1) * C::kQPeTile), tm_qp, 0, row0, qbar);
       }
-      mbar_arrive(bar);
+      if constexpr (C::kParts == 1) mbar_arrive(bar);
       if constexpr (C::kParts == 3) {
-        // boxes 3 (e % 3) .. of 64 rows; the third part's last box would be
+        // boxes 3 (e / 2) .. of 64 rows; the third part's last box would be
         // past the map's 8: it reads zeros, which count as copied bytes too,
         // so its two boxes come one by one
-        const int row = row0 + 64 * (e / 3), part = e % 3;
+        const int row = row0 + 64 * (e % 2), part = e / 2;
         if (part < 2) {
           tma_load_3d(smem_u32(slot), tm_qn, 0, row, 3 * part, qbar);
         } else {
@@ -474,7 +505,7 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
       ++i;
     }
     ++un;
-    for (int vt = u.p0; vt < u.p1 && ok; vt += kCg) {
+    for (int vt = u.p0; vt < u.p1 && ok; vt += kCg, ++jt) {
       if (have_next && vt == pf) {
         const int64_t r0 = static_cast<int64_t>(nx.k.row0) + pr * kRows;
         const int left = nx.k.nrows - pr * kRows, n = left < kRows ? left : kRows;
@@ -487,15 +518,16 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
       const bool have = kCg == 1 || v < u.p1;
       const int y = have ? read_page_id(p, u.k.b, real_page(u.k, v)) * kPage : 0;
       for (int part = 0; part < C::kParts; ++part) {
-        if (!acquire()) {
+        if (!acquire(4 * jt + 3)) {
           ok = false;
           break;
         }
+        if constexpr (C::kParts == 3) bar = smem_u32(&ctrl->kv_full[jt % C::kNTile]);
         if (have) {
-          mbar_expect_tx(bar, static_cast<uint32_t>(C::kSlotS));
+          if (part == 0) mbar_expect_tx(bar, static_cast<uint32_t>(C::kParts * C::kSlotS));
           tma_load_3d(smem_u32(slot), tm_s, 0, y, part * C::kPartBoxes, bar);
           if constexpr (kF8) tma_load_2d(smem_u32(slot + C::kSBoxes * C::kBox), tm_pe, kDL, y, bar);
-        } else {
+        } else if (part == 0) {
           mbar_arrive(bar);
         }
         ++i;
@@ -503,7 +535,7 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
     }
   }
   if (!ok) raise_timeout<kCg>(p, ctrl, kWaitProdS, i);
-  drain_ring<C::kNStS>(ctrl, i, p.timeout_ns);
+  drain_ring<C::kNTile>(ctrl, C::kParts == 3 ? jt : i, p.timeout_ns);
   // the last unit's query rows: a unit cut short by a timeout may not have
   // armed all its bytes, so this wait is bounded too
   if (qloaded) {
@@ -528,7 +560,9 @@ __device__ void produce_o(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
     for (int v = u.p0; v < u.p1; ++v) {
       const int y = read_page_id(p, u.k.b, real_page(u.k, v)) * kPage;
       const int st = static_cast<int>(i % C::kNStO);
-      if (!mbar_wait(smem_u32(&ctrl->kv_empty[st]), ((i / C::kNStO) & 1) ^ 1, abort, p.timeout_ns)) {
+      // with as many P slots as V slots, P's barrier tells both
+      const uint32_t empty = smem_u32(C::kVByP ? &ctrl->p_empty[st] : &ctrl->kv_empty[st]);
+      if (!mbar_wait(empty, ((i / C::kNStO) & 1) ^ 1, abort, p.timeout_ns)) {
         raise_timeout<kCg>(p, ctrl, kWaitProdO, i);
         ok = false;
         break;
@@ -551,26 +585,100 @@ __device__ void produce_o(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
 // are, are NaN already.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) { return b * 128u + (b & 0x00800080u) * 128u; }
 
-// Writes TMEM columns [c0, c1) of one row: bf16 out and lse for a whole
-// block, fp32 partials (normalised O and its lse) for a piece.  Column c of
-// O is latent dimension c, or with kCg = 2 (each PV MMA's N = 256 is half
-// from each CTA of the pair) 256 ((c / 128) % 2) + 128 (c / 256) + c % 128.
+// Column c of O is latent dimension c, or with kCg = 2 (each PV MMA's N = 256
+// is half from each CTA of the pair) 256 ((c / 128) % 2) + 128 (c / 256) + c % 128.
+template <int kCg>
+__device__ __forceinline__ int dim_of(int c) {
+  return kCg == 1 ? c : (((c >> 7) & 1) * 256 + (c >> 8) * 128 + (c & 127));
+}
+
+// Writes a row's log-sum-exp (of the whole block's keys, or of a piece's) and
+// returns the factor of its outputs.
+template <bool kF8>
+__device__ __forceinline__ float store_lse(const Params& p, const Unit& u, int br, bool mine, float m_log2, float l) {
+  const float inv_l = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays NaN
+  if (mine && br < u.k.nrows && u.slot < 2 * p.C) {
+    const float lse_v = l > 0.f ? (m_log2 + __log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
+    if (u.slot < 0) p.lse[static_cast<int64_t>(u.k.row0) + br] = lse_v;
+    else p.lse_part[static_cast<int64_t>(u.slot) * p.BR + br] = lse_v;
+  }
+  return kF8 ? p.kv_scale * 256.f * inv_l : inv_l;  // e4m3 values are in f16 as value / 256
+}
+
+// A warp's 32 rows br0 .. (TMEM lanes), columns [c0, c0 + 256), by way of
+// shared memory: boxes of 32 rows x 64 bytes (64-byte swizzle), two in turn, that
+// TMA writes.  A lane's own stores to its row take a line each: 128 rows of
+// bf16 outputs took 4.9 us that way, half of it with O not yet free for the
+// next block.
+template <bool kF8, int kCg>
+__device__ __forceinline__ void store_staged(const Params& p, const Unit& u, int br0, int c0, uint32_t taddr, float f,
+                                             uint8_t* stage, const CUtensorMap* map) {
+  const int lane = threadIdx.x & 31;
+  const bool whole = u.slot < 0;
+  const int y = whole ? u.k.row0 + br0 : u.slot * p.BR + br0;
+  uint32_t v[2][16];
+  tmem_ld16(taddr + c0, v[0]);
+  tmem_ld16(taddr + c0 + 16, v[1]);
+#pragma unroll 1
+  for (int s = 0; s < 8; ++s) {
+    tmem_wait_ld_tie(v[0]);
+    tmem_wait_ld_tie(v[1]);
+    float x[32];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x[k] = __uint_as_float(v[k >> 4][k & 15]) * f;
+    if (s < 7) {
+      tmem_ld16(taddr + c0 + 32 * s + 32, v[0]);
+      tmem_ld16(taddr + c0 + 32 * s + 48, v[1]);
+    }
+    const int dim = dim_of<kCg>(c0 + 32 * s);
+    auto put = [&](const uint32_t (&w)[16], int buf, int xdim, bool wait) {
+      if (wait) {
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+      }
+      uint8_t* row = stage + buf * 2048 + lane * 64;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        *reinterpret_cast<uint4*>(row + ((c ^ ((lane >> 1) & 3)) << 4)) =
+            make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+      fence_proxy_async_cta();
+      __syncwarp();
+      if (lane == 0) tma_store_2d(map, smem_u32(stage + buf * 2048), xdim, y);
+    };
+    uint32_t w[16];
+    if (whole) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+        w[k] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
+      put(w, s & 1, dim, s >= 2);
+    } else {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(x[16 * h + k]);
+        put(w, h, dim + 16 * h, s >= 1);
+      }
+    }
+  }
+}
+
+// The same for one row from the thread's own stores, columns [c0, c1): bf16
+// out for a whole block, fp32 partials (normalised O) for a piece.
 template <bool kF8, int kCg>
 __device__ __forceinline__ void store_row(const Params& p, const Unit& u, int br, int c0, int c1, uint32_t taddr,
-                                          float m_log2, float l) {
+                                          float f) {
   if (u.slot >= 2 * p.C) {  // cannot happen; a bad schedule never writes out of range
     atomicOr(p.status, MLA_DEV_INTERNAL);
     return;
   }
   const bool real = br < u.k.nrows;
-  const float inv_l = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN sum stays NaN
-  const float f = kF8 ? p.kv_scale * 256.f * inv_l : inv_l;  // e4m3 values are in f16 as value / 256
-  const float lse_v = l > 0.f ? (m_log2 + __log2f(l)) * kLn2 : (l == 0.f ? -INFINITY : l);
   const int64_t orow = static_cast<int64_t>(u.k.row0) + br;
   const int64_t prow = static_cast<int64_t>(u.slot) * p.BR + br;
 #pragma unroll 1
   for (int c = c0; c < c1; c += 32) {
-    const int dim = kCg == 1 ? c : (((c >> 7) & 1) * 256 + (c >> 8) * 128 + (c & 127));
+    const int dim = dim_of<kCg>(c);
     uint32_t v[2][16];
     tmem_ld16(taddr + c, v[0]);
     tmem_ld16(taddr + c + 16, v[1]);
@@ -603,10 +711,6 @@ __device__ __forceinline__ void store_row(const Params& p, const Unit& u, int br
         }
     }
   }
-  if (real && c0 == 0) {
-    if (u.slot < 0) p.lse[orow] = lse_v;
-    else p.lse_part[prow] = lse_v;
-  }
 }
 
 // --------------------------------------------------------------- attention
@@ -614,11 +718,16 @@ template <bool kF8, int kCg>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_chunk_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_s,
                      const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_pe,
-                     const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qp) {
+                     const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qp,
+                     const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_part) {
   using C = Cfg<kF8, kCg>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* data = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* data = smem_raw;
+  if ((smem_u32(data) & 1023u) != 0u) {  // the same in every CTA; swizzled tiles need it
+    griddep_wait();
+    if (threadIdx.x == 0) atomicOr(p.status, MLA_DEV_INTERNAL);
+    return;
+  }
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(data + ((C::kData + 15) & ~15));
   // ranks 0 .. kCg - 1: S CTAs; kCg .. 2 kCg - 1: O CTAs; pr: place in the pair
   const uint32_t rank = cluster_ctarank();
@@ -642,6 +751,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctrl->s_empty[i]), kCg == 1 ? 4 : 16);
     }
     mbar_init(smem_u32(&ctrl->q_full), 8 * kCg);
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctrl->q_part[i]), 8);
     for (int i = 0; i < kMaxP; ++i) {
       mbar_init(smem_u32(&ctrl->p_full[i]), 1);
       mbar_init(smem_u32(&ctrl->p_empty[i]), 1);
@@ -655,7 +765,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctrl->o_empty), C::kCorrWarps);
     mbar_init(smem_u32(&ctrl->resc_req), 1);
     mbar_init(smem_u32(&ctrl->resc_done), C::kCorrWarps);
-    mbar_init(smem_u32(&ctrl->ml_full), 8);
+    mbar_init(smem_u32(&ctrl->ml_full), kCg == 1 ? 8 : 1);  // a pair: by bytes
     mbar_init(smem_u32(&ctrl->ml_empty), C::kCorrWarps);
     mbar_init(smem_u32(&ctrl->drain), 1);
     ctrl->abort = 0;
@@ -693,19 +803,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // The leader's warp issues QK for the pair (the whole warp runs the
       // loop, one elected lane issues); the other CTA's warp passes on that
-      // its entries have landed.  Every entry's barriers are waited for, the
-      // query entries' too, so that no phase is ever missed.
+      // its pages have landed.  Every barrier's every phase is waited for, the
+      // query entries' too, so that none is ever missed.
       UnitIter it;
       it.init(p, cid);
       Unit u;
       uint32_t i = 0, j = 0, un = 0;  // ring entries, tiles, units
       bool ok = true;
       int why = 0;
-      // entry i of this CTA and, for the leader, of the other one have
-      // landed; `extra` is polled along with them (0: nothing)
-      auto landed = [&](uint32_t extra, uint32_t extra_parity) -> bool {
-        const int st = static_cast<int>(i % C::kNStS);
-        const uint32_t ph = (i / C::kNStS) & 1;
+      // barrier n (an entry's, a tile's) of this CTA and, for the leader, of
+      // the other one; `extra` is polled along with them (0: nothing)
+      auto landed = [&](uint32_t n, uint32_t extra, uint32_t extra_parity) -> bool {
+        const int st = static_cast<int>(n % C::kNTile);
+        const uint32_t ph = (n / C::kNTile) & 1;
         if (!mbar_wait_all_warp(smem_u32(&ctrl->kv_full[st]), ph,
                                 kCg == 2 && leader ? smem_u32(&ctrl->peer_kv[st]) : 0u, ph, extra, extra_parity, 0u, 0u,
                                 abort, p.timeout_ns)) {
@@ -717,15 +827,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       while (ok && it.next(u)) {
         const int qe = C::q_entries(u.k.nrows);
-        for (int e = 0; e < qe && ok; ++e, ++i) ok = landed(0u, 0u);
-        if (!ok) break;
+        if constexpr (C::kParts == 3) {
+          i += qe;
+        } else {
+          for (int e = 0; e < qe && ok; ++e, ++i) ok = landed(i, 0u, 0u);
+          if (!ok) break;
+        }
         if (leader) {
           if (!mbar_wait_warp(smem_u32(&ctrl->q_full), un & 1, abort, p.timeout_ns)) {
             ok = false;
             why = kWaitQFull;
             break;
           }
-          if (lane == 0)  // the query entries' slots go back to the producers
+          if (lane == 0 && C::kParts == 1)  // the query entries' slots go back to the producers
             for (int e = qe; e > 0; --e) {
               const uint32_t bar = smem_u32(&ctrl->kv_empty[(i - e) % C::kNStS]);
               mbar_arrive(bar);
@@ -735,21 +849,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const uint32_t qpe = smem_u32(ring + C::kQPeOff + (kF8 ? 0 : (un & 1) * C::kQPeTile));
         ++un;
-        for (int vt = u.p0; vt < u.p1 && ok; vt += kCg, ++j) {
+        for (int vt = u.p0; vt < u.p1; vt += kCg, ++j, i += C::kParts) {
           const int sb = static_cast<int>(j % C::kNSB);
           const uint32_t dcol = tmem + C::kSCol0 + sb * C::kTileCols;
+          if (!landed(C::kParts == 3 ? j : i, leader ? smem_u32(&ctrl->s_empty[sb]) : 0u, ((j / C::kNSB) & 1) ^ 1)) {
+            ok = false;
+            break;
+          }
+          if (!leader) continue;
+          tc_fence_after();
+          if constexpr (!kF8) {
 #pragma unroll
-          for (int part = 0; part < C::kParts; ++part, ++i) {
-            if (!landed(leader && part == 0 ? smem_u32(&ctrl->s_empty[sb]) : 0u, ((j / C::kNSB) & 1) ^ 1)) {
-              ok = false;
-              break;
-            }
-            if (!leader) continue;
-            tc_fence_after();
-            const int st = static_cast<int>(i % C::kNStS);
-            const uint32_t slot_addr = smem_u32(ring + st * C::kSlotS);
-            const uint64_t dlat = smem_desc(slot_addr, 16, 1024, kSwizzle128B);
-            if constexpr (!kF8) {
+            for (int part = 0; part < C::kParts; ++part) {
+              const uint64_t dlat = smem_desc(smem_u32(ring + ((i + part) % C::kNStS) * C::kSlotS), 16, 1024, kSwizzle128B);
 #pragma unroll
               for (int d = 0; d < C::kPartBoxes; ++d)
 #pragma unroll
@@ -762,32 +874,34 @@ __global__ void __launch_bounds__(kThreads, 1)
                   else
                     mma_ts_cg<false, kCg>(dcol, tmem + box * 32 + k * 8, db, C::kIdescQK, (box | k) ? 1u : 0u);
                 }
-            } else {
-              const uint64_t dpe = smem_desc(slot_addr + C::kSBoxes * C::kBox, 16, 512, kSwizzle64B);
+            }
+          } else {
+            const uint32_t slot_addr = smem_u32(ring + (i % C::kNStS) * C::kSlotS);
+            const uint64_t dlat = smem_desc(slot_addr, 16, 1024, kSwizzle128B);
+            const uint64_t dpe = smem_desc(slot_addr + C::kSBoxes * C::kBox, 16, 512, kSwizzle64B);
 #pragma unroll
-              for (int term = 0; term < 2; ++term) {
-                const uint32_t qcol = tmem + (term ? C::kQLoCol : 0u);
+            for (int term = 0; term < 2; ++term) {
+              const uint32_t qcol = tmem + (term ? C::kQLoCol : 0u);
 #pragma unroll
-                for (int d = 0; d < 4; ++d)
+              for (int d = 0; d < 4; ++d)
 #pragma unroll
-                  for (int k = 0; k < 4; ++k)
-                    mma_ts_cg<true, kCg>(dcol, qcol + d * 32 + k * 8,
-                                         dlat + static_cast<uint64_t>(d * (C::kBox >> 4) + k * 2), C::kIdescQK,
-                                         (term | d | k) ? 1u : 0u);
+                for (int k = 0; k < 4; ++k)
+                  mma_ts_cg<true, kCg>(dcol, qcol + d * 32 + k * 8,
+                                       dlat + static_cast<uint64_t>(d * (C::kBox >> 4) + k * 2), C::kIdescQK,
+                                       (term | d | k) ? 1u : 0u);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  if constexpr (C::kPeSmem)
-                    mma_ss_f8_cg<kCg>(dcol, smem_desc(qpe + term * C::kQPeTile, 128, 512, kSwizzleNone) +
-                                                static_cast<uint64_t>(k * (256 >> 4)),
-                                      dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
-                  else
-                    mma_ts_cg<true, kCg>(dcol, qcol + 128 + k * 8, dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
-                }
+              for (int k = 0; k < 2; ++k) {
+                if constexpr (C::kPeSmem)
+                  mma_ss_f8_cg<kCg>(dcol, smem_desc(qpe + term * C::kQPeTile, 128, 512, kSwizzleNone) +
+                                              static_cast<uint64_t>(k * (256 >> 4)),
+                                    dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
+                else
+                  mma_ts_cg<true, kCg>(dcol, qcol + 128 + k * 8, dpe + static_cast<uint64_t>(k * 2), C::kIdescQK, 1u);
               }
             }
-            mma_commit_cg<kCg>(smem_u32(&ctrl->kv_empty[st]), kMaskS);
           }
-          if (ok && leader) mma_commit_cg<kCg>(smem_u32(&ctrl->s_full[sb]), kMaskS);
+          if (C::kParts == 1) mma_commit_cg<kCg>(smem_u32(&ctrl->kv_empty[i % C::kNStS]), kMaskS);
+          mma_commit_cg<kCg>(smem_u32(&ctrl->s_full[sb]), kMaskS);
         }
       }
       if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
@@ -847,9 +961,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else if constexpr (kF8) {
           uint8_t* pe_tile = data + C::kQPeOff;
           qs = q_row_e4m3<kCg>(ring, i, r, tmem + lane_base, pe_tile, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9);
+        } else if constexpr (C::kParts == 3) {
+          auto part_read = [&](int part) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&ctrl->q_part[part]));
+          };
+          q_row_bf16<kCg, 12>(ring, i, r, tmem + lane_base, 12 * gg);
+          part_read(0);
+          q_row_bf16<kCg, 12>(ring, i, r, tmem + lane_base, 24 + 12 * gg);
+          part_read(1);
+          q_row_bf16<kCg, 8>(ring, i, r, tmem + lane_base, 48 + 8 * gg);
+          part_read(2);
+          tmem_wait_st();
         } else {
-          constexpr int kN = C::kPeSmem ? 32 : 36;
-          q_row_bf16<kCg, kN>(ring, i, r, tmem + lane_base, kN * gg);
+          q_row_bf16<kCg, 36>(ring, i, r, tmem + lane_base, 36 * gg);
+          tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
@@ -980,11 +1106,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           why = kWaitMlEmpty;
           break;
         }
-        float* ml = reinterpret_cast<float*>(data + C::kMlOff);
-        ml[4 * r + 2 * gg] = m_run;
-        ml[4 * r + 2 * gg + 1] = l;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mlfull_remote);
+        if constexpr (kCg == 2) {
+          // straight into the staging of the two O warps that store the row:
+          // an arrival that releases local stores would wait for P's as well
+          const uint32_t dst = p_remote + C::kStageOff + (warp & 3) * C::kStage + lane * 16 + gg * 8;
+          st_async_v2(dst, __float_as_uint(m_run), __float_as_uint(l), mlfull_remote);
+          st_async_v2(dst + 4 * C::kStage, __float_as_uint(m_run), __float_as_uint(l), mlfull_remote);
+        } else {
+          float* ml = reinterpret_cast<float*>(data + C::kMlOff);
+          ml[4 * r + 2 * gg] = m_run;
+          ml[4 * r + 2 * gg + 1] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mlfull_remote);
+        }
         ++un;
         j0 += static_cast<uint32_t>(u.p1 - u.p0);
       }
@@ -1007,8 +1141,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t j = 0, un = 0, nreq = 0;
       bool ok = true;
       int why = 0;
-      if (lane == 0)
+      if (lane == 0) {
         for (int k = 0; k < C::kNP; ++k) mbar_expect_tx(smem_u32(&ctrl->p_full[k]), C::kPTx);
+        if (kCg == 2) mbar_expect_tx(smem_u32(&ctrl->ml_full), C::kMlTx);
+      }
       __syncwarp();
       while (ok && it.next(u)) {
         for (int vp = u.p0; vp < u.p1; ++vp, ++j) {
@@ -1074,7 +1210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               mma_ss_cg<kCg>(tmem + h * 256, dp + static_cast<uint64_t>(k * (2 * C::kPLbo >> 4)),
                              dv + static_cast<uint64_t>((h * (C::kVBoxes / 2) * C::kVBox + k * 2048) >> 4),
                              C::kIdescPV, (first && k == 0) ? 0u : 1u);
-          mma_commit_cg<kCg>(kF8 ? smem_u32(&ctrl->v_empty[vs & 3]) : smem_u32(&ctrl->kv_empty[vs]), kMaskO);
+          if (!C::kVByP) mma_commit_cg<kCg>(smem_u32(kF8 ? &ctrl->v_empty[vs & 3] : &ctrl->kv_empty[vs]), kMaskO);
           mma_commit_cg<kCg>(smem_u32(&ctrl->p_empty[ps]), kMaskAll);
           if (vp == u.p1 - 1) mma_commit_cg<kCg>(smem_u32(&ctrl->o_full), kMaskO);
         }
@@ -1103,6 +1239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const float* factors = reinterpret_cast<const float*>(data + C::kRefOff);
       const uint32_t ml_remote = mapa(smem_u32(data + C::kMlOff), static_cast<uint32_t>(pr));
+      uint8_t* stage = data + C::kStageOff + (warp - 4) * C::kStage;
       const uint32_t mlempty_remote = mapa(smem_u32(&ctrl->ml_empty), static_cast<uint32_t>(pr));
       const int br = pr * kRows + r;
       UnitIter it;
@@ -1217,21 +1354,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const float m0 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r));
-        const float l0 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 4));
-        const float m1 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 8));
-        const float l1 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 12));
+        float m0, l0, m1, l1;
+        if constexpr (kCg == 2) {
+          const float4 ml = *reinterpret_cast<const float4*>(stage + lane * 16);
+          m0 = ml.x; l0 = ml.y; m1 = ml.z; l1 = ml.w;
+          if (warp == 4 && lane == 0) mbar_expect_tx(mf, C::kMlTx);  // before the S CTA may send the next unit's
+        } else {
+          m0 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r));
+          l0 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 4));
+          m1 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 8));
+          l1 = __uint_as_float(ld_cluster_u32(ml_remote + 16 * r + 12));
+        }
         const float m_log2 = fmaxf(m0, m1);
         const float l = l0 * ex2_approx(m0 - m_log2) + l1 * ex2_approx(m1 - m_log2);
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mlempty_remote);
-        store_row<kF8, kCg>(p, u, br, c0, c0 + kCols, tmem + lane_base, m_log2, l);
+        const int br0 = br - lane;  // the warp's first row
+        bool staged = false;
+        if constexpr (C::kStage >= 4096) staged = u.slot >= 0 ? u.slot < 2 * p.C : br0 + 32 <= u.k.nrows;
+        if (!staged && lane == 0) mbar_arrive_cluster(mlempty_remote);
+        const float f = store_lse<kF8>(p, u, br, c0 == 0, m_log2, l);
+        if (staged) {
+          store_staged<kF8, kCg>(p, u, br0, c0, tmem + lane_base, f, stage, u.slot < 0 ? &tm_out : &tm_part);
+        } else {
+          store_row<kF8, kCg>(p, u, br, c0, c0 + kCols, tmem + lane_base, f);
+        }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctrl->o_empty));
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctrl->o_empty));
+          if (staged) {  // the S CTA's sums of the next unit come into the staging
+            bulk_wait_read<0>();
+            mbar_arrive_cluster(mlempty_remote);
+          }
+        }
         ++un;
       }
       if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
+      if (lane == 0 && C::kStage >= 4096) bulk_wait_all();
     }
   }
 

@@ -417,6 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float qs = 1.f;
       if constexpr (kF8) qs = chunk::q_row_e4m3<1>(ring, i, r, tmem + lane_base, nullptr, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9);
       else chunk::q_row_bf16<1, 36>(ring, i, r, tmem + lane_base, 36 * gg);
+      tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl->q_full));

@@ -43,6 +43,7 @@ struct Cfg {
   static constexpr int kPartBoxes = kSBoxes / kParts;
   static constexpr int kSlotS = kPartBoxes * kBox + kPeBytes;
   static constexpr int kNStS = kF8 ? (kCg == 1 ? 6 : 5) : (kCg == 1 ? 3 : 7);
+  static constexpr int kNTile = kParts == 3 ? 3 : kNStS;  // barriers that pages land on: tiles the ring can hold, or entries
   // TMEM columns: queries, then kNSB score buffers of a tile each.  A pair
   // keeps the rope part of the queries in shared memory (A of its QK steps),
   // which leaves 256 columns for two tiles of 128 keys.
@@ -52,8 +53,8 @@ struct Cfg {
   static constexpr uint32_t kTileCols = 64 * kCg;
   static constexpr uint32_t kQLoCol = kCg == 1 ? 144 : 128;  // e4m3: the lo terms' first column
   // ring entries of a block's bf16 query rows.  bf16 pair: q_nope of 64 rows
-  // like a page (parts of 3, 3 and 2 boxes), q_pe straight into its tile;
-  // else kQRows rows with q_pe as a ninth box
+  // like a page (parts of 3, 3 and 2 boxes; entry 2 part + half), q_pe
+  // straight into its tile; else kQRows rows with q_pe as a ninth box
   static constexpr int kQRows = kParts == 3 ? 64 : kSlotS / 1152;
   static constexpr int kQEntries = kParts * kRows / kQRows;
   // O CTA: 512 / kCg latent dimensions of every page
@@ -68,6 +69,7 @@ struct Cfg {
   static constexpr int kNStO = kF8 ? kNRaw : kNV;        // slots that TMA fills
   static constexpr int kSlotO = kF8 ? kSlotRaw : kSlotV;
   static constexpr int kNP = kCg == 1 ? 2 : 4;           // P slots
+  static constexpr bool kVByP = !kF8 && kNP == kNV;      // a V slot is free when its page's P slot is
   static constexpr int kPBytes = kRows * kPage * 2;
   // P: K-major without swizzle, core matrices of 8 rows x 16 bytes; the
   // 16-byte chunk c of row r at (r / 8) * 1024 + c * 128 + (r % 8) * 16
@@ -82,15 +84,20 @@ struct Cfg {
   static constexpr int kMlOff = kQPeOff + (kPeSmem ? 2 * kQPeTile : 0);  // S: (m0, l0, m1, l1)[128]
   static constexpr int kPubOff = kMlOff + kRows * 16;    // S: row references of the last 4 pages
   static constexpr int kDataS = kPubOff + 4 * kRows * 8;
-  static constexpr int kVOff = kNP * kPBytes;            // O: P slots, V ring, raw ring, row factors, flags
+  static constexpr int kVOff = kNP * kPBytes;            // O: P slots, V ring, raw ring, staging, row factors, flags
   static constexpr int kRawOff = kVOff + kNV * kSlotV;
-  static constexpr int kRefOff = kRawOff + kNRaw * kSlotRaw;
+  static constexpr int kStageOff = kRawOff + kNRaw * kSlotRaw;
+  // per row warp of a pair's O CTA: its rows' sums as they come from the S
+  // CTA, then (bf16) two boxes of outputs on their way to memory
+  static constexpr int kStage = kCg == 1 ? 0 : (kF8 ? 512 : 4096);
+  static constexpr int kRefOff = kStageOff + 8 * kStage;
   static constexpr int kFlagOff = kRefOff + kNP * kRows * 4;
   static constexpr int kDataO = kFlagOff + kNP * 16;
   static constexpr int kData = kDataS > kDataO ? kDataS : kDataO;
-  static constexpr int kSmem = 1024 + ((kData + 15) & ~15) + kCtrlBytes;
+  static constexpr int kSmem = ((kData + 15) & ~15) + kCtrlBytes;  // at a 1024-byte boundary
   // bytes an S CTA sends per page: every row's P and O factor, a flag word per softmax warp
   static constexpr uint32_t kPTx = kRows * (kPage * 2 + 4) + 4 * 4;
+  static constexpr uint32_t kMlTx = kRows * 16 * 2;  // per unit: every row's two (m, l), for the two warps of the row
   static constexpr int kCorrWarps = 8;  // O rows are corrected and stored by 8 warps, a half of the columns each
   static_assert(kSmem <= 232448, "shared memory budget");
   // Ring entries of a block with `rows` rows in the first CTA (the pair's CTAs
@@ -113,12 +120,13 @@ template <bool kF8, int kCg>
 __device__ __forceinline__ const uint8_t* q_chunk(const uint8_t* ring, uint32_t i, int r, int c) {
   using C = Cfg<kF8, kCg>;
   const int e = r / C::kQRows, rq = r % C::kQRows, box = c >> 3;
-  const uint32_t entry = C::kParts == 3 ? i + 3 * e + box / 3 : i + e;
+  const uint32_t entry = C::kParts == 3 ? i + 2 * (box / 3) + e : i + e;
   const int in_slot = C::kParts == 3 ? box % 3 : box;
   return ring + (entry % C::kNStS) * C::kSlotS + in_slot * (C::kQRows * 128) + rq * 128 + (((c & 7) ^ (rq & 7)) << 4);
 }
 
-// Query row r into TMEM lane r (bf16): 16-byte chunks [c0, c0 + kN).
+// Query row r into TMEM lane r (bf16): 16-byte chunks [c0, c0 + kN).  The
+// shared memory has been read when it returns; the stores need tmem_wait_st.
 template <int kCg, int kN>
 __device__ __forceinline__ void q_row_bf16(const uint8_t* ring, uint32_t i, int r, uint32_t taddr, int c0) {
   constexpr int kStep = kN % 12 == 0 ? 12 : 8;
@@ -136,7 +144,6 @@ __device__ __forceinline__ void q_row_bf16(const uint8_t* ring, uint32_t i, int 
       tmem_st16(taddr + (c0 + c + 4 * s4) * 4, w);
     }
   }
-  tmem_wait_st();
 }
 
 // The same for an e4m3 cache: the row as hi + lo e4m3 terms of q / scale.
