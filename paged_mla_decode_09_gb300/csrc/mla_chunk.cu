@@ -142,7 +142,7 @@ struct Maps {
 
 // s: an S CTA's part of a page; o: an O CTA's dimensions of a page; pe: the
 // e4m3 k_pe rows, or (bf16 pair) single boxes of q_nope; qn, qp: query rows;
-// out, part (bf16 pair): where the outputs and the partial ones go.
+// out, part (pairs): where the outputs and the partial ones go.
 template <bool kF8, int kCg>
 bool make_maps(const void* q_nope, const void* q_pe, const void* kv, const Shape& s, const Params& p, Maps* m) {
   using C = Cfg<kF8, kCg>;
@@ -157,7 +157,7 @@ bool make_maps(const void* q_nope, const void* q_pe, const void* kv, const Shape
   if (ok && kF8) ok = map2(&m->pe, kv, krows, 576, 1, 64, 64, CU_TENSOR_MAP_SWIZZLE_64B);
   if (ok && kPair16) ok = map2(&m->pe, q_nope, qrows, 512, 2, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B);
   m->out = m->part = m->s;
-  if (ok && kPair16)
+  if (ok && kCg == 2)
     ok = map2(&m->out, p.out, qrows, 512, 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B) &&
          map2(&m->part, p.o_part, 2ll * p.C * p.BR, 512, 4, 16, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   return ok;

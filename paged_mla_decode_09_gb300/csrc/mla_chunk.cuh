@@ -73,6 +73,7 @@ struct __align__(8) Ctrl {
   uint64_t s_full[kMaxSB];
   uint64_t s_empty[kMaxSB];         // S leader: both CTAs read the S buffer
   uint64_t q_full;               // S leader: queries in TMEM (both CTAs)
+  uint64_t qs_full[2];           // e4m3: the unit's query scales (alternating units, as the ring may hold two)
   uint64_t q_part[3];            // bf16 pair: a part of the queries has been read
   uint64_t p_full[kMaxP];
   uint64_t p_empty[kMaxP];
@@ -381,7 +382,7 @@ __device__ __forceinline__ int real_page(const Block& k, int v) { return v + (v 
 enum WaitTag : int {
   kWaitProdS = 101, kWaitProdO, kWaitQFull, kWaitKvS, kWaitPeerKv, kWaitSFull, kWaitPEmpty, kWaitMlEmpty, kWaitPage,
   kWaitRescDone, kWaitPeerPv, kWaitPvPrev, kWaitOFull, kWaitMlFull, kWaitSPrev, kWaitQEntry, kWaitPub, kWaitRaw,
-  kWaitVEmpty
+  kWaitVEmpty, kWaitQScale
 };
 
 template <int kCg>
@@ -576,15 +577,6 @@ __device__ void produce_o(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
   drain_ring<C::kNStO>(ctrl, i, p.timeout_ns);
 }
 
-// Two e4m3 codes, in the low bytes of the halves, as f16 values times 2^-8:
-// moving exponent and mantissa to f16's place (exponent bias 15 instead of 7)
-// scales every finite code by exactly 2^-8, subnormals included; the outputs'
-// scale puts it back.  (b & 127) << 7 | (b & 128) << 8 = (b + (b & 128)) * 128,
-// half of it on the multiply pipe; the conversion instruction took twice as
-// long.  A NaN code becomes 1.875: its key's scores, from the codes as they
-// are, are NaN already.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) { return b * 128u + (b & 0x00800080u) * 128u; }
-
 // Column c of O is latent dimension c, or with kCg = 2 (each PV MMA's N = 256
 // is half from each CTA of the pair) 256 ((c / 128) % 2) + 128 (c / 256) + c % 128.
 template <int kCg>
@@ -606,13 +598,14 @@ __device__ __forceinline__ float store_lse(const Params& p, const Unit& u, int b
 }
 
 // A warp's 32 rows br0 .. (TMEM lanes), columns [c0, c0 + 256), by way of
-// shared memory: boxes of 32 rows x 64 bytes (64-byte swizzle), two in turn, that
-// TMA writes.  A lane's own stores to its row take a line each: 128 rows of
+// shared memory: boxes of 32 rows x 64 bytes (64-byte swizzle), kBufs in turn,
+// that TMA writes.  A lane's own stores to its row take a line each: 128 rows of
 // bf16 outputs took 4.9 us that way, half of it with O not yet free for the
 // next block.
 template <bool kF8, int kCg>
 __device__ __forceinline__ void store_staged(const Params& p, const Unit& u, int br0, int c0, uint32_t taddr, float f,
                                              uint8_t* stage, const CUtensorMap* map) {
+  constexpr int kBufs = Cfg<kF8, kCg>::kStage > 2048 ? 2 : 1;
   const int lane = threadIdx.x & 31;
   const bool whole = u.slot < 0;
   const int y = whole ? u.k.row0 + br0 : u.slot * p.BR + br0;
@@ -633,7 +626,7 @@ __device__ __forceinline__ void store_staged(const Params& p, const Unit& u, int
     const int dim = dim_of<kCg>(c0 + 32 * s);
     auto put = [&](const uint32_t (&w)[16], int buf, int xdim, bool wait) {
       if (wait) {
-        if (lane == 0) bulk_wait_read<1>();
+        if (lane == 0) bulk_wait_read<kBufs - 1>();
         __syncwarp();
       }
       uint8_t* row = stage + buf * 2048 + lane * 64;
@@ -652,13 +645,13 @@ __device__ __forceinline__ void store_staged(const Params& p, const Unit& u, int
         const __nv_bfloat162 b2 = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
         w[k] = *reinterpret_cast<const uint32_t*>(&b2);
       }
-      put(w, s & 1, dim, s >= 2);
+      put(w, s % kBufs, dim, s >= kBufs);
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(x[16 * h + k]);
-        put(w, h, dim + 16 * h, s >= 1);
+        put(w, h % kBufs, dim + 16 * h, 2 * s + h >= kBufs);
       }
     }
   }
@@ -752,6 +745,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&ctrl->q_full), 8 * kCg);
     for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctrl->q_part[i]), 8);
+    for (int i = 0; i < 2; ++i) mbar_init(smem_u32(&ctrl->qs_full[i]), 2);
     for (int i = 0; i < kMaxP; ++i) {
       mbar_init(smem_u32(&ctrl->p_full[i]), 1);
       mbar_init(smem_u32(&ctrl->p_empty[i]), 1);
@@ -861,7 +855,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (!kF8) {
 #pragma unroll
             for (int part = 0; part < C::kParts; ++part) {
-              const uint64_t dlat = smem_desc(smem_u32(ring + ((i + part) % C::kNStS) * C::kSlotS), 16, 1024, kSwizzle128B);
+              const uint32_t slot_addr = smem_u32(ring + ((i + part) % C::kNStS) * C::kSlotS);
+              const uint64_t dlat = smem_desc(slot_addr, 16, 1024, kSwizzle128B);
 #pragma unroll
               for (int d = 0; d < C::kPartBoxes; ++d)
 #pragma unroll
@@ -915,6 +910,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
+    } else if (kF8 && warp < 4) {
+      // ---- warps 2 and 3: every row's query scale, while the row warps are
+      // still at the unit before (two buffers: the next unit's queries come
+      // into the ring after this unit's are in TMEM)
+      UnitIter it;
+      it.init(p, cid);
+      Unit u;
+      uint32_t i = 0, un = 0;
+      bool ok = true;
+      float* scales = reinterpret_cast<float*>(data + C::kQsOff);
+      while (it.next(u)) {
+        ok = mbar_wait_warp<false, true>(smem_u32(&ctrl->q_bar[un & 1]), (un >> 1) & 1, abort, p.timeout_ns);
+        if (!ok) break;
+        const int qe = C::q_entries(u.k.nrows);
+        for (int r = (warp - 2) * 64 + lane; r < (warp - 1) * 64; r += 32)
+          if (r < qe * C::kQRows) scales[(un & 1) * kRows + r] = q_row_scale<kCg>(ring, i, r);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->qs_full[un & 1]));
+        i += qe + C::kParts * static_cast<uint32_t>((u.p1 - u.p0 + kCg - 1) / kCg);
+        ++un;
+      }
+      if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, kWaitQScale, un);
     } else if (warp >= 4) {
       // ---- softmax: thread r of group gg (warps 4-7: 0, warps 8-11: 1) takes
       // row r of this CTA, the groups alternate pages (tiles of one page, or
@@ -953,6 +970,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           why = kWaitQEntry;
           break;
         }
+        if (kF8 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->qs_full[un & 1]), (un >> 1) & 1, abort, p.timeout_ns)) {
+          ok = false;
+          why = kWaitQScale;
+          break;
+        }
         float qs = 1.f;
         const int qe = C::q_entries(u.k.nrows);
         // (rows past the block's entries keep what TMEM holds: their results go nowhere)
@@ -960,7 +982,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!loads) {
         } else if constexpr (kF8) {
           uint8_t* pe_tile = data + C::kQPeOff;
-          qs = q_row_e4m3<kCg>(ring, i, r, tmem + lane_base, pe_tile, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9);
+          qs = reinterpret_cast<const float*>(data + C::kQsOff)[(un & 1) * kRows + r];
+          q_row_e4m3<kCg>(ring, i, r, tmem + lane_base, pe_tile, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9, qs);
         } else if constexpr (C::kParts == 3) {
           auto part_read = [&](int part) {
             __syncwarp();
@@ -1370,7 +1393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         const int br0 = br - lane;  // the warp's first row
         bool staged = false;
-        if constexpr (C::kStage >= 4096) staged = u.slot >= 0 ? u.slot < 2 * p.C : br0 + 32 <= u.k.nrows;
+        if constexpr (C::kStage > 0) staged = u.slot >= 0 ? u.slot < 2 * p.C : br0 + 32 <= u.k.nrows;
         if (!staged && lane == 0) mbar_arrive_cluster(mlempty_remote);
         const float f = store_lse<kF8>(p, u, br, c0 == 0, m_log2, l);
         if (staged) {
@@ -1390,7 +1413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++un;
       }
       if (!ok && lane == 0) raise_timeout<kCg>(p, ctrl, why, j);
-      if (lane == 0 && C::kStage >= 4096) bulk_wait_all();
+      if (lane == 0 && C::kStage > 0) bulk_wait_all();
     }
   }
 

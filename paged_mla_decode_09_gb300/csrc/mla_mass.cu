@@ -415,9 +415,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl = -l * kLog2e;
       }
       float qs = 1.f;
-      if constexpr (kF8) qs = chunk::q_row_e4m3<1>(ring, i, r, tmem + lane_base, nullptr, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9);
-      else chunk::q_row_bf16<1, 36>(ring, i, r, tmem + lane_base, 36 * gg);
-      tmem_wait_st();
+      if constexpr (kF8) {
+        qs = chunk::q_row_scale<1>(ring, i, r);
+        chunk::q_row_e4m3<1>(ring, i, r, tmem + lane_base, nullptr, gg == 0 ? 0 : 5, gg == 0 ? 5 : 9, qs);
+      } else {
+        chunk::q_row_bf16<1, 36>(ring, i, r, tmem + lane_base, 36 * gg);
+        tmem_wait_st();
+      }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctrl->q_full));
@@ -608,16 +612,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       // per key tile its pages (ring entries that complete on q_bar), then
-      // the request's row tiles
-      uint32_t i = 0;
-      auto acquire = [&]() -> bool {
-        return mbar_wait(smem_u32(&ctrl->kv_empty[i % kSlots]), ((i / kSlots) & 1) ^ 1, abort, p.timeout_ns);
+      // the request's row tiles.  An entry's slot is free once the rows that
+      // it held are scored (s_full) or the keys are in TMEM (q_full): no
+      // commit of their own (a commit and its wait cost the issuing warp
+      // about as long as four MMAs).
+      uint32_t i = 0, j = 0;
+      uint32_t held[kSlots] = {0, 0, 0};  // entries i - 3, i - 2, i - 1: 2 tile, or 2 unit + 1
+      auto acquire = [&](uint32_t what) -> bool {
+        if (i >= kSlots) {
+          const uint32_t k = held[0] >> 1;
+          if (!mbar_wait(smem_u32(held[0] & 1u ? &ctrl->q_full : &ctrl->s_full[k % 3]),
+                         (held[0] & 1u ? k : k / 3) & 1, abort, p.timeout_ns))
+            return false;
+        }
+        held[0] = held[1];
+        held[1] = held[2];
+        held[2] = what;
+        return true;
       };
       while (ok && it.next(u)) {
         const uint32_t qbar = smem_u32(&ctrl->q_bar[un & 1]);
         const int pages = u.t0 + kPage < u.L ? 2 : 1;
         for (int e = 0; e < 2; ++e, ++i) {
-          if (!acquire()) {
+          if (!acquire(2 * un + 1)) {
             ok = false;
             break;
           }
@@ -634,8 +651,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if constexpr (kF8) tma_load_2d(slot + 4 * 8192, &tm_pe, kDL, pid * kPage, qbar);
         }
         ++un;
-        for (int n = first; n < all_tiles && ok; n += step, ++i) {
-          if (!acquire()) {
+        for (int n = first; n < all_tiles && ok; n += step, ++i, ++j) {
+          if (!acquire(2 * j)) {
             ok = false;
             break;
           }
@@ -672,11 +689,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         why = kWaitQFull;
         break;
       }
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&ctrl->kv_empty[(i - 2) % kSlots]));
-        mbar_arrive(smem_u32(&ctrl->kv_empty[(i - 1) % kSlots]));
-      }
-      __syncwarp();
       ++un;
       for (int n = first; n < all_tiles; n += step, ++j, ++i) {
         const int st = static_cast<int>(i % kSlots), sb = static_cast<int>(j % 3);
@@ -695,7 +707,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k)
             mma_ts_e<false>(dcol, tmem + d * 32 + k * 8, dq + static_cast<uint64_t>(d * (8192 >> 4) + k * 2),
                             C::kIdescQK, (d | k) ? 1u : 0u);
-        mma_commit_e(smem_u32(&ctrl->kv_empty[st]));
         mma_commit_e(smem_u32(&ctrl->s_full[sb]));
       }
     }

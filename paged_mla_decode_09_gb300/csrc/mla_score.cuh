@@ -17,7 +17,7 @@ constexpr int kPage = 64;
 constexpr int kDL = 512;
 constexpr int kDR = 64;
 constexpr int kRows = 128;    // rows per CTA
-// warps: 0 TMA, 1 MMA, 2 TMEM alloc, 3 idle, 4-11 row warps
+// warps: 0 TMA, 1 MMA, 2 TMEM alloc, 4-11 row warps (2, 3: query scales of an e4m3 cache, -lse of the mass)
 constexpr int kThreads = 384;
 constexpr int kMaxSB = 3;      // S buffers
 constexpr int kCtrlBytes = 640;
@@ -83,13 +83,15 @@ struct Cfg {
   static constexpr int kQPeTile = kF8 ? 8192 : 16384;
   static constexpr int kMlOff = kQPeOff + (kPeSmem ? 2 * kQPeTile : 0);  // S: (m0, l0, m1, l1)[128]
   static constexpr int kPubOff = kMlOff + kRows * 16;    // S: row references of the last 4 pages
-  static constexpr int kDataS = kPubOff + 4 * kRows * 8;
+  static constexpr int kQsOff = kPubOff + 4 * kRows * 8;  // S, e4m3: two units' query scales
+  static constexpr int kDataS = kQsOff + (kF8 ? 2 * kRows * 4 : 0);
   static constexpr int kVOff = kNP * kPBytes;            // O: P slots, V ring, raw ring, staging, row factors, flags
   static constexpr int kRawOff = kVOff + kNV * kSlotV;
   static constexpr int kStageOff = kRawOff + kNRaw * kSlotRaw;
   // per row warp of a pair's O CTA: its rows' sums as they come from the S
-  // CTA, then (bf16) two boxes of outputs on their way to memory
-  static constexpr int kStage = kCg == 1 ? 0 : (kF8 ? 512 : 4096);
+  // CTA, then boxes (2 KB) of outputs on their way to memory: two, or the one
+  // that fits beside an e4m3 pair's rings
+  static constexpr int kStage = kCg == 1 ? 0 : (kF8 ? 2048 : 4096);
   static constexpr int kRefOff = kStageOff + 8 * kStage;
   static constexpr int kFlagOff = kRefOff + kNP * kRows * 4;
   static constexpr int kDataO = kFlagOff + kNP * 16;
@@ -146,17 +148,20 @@ __device__ __forceinline__ void q_row_bf16(const uint8_t* ring, uint32_t i, int 
   }
 }
 
-// The same for an e4m3 cache: the row as hi + lo e4m3 terms of q / scale.
-// scale is the power of two that puts the row's largest |q| into [2^7, 2^8)
-// (2^-107 at least, so that its reciprocal stays finite); groups of 8 chunks
-// [g0, g1), group 8 being the rope part, which a pair keeps in shared memory
-// (K-major core matrices: the 16-byte chunk c of row r at (r / 8) * 512 +
-// c * 128 + (r % 8) * 16).  Returns scale (NaN for a row with an infinity or
-// a NaN).
+// Two e4m3 codes, in the low bytes of the halves, as f16 values times 2^-8:
+// moving exponent and mantissa to f16's place (exponent bias 15 instead of 7)
+// scales every finite code by exactly 2^-8, subnormals included; the outputs'
+// scale puts it back.  (b & 127) << 7 | (b & 128) << 8 = (b + (b & 128)) * 128,
+// half of it on the multiply pipe; the conversion instruction took twice as
+// long.  A NaN code becomes 1.875: its key's scores, from the codes as they
+// are, are NaN already.
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t b) { return b * 128u + (b & 0x00800080u) * 128u; }
+
+// An e4m3 cache's scale of query row r: the power of two that puts the row's
+// largest |q| into [2^7, 2^8) (2^-107 at least, so that its reciprocal stays
+// finite); NaN for a row with an infinity or a NaN.
 template <int kCg>
-__device__ __forceinline__ float q_row_e4m3(const uint8_t* ring, uint32_t i, int r, uint32_t taddr, uint8_t* pe_tile,
-                                            int g0, int g1) {
-  using C = Cfg<true, kCg>;
+__device__ __forceinline__ float q_row_scale(const uint8_t* ring, uint32_t i, int r) {
   // the largest |q| (a NaN stays), two lanes in each of four chains
   __nv_bfloat162 m4[4];
 #pragma unroll
@@ -172,8 +177,19 @@ __device__ __forceinline__ float q_row_e4m3(const uint8_t* ring, uint32_t i, int
   const uint32_t top = __bfloat16_as_ushort(__hmax_nan(m2.x, m2.y));
   int e = static_cast<int>(top >> 7) - 127 - 7;  // exponent of the scale
   e = e < -107 ? -107 : e;
-  const float scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-  const uint32_t inv_bits = static_cast<uint32_t>(127 - e) << 7;  // 1 / scale, a power of two in bf16 too
+  return __uint_as_float(top >= 0x7F80u ? 0x7FC00000u : static_cast<uint32_t>(e + 127) << 23);
+}
+
+// Query row r into TMEM for an e4m3 cache: the row as hi + lo e4m3 terms of
+// q / scale; groups of 8 chunks [g0, g1), group 8 being the rope part, which a
+// pair keeps in shared memory (K-major core matrices: the 16-byte chunk c of
+// row r at (r / 8) * 512 + c * 128 + (r % 8) * 16).
+template <int kCg>
+__device__ __forceinline__ void q_row_e4m3(const uint8_t* ring, uint32_t i, int r, uint32_t taddr, uint8_t* pe_tile,
+                                           int g0, int g1, float scale) {
+  using C = Cfg<true, kCg>;
+  // 1 / scale, a power of two in bf16 too (of a NaN an infinity: the row's scores are NaN by the scale)
+  const uint32_t inv_bits = (254u - ((__float_as_uint(scale) >> 23) & 255u)) << 7 & 0x7F80u;
   const uint32_t inv_pair = inv_bits | (inv_bits << 16);
   const __nv_bfloat162 inv2 = *reinterpret_cast<const __nv_bfloat162*>(&inv_pair);
 #pragma unroll 1
@@ -218,7 +234,6 @@ __device__ __forceinline__ float q_row_e4m3(const uint8_t* ring, uint32_t i, int
   }
   tmem_wait_st();
   if (C::kPeSmem) fence_proxy_async_cta();  // the rope tile is read by MMAs
-  return top >= 0x7F80u ? __uint_as_float(0x7FC00000u) : scale;
 }
 
 }  // namespace chunk
