@@ -227,6 +227,14 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   // e4m3 pair splits its 256 query rows for ~5 us (ragged chunks 1540 us at 6,
   // 1445 at 15; two drafts over windows 148 and 144)
   p.unit_cost = s.f8 && cg == 2 ? 15 : 6;
+  // what a cut costs, in pages of a cluster's time (~0.75 us): a launch's worth
+  // of latency, a block's partials stored by one CTA, all partials written and
+  // read.  Measured, one block per cluster against even slices: 1 x 16 heads
+  // equal at 5 pages (17.4 us), 1 x 128 at 8, 8 x 64 at 11, 8 x 128 at 15;
+  // 64 x 64 heads x 66 pages (56 in even slices) 78 us against 86
+  const int64_t total_rows = s.T * s.H, rows = total_rows / s.B < p.BR ? total_rows / s.B : p.BR;
+  const int64_t whole = 5 + rows / 24 + total_rows / 600;
+  p.whole_pages = static_cast<int32_t>(whole < 1000 ? whole : 1000);
   p.c2 = mla::host::log2_scale(scale, s.f8 ? kv_scale : 1.f);
   p.kv_scale = s.f8 ? kv_scale : 1.f;
   p.timeout_ns = kTimeoutNs;
@@ -247,9 +255,9 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
     // a column per block that may be cut, at most one per slice boundary; a
     // warp per row, or four where that still fits the SMs about once
     const int64_t cuts = s.blocks() < C ? s.blocks() : C;
-    const int64_t rows = s.T * s.H < p.BR ? s.T * s.H : p.BR;
-    const bool four = cuts * rows * 4 <= 152 * 32;
-    const int64_t items = rows * (four ? 4 : 1);
+    const int64_t most = s.T * s.H < p.BR ? s.T * s.H : p.BR;
+    const bool four = cuts * most * 4 <= 152 * 32;
+    const int64_t items = most * (four ? 4 : 1);
     const dim3 grid(static_cast<unsigned>(cuts),
                     static_cast<unsigned>((items + mla::chunk::kCombineWarps - 1) / mla::chunk::kCombineWarps));
     const dim3 block(mla::chunk::kCombineWarps * 32);

@@ -128,6 +128,7 @@ struct Params {
   int32_t num_pages, max_pages, pt_stride;
   int32_t window, sinks;    // window 0: everything up to the row's own position
   int32_t unit_cost;        // schedule weight of starting a piece, in pages
+  int32_t whole_pages;      // pages that a slice may have beyond the mean for blocks to stay whole
   float c2;                 // scale log2(e) (kv_scale), rounded once: scores in log2 units per product
   float kv_scale;
   uint64_t timeout_ns;
@@ -137,7 +138,9 @@ struct Params {
 // One block of 1024 threads: the row blocks of every request, their page
 // counts, and each cluster's slice of all pages.  Slices are cut in a
 // weighted order (a piece of a block costs unit_cost pages to start), so that
-// clusters with many short blocks get fewer pages.
+// clusters with many short blocks get fewer pages.  A few blocks of about the
+// same length get a cluster each instead: what a cut costs (fp32 partials, the
+// combine) is more than what the even slices gain.
 constexpr int kSchedThreads = 1024;  // or 256 for small batches (fewer warps at each barrier)
 constexpr int kSchedSmemNB = 8192;  // blocks and requests whose sums are kept in shared memory for the searches
 constexpr int kSchedSmemB = 2048;
@@ -170,7 +173,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  //
 
 __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const __grid_constant__ Params p) {
   __shared__ int warp_tot[32];
-  __shared__ int carry_s, ncuts;
+  __shared__ int carry_s, ncuts, longest;
   __shared__ int32_t sp[kSchedSmemNB + 1];    // page prefix sums, first block of each request: copies for the
   __shared__ int32_t sb[kSchedSmemB + 1];     // searches (a search through global memory waits ~0.7 us a step)
   __shared__ int cb[kMaxClusters + 1];        // where the slices begin
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
   griddep_launch_dependents();
   const int tid = threadIdx.x, nt = static_cast<int>(blockDim.x);
   if (tid < 4) p.status[tid] = 0;
-  if (tid == 0) carry_s = ncuts = 0;
+  if (tid == 0) carry_s = ncuts = longest = 0;
   __syncthreads();
   const bool sb_ok = p.B <= kSchedSmemB, sp_ok = p.NB <= kSchedSmemNB;
   // request b's query tokens [q0, q1); an invalid range is left out
@@ -261,12 +264,14 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
     return k;
   };
   // each block's rows and pages
+  int most = 0;
   for (int base = 0; base < p.NB; base += nt) {
     const int n = base + tid;
     int np = 0;
     if (n < nblocks) {
       const Block k = block_at(n);
       np = last_page(k, p.H) + 1 - k.skip;
+      most = np > most ? np : most;
       p.blk[n] = k;
     }
     const int incl = block_scan(np, warp_tot, carry_s);
@@ -278,6 +283,8 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
     if (tid == nt - 1) carry_s = incl;
     __syncthreads();
   }
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((tid & 31) == 0) atomicMax(&longest, most);
   if (tid == 0) {
     p.prefix[0] = 0;
     sp[0] = 0;
@@ -311,12 +318,13 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
     }
     return lo;
   };
+  const bool whole = nblocks <= p.C && longest <= pre[nblocks] / p.C + p.whole_pages;
   const bool cut32 = W * p.C < (static_cast<int64_t>(1) << 31);  // a 32-bit division where it fits
   for (int c = tid; c <= p.C; c += nt) {
     const int64_t x = cut32 ? static_cast<int64_t>(static_cast<uint32_t>(W) * static_cast<uint32_t>(c) /
                                                    static_cast<uint32_t>(p.C))
                             : W * c / p.C;
-    cb[c] = c == 0 ? 0 : (c == p.C ? pre[nblocks] : page_at(x));
+    cb[c] = c == 0 ? 0 : (c == p.C ? pre[nblocks] : (whole ? pre[c < nblocks ? c : nblocks] : page_at(x)));
   }
   __syncthreads();
   for (int c = tid; c < p.C; c += nt) {
