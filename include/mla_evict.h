@@ -60,8 +60,8 @@ size_t mla_attn_mass_workspace_size(const mla_dims* d, int device);
  *               MLA_DEV_BAD_SEQ_LEN, and the length is clamped)
  *   mass_out    fp32 [B][mass_cols]; may be mass itself
  *   workspace   >= mla_attn_mass_workspace_size bytes, 256-byte aligned
- * Returns MLA_ERR_UNSUPPORTED where B * max_pages_per_req * 64 or
- * B * q_len * H does not fit in int32.
+ * Returns MLA_ERR_UNSUPPORTED where B * max_pages_per_req * 64 is beyond 2^30
+ * or B * q_len * H does not fit in int32.
  */
 int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const void* kv_cache,
                   const int32_t* page_table, const int32_t* seq_lens, const float* lse, int32_t num_fresh, float scale,
@@ -70,7 +70,8 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
 
 typedef struct {
   int32_t batch;             /* B >= 1 requests */
-  int32_t mass_cols;         /* row length of mass, positions and their outputs, >= 1 */
+  int32_t mass_cols;         /* row length of mass, positions and their outputs, >= 1; mass_cols or budget beyond 2^30
+                                or batch beyond 65535: MLA_ERR_UNSUPPORTED */
   int32_t num_pages;         /* pool size; valid page ids are [0, num_pages) */
   int32_t max_pages_per_req; /* columns of the page table a request may use */
   int32_t page_table_stride; /* int32 elements between page-table rows (>= max_pages_per_req) */

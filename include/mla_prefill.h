@@ -47,8 +47,9 @@ typedef struct {
   int32_t page_size;         /* must be 64 */
   int32_t num_pages;         /* pool size; valid page ids are [0, num_pages) */
   int32_t max_pages_per_req; /* columns of the page table a request may use; max_pages_per_req * 64 must fit in int32,
-                                and so must the pages that all 256-row blocks of queries could visit,
-                                (total_q * H / 128 + B) * max_pages_per_req (else MLA_ERR_UNSUPPORTED) */
+                                and so must the pages that all blocks of queries could visit,
+                                (total_q * H / 128 + B) * max_pages_per_req; the blocks alone at most 2^30 (else
+                                MLA_ERR_UNSUPPORTED) */
   int32_t page_table_stride; /* int32 elements between page-table rows (>= max_pages_per_req) */
   int32_t kv_dtype;          /* mla_kv_dtype */
 } mla_prefill_dims;

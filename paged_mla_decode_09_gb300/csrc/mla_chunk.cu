@@ -73,7 +73,8 @@ int check_shape(const Shape& s, int page_size, int kv_dtype) {
   if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
   if (s.T > INT_MAX || s.T * s.H > INT_MAX) return MLA_ERR_UNSUPPORTED;
   if (s.num_pages * 64 > INT_MAX || s.max_pages * 64 > INT_MAX) return MLA_ERR_UNSUPPORTED;
-  if ((s.T * s.H / 128 + s.B) * s.max_pages > INT_MAX) return MLA_ERR_UNSUPPORTED;  // the schedule's page sums
+  const int64_t most = s.T * s.H / 128 + s.B;  // blocks
+  if (most > 1 << 30 || most * s.max_pages > INT_MAX) return MLA_ERR_UNSUPPORTED;  // the schedule's sums
   return MLA_OK;
 }
 

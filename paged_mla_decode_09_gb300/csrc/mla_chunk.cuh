@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
       if (sb_ok) sb[b + 1] = v;
     }
     __syncthreads();
-    if (tid == nt - 1) carry_s = incl;
+    if (tid == nt - 1) carry_s = incl <= p.NB ? incl : p.NB + 1;  // ranges that overlap could pass 32 bits
     __syncthreads();
   }
   if (tid == 0) {

@@ -329,6 +329,8 @@ namespace {
 using mla::evict::Params;
 using namespace mla::host;
 
+constexpr int kMaxTokens = 1 << 30;  // a walk's slot and step then stay within int32
+
 struct Layout {
   size_t counts, movers, holes, total;
 };
@@ -361,7 +363,7 @@ int mla_evict(const mla_evict_dims* d, const float* mass, const int32_t* positio
     return MLA_ERR_INVALID_ARG;
   if (d->kv_dtype != MLA_KV_BF16 && d->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(d->num_pages) * 64 > INT_MAX || static_cast<int64_t>(d->max_pages_per_req) * 64 > INT_MAX ||
-      d->batch > 65535)  // the move grid's y extent
+      d->mass_cols > kMaxTokens || d->budget > kMaxTokens || d->batch > 65535)  // the move grid's y extent
     return MLA_ERR_UNSUPPORTED;
   if (!aligned(mass, 4) || !aligned(positions, 4) || !aligned(seq_lens, 4) || !aligned(page_table, 4) ||
       !aligned(kv_cache, 16) || !aligned(new_lens, 4) || !aligned(kept, 4) || !aligned(mass_out, 4) ||

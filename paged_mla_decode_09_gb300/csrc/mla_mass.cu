@@ -917,7 +917,7 @@ int check_mass_dims(const mla_dims* d) {
   if (d->page_size != 64) return MLA_ERR_UNSUPPORTED;
   if (d->kv_dtype != MLA_KV_BF16 && d->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
   const int64_t B = d->batch;
-  if (static_cast<int64_t>(d->num_pages) * 64 > INT_MAX || B * d->max_pages_per_req > INT_MAX / 64 ||
+  if (static_cast<int64_t>(d->num_pages) * 64 > INT_MAX || B * d->max_pages_per_req > (1 << 30) / 64 ||
       B * d->q_len > INT_MAX || B * d->q_len * d->num_heads > INT_MAX)
     return MLA_ERR_UNSUPPORTED;
   return MLA_OK;

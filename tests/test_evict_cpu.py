@@ -48,6 +48,7 @@ def _evict(lib, d, ptrs=None, ws=1 << 40):
     (dict(batch=0), -1), (dict(num_heads=0), -1), (dict(q_len=0), -1), (dict(num_pages=0), -1),
     (dict(max_pages_per_req=0), -1), (dict(page_table_stride=4), -1), (dict(page_size=32), -2), (dict(kv_dtype=9), -2),
     (dict(num_pages=1 << 26), -2), (dict(batch=1 << 14, max_pages_per_req=1 << 12, page_table_stride=1 << 12), -2),
+    (dict(batch=1, max_pages_per_req=(1 << 24) + 1, page_table_stride=1 << 25), -2),
     (dict(batch=1 << 20, q_len=1 << 11), -2), (dict(batch=1 << 12, q_len=1 << 10, num_heads=1 << 10), -2)])
 def test_mass_refuses_dims(lib, bad, rc):
     assert _mass(lib, _dims(**bad)) == rc
@@ -78,6 +79,7 @@ def test_mass_refuses_arguments(lib):
     (dict(page_table_stride=4), -1), (dict(budget=0), -1), (dict(num_sinks=-1), -1), (dict(num_recent=-1), -1),
     (dict(num_sinks=60, num_recent=5), -1), (dict(num_sinks=2**31 - 1, num_recent=2**31 - 1), -1),
     (dict(kv_dtype=3), -2), (dict(num_pages=1 << 26), -2), (dict(batch=65536), -2),
+    (dict(mass_cols=(1 << 30) + 1), -2), (dict(budget=(1 << 30) + 1), -2),
     (dict(max_pages_per_req=1 << 26, page_table_stride=1 << 26), -2)])
 def test_evict_refuses_dims(lib, bad, rc):
     assert _evict(lib, _edims(**bad)) == rc

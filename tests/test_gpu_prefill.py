@@ -97,6 +97,10 @@ CASES = {
     "many_requests": dict(new=[1 + k % 3 for k in range(150)], total=[40 + 7 * k for k in range(150)], heads=8),
     "full_blocks": dict(new=[70], total=[700], heads=64),
     "full_blocks_pieces": dict(new=[16, 40], total=[6000, 41], heads=32),
+    # several blocks per cluster, blocks' last rows in the middle of a warp's
+    "many_full_blocks": dict(new=[33] * 8 + [7], total=[90 + 83 * k for k in range(9)], heads=64),
+    "many_ragged_blocks": dict(new=[33 + k for k in range(14)], total=[60 + 97 * k for k in range(14)], heads=20),
+    "even_blocks": dict(new=[1] * 60, total=[260 + k for k in range(60)], heads=64),  # a cluster each, uncut
     "rows_behind": dict(new=[9, 3], total=[100, 64], heads=16, extra_q=5),
 }
 

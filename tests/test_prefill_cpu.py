@@ -53,6 +53,7 @@ def test_prefill_refuses_bad_dims(lib, bad):
 
 @pytest.mark.parametrize("bad", [dict(page_size=32), dict(kv_dtype=2), dict(total_q=1 << 28),
                                  dict(max_pages_per_req=1 << 26, page_table_stride=1 << 26), dict(num_pages=1 << 26),
+                                 dict(batch=(1 << 30) + 1, max_pages_per_req=1, page_table_stride=1),
                                  dict(total_q=1 << 20, num_heads=128, max_pages_per_req=1 << 12,
                                       page_table_stride=1 << 12)])
 def test_prefill_refuses_what_it_does_not_support(lib, bad):
