@@ -19,6 +19,7 @@ using mla::chunk::Cfg;
 using mla::chunk::Params;
 
 constexpr uint64_t kTimeoutNs = 2000000000ull;  // 2 s per pipeline wait
+constexpr int kUncutPages = 3;                  // what the combine's launch costs, in pages
 
 using mla::host::align256;
 using mla::host::aligned;
@@ -234,8 +235,19 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   // equal at 5 pages (17.4 us), 1 x 128 at 8, 8 x 64 at 11, 8 x 128 at 15;
   // 64 x 64 heads x 66 pages (56 in even slices) 78 us against 86
   const int64_t total_rows = s.T * s.H, rows = total_rows / s.B < p.BR ? total_rows / s.B : p.BR;
-  const int64_t whole = 5 + rows / 24 + total_rows / 600;
+  const int64_t whole = 5 + rows / 40 + total_rows / 600;
   p.whole_pages = static_cast<int32_t>(whole < 1000 ? whole : 1000);
+  // where no block can have many more pages than that (a window, a short
+  // table), none is cut and the combine is left out: 1 x 16 heads over a
+  // window of 256 17.5 -> 16.8 us, host 15.0 -> 11.5
+  const int64_t tokens = s.T < p.BR / s.H + 2 ? s.T : p.BR / s.H + 2;  // of a block
+  int64_t pages = s.max_pages;
+  if (window > 0) {
+    const int64_t seen = (window + tokens + 62) / 64 + 1 + (static_cast<int64_t>(sinks) + 63) / 64;
+    pages = seen < pages ? seen : pages;
+  }
+  const bool uncut = s.blocks() <= C && pages <= whole + kUncutPages;
+  if (uncut) p.whole_pages = INT_MAX / 2;
   p.c2 = mla::host::log2_scale(scale, s.f8 ? kv_scale : 1.f);
   p.kv_scale = s.f8 ? kv_scale : 1.f;
   p.timeout_ns = kTimeoutNs;
@@ -252,7 +264,7 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   if (e == cudaSuccess)
     e = s.f8 ? (cg == 2 ? launch_attention<true, 2>(p, m, stream) : launch_attention<true, 1>(p, m, stream))
              : (cg == 2 ? launch_attention<false, 2>(p, m, stream) : launch_attention<false, 1>(p, m, stream));
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && !uncut) {
     // a column per block that may be cut, at most one per slice boundary; a
     // warp per row, or four where that still fits the SMs about once
     const int64_t cuts = s.blocks() < C ? s.blocks() : C;
