@@ -40,11 +40,11 @@ struct Shape {
 };
 
 // Rows per block: 256 (two CTAs per MMA) where a request brings more than 128
-// rows on average, else 128.  Measured on GB300: 128 heads x 2 tokens per
-// request over windows of 2048 (e4m3) 179 us at 256 against 235 at 128; 512
-// tokens of 128 heads over 8K keys 1351 against 1519; 64 heads x 1 token over
-// windows of 4096, where three quarters of a 256-row block are padding, 124
-// against 91.
+// rows on average, else 128.  Measured on GB300: 128 x 2 tokens x 128 heads
+// over windows of 2048 (e4m3) 137 us at 256 against 178 at 128; 2 x 512 tokens
+// of 128 heads over 8K keys 1279 against 1471; 64 x 64 heads x 1 token over
+// windows of 4096, where three quarters of a 256-row block are padding, 125
+// against 78.
 int Shape::cg() const { return T * H > 128 * B ? 2 : 1; }
 
 // [status | blkoff | blocks | prefix | cinfo | cut blocks | partial outputs | partial lse]
@@ -225,9 +225,9 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   p.pt_stride = static_cast<int32_t>(s.stride);
   p.window = window;
   p.sinks = sinks;
-  // a piece's start in pages' time: swept 3 to 22 on GB300; flat for bf16, an
-  // e4m3 pair splits its 256 query rows for ~5 us (ragged chunks 1540 us at 6,
-  // 1445 at 15; two drafts over windows 148 and 144)
+  // a piece's start in pages' time: swept on GB300; flat for bf16, an e4m3
+  // pair splits its 256 query rows meanwhile (ragged chunks 1477 us at 6, 1427
+  // at 10, 1429 at 15, 1459 at 20; two drafts over windows 148, 145, 145, 149)
   p.unit_cost = s.f8 && cg == 2 ? 15 : 6;
   // what a cut costs, in pages of a cluster's time (~0.75 us): a launch's worth
   // of latency, a block's partials stored by one CTA, all partials written and

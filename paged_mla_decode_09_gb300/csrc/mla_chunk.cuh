@@ -27,7 +27,9 @@
 // bytes a cycle that shared memory has.  A pair scores 128 keys at a time
 // (one page in each S CTA): an MMA of N = 64 lasts 32 cycles, no longer than
 // its issue takes, so that every wait of the issuing warp (~200 cycles each)
-// left the tensor pipe idle; at N = 128 the queue covers the waits.
+// left the tensor pipe idle; at N = 128 the queue covers one wait per tile.
+// Measured: 2 x 512 tokens x 128 heads over 8K keys 1279 us (1885 TFLOP/s;
+// 1738 in a loop, under the power limit), the tensor pipes 87.6 % busy.
 //
 // An e4m3 cache: QK runs on the codes as they are (kind::f8f6f4), the queries
 // as two e4m3 terms hi + lo of q / 2^k.  A bf16 value has 8 significant bits
@@ -51,7 +53,7 @@
 namespace mla {
 namespace chunk {
 
-// O is rescaled (a round trip through TMEM that stalls PV: ~1.3 us) only when
+// O is rescaled (a round trip through TMEM that stalls PV, ~1.3 us) only when
 // a row's maximum grows by more than 2^threshold over its reference.  P and
 // the fp32 sums then reach 2^threshold; a float's relative precision does not
 // depend on it.  bf16 P has fp32's range, so the threshold only has to keep
@@ -607,9 +609,9 @@ __device__ __forceinline__ float store_lse(const Params& p, const Unit& u, int b
 
 // A warp's 32 rows br0 .. (TMEM lanes), columns [c0, c0 + 256), by way of
 // shared memory: boxes of 32 rows x 64 bytes (64-byte swizzle), kBufs in turn,
-// that TMA writes.  A lane's own stores to its row take a line each: 128 rows of
-// bf16 outputs took 4.9 us that way, half of it with O not yet free for the
-// next block.
+// that TMA writes.  (A lane's own stores to its row take a line each: a block's
+// bf16 outputs took 4.9 us that way, 2.5 this way, and O is not free for the
+// next block before that.)
 template <bool kF8, int kCg>
 __device__ __forceinline__ void store_staged(const Params& p, const Unit& u, int br0, int c0, uint32_t taddr, float f,
                                              uint8_t* stage, const CUtensorMap* map) {

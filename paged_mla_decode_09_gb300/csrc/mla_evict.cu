@@ -20,8 +20,11 @@
 // for 4096 of 4224 tokens about 4000 rows of a request instead of 125.)
 //
 // What bounds it: the latency of about a dozen walks and barriers (a block per
-// request took 59 us for 16 requests of up to 32K tokens), then the moved
-// rows' bytes.
+// request took 59 us for 16 requests of up to 32K tokens, clusters take 32), then
+// the moved rows' bytes.  64 requests of 4.2K tokens take 18 us, one of 600
+// 8.7.  (The moves by the selecting blocks themselves took 3 to 9 us longer: a
+// launch of their own finds its blocks resident already and spreads the rows
+// over every SM.)
 #include <cuda_runtime.h>
 
 #include <climits>
