@@ -259,8 +259,11 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
                                   : make_maps<false, 1>(q_nope, q_pe, kv_cache, s, p, &m));
   if (!ok) return MLA_ERR_CUDA;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
-  const int nt = s.B <= 256 && p.NB <= 256 && C <= 256 ? 256 : mla::chunk::kSchedThreads;
-  cudaError_t e = launch_pdl(mla::chunk::mla_chunk_schedule_kernel, dim3(1), dim3(nt), 0, stream, 0, p);
+  using mla::chunk::kSchedSmall;
+  cudaError_t e = s.B <= kSchedSmall && p.NB <= kSchedSmall
+                      ? launch_pdl(mla::chunk::mla_chunk_schedule_kernel<true>, dim3(1), dim3(kSchedSmall), 0, stream, 0, p)
+                      : launch_pdl(mla::chunk::mla_chunk_schedule_kernel<false>, dim3(1),
+                                   dim3(mla::chunk::kSchedThreads), 0, stream, 0, p);
   if (e == cudaSuccess)
     e = s.f8 ? (cg == 2 ? launch_attention<true, 2>(p, m, stream) : launch_attention<true, 1>(p, m, stream))
              : (cg == 2 ? launch_attention<false, 2>(p, m, stream) : launch_attention<false, 1>(p, m, stream));

@@ -143,9 +143,13 @@ struct Params {
 // clusters with many short blocks get fewer pages.  A few blocks of about the
 // same length get a cluster each instead: what a cut costs (fp32 partials, the
 // combine) is more than what the even slices gain.
-constexpr int kSchedThreads = 1024;  // or 256 for small batches (fewer warps at each barrier)
-constexpr int kSchedSmemNB = 8192;  // blocks and requests whose sums are kept in shared memory for the searches
-constexpr int kSchedSmemB = 2048;
+// Up to 256 requests and blocks (kSmall) every thread has one of each and all
+// of it stays in shared memory; that form is half the code, and what a small
+// call waits for here is mostly the first fetch of instructions.
+constexpr int kSchedThreads = 1024;
+constexpr int kSchedSmall = 256;    // threads, requests and blocks of the small form
+constexpr int kSchedSmemNB = 8192;  // the other form: blocks and requests whose sums are kept in shared memory for
+constexpr int kSchedSmemB = 2048;   // the searches
 
 // The page of the last key that the block's last row sees.
 __device__ __forceinline__ int last_page(const Block& k, int H) {
@@ -173,19 +177,43 @@ __device__ __forceinline__ int block_scan(int v, int* warp_tot, int carry) {  //
   return v + ((tid >> 5) ? warp_tot[(tid >> 5) - 1] : 0) + carry;
 }
 
-__global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const __grid_constant__ Params p) {
+// The same for the small form, with one barrier; `tot` is written once per kernel.
+__device__ __forceinline__ int block_scan_small(int v, int (&tot)[kSchedSmall / 32]) {
+  const int tid = threadIdx.x;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, v, o);
+    if ((tid & 31) >= o) v += t;
+  }
+  if ((tid & 31) == 31) tot[tid >> 5] = v;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kSchedSmall / 32; ++w) v += w < (tid >> 5) ? tot[w] : 0;
+  return v;
+}
+
+template <bool kSmall>
+__global__ void __launch_bounds__(kSmall ? kSchedSmall : kSchedThreads)
+    mla_chunk_schedule_kernel(const __grid_constant__ Params p) {
   __shared__ int warp_tot[32];
+  __shared__ __align__(16) int tot_b[kSchedSmall / 32], tot_n[kSchedSmall / 32];
   __shared__ int carry_s, ncuts, longest;
-  __shared__ int32_t sp[kSchedSmemNB + 1];    // page prefix sums, first block of each request: copies for the
-  __shared__ int32_t sb[kSchedSmemB + 1];     // searches (a search through global memory waits ~0.7 us a step)
-  __shared__ int cb[kMaxClusters + 1];        // where the slices begin
+  // page prefix sums, first block of each request: copies for the searches (a
+  // search through global memory waits ~0.7 us a step)
+  __shared__ int32_t sp[(kSmall ? kSchedSmall : kSchedSmemNB) + 1];
+  __shared__ int32_t sb[(kSmall ? kSchedSmall : kSchedSmemB) + 1];
+  __shared__ int cb[kMaxClusters + 1];        // where the slices begin: page,
+  __shared__ int cf[kMaxClusters + 1];        // and the block that holds it
+  constexpr int kKept = kSmall ? kSchedSmall : 1;
+  __shared__ int s_q0[kKept], s_nq[kKept], s_len[kKept];
+  __shared__ int2 s_rows[kKept];              // a block's first row, rows
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, nt = static_cast<int>(blockDim.x);
+  const int tid = threadIdx.x;
+  constexpr int nt = kSmall ? kSchedSmall : kSchedThreads;
   if (tid < 4) p.status[tid] = 0;
   if (tid == 0) carry_s = ncuts = longest = 0;
   __syncthreads();
-  const bool sb_ok = p.B <= kSchedSmemB, sp_ok = p.NB <= kSchedSmemNB;
+  const bool sb_ok = kSmall || p.B <= kSchedSmemB, sp_ok = kSmall || p.NB <= kSchedSmemNB;
   // request b's query tokens [q0, q1); an invalid range is left out
   auto range = [&](int b, int& q0, int& q1) -> bool {
     if (!p.cu_q) {
@@ -200,32 +228,40 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
     return false;
   };
   // row blocks per request
-  for (int base = 0; base < p.B; base += nt) {
+  for (int base = 0; base < (kSmall ? 1 : p.B); base += nt) {
     const int b = base + tid;
     int nblk = 0;
     if (b < p.B) {
+      const int L = p.seq_lens[b];
       int q0, q1;
       if (!range(b, q0, q1)) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
-      const int L = p.seq_lens[b];
       if (q1 > q0 && (L < q1 - q0 || L > p.max_pages * kPage)) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
-      nblk = static_cast<int>((static_cast<int64_t>(q1 - q0) * p.H + p.BR - 1) / p.BR);
+      // (rows fit in 31 bits, rounded up in 32)
+      nblk = static_cast<int>((static_cast<uint32_t>(q1 - q0) * static_cast<uint32_t>(p.H) + (p.BR - 1)) >>
+                              (p.BR == 256 ? 8 : 7));
+      if constexpr (kSmall) {
+        s_q0[b] = q0;
+        s_nq[b] = q1 - q0;
+        s_len[b] = L;
+      }
     }
-    const int incl = block_scan(nblk, warp_tot, carry_s);
+    const int incl = kSmall ? block_scan_small(nblk, tot_b) : block_scan(nblk, warp_tot, carry_s);
     if (b < p.B) {
       const int v = incl < p.NB ? incl : p.NB;  // never beyond the arrays
-      p.blkoff[b + 1] = v;
       if (sb_ok) sb[b + 1] = v;
+      else p.blkoff[b + 1] = v;
     }
     __syncthreads();
     if (tid == nt - 1) carry_s = incl <= p.NB ? incl : p.NB + 1;  // ranges that overlap could pass 32 bits
-    __syncthreads();
+    if (!kSmall) __syncthreads();
   }
   if (tid == 0) {
-    p.blkoff[0] = 0;
+    if (!sb_ok) p.blkoff[0] = 0;
     sb[0] = 0;
-    if (carry_s > p.NB) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
-    carry_s = 0;
+    if (!kSmall && carry_s > p.NB) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
+    if (!kSmall) carry_s = 0;
   }
+  if (kSmall && tid == nt - 1 && carry_s > p.NB) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
   __syncthreads();
   const int32_t* off = sb_ok ? sb : p.blkoff;
   const int nblocks = off[p.B];
@@ -235,29 +271,35 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
       const int mid = (lo + hi + 1) >> 1;
       if (off[mid] <= n) lo = mid; else hi = mid - 1;
     }
-    int q0, q1;
-    range(lo, q0, q1);
-    const int nq = q1 - q0;
-    const int64_t r0 = static_cast<int64_t>(n - off[lo]) * p.BR;  // within the request
-    const int64_t left = static_cast<int64_t>(nq) * p.H - r0;
-    const int Lraw = p.seq_lens[lo];
+    int q0, nq, Lraw;
+    if constexpr (kSmall) {
+      q0 = s_q0[lo];
+      nq = s_nq[lo];
+      Lraw = s_len[lo];
+    } else {
+      int q1;
+      range(lo, q0, q1);
+      nq = q1 - q0;
+      Lraw = p.seq_lens[lo];
+    }
+    // a request's rows fit in 31 bits (total_q * H does)
+    const uint32_t r0 = static_cast<uint32_t>(n - off[lo]) * static_cast<uint32_t>(p.BR);  // within the request
+    const uint32_t left = static_cast<uint32_t>(nq) * static_cast<uint32_t>(p.H) - r0;
     const int L = Lraw < 0 ? 0 : (Lraw > p.max_pages * kPage ? p.max_pages * kPage : Lraw);
     Block k;
     k.b = lo;
-    k.row0 = static_cast<int32_t>(static_cast<int64_t>(q0) * p.H + r0);
-    k.nrows = static_cast<int32_t>(left < p.BR ? left : p.BR);
-    // rows of a request fit in 32 bits (total_q * H does)
-    const uint32_t i0 = static_cast<uint32_t>(r0) / static_cast<uint32_t>(p.H);
-    k.h0 = static_cast<int32_t>(static_cast<uint32_t>(r0) - i0 * static_cast<uint32_t>(p.H));
+    k.row0 = static_cast<int32_t>(static_cast<uint32_t>(q0) * static_cast<uint32_t>(p.H) + r0);
+    k.nrows = static_cast<int32_t>(left < static_cast<uint32_t>(p.BR) ? left : static_cast<uint32_t>(p.BR));
+    const uint32_t i0 = r0 / static_cast<uint32_t>(p.H);
+    k.h0 = static_cast<int32_t>(r0 - i0 * static_cast<uint32_t>(p.H));
     k.pos0 = L - nq + static_cast<int>(i0);
     k.len = L;
     const int last = last_page(k, p.H);  // at least one page, all of it masked if nothing is seen
     k.sp = last + 1;
     k.skip = 0;
     if (p.window > 0) {
-      const int64_t wlo = static_cast<int64_t>(k.pos0) + 1 - p.window;  // first key of the first row's window
-      const int wp = wlo > 0 ? static_cast<int>(wlo / kPage) : 0;
-      const int ns = static_cast<int>((static_cast<int64_t>(p.sinks) + kPage - 1) / kPage);
+      const int wp = k.pos0 + 1 > p.window ? (k.pos0 + 1 - p.window) / kPage : 0;  // page of the first row's first key
+      const int ns = p.sinks / kPage + (p.sinks % kPage != 0);
       if (wp > ns) {
         k.sp = ns;
         k.skip = wp - ns;
@@ -267,7 +309,7 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
   };
   // each block's rows and pages
   int most = 0;
-  for (int base = 0; base < p.NB; base += nt) {
+  for (int base = 0; base < (kSmall ? 1 : p.NB); base += nt) {
     const int n = base + tid;
     int np = 0;
     if (n < nblocks) {
@@ -275,15 +317,18 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
       np = last_page(k, p.H) + 1 - k.skip;
       most = np > most ? np : most;
       p.blk[n] = k;
+      if constexpr (kSmall) s_rows[n] = make_int2(k.row0, k.nrows);
     }
-    const int incl = block_scan(np, warp_tot, carry_s);
+    const int incl = kSmall ? block_scan_small(np, tot_n) : block_scan(np, warp_tot, carry_s);
     if (n < p.NB) {
       p.prefix[n + 1] = incl;
       if (sp_ok) sp[n + 1] = incl;
     }
-    __syncthreads();
-    if (tid == nt - 1) carry_s = incl;
-    __syncthreads();
+    if (!kSmall) {
+      __syncthreads();
+      if (tid == nt - 1) carry_s = incl;
+      __syncthreads();
+    }
   }
   most = __reduce_max_sync(0xffffffffu, most);
   if ((tid & 31) == 0) atomicMax(&longest, most);
@@ -301,37 +346,36 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
   }
   // slices: weighted position of block n's first page is pre[n] + unit_cost * (n + 1)
   const int64_t W = static_cast<int64_t>(pre[nblocks]) + static_cast<int64_t>(p.unit_cost) * nblocks;
-  auto page_at = [&](int64_t x) -> int {
+  auto slice_at = [&](int c, int64_t x) {
     int lo = 0, hi = nblocks - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
       if (pre[mid] + static_cast<int64_t>(p.unit_cost) * mid <= x) lo = mid; else hi = mid - 1;
     }
     const int64_t np = pre[lo + 1] - pre[lo];
-    int64_t off_p = x - pre[lo] - static_cast<int64_t>(p.unit_cost) * (lo + 1);
-    off_p = off_p < 0 ? 0 : (off_p > np ? np : off_p);
-    return static_cast<int>(pre[lo] + off_p);
-  };
-  auto block_of = [&](int page) -> int {  // the block that holds the page
-    int lo = 0, hi = nblocks - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= page) lo = mid; else hi = mid - 1;
-    }
-    return lo;
+    const int64_t off_p = x - pre[lo] - static_cast<int64_t>(p.unit_cost) * (lo + 1);
+    cb[c] = off_p < 0 ? pre[lo] : (off_p >= np ? pre[lo + 1] : static_cast<int>(pre[lo] + off_p));
+    cf[c] = off_p >= np ? lo + 1 : lo;  // (every block has a page)
   };
   const bool whole = nblocks <= p.C && longest <= pre[nblocks] / p.C + p.whole_pages;
-  const bool cut32 = W * p.C < (static_cast<int64_t>(1) << 31);  // a 32-bit division where it fits
+  // W c / C without a 64-bit division: W = C quo + rem
+  const int64_t quo = W < (static_cast<int64_t>(1) << 32) ? static_cast<uint32_t>(W) / static_cast<uint32_t>(p.C)
+                                                          : W / p.C;
+  const uint32_t rem = static_cast<uint32_t>(W - quo * p.C);
   for (int c = tid; c <= p.C; c += nt) {
-    const int64_t x = cut32 ? static_cast<int64_t>(static_cast<uint32_t>(W) * static_cast<uint32_t>(c) /
-                                                   static_cast<uint32_t>(p.C))
-                            : W * c / p.C;
-    cb[c] = c == 0 ? 0 : (c == p.C ? pre[nblocks] : (whole ? pre[c < nblocks ? c : nblocks] : page_at(x)));
+    const int64_t x = quo * c + rem * static_cast<uint32_t>(c) / static_cast<uint32_t>(p.C);
+    if (c == 0 || c == p.C || whole) {
+      const int n = c == 0 ? 0 : (c == p.C || c > nblocks ? nblocks : c);
+      cb[c] = pre[n];
+      cf[c] = n;
+    } else {
+      slice_at(c, x);
+    }
   }
   __syncthreads();
   for (int c = tid; c < p.C; c += nt) {
     const int s = cb[c], e = cb[c + 1];
-    const int first = s < e ? block_of(s) : 0, last = s < e ? block_of(e - 1) : 0;
+    const int first = s < e ? cf[c] : 0, last = s < e ? cf[c + 1] - (pre[cf[c + 1]] == e ? 1 : 0) : 0;
     *reinterpret_cast<int4*>(p.cinfo + 4 * c) = make_int4(s, e, first, last);
     // the block that starts in this slice (or exactly with it) and goes on
     // behind it, if there is one: an entry of the combine's list
@@ -341,10 +385,12 @@ __global__ void __launch_bounds__(kSchedThreads) mla_chunk_schedule_kernel(const
         const int mid = (lo + hi + 1) >> 1;
         if (cb[mid] < pre[last + 1]) lo = mid; else hi = mid - 1;
       }
-      const Block k = block_at(last);
+      int2 rows;
+      if constexpr (kSmall) rows = s_rows[last];
+      else rows = make_int2(p.blk[last].row0, p.blk[last].nrows);
       int4* dst = reinterpret_cast<int4*>(p.cuts + 8 * (1 + atomicAdd(&ncuts, 1)));
       dst[0] = make_int4(last, c, lo, 2 * c + (first != last ? 1 : 0));
-      dst[1] = make_int4(k.row0, k.nrows, 0, 0);
+      dst[1] = make_int4(rows.x, rows.y, 0, 0);
     }
   }
   __syncthreads();
