@@ -20,9 +20,9 @@
 // for 4096 of 4224 tokens about 4000 rows of a request instead of 125.)
 //
 // What bounds it: the latency of about a dozen walks and barriers (a block per
-// request took 59 us for 16 requests of up to 32K tokens, clusters take 32), then
+// request took 59 us for 16 requests of up to 32K tokens, clusters take 28), then
 // the moved rows' bytes.  64 requests of 4.2K tokens take 18 us, one of 600
-// 8.7.  (The moves by the selecting blocks themselves took 3 to 9 us longer: a
+// 7.8.  (The moves by the selecting blocks themselves took 3 to 9 us longer: a
 // launch of their own finds its blocks resident already and spreads the rows
 // over every SM.)
 #include <cuda_runtime.h>
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
   extern __shared__ uint32_t keys[];  // keys of the block's slots, then their positions
   __shared__ int hist[4][kBins];
   __shared__ int buf[kWarps];
-  __shared__ int pick[2];          // the digit of the k-th key, keys above it
+  __shared__ int pick[3];          // the digit of the k-th key, keys above it, whether all keys of it are kept
   __shared__ int4 counts_w[kWarps];  // per warp, see below
   __shared__ int4 share;           // the block's sums of them, and its greatest position: read by the other blocks
   __shared__ int share_pos;
@@ -106,23 +106,32 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
     for (int i = tid; i < 4 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
     int last = L - 1;  // the greatest position
     {
+      // Every slot below k gets its own weight and position back, also those
+      // that a mover takes over below: the values are at hand, and a later walk
+      // would wait for each of them (the outputs may be the inputs).
       int m = -1;
-      for (int t = r0 + tid; t < r1; t += 4 * kThreads) {  // eight loads in flight
-        int q4[4];
-        float x4[4];
+      constexpr int kFly = 8;
+      for (int t = r0 + tid; t < r1; t += kFly * kThreads) {  // 16 loads in flight
+        int qv[kFly];
+        float xv[kFly];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const bool in = t + q * kThreads < r1;
-          q4[q] = pos && in ? pos[t + q * kThreads] : -1;
-          x4[q] = cached && in ? mass[t + q * kThreads] : 0.f;
+        for (int q = 0; q < kFly; ++q) {
+          const int at = t + q * kThreads;
+          qv[q] = pos && at < r1 ? pos[at] : -1;
+          xv[q] = at < r1 && (cached || at < k) ? mass[at] : 0.f;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          m = max(m, q4[q]);
-          const int at = t + q * kThreads - r0;
-          if (cached && t + q * kThreads < r1) {
-            keys[at] = weight_key(x4[q]);
-            if (pos) spos[at] = q4[q];
+        for (int q = 0; q < kFly; ++q) {
+          const int at = t + q * kThreads;
+          if (at >= r1) break;
+          m = max(m, qv[q]);
+          if (cached) {
+            keys[at - r0] = weight_key(xv[q]);
+            if (pos) spos[at - r0] = qv[q];
+          }
+          if (at < k) {
+            mass_out[at] = xv[q];
+            if (pos) pos_out[at] = qv[q];
           }
         }
       }
@@ -189,11 +198,17 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
       if (tid < kBins && before < need && before + own >= need) {  // one thread
         pick[0] = kBins - 1 - tid;
         pick[1] = before;
+        pick[2] = before + own == need;
       }
       __syncthreads();
       prefix |= static_cast<uint32_t>(pick[0]) << shift;
       mask |= 255u << shift;
       need -= pick[1];
+      if (pick[2]) {  // the keys from prefix on are the k (not all L, so prefix is not 0): no ties, no more digits
+        prefix -= 1;
+        need = 0;
+        break;
+      }
     }
     auto key = [&](int t) -> uint32_t { return cached ? (t < r1 ? keys[t - r0] : 0u) : form(t); };
     // Keys above prefix are kept, and of the keys equal to it the `need`
@@ -223,27 +238,45 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
       share = a;
     }
     sync_ranks();
-    // free slots and movers of the blocks and warps before this warp
+    // Free slots and movers of the blocks and warps before this warp: lane i
+    // has part i (a block, then a warp of this block); `need` less the ties
+    // before it says how many of its ties are kept, and scans add up the rest.
     int tie = 0, h = 0, m = 0;
-    auto add = [&](const int4& c) {
-      const int lo = min(max(need - tie, 0), c.x);            // kept ties below k
-      const int hi = min(max(need - tie - c.x, 0), c.y);      // and from k on
-      tie += c.x + c.y;
-      h += c.z - lo;
-      m += c.w + hi;
-    };
-    int tie_b = 0, h_b = 0, m_b = 0;
-    for (int r = 0; r < cs; ++r) {
-      if (r == rank) {
-        tie_b = tie; h_b = h; m_b = m;
+    auto scan = [&](int v) {
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        const int t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
       }
-      const uint32_t at = mapa(smem_u32(&share), r);
-      add(make_int4(static_cast<int>(ld_cluster_u32(at)), static_cast<int>(ld_cluster_u32(at + 4)),
-                    static_cast<int>(ld_cluster_u32(at + 8)), static_cast<int>(ld_cluster_u32(at + 12))));
+      return v;
+    };
+    // adds the parts before part `at` to (tie, h, m); the last lane's sums in all[]
+    int all_m = 0;
+    auto add_before = [&](int4 c, int at) {
+      const int ties = scan(c.x + c.y), before = tie + ties - (c.x + c.y);
+      const int lo = min(max(need - before, 0), c.x);        // kept ties below k
+      const int hi = min(max(need - before - c.x, 0), c.y);  // and from k on
+      const int hs = scan(c.z - lo), ms = scan(c.w + hi);
+      all_m = m + __shfl_sync(0xffffffffu, ms, 15);
+      const int src = at > 0 ? at - 1 : 0;
+      const int t1 = __shfl_sync(0xffffffffu, ties, src), h1 = __shfl_sync(0xffffffffu, hs, src),
+                m1 = __shfl_sync(0xffffffffu, ms, src);
+      if (at > 0) {
+        tie += t1;
+        h += h1;
+        m += m1;
+      }
+    };
+    int4 c = make_int4(0, 0, 0, 0);
+    if (lane < cs) {
+      const uint32_t at = mapa(smem_u32(&share), lane);
+      c = make_int4(static_cast<int>(ld_cluster_u32(at)), static_cast<int>(ld_cluster_u32(at + 4)),
+                    static_cast<int>(ld_cluster_u32(at + 8)), static_cast<int>(ld_cluster_u32(at + 12)));
     }
-    moves = m;
-    tie = tie_b; h = h_b; m = m_b;
-    for (int w = 0; w < warp; ++w) add(counts_w[w]);
+    add_before(c, rank);
+    moves = all_m;
+    c = lane < kWarps ? counts_w[lane] : make_int4(0, 0, 0, 0);
+    add_before(c, warp);
     const unsigned below = (1u << lane) - 1u;
     for (int t = t0 + lane; t - lane < t1; t += 32) {
       const bool in = t < t1;
@@ -255,17 +288,12 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
       const unsigned mb = __ballot_sync(0xffffffffu, in && t >= k && keep);
       if (in && t < k && !keep) holes[h + __popc(hb & below)] = t;
       if (in && t >= k && keep) movers[m + __popc(mb & below)] = t;
-      // outputs: only slots below k are written, and only slots that stay
-      // below k or movers from k on are read for them, so they may be the inputs
-      if (in && t < k && keep) {
-        kept[t] = t;
-        mass_out[t] = mass[t];
-        if (pos) pos_out[t] = pos[t];
-      }
+      if (in && t < k && keep) kept[t] = t;
       h += __popc(hb);
       m += __popc(mb);
     }
     sync_ranks();  // the lists are whole, every key has been read, and no block reads another's memory any more
+    // only slots below k are written, only ones from k on are read
     for (int j = first; j < moves; j += step) {
       const int t = holes[j], o = movers[j];
       kept[t] = o;
