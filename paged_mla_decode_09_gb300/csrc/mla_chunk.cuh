@@ -67,7 +67,8 @@ struct Rescale {
 };
 constexpr int kMaxClusters = 96;       // the combine's lanes take 3 clusters each
 
-struct __align__(8) Ctrl {
+struct __align__(16) Ctrl {
+  int4 unit[2][2];               // S: the unit whose queries land on q_bar (p0, p1, nrows, pos0), (h0, sp, skip, -)
   uint64_t kv_full[kMaxStages];
   uint64_t kv_empty[kMaxStages];
   uint64_t peer_kv[kMaxStages];  // S leader: the other S CTA's entry has landed
@@ -537,6 +538,8 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
         break;
       }
       if (e == 0) {
+        ctrl->unit[un & 1][0] = make_int4(u.p0, u.p1, u.k.nrows, u.k.pos0);
+        ctrl->unit[un & 1][1] = make_int4(u.k.h0, u.k.sp, u.k.skip, 0);
         mbar_expect_tx(qbar, static_cast<uint32_t>(C::kParts == 3 ? kRows * 1152 : qe * C::kQRows * 1152));
         qloaded = un + 1;
         if constexpr (C::kParts == 3)
@@ -1012,7 +1015,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t j = 0;                          // page
       bool ok = true;
       int why = 0;
-      while (ok && it.next(u)) {
+      // units come from the producer with their queries: loads of the schedule
+      // would stand between a unit's last P and the next one's queries
+      const uint32_t units = it.s < it.e ? static_cast<uint32_t>(it.nlast - it.nfirst + 1) : 0u;
+      while (ok && un < units) {
         // the unit's queries replace the previous unit's in TMEM once every
         // QK of that unit is done: the S of its last tile has landed
         if (jt > 0 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(jt - 1) % C::kNSB]),
@@ -1025,6 +1031,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           why = kWaitQEntry;
           break;
+        }
+        {
+          const int4 x = ctrl->unit[un & 1][0], y = ctrl->unit[un & 1][1];
+          u.p0 = x.x; u.p1 = x.y; u.k.nrows = x.z; u.k.pos0 = x.w;
+          u.k.h0 = y.x; u.k.sp = y.y; u.k.skip = y.z;
         }
         if (kF8 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->qs_full[un & 1]), (un >> 1) & 1, abort, p.timeout_ns)) {
           ok = false;

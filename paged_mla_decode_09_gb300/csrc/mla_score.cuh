@@ -20,7 +20,7 @@ constexpr int kRows = 128;    // rows per CTA
 // warps: 0 TMA, 1 MMA, 2 TMEM alloc, 4-11 row warps (2, 3: query scales of an e4m3 cache, -lse of the mass)
 constexpr int kThreads = 384;
 constexpr int kMaxSB = 3;      // S buffers
-constexpr int kCtrlBytes = 640;
+constexpr int kCtrlBytes = 768;
 constexpr int kMaxStages = 10;
 constexpr int kMaxP = 4;
 constexpr float kLog2e = 1.4426950408889634f;
