@@ -73,6 +73,8 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
   __shared__ int hist[4][kBins];
   __shared__ int buf[kWarps];
   __shared__ int pick[3];          // the digit of the k-th key, keys above it, whether all keys of it are kept
+  __shared__ uint32_t lim[4][2];   // least and greatest of a pass's keys
+  __shared__ uint32_t lims[2];     // the same over the cluster
   __shared__ int4 counts_w[kWarps];  // per warp, see below
   __shared__ int4 share;           // the block's sums of them, and its greatest position: read by the other blocks
   __shared__ int share_pos;
@@ -104,6 +106,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
     const bool cached = part <= p.smem_keys;
     int32_t* spos = reinterpret_cast<int32_t*>(keys) + p.smem_keys;
     for (int i = tid; i < 4 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
+    if (tid < 8) lim[tid >> 1][tid & 1] = tid & 1 ? 0u : 0xFFFFFFFFu;
     int last = L - 1;  // the greatest position
     {
       // Every slot below k gets its own weight and position back, also those
@@ -163,6 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
 #pragma unroll 1
     for (int pass = 0; pass < 4; ++pass) {
       const int shift = 24 - 8 * pass;
+      uint32_t least = 0xFFFFFFFFu, most = 0u;
       for (int t = r0 + tid; t - lane < r1; t += kThreads) {
         uint32_t x;
         if (pass == 0 || !cached) {
@@ -172,7 +176,17 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
           x = t < r1 ? keys[t - r0] : 0u;
         }
         const bool in = t < r1 && (x & mask) == prefix;
-        if (in) atomicAdd(&hist[pass][(x >> shift) & 255u], 1);
+        if (in) {
+          atomicAdd(&hist[pass][(x >> shift) & 255u], 1);
+          least = min(least, x);
+          most = max(most, x);
+        }
+      }
+      least = __reduce_min_sync(0xffffffffu, least);
+      most = __reduce_max_sync(0xffffffffu, most);
+      if (lane == 0) {
+        atomicMin(&lim[pass][0], least);
+        atomicMax(&lim[pass][1], most);
       }
       sync_ranks();
       // from the greatest digit down: thread i has bin 255 - i of all blocks
@@ -184,6 +198,15 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
         for (int r = 0; r < 8; ++r) c[r] = r < cs ? ld_cluster_u32(mapa(at, r)) : 0u;
 #pragma unroll
         for (int r = 0; r < 8; ++r) own += static_cast<int>(c[r]);
+      } else if (warp == kBins / 32) {  // lanes r and 8 + r: block r's least and greatest key
+        const int r = lane & 7, w = lane >> 3 & 1;
+        const uint32_t x = r < cs ? ld_cluster_u32(mapa(smem_u32(&lim[pass][w]), r)) : (w ? 0u : 0xFFFFFFFFu);
+        const uint32_t a = __reduce_min_sync(0xffffffffu, w ? 0xFFFFFFFFu : x);
+        const uint32_t b = __reduce_max_sync(0xffffffffu, w ? x : 0u);
+        if (lane == 0) {
+          lims[0] = a;
+          lims[1] = b;
+        }
       }
       int sum = own;
 #pragma unroll
@@ -201,6 +224,10 @@ __global__ void __launch_bounds__(kThreads, 2) mla_evict_select_kernel(const __g
         pick[2] = before + own == need;
       }
       __syncthreads();
+      if (lims[0] == lims[1]) {  // equal keys (tokens never attended to, say): that is the k-th, ties by slot
+        prefix = lims[0];
+        break;
+      }
       prefix |= static_cast<uint32_t>(pick[0]) << shift;
       mask |= 255u << shift;
       need -= pick[1];
