@@ -285,6 +285,19 @@ def test_evict_longer_than_shared_memory(positions):
     check_evict(r)
 
 
+def test_evict_longer_than_shared_memory_in_place():
+    e = evict_case([170000, 90], 3000, 4, 100, kv_dtype="fp8_e4m3", seed=3)
+    r = Evict(e)
+    r.mass_out, r.pos_out, r.new_lens = r.mass, r.pos, r.lens
+    r.launch()
+    assert r.status() == 0
+    n, kept, mo, po, cache = oracle.evict_ref(e["mass"], e["positions"], e["seq_lens"], e["page_table"], e["kv_cache"],
+                                              3000, 4, 100)
+    assert np.array_equal(r.lens.cpu().numpy(), n) and np.array_equal(r.kept.cpu().numpy(), kept)
+    assert np.array_equal(r.mass.cpu().numpy(), mo) and np.array_equal(r.pos.cpu().numpy(), po)
+    assert np.array_equal(r.bits(), cache)
+
+
 def test_evict_in_place_outputs():
     e = evict_case([700, 64, 1300], 200, 4, 40, seed=6)
     r = Evict(e)
