@@ -501,6 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 constexpr int kKeys = 128;   // keys of a tile (M of the MMAs)
 constexpr int kSlot = 73728;  // a page of the cache, or 64 query rows
 constexpr int kSlots = 3;
+constexpr int kFull = 2 * kSlots;  // barriers of the ring's entries: two rounds, see the issuing warps
 constexpr int kNlOff = kSlots * kSlot;            // [3][64] -lse of a row tile, in log2 units
 constexpr int kPartOff = kNlOff + 3 * 64 * 4;     // [2][128] the second group's sums
 constexpr int kClusOff = kPartOff + 2 * kKeys * 4;  // [8][128] the sums of the cluster's CTAs (in its first)
@@ -567,9 +568,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   Ctrl* ctrl = reinterpret_cast<Ctrl*>(data + kRowsData);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&ctrl->kv_full[i]), 1);
-      mbar_init(smem_u32(&ctrl->kv_empty[i]), 1);
+    for (int i = 0; i < kFull; ++i) mbar_init(smem_u32(&ctrl->kv_full[i]), 1);
+    for (int i = 0; i < 3; ++i) {
       mbar_init(smem_u32(&ctrl->s_full[i]), 2);   // the tile's QK and its -lse (warp 3)
       mbar_init(smem_u32(&ctrl->s_empty[i]), 4);  // the group that read it
     }
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctrl->sums[i]), 4);
     }
     mbar_init(smem_u32(&ctrl->q_full), 8);
-    mbar_init(smem_u32(&ctrl->drain), 1);
+    mbar_init(smem_u32(&ctrl->drain), 2);  // both issuing warps
     ctrl->abort = 0;
     ctrl->first = p.B;
     ctrl->start = 0;
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const uint32_t slot = smem_u32(ring + (i % kSlots) * kSlot);
           if (e == 0) mbar_expect_tx(qbar, static_cast<uint32_t>(pages * kPage * (kF8 ? 576 : 1152)));
-          mbar_arrive(smem_u32(&ctrl->kv_full[i % kSlots]));
+          mbar_arrive(smem_u32(&ctrl->kv_full[i % kFull]));
           if (e >= pages) continue;  // an odd last page: its lanes are not stored
           int32_t pid = __ldg(p.page_table + static_cast<int64_t>(u.b) * p.pt_stride + u.t0 / kPage + e);
           if (pid < 0 || pid >= p.num_pages) {
@@ -658,7 +658,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t slot = smem_u32(ring + (i % kSlots) * kSlot), bar = smem_u32(&ctrl->kv_full[i % kSlots]);
+          const uint32_t slot = smem_u32(ring + (i % kSlots) * kSlot), bar = smem_u32(&ctrl->kv_full[i % kFull]);
           const int row = u.b * p.R + 64 * n;
           mbar_expect_tx(bar, static_cast<uint32_t>(kSlot));
           tma_load_3d(slot, &tm_qn, 0, row, 0, bar);
@@ -666,10 +666,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) raise_timeout(p, ctrl, kWaitEmpty, i);
-      for (uint32_t q = 0; q < static_cast<uint32_t>(kSlots) && q < i; ++q) {
-        const uint32_t last = i - 1 - ((i - 1 - q) % kSlots);
+      for (uint32_t q = 0; q < static_cast<uint32_t>(kFull) && q < i; ++q) {
+        const uint32_t last = i - 1 - ((i - 1 - q) % kFull);
         const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(smem_u32(&ctrl->kv_full[q]), (last / kSlots) & 1) && globaltimer_ns() - t0 < p.timeout_ns) {
+        while (!mbar_try_wait(smem_u32(&ctrl->kv_full[q]), (last / kFull) & 1) && globaltimer_ns() - t0 < p.timeout_ns) {
         }
       }
       if (un) {
@@ -679,13 +679,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == 1) {
+  } else if (warp < 3) {
+    // Warps 1 and 2 issue the even and the odd row tiles: what a warp spends on
+    // a wait and a commit (~230 cycles beside the row warps) passes while the
+    // other one's MMAs run.  A warp waits for its own tiles alone.  No phase
+    // can pass it by: an entry's barrier comes again six entries later, when
+    // the slot has been used once more, and that needs this entry consumed.
+    // (Every key tile has row tiles of both warps, or is the CTA's only one.)
     uint32_t i = 0, j = 0;
     while (ok && it.next(u)) {
-      for (int e = 0; e < 2 && ok; ++e, ++i)
-        ok = mbar_wait_warp(smem_u32(&ctrl->kv_full[i % kSlots]), (i / kSlots) & 1, abort, p.timeout_ns);
-      why = kWaitLanded;
-      if (!ok) break;
+      i += 2;
       if (!mbar_wait_warp(smem_u32(&ctrl->q_full), un & 1, abort, p.timeout_ns)) {
         ok = false;
         why = kWaitQFull;
@@ -693,8 +696,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++un;
       for (int n = first; n < all_tiles; n += step, ++j, ++i) {
+        if ((j & 1u) != static_cast<uint32_t>(warp - 1)) continue;
         const int st = static_cast<int>(i % kSlots), sb = static_cast<int>(j % 3);
-        if (!mbar_wait_all_warp(smem_u32(&ctrl->kv_full[st]), (i / kSlots) & 1, smem_u32(&ctrl->s_empty[sb]),
+        // (that this tile has landed also says that the tile three before it,
+        // whose score buffer it takes, was issued)
+        if (!mbar_wait_all_warp(smem_u32(&ctrl->kv_full[i % kFull]), (i / kFull) & 1, smem_u32(&ctrl->s_empty[sb]),
                                 ((j / 3) & 1) ^ 1, 0u, 0u, 0u, 0u, abort, p.timeout_ns)) {
           ok = false;
           why = kWaitLanded;
@@ -758,10 +764,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t i = 0, j = 0;
     while (ok && it.next(u)) {
       // the tile's keys replace the earlier ones in TMEM once every QK with
-      // those is done
-      if (j > 0 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - 1) % 3]), ((j - 1) / 3) & 1, abort,
-                                                p.timeout_ns)) {
-        ok = false;
+      // those is done: the last tile of either issuing warp
+      for (uint32_t back = 1; back <= 2 && ok; ++back)
+        ok = j < back || mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - back) % 3]), ((j - back) / 3) & 1,
+                                                     abort, p.timeout_ns);
+      if (!ok) {
         why = kWaitSPrev;
         break;
       }
