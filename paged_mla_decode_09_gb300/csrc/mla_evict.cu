@@ -21,8 +21,8 @@
 //
 // What bounds it: the latency of about a dozen walks and barriers (a block per
 // request took 59 us for 16 requests of up to 32K tokens, clusters take 28), then
-// the moved rows' bytes.  64 requests of 4.2K tokens take 18 us, one of 600
-// 7.8.  (The moves by the selecting blocks themselves took 3 to 9 us longer: a
+// the moved rows' bytes.  64 requests of 4.2K tokens take 15.5 us, one of 600
+// 7.7.  (The moves by the selecting blocks themselves took 3 to 9 us longer: a
 // launch of their own finds its blocks resident already and spreads the rows
 // over every SM.)
 #include <cuda_runtime.h>
