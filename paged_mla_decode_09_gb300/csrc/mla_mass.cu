@@ -66,7 +66,7 @@ struct __align__(8) Ctrl {
   uint64_t kv_full[chunk::kMaxStages];
   uint64_t kv_empty[chunk::kMaxStages];
   uint64_t q_bar[2];
-  uint64_t s_full[3];
+  uint64_t s_full[6];  // mla_mass_kernel: 3
   uint64_t s_empty[3];
   uint64_t q_full;
   uint64_t sums[2];
@@ -502,6 +502,17 @@ constexpr int kKeys = 128;   // keys of a tile (M of the MMAs)
 constexpr int kSlot = 73728;  // a page of the cache, or 64 query rows
 constexpr int kSlots = 3;
 constexpr int kFull = 2 * kSlots;  // barriers of the ring's entries: two rounds, see the issuing warps
+// Barriers that say a row tile is scored (tile j: barrier j % 6, phase j / 6),
+// two rounds of the three score buffers.  A parity wait for a phase also passes
+// while the phase two before it was the last to complete, so whoever waits for
+// tile j must know that tile j - 6 is complete, and tile j + 6 must not
+// complete before the wait has passed.  A row group knows of j - 6: it has the
+// same parity, so the group read it itself.  And j + 6 needs j + 3 read out of
+// the score buffer, which was not issued before this group had read j.  (With
+// three barriers a group would have to know of tile j - 3, which the other
+// group reads and the other warp issues: where its rows land late, tile j - 2
+// comes first and the wait for j passes at once.)
+constexpr int kScoreFull = 6;
 constexpr int kNlOff = kSlots * kSlot;            // [3][64] -lse of a row tile, in log2 units
 constexpr int kPartOff = kNlOff + 3 * 64 * 4;     // [2][128] the second group's sums
 constexpr int kClusOff = kPartOff + 2 * kKeys * 4;  // [8][128] the sums of the cluster's CTAs (in its first)
@@ -569,10 +580,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kFull; ++i) mbar_init(smem_u32(&ctrl->kv_full[i]), 1);
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(smem_u32(&ctrl->s_full[i]), 2);   // the tile's QK and its -lse (warp 3)
-      mbar_init(smem_u32(&ctrl->s_empty[i]), 4);  // the group that read it
-    }
+    for (int i = 0; i < kScoreFull; ++i) mbar_init(smem_u32(&ctrl->s_full[i]), 2);  // a tile's QK, its -lse (warp 3)
+    for (int i = 0; i < 3; ++i) mbar_init(smem_u32(&ctrl->s_empty[i]), 4);          // the group that read it
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctrl->q_bar[i]), 1);
       mbar_init(smem_u32(&ctrl->sums[i]), 4);
@@ -623,8 +632,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto acquire = [&](uint32_t what) -> bool {
         if (i >= kSlots) {
           const uint32_t k = held[0] >> 1;
-          if (!mbar_wait(smem_u32(held[0] & 1u ? &ctrl->q_full : &ctrl->s_full[k % 3]),
-                         (held[0] & 1u ? k : k / 3) & 1, abort, p.timeout_ns))
+          if (!mbar_wait(smem_u32(held[0] & 1u ? &ctrl->q_full : &ctrl->s_full[k % kScoreFull]),
+                         (held[0] & 1u ? k : k / kScoreFull) & 1, abort, p.timeout_ns))
             return false;
         }
         held[0] = held[1];
@@ -715,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int k = 0; k < 4; ++k)
             mma_ts_e<false>(dcol, tmem + d * 32 + k * 8, dq + static_cast<uint64_t>(d * (8192 >> 4) + k * 2),
                             C::kIdescQK, (d | k) ? 1u : 0u);
-        mma_commit_e(smem_u32(&ctrl->s_full[sb]));
+        mma_commit_e(smem_u32(&ctrl->s_full[j % kScoreFull]));
       }
     }
     if (!ok && lane == 0) raise_timeout(p, ctrl, why, j);
@@ -751,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         nl[sb * 64 + lane] = v[0];
         nl[sb * 64 + 32 + lane] = v[1];
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctrl->s_full[sb]));
+        if (lane == 0) mbar_arrive(smem_u32(&ctrl->s_full[j % kScoreFull]));
       }
     }
     if (!ok && lane == 0) raise_timeout(p, ctrl, why, j);
@@ -766,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the tile's keys replace the earlier ones in TMEM once every QK with
       // those is done: the last tile of either issuing warp
       for (uint32_t back = 1; back <= 2 && ok; ++back)
-        ok = j < back || mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - back) % 3]), ((j - back) / 3) & 1,
-                                                     abort, p.timeout_ns);
+        ok = j < back || mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[(j - back) % kScoreFull]),
+                                                     ((j - back) / kScoreFull) & 1, abort, p.timeout_ns);
       if (!ok) {
         why = kWaitSPrev;
         break;
@@ -820,7 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = first; n < all_tiles; n += step, ++j) {
         if ((j & 1u) != static_cast<uint32_t>(gg)) continue;
         const int sb = static_cast<int>(j % 3);
-        if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (j / 3) & 1, abort, p.timeout_ns)) {
+        if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[j % kScoreFull]), (j / kScoreFull) & 1, abort,
+                                         p.timeout_ns)) {
           ok = false;
           why = kWaitS;
           break;
