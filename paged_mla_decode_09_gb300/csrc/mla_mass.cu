@@ -40,6 +40,7 @@
 
 #include "mla_evict.h"
 #include "mla_host.h"
+#include "mla_mass_plan.h"
 #include "mla_score.cuh"
 
 namespace mla {
@@ -901,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp == 2) tmem_dealloc(tmem, 512);
-  if (step > 1) {  // a cluster has one key tile at most
+  if (step > 1) {  // a cluster has one key tile at most (cluster_of)
     __syncwarp();
     cluster_sync();
     TileIter last;
@@ -1022,13 +1023,10 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
   p.cols = mass_cols;
   p.cap = d->max_pages_per_req * 64 < mass_cols ? d->max_pages_per_req * 64 : mass_cols;
   p.num_fresh = num_fresh;
-  // CTAs per key tile: while every tile that the lengths allow can have twice
-  // as many (128 CTAs in clusters of 8 fit at once), and row tiles for each
-  p.cluster = 1;
-  if (rows) {
-    const int64_t tiles = static_cast<int64_t>(d->batch) * ((p.cap + mla::mass::kKeys - 1) / mla::mass::kKeys);
-    while (p.cluster < 8 && 2 * p.cluster * tiles <= 128 && 2 * p.cluster * 64 <= R) p.cluster *= 2;
-  }
+  // CTAs per key tile, by the most tiles that the lengths allow
+  p.cluster = rows ? mla::mass::cluster_of(
+                         static_cast<int64_t>(d->batch) * ((p.cap + mla::mass::kKeys - 1) / mla::mass::kKeys), R, sms)
+                   : 1;
   p.c2 = log2_scale(scale, f8 ? kv_scale : 1.f);
   p.timeout_ns = 2000000000ull;
   cudaStream_t stream = static_cast<cudaStream_t>(stream_v);
