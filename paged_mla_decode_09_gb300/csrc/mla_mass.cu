@@ -29,8 +29,9 @@
 //     Where a call has few key tiles, a cluster of 2 to 8 CTAs shares one,
 //     every CTA some of the row tiles, and the first adds up their sums.
 //
-// No atomics: a key belongs to one CTA, which adds in a fixed order, so
-// results do not depend on timing or slicing.
+// No atomics: a key belongs to one CTA, or to one cluster whose first CTA adds
+// up the others' sums, in a fixed order either way, so results do not depend
+// on timing or slicing.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -606,6 +607,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.cluster > 1) {  // the first CTA has begun before the others write to its shared memory
+    __syncwarp();
+    cluster_sync();
+  }
   griddep_wait();
   griddep_launch_dependents();
   if (bad && blockIdx.x == 0) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);

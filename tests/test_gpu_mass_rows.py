@@ -153,3 +153,22 @@ def test_loops_of_calls_agree_bit_for_bit(B, Q, H, kv_dtype):
         if k % 50 == 49:
             assert c.status() == 0
     assert not bool(differs)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("B,Q,H,lens", [(2, 8, 64, [1000, 65]), (1, 32, 32, [2048]), (5, 3, 100, [700, 128, 1, 640, 333])])
+def test_clusters_that_share_a_key_tile(B, Q, H, lens, kv_dtype):
+    """8 and 2 CTAs of a cluster share a key tile; calls one behind the other,
+    so that a cluster begins while the kernel before it ends."""
+    assert sum(-(-max(lens) // 128) for _ in lens) <= 32
+    lens = [max(n, Q) for n in lens]
+    c = Call(B, Q, H, lens, kv_dtype, seed=Q)
+    c.launch(1, c.mass, c.out)
+    assert c.status() == 0
+    c.check(c.out, 1, c.mass)
+    first, other = c.out.clone(), [torch.full_like(c.out, -1.0) for _ in range(20)]
+    for _ in range(10):
+        for o in other:
+            c.launch(1, c.mass, o)
+        assert c.status() == 0
+        assert all(torch.equal(o, first) for o in other)
