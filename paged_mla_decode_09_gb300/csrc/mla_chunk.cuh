@@ -892,6 +892,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             why = kWaitQFull;
             break;
           }
+          if constexpr (kF8 && kCg == 2) mbar_acquire_shared(smem_u32(&ctrl->q_full), un & 1);  // both rope tiles
           if (lane == 0 && C::kParts == 1)  // the query entries' slots go back to the producers
             for (int e = qe; e > 0; --e) {
               const uint32_t bar = smem_u32(&ctrl->kv_empty[(i - e) % C::kNStS]);
@@ -1069,8 +1070,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          if (kCg == 2) mbar_arrive_remote(mapa(smem_u32(&ctrl->q_full), 0));
+        if (lane == 0) {  // (an e4m3 pair's rope tile is ordinary stores that the leader's MMAs read)
+          if (kCg == 2 && kF8) mbar_arrive_shared(mapa(smem_u32(&ctrl->q_full), 0));
+          else if (kCg == 2) mbar_arrive_remote(mapa(smem_u32(&ctrl->q_full), 0));
           else mbar_arrive(smem_u32(&ctrl->q_full));
         }
         i += qe + C::kParts * static_cast<uint32_t>((u.p1 - u.p0 + kCg - 1) / kCg);
@@ -1270,8 +1272,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           // come only after PV(j)
           if (lane == 0) mbar_expect_tx(smem_u32(&ctrl->p_full[ps]), C::kPTx);
           uint8_t* slot = vring + vs * C::kSlotV;
+          // V rows that this page has from ordinary stores: a pair's leader
+          // and the other CTA order them at cluster scope
+          const int valid = u.k.len - real_page(u.k, vp) * kPage;
+          const bool stored = kF8 || valid < kPage;
           if constexpr (!kF8) {
-            const int valid = u.k.len - real_page(u.k, vp) * kPage;
             if (valid < kPage) {
               const int v0 = valid > 0 ? valid : 0;
               for (int row = v0 + (lane >> 3); row < kPage; row += 4)
@@ -1287,9 +1292,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (kCg == 2 && !leader) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(mapa(smem_u32(&ctrl->peer_pv[ps]), kCg));
+            if (lane == 0) {
+              const uint32_t bar = mapa(smem_u32(&ctrl->peer_pv[ps]), kCg);
+              if (stored) mbar_arrive_shared(bar);
+              else mbar_arrive_remote(bar);
+            }
             continue;
           }
+          if (kCg == 2 && stored) mbar_acquire_shared(smem_u32(&ctrl->peer_pv[ps]), (j / C::kNP) & 1);
           const uint64_t dv = smem_desc(smem_u32(slot), C::kVBox, 1024, kSwizzle128B);
           const uint64_t dp = smem_desc(smem_u32(data + ps * C::kPBytes), C::kPLbo, C::kPSbo, kSwizzleNone);
           // MMA h: N = 256 columns, each CTA's boxes (kVBoxes / 2) h ..

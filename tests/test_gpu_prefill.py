@@ -277,3 +277,19 @@ def test_many_blocks_per_cluster(window, sinks, kv_dtype):
             ro, rl = oracle.attend(q, rows, rows.shape[0], c.scale)
             to, tl = K.error_bounds(c, b, i)
             assert np.all(np.abs(out[t] - ro) <= to) and np.all(np.abs(lse[t] - rl) <= tl), (b, i)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+def test_pairs_with_garbage_behind_every_sequence_repeat_bit_for_bit(kv_dtype):
+    """A pair's two CTAs each clear (bf16) or expand (e4m3) their half of a
+    page with ordinary stores, which the other CTA's products read: NaN behind
+    each of many sequences must never show, call after call."""
+    c = K.make([5] * 24, [5 + (61 * k) % 700 for k in range(24)], 64, kv_dtype=kv_dtype, seed=77)
+    r = run_and_check(c)
+    out, lse = r.out.clone(), r.lse.clone()
+    differs = torch.zeros((), dtype=torch.bool, device="cuda")
+    for _ in range(300):
+        r.out.zero_()
+        r.launch()
+        differs |= (r.out != out).any() | (r.lse != lse).any()
+    assert r.result()[2] == 0 and not bool(differs)
