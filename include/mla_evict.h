@@ -50,7 +50,8 @@ size_t mla_attn_mass_workspace_size(const mla_dims* d, int device);
  * nothing) adds nothing.
  *
  *   d, q_nope, q_pe, kv_cache, page_table, seq_lens, scale, kv_scale: as for
- *               mla_decode; every page of a request's L tokens is read
+ *               mla_decode, and scale * kv_scale * log2(e) finite and above 0
+ *               in fp32; every page of a request's L tokens is read
  *   lse         fp32 [B][q_len][H], as the attention returned it
  *   num_fresh   the last num_fresh tokens start from zero instead of mass
  *               (a step's new tokens), >= 0

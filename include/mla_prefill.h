@@ -78,7 +78,8 @@ size_t mla_prefill_workspace_size(const mla_prefill_dims* d, int device);
  *   window      0: none; >= 1 (MLA_ERR_INVALID_ARG below 0)
  *   num_sinks   >= 0; without a window it changes nothing
  *   scale       softmax scale, > 0 and finite
- *   kv_scale    e4m3 cache: > 0 and finite; bf16 cache: ignored
+ *   kv_scale    e4m3 cache: > 0 and finite; bf16 cache: ignored.
+ *               scale * kv_scale * log2(e) must be finite and above 0 in fp32
  *   out         bf16 [total_q][H][512], 32-byte aligned
  *   lse         fp32 [total_q][H]
  *   workspace   >= mla_prefill_workspace_size bytes, 256-byte aligned; not

@@ -179,8 +179,7 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   if (!q_nope || !q_pe || !kv_cache || !page_table || !seq_lens || !out || !lse || !workspace)
     return MLA_ERR_INVALID_ARG;
   if (window < 0 || sinks < 0) return MLA_ERR_INVALID_ARG;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
-  if (s.f8 && (!(kv_scale > 0.f) || !std::isfinite(kv_scale))) return MLA_ERR_INVALID_ARG;
+  if (!mla::host::scale_ok(scale, kv_scale, s.f8)) return MLA_ERR_INVALID_ARG;
   if (!aligned(q_nope, 32) || !aligned(q_pe, 32) || !aligned(kv_cache, 16) || !aligned(out, 32) || !aligned(lse, 4) ||
       !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(workspace, 256))
     return MLA_ERR_ALIGNMENT;

@@ -1076,7 +1076,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           else mbar_arrive(smem_u32(&ctrl->q_full));
         }
         i += qe + C::kParts * static_cast<uint32_t>((u.p1 - u.p0 + kCg - 1) / kCg);
-        const float c2 = kF8 ? p.c2 * qs : p.c2;  // qs is a power of two
+        // qs is a power of two, 2^-107 of a row of zeros: a product that small
+        // counts as the least normal value (its scores are below 2^-90 in
+        // either case), as 0 would turn masked scores into NaN
+        float c2 = kF8 ? p.c2 * qs : p.c2;
+        if (kF8 && c2 < 0x1p-126f) c2 = 0x1p-126f;
         const bool real = br < u.k.nrows;
         // padding rows follow the block's last row (their results go nowhere)
         const int pos = u.k.pos0 + (u.k.h0 + (real ? br : u.k.nrows - 1)) / p.H;

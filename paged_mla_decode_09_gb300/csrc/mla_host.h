@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <cmath>
 #include <cstddef>
 #include <cstdint>
 #include <mutex>
@@ -69,9 +70,17 @@ inline bool map2(CUtensorMap* m, const void* base, int64_t rows, int width, int 
 }
 
 // scale * log2(e) * kv_scale rounded to fp32 once: the factor of every score,
-// so that its error (2^-24 relative) is that of one rounding.
+// so that its error (2^-24 relative) is that of one rounding.  It has to be
+// finite and above 0: 0 times an infinity, of a masked score or of the factor,
+// is a NaN.
 inline float log2_scale(float scale, float kv_scale) {
   return static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074 * static_cast<double>(kv_scale));
+}
+inline bool scale_ok(float scale, float kv_scale, bool f8) {
+  if (!(scale > 0.f) || !std::isfinite(scale)) return false;
+  if (f8 && (!(kv_scale > 0.f) || !std::isfinite(kv_scale))) return false;
+  const float c = log2_scale(scale, f8 ? kv_scale : 1.f);
+  return c > 0.f && std::isfinite(c);
 }
 
 // Launches a kernel with programmatic stream serialization: it may begin while

@@ -976,8 +976,7 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
       num_fresh < 0)
     return MLA_ERR_INVALID_ARG;
   const bool f8 = d->kv_dtype == MLA_KV_FP8_E4M3;
-  if (!(scale > 0.f) || !std::isfinite(scale)) return MLA_ERR_INVALID_ARG;
-  if (f8 && (!(kv_scale > 0.f) || !std::isfinite(kv_scale))) return MLA_ERR_INVALID_ARG;
+  if (!scale_ok(scale, kv_scale, f8)) return MLA_ERR_INVALID_ARG;
   if (!aligned(q_nope, 32) || !aligned(q_pe, 32) || !aligned(kv_cache, 16) || !aligned(page_table, 4) ||
       !aligned(seq_lens, 4) || !aligned(lse, 4) || !aligned(mass, 4) || !aligned(mass_out, 4) || !aligned(workspace, 256))
     return MLA_ERR_ALIGNMENT;

@@ -293,3 +293,15 @@ def test_pairs_with_garbage_behind_every_sequence_repeat_bit_for_bit(kv_dtype):
         r.launch()
         differs |= (r.out != out).any() | (r.lse != lse).any()
     assert r.result()[2] == 0 and not bool(differs)
+
+
+@pytest.mark.parametrize("heads", [16, 160])
+def test_zero_queries_under_a_tiny_cache_scale(heads):
+    """An e4m3 cache's queries carry their row's power-of-two scale, 2^-107 for
+    a row of zeros; times a small kv_scale that is below what fp32 holds.  The
+    row's scores are 0, its weights even, also where a page is only partly seen."""
+    c = K.make([3, 1], [200, 70], heads=heads, kv_dtype="fp8_e4m3", window=90, sinks=2, seed=51)
+    c.kv_scale = 1e-13
+    c.q_nope[:, ::2] = 0
+    c.q_pe[:, ::2] = 0
+    run_and_check(c)
