@@ -12,10 +12,27 @@
  *                  and latest ones), and moves the rows kept behind the budget
  *                  into the places of the dropped ones.
  *
- * A step writes its rows (mla_kv_pack), attends (mla_prefill, mla_decode,
- * mla_decode_window), accumulates (mla_attn_mass, from the same queries and
- * the log-sum-exps that the attention returned) and, when a request is over
- * its budget, evicts.  Conventions as in mla_decode.h: caller-owned device
+ * A step writes its rows (mla_kv_pack), attends (mla_decode, or mla_prefill
+ * without a window), accumulates (mla_attn_mass, from the same queries and the
+ * log-sum-exps that the attention returned) and, when a request is over its
+ * budget, evicts.  What does not go together:
+ *
+ *   - A windowed or top-k step (mla_decode_window, mla_prefill with a window,
+ *     mla_decode_sparse) and mla_attn_mass.  The mass is over every token up to
+ *     the query's own; with a log-sum-exp over fewer keys exp(s - lse) is no
+ *     share of a softmax (it may pass 1), and the pages of tokens outside a
+ *     window, which the caller may have freed, would be read.
+ *   - mla_evict and windows.  After an eviction a slot is no longer a position:
+ *     the kept tokens from behind the budget, the latest among them, sit in
+ *     whatever slots were free.  mla_decode_window and mla_prefill with a
+ *     window choose keys by slot, so from then on the request is attended to
+ *     without a window.
+ *
+ * mla_attn_mass takes the same number of queries for every request.  After a
+ * ragged mla_prefill the caller gathers the last q_len tokens' queries and
+ * log-sum-exps of each request, with q_len at most the fewest that one brought.
+ *
+ * Conventions as in mla_decode.h: caller-owned device
  * buffers, asynchronous on `stream`, no allocation, no synchronisation, an
  * mla_status return, device errors OR-ed into word 0 of the workspace (read
  * it with mla_query_status).  The calls can be captured into a CUDA graph.
@@ -52,7 +69,8 @@ size_t mla_attn_mass_workspace_size(const mla_dims* d, int device);
  *   d, q_nope, q_pe, kv_cache, page_table, seq_lens, scale, kv_scale: as for
  *               mla_decode, and scale * kv_scale * log2(e) finite and above 0
  *               in fp32; every page of a request's L tokens is read
- *   lse         fp32 [B][q_len][H], as the attention returned it
+ *   lse         fp32 [B][q_len][H], as the attention over all tokens up to the
+ *               query's own returned it
  *   num_fresh   the last num_fresh tokens start from zero instead of mass
  *               (a step's new tokens), >= 0
  *   mass        fp32 [B][mass_cols], or null: every token starts from zero
@@ -103,14 +121,16 @@ size_t mla_evict_workspace_size(int32_t batch, int32_t budget);
  *     positions_out[b][t] = positions[b][o];   kept[b][t] = -1 for t >= k.
  *
  * Entries of mass_out and positions_out from k on are not touched.  The rows
- * behind k stay in the cache, unused.  (Attention over the kept rows does not
- * depend on their order; the latest tokens of later steps follow in slot k.)
+ * behind k stay in the cache, unused.  (Attention without a window does not
+ * depend on the order of the kept rows; the tokens of later steps follow in
+ * slot k.)
  *
  *   mass        fp32 [B][mass_cols]; seq_lens[b] is in
  *               [0, min(mass_cols, max_pages_per_req * 64)] (else
  *               MLA_DEV_BAD_SEQ_LEN, and the length is clamped)
  *   positions   int32 [B][mass_cols], >= 0, or null (positions_out is then
- *               not written and may be null)
+ *               not written and may be null).  Null is right for a request's
+ *               first eviction only: after it a slot is no longer a position
  *   kv_cache    [num_pages][64][576], 16-byte aligned; only rows that receive
  *               a token are written, so a page may be shared with another
  *               request only while all of its slots stay where they are in

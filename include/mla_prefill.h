@@ -17,6 +17,10 @@
  *     s_t = (q_nope . c_kv[t] + q_pe . k_pe[t]) * scale
  *     out = sum_t softmax(s)_t * c_kv[t],   lse = ln sum_t exp(s_t)
  *
+ * Key t is the row in slot t of the request.  On a cache that mla_evict (see
+ * mla_evict.h) has shortened, slots are no longer positions: call without a
+ * window there.
+ *
  * Conventions as in mla_decode.h: caller-owned device buffers, asynchronous
  * on `stream`, no allocation, no synchronisation, an mla_status return, and
  * device errors OR-ed into the status word of the workspace (read it with
@@ -101,6 +105,8 @@ size_t mla_decode_window_workspace_size(const mla_dims* d, int device);
  * window of `window` >= 1 tokens that ends with itself and the first
  * num_sinks >= 0 tokens.  Only the pages that hold them are read, so the
  * caller may have freed the others (their table entries are not looked at).
+ * Not for a request that mla_evict has shortened, and its log-sum-exps are not
+ * for mla_attn_mass (see mla_evict.h for both).
  * Works like mla_prefill with n_b = q_len for every request.
  */
 int mla_decode_window(const mla_dims* d, const void* q_nope, const void* q_pe, const void* kv_cache,
