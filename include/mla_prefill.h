@@ -17,6 +17,13 @@
  *     s_t = (q_nope . c_kv[t] + q_pe . k_pe[t]) * scale
  *     out = sum_t softmax(s)_t * c_kv[t],   lse = ln sum_t exp(s_t)
  *
+ * The weights are rounded before they multiply the rows: to bf16 with a bf16
+ * cache; with an e4m3 cache to f16, as shares of a reference that is at most the
+ * row's greatest weight.  There a weight below 2^-25 (e^-17) of the greatest
+ * counts as none, so that out misses at most 2^-25 of the greatest weight times
+ * the sum of |c_kv[t]| over such keys.  (It shows where a few tokens take nearly
+ * all the weight and have values near 0.)  lse counts every key in full.
+ *
  * Key t is the row in slot t of the request.  On a cache that mla_evict (see
  * mla_evict.h) has shortened, slots are no longer positions: call without a
  * window there.

@@ -7,6 +7,7 @@ import pytest
 
 import chunk_cases as K
 import oracle
+from paged_mla_decode_09_gb300 import workloads as W
 
 pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
@@ -305,3 +306,56 @@ def test_zero_queries_under_a_tiny_cache_scale(heads):
     c.q_nope[:, ::2] = 0
     c.q_pe[:, ::2] = 0
     run_and_check(c)
+
+
+@pytest.mark.parametrize("spikes", [(0,), (0, 330)])
+@pytest.mark.parametrize("gap", [10.0, 17.0, 22.0, 30.0])
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("B,Q,H", [(90, 1, 64), (40, 3, 128), (1, 2, 64)])
+def test_tokens_that_take_the_weight_and_give_nothing(B, Q, H, kv_dtype, gap, spikes):
+    """Sink tokens: scores `gap` above the others' (weights e^-gap of theirs for
+    the rest, down to 1e-13) and values of 0, so that the outputs are what the
+    others give.  A bf16 cache's weights keep their 8 bits however small they
+    are.  An e4m3 cache's are f16 against a reference that is no more than the
+    row's greatest score, so that rounding moves a weight by at most 2^-11 of
+    itself or, below 2^-14, half of f16's least step 2^-24, times the greatest
+    weight: 2^-25 w_max |v| more per key."""
+    c = K.make([Q] * B, [640] * B, H, kv_dtype=kv_dtype, seed=61, q_gain=0.2)
+    one = W.f32_to_bf16_bits(np.array([16.0], dtype=np.float32))[0]
+    c.q_pe[:] = 0
+    c.q_pe[:, :, 0] = one
+    top = np.float32(gap / (16.0 * c.scale))
+    zero_code = c.kv_cache.dtype.type(0)
+    for b in range(B):
+        for p in range(10):
+            c.kv_cache[c.page_table[b, p], :, 512:] = zero_code
+        for t in spikes:
+            row = c.kv_cache[c.page_table[b, t // 64], t % 64]
+            row[:] = zero_code
+            if kv_dtype == "bf16":
+                row[512] = W.f32_to_bf16_bits(np.array([top], dtype=np.float32))[0]
+            else:
+                row[512] = torch.tensor([top / c.kv_scale]).clamp(max=448).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    if kv_dtype != "bf16":  # a scale under which the sinks' keys fit
+        c.kv_scale = max(c.kv_scale, float(top) / 448.0 * 1.001)
+        for b in range(B):
+            for t in spikes:
+                c.kv_cache[c.page_table[b, t // 64], t % 64, 512] = \
+                    torch.tensor([top / c.kv_scale]).to(torch.float8_e4m3fn).view(torch.uint8).item()
+    r = Run(c)
+    r.launch()
+    out, lse, status = r.result()
+    assert status == 0
+    for b in sorted({0, B // 2, B - 1}):
+        for i in range(Q):
+            t = b * Q + i
+            keys = oracle.seen_keys(640 - Q + i, 0, 0)
+            rows = oracle.cache_rows_at(c.kv_cache, c.page_table[b], keys, kv_dtype, c.kv_scale)
+            q = np.concatenate([oracle.bf16_bits_to_f64(c.q_nope[t]), oracle.bf16_bits_to_f64(c.q_pe[t])], axis=-1)
+            ro, rl = oracle.attend(q, rows, rows.shape[0], c.scale)
+            to, tl = K.error_bounds(c, b, i)
+            if kv_dtype != "bf16":
+                w_max = np.exp(((q @ rows.T) * c.scale).max(axis=1) - rl)
+                to = to + 2.0**-25 * w_max[:, None] * np.abs(rows[:, :512]).sum(axis=0)
+            assert np.all(np.abs(lse[t] - rl) <= tl)
+            assert np.all(np.abs(out[t] - ro) <= to), (b, i, float((np.abs(out[t] - ro) / to).max()))
