@@ -41,10 +41,11 @@ struct Shape {
 
 // Rows per block: 256 (two CTAs per MMA) where a request brings more than 128
 // rows on average, else 128.  Measured on GB300: 128 x 2 tokens x 128 heads
-// over windows of 2048 (e4m3) 137 us at 256 against 178 at 128; 2 x 512 tokens
+// over windows of 2048 (e4m3) 142 us at 256 against 178 at 128; 2 x 512 tokens
 // of 128 heads over 8K keys 1279 against 1471; 64 x 64 heads x 1 token over
 // windows of 4096, where three quarters of a 256-row block are padding, 125
-// against 78.
+// against 78.  (Calls with the same rows for every request.  Where one long
+// chunk lifts the mean of many short requests, these pad like the last.)
 int Shape::cg() const { return T * H > 128 * B ? 2 : 1; }
 
 // [status | blkoff | blocks | prefix | cinfo | cut blocks | partial outputs | partial lse]
@@ -226,13 +227,15 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   p.sinks = sinks;
   // a piece's start in pages' time: swept on GB300; flat for bf16, an e4m3
   // pair splits its 256 query rows meanwhile (ragged chunks 1477 us at 6, 1427
-  // at 10, 1429 at 15, 1459 at 20; two drafts over windows 148, 145, 145, 149)
+  // at 10, 1429 at 15, 1459 at 20; two drafts over windows 148, 145, 145, 149;
+  // all about 2 % longer since a pair's CTAs order their stores)
   p.unit_cost = s.f8 && cg == 2 ? 15 : 6;
   // what a cut costs, in pages of a cluster's time (~0.75 us): a launch's worth
   // of latency, a block's partials stored by one CTA, all partials written and
   // read.  Measured, one block per cluster against even slices: 1 x 16 heads
   // equal at 5 pages (17.4 us), 1 x 128 at 8, 8 x 64 at 11, 8 x 128 at 15;
-  // 64 x 64 heads x 66 pages (56 in even slices) 78 us against 86
+  // 64 x 64 heads x 66 pages (56 in even slices) 78 us against 86.  The rule is
+  // a line through these points, not measured between them
   const int64_t total_rows = s.T * s.H, rows = total_rows / s.B < p.BR ? total_rows / s.B : p.BR;
   const int64_t whole = 5 + rows / 40 + total_rows / 600;
   p.whole_pages = static_cast<int32_t>(whole < 1000 ? whole : 1000);

@@ -25,7 +25,7 @@
 //     cycles per 128 keys x 64 rows.  (With the queries kept instead, every
 //     CTA moved and split all row blocks for the few pages of its slice: 503
 //     us for 32 tokens x 128 heads over 75K keys of four requests, e4m3; this
-//     way 194, the pipe 87 % busy.)
+//     way 192, the pipe 87 % busy.)
 //     Where a call has few key tiles, a cluster of 2 to 8 CTAs shares one,
 //     every CTA some of the row tiles, and the first adds up their sums.
 //
