@@ -13,7 +13,10 @@ from .chunk import cache_rows_at, mla_prefill_ref, seen_keys
 from .e4m3 import e4m3_decode_table, e4m3_encode, e4m3_to_f64
 from .evict import attn_mass_ref, evict_ref
 from .kv_pack import kv_pack_ref
+from .pages import page_fork_ref, page_resize_ref
+from .rope import new_slots, rope_frequencies_ref, rotate_ref
 from .sparse import mla_decode_sparse_ref
+from .tree import ancestors, mla_tree_ref, tree_commit_ref, tree_keys, verify_ref
 from .mla_oracle import (
     attend,
     bf16_bits_to_f64,
@@ -26,6 +29,7 @@ from .mla_oracle import (
 )
 
 __all__ = [
+    "ancestors",
     "attend",
     "attn_mass_ref",
     "cache_rows_at",
@@ -42,6 +46,15 @@ __all__ = [
     "mla_decode_ref_pieces",
     "mla_decode_sparse_ref",
     "mla_prefill_ref",
+    "mla_tree_ref",
+    "new_slots",
+    "page_fork_ref",
+    "page_resize_ref",
+    "rope_frequencies_ref",
+    "rotate_ref",
     "seen_keys",
+    "tree_commit_ref",
+    "tree_keys",
+    "verify_ref",
     "visible_keys",
 ]

@@ -1,6 +1,7 @@
 """Paged MLA decode for GB300: Python binding of the C ABI in include/mla_decode.h,
 include/mla_kv_pack.h, include/mla_sparse.h, include/mla_cascade.h,
-include/mla_prefill.h and include/mla_evict.h.
+include/mla_prefill.h, include/mla_evict.h, include/mla_tree.h,
+include/mla_verify.h, include/mla_pages.h and include/mla_rope.h.
 
 The functions here only marshal arguments (torch tensors -> device
 pointers, shapes -> ``mla_dims``); every step of the decode runs in the
@@ -25,6 +26,11 @@ MLA_DEV_INTERNAL = 8
 MLA_DEV_BAD_INDEX = 16
 MLA_DEV_BAD_PREFIX = 32
 MLA_DEV_BAD_QUERY_RANGE = 64
+MLA_DEV_BAD_TREE = 128
+MLA_DEV_BAD_PROBS = 256
+MLA_DEV_NO_PAGES = 512
+MLA_DEV_BAD_REFS = 1024
+MLA_TREE_MAX_NODES = 256
 
 ENTRY_POINTS = (
     "mla_decode_workspace_size",
@@ -51,6 +57,17 @@ ENTRY_POINTS = (
     "mla_attn_mass",
     "mla_evict_workspace_size",
     "mla_evict",
+    "mla_decode_tree_workspace_size",
+    "mla_decode_tree",
+    "mla_tree_commit",
+    "mla_verify",
+    "mla_page_resize_workspace_size",
+    "mla_page_resize",
+    "mla_page_fork_workspace_size",
+    "mla_page_fork",
+    "mla_rope_frequencies",
+    "mla_rope_plan_init",
+    "mla_rope_pack",
 )
 
 
@@ -108,6 +125,81 @@ class MlaEvictDims(ctypes.Structure):
         ("budget", ctypes.c_int32),
         ("num_sinks", ctypes.c_int32),
         ("num_recent", ctypes.c_int32),
+    ]
+
+
+class MlaTreeCommitDims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_layers", ctypes.c_int32),
+        ("path_cols", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("page_table_stride", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("layer_stride", ctypes.c_int64),
+    ]
+
+
+class MlaVerifyDims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("total_q", ctypes.c_int32),
+        ("vocab", ctypes.c_int32),
+        ("path_cols", ctypes.c_int32),
+        ("target_stride", ctypes.c_int64),
+        ("draft_stride", ctypes.c_int64),
+    ]
+
+
+class MlaPageResizeDims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("table_stride", ctypes.c_int32),
+        ("out_stride", ctypes.c_int32),
+    ]
+
+
+class MlaPageForkDims(ctypes.Structure):
+    _fields_ = [
+        ("sources", ctypes.c_int32),
+        ("children", ctypes.c_int32),
+        ("num_layers", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("table_stride", ctypes.c_int32),
+        ("out_stride", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("layer_stride", ctypes.c_int64),
+    ]
+
+
+class MlaRopePlan(ctypes.Structure):
+    _fields_ = [
+        ("turn", ctypes.c_uint64 * 32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("amplitude", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+    ]
+
+
+class MlaRopeDims(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("num_heads", ctypes.c_int32),
+        ("total_q", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32),
+        ("max_pages_per_req", ctypes.c_int32),
+        ("page_table_stride", ctypes.c_int32),
+        ("kv_dtype", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("q_token_stride", ctypes.c_int64),
+        ("q_head_stride", ctypes.c_int64),
+        ("row_stride", ctypes.c_int64),
     ]
 
 
@@ -181,6 +273,29 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     lib.mla_evict_workspace_size.restype = SZ
     lib.mla_evict.argtypes = [ctypes.POINTER(MlaEvictDims), P, P, P, P, P, P, P, P, P, P, SZ, P]
     lib.mla_evict.restype = ctypes.c_int
+    lib.mla_decode_tree_workspace_size.argtypes = [PD, ctypes.c_int]
+    lib.mla_decode_tree_workspace_size.restype = SZ
+    lib.mla_decode_tree.argtypes = [PD, P, P, P, P, P, P, P, F, F, P, P, P, SZ, P]
+    lib.mla_decode_tree.restype = ctypes.c_int
+    lib.mla_tree_commit.argtypes = [ctypes.POINTER(MlaTreeCommitDims), P, P, P, P, P, P, P, P, P]
+    lib.mla_tree_commit.restype = ctypes.c_int
+    lib.mla_verify.argtypes = [ctypes.POINTER(MlaVerifyDims), P, P, P, P, P, P, P, P, P, P, P, P]
+    lib.mla_verify.restype = ctypes.c_int
+    lib.mla_page_resize_workspace_size.argtypes = [I32, I32, I32]
+    lib.mla_page_resize_workspace_size.restype = SZ
+    lib.mla_page_resize.argtypes = [ctypes.POINTER(MlaPageResizeDims), P, P, P, P, P, P, SZ, P]
+    lib.mla_page_resize.restype = ctypes.c_int
+    lib.mla_page_fork_workspace_size.argtypes = [I32, I32, I32, I32]
+    lib.mla_page_fork_workspace_size.restype = SZ
+    lib.mla_page_fork.argtypes = [ctypes.POINTER(MlaPageForkDims), P, P, P, P, P, P, P, P, SZ, P]
+    lib.mla_page_fork.restype = ctypes.c_int
+    DP, R = ctypes.POINTER(ctypes.c_double), ctypes.POINTER(MlaRopePlan)
+    lib.mla_rope_frequencies.argtypes = [I32, ctypes.c_double, ctypes.c_double, I32, ctypes.c_double, ctypes.c_double, DP]
+    lib.mla_rope_frequencies.restype = ctypes.c_int
+    lib.mla_rope_plan_init.argtypes = [I32, I32, F, DP, R]
+    lib.mla_rope_plan_init.restype = ctypes.c_int
+    lib.mla_rope_pack.argtypes = [ctypes.POINTER(MlaRopeDims), R, P, P, P, P, P, P, F, P, P, P, P]
+    lib.mla_rope_pack.restype = ctypes.c_int
     if path is None:
         _lib = lib
     return lib
@@ -810,6 +925,307 @@ def mla_evict(mass, positions, seq_lens, page_table, kv_cache, budget, num_sinks
         _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_evict")
+
+
+# ---- trees of drafted tokens (include/mla_tree.h, include/mla_verify.h) ----
+
+def mla_decode_tree_workspace_size(dims: MlaPrefillDims, device: int | None = None) -> int:
+    import torch
+
+    dev = torch.cuda.current_device() if device is None else device
+    n = load_library().mla_decode_tree_workspace_size(ctypes.byref(dims), dev)
+    if n == 0:
+        raise MlaError(-1, "mla_decode_tree_workspace_size")
+    return int(n)
+
+
+def mla_decode_tree(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, parents, scale, kv_scale, out, lse,
+                    workspace, stream=None) -> None:
+    """Enqueue the attention of trees of drafted tokens (see
+    include/mla_tree.h): tensors as for mla_prefill; parents int32 [total_q],
+    each node's parent within its request, -1 = none."""
+    if not (_prefill_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+            and _fits(parents, q_nope.shape[:1], _t().i32, q_nope.get_device())):
+        _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, parents, out, lse, workspace)
+        _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+        _check_vectors(q_nope.device, parents=(parents, q_nope.shape[:1]))
+        raise ValueError("tree tensors do not have the shapes, types and layouts the library expects")
+    dev = q_nope.get_device()
+    _check_current_device(dev)
+    dims = make_prefill_dims(q_nope, kv_cache, page_table, seq_lens)
+    rc = load_library().mla_decode_tree(
+        ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), cu_q_lens.data_ptr(), parents.data_ptr(), float(scale), float(kv_scale), out.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream, dev))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_decode_tree")
+
+
+def _check_vectors(device, **named):
+    """name=(tensor, shape): contiguous int32 tensors on one device."""
+    for name, (t, shape) in named.items():
+        _check_layout(name, t, shape, (_t().i32,))
+        if t.device != device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _layers_of(kv_cache):
+    """(layers, pages, page size, bytes between layers) of a cache
+    [num_pages, 64, 576] or caches [num_layers, num_pages, 64, 576], or None."""
+    s, k = kv_cache.shape, kv_cache.stride()
+    if len(s) not in (3, 4) or s[-1] != 576 or s[-2] != 64 or kv_cache.dtype not in _t().cache_codes:
+        return None
+    if k[-1] != 1 or k[-2] != 576 or (s[-3] > 1 and k[-3] != 64 * 576):
+        return None
+    if len(s) == 3:
+        return 1, s[0], 0
+    return s[0], s[1], k[0] * kv_cache.element_size() if s[0] > 1 else 0
+
+
+def _check_layers(kv_cache):
+    if _layers_of(kv_cache) is None:
+        raise ValueError("kv_cache must be bf16 or e4m3 [num_pages, 64, 576], or [num_layers, num_pages, 64, 576] "
+                         "with contiguous layers")
+
+
+def _check_table(name, table, rows):
+    if (table.dtype != _t().i32 or table.dim() != 2 or (rows is not None and table.shape[0] != rows)
+            or table.stride(1) != 1 or table.stride(0) < table.shape[1]):
+        raise ValueError(f"{name} must be an int32 [{'rows' if rows is None else rows}, max_pages] tensor with unit "
+                         "column stride")
+
+
+def _check_devices(device, *tensors):
+    for t in tensors:
+        if t.device != device:
+            raise ValueError("all tensors must be on one device")
+
+
+def _check_status(status):
+    if status.dtype != _t().i32 or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor of at least one element")
+
+
+def mla_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status, stream=None) -> None:
+    """Enqueue the move of the accepted nodes' rows (see include/mla_tree.h).
+
+    kv_cache: [num_pages, 64, 576], or one such cache per layer as
+    [num_layers, num_pages, 64, 576]; path int32 [B, cols], num_path and
+    new_lens int32 [B] (new_lens not seq_lens itself); status int32 [1]."""
+    _check_cuda(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status)
+    _check_layers(kv_cache)
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    if path.dim() != 2:
+        raise ValueError("path must be [B, path_cols]")
+    dev = kv_cache.device
+    _check_vectors(dev, seq_lens=(seq_lens, (B,)), cu_q_lens=(cu_q_lens, (B + 1,)), path=(path, (B, path.shape[1])),
+                   num_path=(num_path, (B,)), new_lens=(new_lens, (B,)))
+    _check_table("page_table", page_table, B)
+    _check_status(status)
+    _check_devices(dev, page_table, status)
+    _check_current_device(dev.index)
+    layers, pages, step = _layers_of(kv_cache)
+    dims = MlaTreeCommitDims(B, layers, path.shape[1], pages, page_table.shape[1], page_table.stride(0),
+                             _t().cache_codes[kv_cache.dtype], 0, step)
+    rc = load_library().mla_tree_commit(
+        ctypes.byref(dims), kv_cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), cu_q_lens.data_ptr(),
+        path.data_ptr(), num_path.data_ptr(), new_lens.data_ptr(), status.data_ptr(), _stream_int(stream, dev.index))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_tree_commit")
+
+
+def _check_probs(name, t, rows, vocab):
+    if (t.dtype != _t().f32 or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != vocab or t.stride(1) != 1
+            or (rows > 1 and t.stride(0) < vocab)):
+        raise ValueError(f"{name} must be an fp32 [total_q, vocab] tensor with unit column stride")
+
+
+def mla_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status,
+               stream=None) -> None:
+    """Enqueue the verification of drafted tokens (see include/mla_verify.h).
+
+    target and draft (None: fixed proposals) fp32 [total_q, vocab]; tokens,
+    parents int32 and accept fp32 [total_q]; sample fp32 [B]; path and
+    tokens_out int32 [B, cols], num_out int32 [B]; status int32 [1]."""
+    _check_cuda(target, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status)
+    if target.dim() != 2:
+        raise ValueError("target must be [total_q, vocab]")
+    T, V = target.shape
+    dev = target.device
+    _check_probs("target", target, T, V)
+    if draft is not None:
+        _check_cuda(draft)
+        _check_probs("draft", draft, T, V)
+        _check_devices(dev, draft)
+    B = sample.shape[0] if sample.dim() == 1 else -1
+    if path.dim() != 2:
+        raise ValueError("path must be [B, path_cols]")
+    _check_layout("accept", accept, (T,), (_t().f32,))
+    _check_layout("sample", sample, (B,), (_t().f32,))
+    shape = (B, path.shape[1])
+    _check_vectors(dev, tokens=(tokens, (T,)), parents=(parents, (T,)), cu_q_lens=(cu_q_lens, (B + 1,)),
+                   path=(path, shape), tokens_out=(tokens_out, shape), num_out=(num_out, (B,)))
+    _check_status(status)
+    _check_devices(dev, accept, sample, status)
+    _check_current_device(dev.index)
+    dims = MlaVerifyDims(B, T, V, path.shape[1], target.stride(0) if T > 1 else V,
+                         (draft.stride(0) if T > 1 else V) if draft is not None else 0)
+    rc = load_library().mla_verify(
+        ctypes.byref(dims), target.data_ptr(), None if draft is None else draft.data_ptr(), tokens.data_ptr(),
+        parents.data_ptr(), cu_q_lens.data_ptr(), accept.data_ptr(), sample.data_ptr(), path.data_ptr(),
+        tokens_out.data_ptr(), num_out.data_ptr(), status.data_ptr(), _stream_int(stream, dev.index))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_verify")
+
+
+# ---- page operations (include/mla_pages.h) ----
+
+def mla_page_resize_workspace_size(batch: int, max_pages: int, num_pages: int) -> int:
+    n = load_library().mla_page_resize_workspace_size(_int32_arg("batch", batch), _int32_arg("max_pages", max_pages),
+                                                      _int32_arg("num_pages", num_pages))
+    if n == 0:
+        raise MlaError(-1, "mla_page_resize_workspace_size")
+    return int(n)
+
+
+def _stride_of(table):
+    return table.stride(0) if table.shape[0] > 1 else max(table.stride(0), table.shape[1])
+
+
+def mla_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace, stream=None) -> None:
+    """Enqueue handing out and freeing pages for the requests' new lengths (see
+    include/mla_pages.h); page_table_out and page_refs_out may be the inputs."""
+    _check_cuda(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace)
+    B = new_lens.shape[0] if new_lens.dim() == 1 else -1
+    dev = new_lens.device
+    if page_refs.dim() != 1:
+        raise ValueError("page_refs must be [num_pages]")
+    _check_vectors(dev, new_lens=(new_lens, (B,)), page_refs=(page_refs, page_refs.shape),
+                   page_refs_out=(page_refs_out, page_refs.shape))
+    _check_table("page_table", page_table, B)
+    _check_table("page_table_out", page_table_out, B)
+    if page_table.shape != page_table_out.shape:
+        raise ValueError("page_table and page_table_out must have the same shape")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check_devices(dev, page_table, page_table_out, workspace)
+    _check_current_device(dev.index)
+    dims = MlaPageResizeDims(B, page_refs.shape[0], page_table.shape[1], _stride_of(page_table),
+                             _stride_of(page_table_out))
+    rc = load_library().mla_page_resize(
+        ctypes.byref(dims), new_lens.data_ptr(), page_table.data_ptr(), page_refs.data_ptr(),
+        page_table_out.data_ptr(), page_refs_out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+        _stream_int(stream, dev.index))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_page_resize")
+
+
+def mla_page_fork_workspace_size(sources: int, children: int, max_pages: int, num_pages: int) -> int:
+    n = load_library().mla_page_fork_workspace_size(
+        _int32_arg("sources", sources), _int32_arg("children", children), _int32_arg("max_pages", max_pages),
+        _int32_arg("num_pages", num_pages))
+    if n == 0:
+        raise MlaError(-1, "mla_page_fork_workspace_size")
+    return int(n)
+
+
+def mla_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace,
+                  stream=None) -> None:
+    """Enqueue the fork of requests (see include/mla_pages.h): child c continues
+    request src[c] (int32 [children], -1 = an empty row); kv_cache as for
+    mla_tree_commit; page_refs_out may be page_refs."""
+    _check_cuda(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace)
+    _check_layers(kv_cache)
+    S = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    C = src.shape[0] if src.dim() == 1 else -1
+    layers, pages, step = _layers_of(kv_cache)
+    dev = kv_cache.device
+    _check_vectors(dev, src=(src, (C,)), seq_lens=(seq_lens, (S,)), page_refs=(page_refs, (pages,)),
+                   page_refs_out=(page_refs_out, (pages,)))
+    _check_table("page_table", page_table, S)
+    _check_table("page_table_out", page_table_out, C)
+    if page_table.shape[1] != page_table_out.shape[1]:
+        raise ValueError("page_table and page_table_out must have the same number of columns")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _check_devices(dev, page_table, page_table_out, workspace)
+    _check_current_device(dev.index)
+    dims = MlaPageForkDims(S, C, layers, pages, page_table.shape[1], _stride_of(page_table),
+                           _stride_of(page_table_out), _t().cache_codes[kv_cache.dtype], step)
+    rc = load_library().mla_page_fork(
+        ctypes.byref(dims), src.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), page_refs.data_ptr(),
+        kv_cache.data_ptr(), page_table_out.data_ptr(), page_refs_out.data_ptr(), workspace.data_ptr(),
+        workspace.nbytes, _stream_int(stream, dev.index))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_page_fork")
+
+
+# ---- rotary positions (include/mla_rope.h) ----
+
+def mla_rope_frequencies(rotary_dim, base=10000.0, factor=1.0, original_len=0, fast=32.0, slow=1.0) -> list:
+    """Radians a position of every rotated pair (see include/mla_rope.h)."""
+    out = (ctypes.c_double * 32)()
+    rc = load_library().mla_rope_frequencies(_int32_arg("rotary_dim", rotary_dim), float(base), float(factor),
+                                             _int32_arg("original_len", original_len), float(fast), float(slow), out)
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_rope_frequencies")
+    return list(out)[:rotary_dim // 2]
+
+
+def mla_rope_plan(rotary_dim, base=10000.0, factor=1.0, original_len=0, fast=32.0, slow=1.0, interleaved=True,
+                  amplitude=1.0, frequencies=None) -> MlaRopePlan:
+    """The plan of a rotation: from base and scaling, or from the frequencies
+    themselves (rotary_dim / 2 of them)."""
+    if frequencies is None:
+        frequencies = mla_rope_frequencies(rotary_dim, base, factor, original_len, fast, slow)
+    elif len(frequencies) != rotary_dim // 2:
+        raise ValueError(f"rotary_dim {rotary_dim} needs {rotary_dim // 2} frequencies, got {len(frequencies)}")
+    plan = MlaRopePlan()
+    rc = load_library().mla_rope_plan_init(_int32_arg("rotary_dim", rotary_dim), int(bool(interleaved)),
+                                           float(amplitude), (ctypes.c_double * len(frequencies))(*frequencies),
+                                           ctypes.byref(plan))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_rope_plan_init")
+    return plan
+
+
+def mla_rope_pack(plan, q_pe, rows, positions, page_table, seq_lens, cu_q_lens, kv_scale, q_out, kv_cache, status,
+                  stream=None) -> None:
+    """Enqueue the rotation of a step's q_pe and k_pe and the cache write of its
+    rows (see include/mla_rope.h).
+
+    q_pe bf16 [total_q, H, 64] and rows bf16 [total_q, 576], with unit stride in
+    the last dimension; positions int32 [total_q], or None: the tokens' slots;
+    q_out bf16 [total_q, H, 64], contiguous (q_pe itself if that is)."""
+    t = _t()
+    _check_cuda(q_pe, rows, page_table, seq_lens, cu_q_lens, q_out, kv_cache, status)
+    if q_pe.dim() != 3 or q_pe.shape[2] != 64 or q_pe.dtype != t.bf16 or q_pe.stride(2) != 1:
+        raise ValueError("q_pe must be a bf16 [total_q, H, 64] tensor with unit stride in the last dimension")
+    T, H, _ = q_pe.shape
+    if tuple(rows.shape) != (T, 576) or rows.dtype != t.bf16 or rows.stride(1) != 1:
+        raise ValueError("rows must be a bf16 [total_q, 576] tensor with unit stride in the last dimension")
+    dev = q_pe.device
+    _check_layout("q_out", q_out, (T, H, 64), (t.bf16,))
+    B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
+    _check_cache_and_table(kv_cache, page_table, seq_lens, B)
+    if kv_cache.shape[1] != 64:
+        raise ValueError("kv_cache must have pages of 64 tokens")
+    _check_vectors(dev, cu_q_lens=(cu_q_lens, (B + 1,)))
+    if positions is not None:
+        _check_cuda(positions)
+        _check_vectors(dev, positions=(positions, (T,)))
+    _check_status(status)
+    _check_devices(dev, rows, q_out, kv_cache, page_table, seq_lens, status)
+    _check_current_device(dev.index)
+    dims = MlaRopeDims(B, H, T, kv_cache.shape[0], page_table.shape[1], page_table.stride(0),
+                       t.cache_codes[kv_cache.dtype], 0, q_pe.stride(0), q_pe.stride(1), rows.stride(0))
+    rc = load_library().mla_rope_pack(
+        ctypes.byref(dims), ctypes.byref(plan), q_pe.data_ptr(), rows.data_ptr(),
+        None if positions is None else positions.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
+        cu_q_lens.data_ptr(), float(kv_scale), q_out.data_ptr(), kv_cache.data_ptr(), status.data_ptr(),
+        _stream_int(stream, dev.index))
+    if rc != MLA_OK:
+        raise MlaError(rc, "mla_rope_pack")
 
 
 @dataclass

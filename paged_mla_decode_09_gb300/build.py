@@ -4,9 +4,12 @@
 ``csrc/mla_decode.cu`` (the decode), ``csrc/mla_kv_pack.cu`` (the cache
 write), ``csrc/mla_sparse.cu`` (the top-k decode), ``csrc/mla_cascade.cu``
 (the shared-prefix cascade), ``csrc/mla_chunk.cu`` (prompt chunks and
-windows), ``csrc/mla_mass.cu`` (attention mass) and ``csrc/mla_evict.cu``
-(eviction) with nvcc into ``libmla_decode.so`` next to this file.  One
-``-gencode``, the files in parallel; a few seconds.
+windows), ``csrc/mla_mass.cu`` (attention mass), ``csrc/mla_evict.cu``
+(eviction), ``csrc/mla_tree.cu`` (trees of drafts), ``csrc/mla_verify.cu``
+(their verification), ``csrc/mla_pages.cu`` (page operations) and
+``csrc/mla_rope.cu`` (rotary cache write) with nvcc into
+``libmla_decode.so`` next to this file.  One ``-gencode``, the files in
+parallel; a few seconds.
 """
 from __future__ import annotations
 
@@ -22,7 +25,8 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmla_decode.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "mla_kv_pack.cu", "mla_sparse.cu", "mla_cascade.cu",
-                                               "mla_chunk.cu", "mla_mass.cu", "mla_evict.cu")]
+                                               "mla_chunk.cu", "mla_mass.cu", "mla_evict.cu", "mla_tree.cu", "mla_verify.cu",
+                                               "mla_pages.cu", "mla_rope.cu")]
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,5 +1,5 @@
-// Device code of the chunk attention behind mla_prefill and
-// mla_decode_window: schedule, split-KV attention, log-sum-exp combine.
+// Device code of the chunk attention behind mla_prefill, mla_decode_window and
+// mla_decode_tree: schedule, split-KV attention, log-sum-exp combine.
 //
 // Row r of the flattened queries [T * H] belongs to token r / H, head r % H.
 // A request's rows are cut into blocks of kCg * 128 consecutive rows; a
@@ -44,6 +44,13 @@
 // 0.3 % of the output at 14, 6 % at 17, 15 % from 20 on).  bf16 weights on codes expanded to bf16 would keep
 // them, at 3 bits less in every weight: ordinary inputs' outputs would be 0.0021
 // off in the mean instead of 0.0017 (most of it their own rounding).
+//
+// A tree of drafted tokens (kTree): a node's keys are those before the tree,
+// its ancestors and itself.  Ancestors come before their nodes, so the causal
+// page ranges hold as they are, and only a page that reaches into the tree is
+// masked, by 64 bits of the node's ancestor set.  The sets (256 bits a node)
+// are found by further blocks of the schedule's launch, which run beside the
+// block that schedules: a launch of their own would stand in the call's chain.
 #pragma once
 
 #include <cstdint>
@@ -54,6 +61,7 @@
 #include "mla_decode.h"
 #include "mla_prefill.h"
 #include "mla_score.cuh"
+#include "mla_tree.h"
 #include "sm100_ptx.cuh"
 
 namespace mla {
@@ -72,6 +80,10 @@ struct Rescale {
   static constexpr float kThreshold = kF8 ? 14.0f : 40.0f;
 };
 constexpr int kMaxClusters = 96;       // the combine's lanes take 3 clusters each
+constexpr int kTreeNodes = MLA_TREE_MAX_NODES;  // of a request
+constexpr int kTreeWords = kTreeNodes / 64;     // of a node's ancestor set
+constexpr int kTreeBlocks = 448;                // blocks that find ancestors, at most
+static_assert(kTreeNodes == 256, "a thread of the small schedule per node; the words are registers");
 
 struct __align__(16) Ctrl {
   int4 unit[2][2];               // S: the unit whose queries land on q_bar (p0, p1, nrows, pos0), (h0, sp, skip, -)
@@ -108,7 +120,7 @@ struct Block {
   int32_t b;       // request
   int32_t row0;    // first row of the flattened [T * H]
   int32_t nrows;
-  int32_t sp;      // virtual pages before the skip
+  int32_t sp;      // virtual pages before the skip; a tree's: the slot of its first node (skip is 0)
   int32_t skip;    // real page = v + (v >= sp ? skip : 0)
   int32_t pos0;    // position of the first row's token (< 0: sees nothing)
   int32_t h0;      // head of the first row
@@ -122,6 +134,9 @@ struct Params {
   const int32_t* page_table;
   const int32_t* seq_lens;
   const int32_t* cu_q;      // [B + 1] first query token of each request; null: request b has tokens b*q_len ..
+  const int32_t* parents;   // tree: [T] each node's parent within its request, -1: none
+  int32_t* bad;             // tree: [tree_blocks] whether a block has met a bad parent
+  uint64_t* anc;            // tree: [T][kTreeWords] bit j: node j is the node itself or an ancestor
   uint8_t* out;
   float* lse;
   float* o_part;            // [2C][128 kCg][512]
@@ -134,6 +149,7 @@ struct Params {
   int32_t* cuts;            // [8] count, then [min(NB, C)][8] per block cut into pieces (any order): block, first
                             // cluster, last cluster, partial slot of the first piece, first row, rows
   int32_t B, H, q_len, T, NB, C, BR;  // BR = rows per block
+  int32_t tree_blocks;
   int32_t num_pages, max_pages, pt_stride;
   int32_t window, sinks;    // window 0: everything up to the row's own position
   int32_t unit_cost;        // schedule weight of starting a piece, in pages
@@ -198,7 +214,59 @@ __device__ __forceinline__ int block_scan_small(int v, int (&tot)[kSchedSmall / 
   return v;
 }
 
-template <bool kSmall>
+// The ancestor sets of requests first, first + step, ..: a thread per node
+// walks up (parents come before their nodes, so every walk ends).
+__device__ __forceinline__ void find_ancestors(const Params& p, int first, int step) {
+  __shared__ int par[kTreeNodes];
+  const int tid = threadIdx.x;
+  int bad = 0;
+  for (int b = first; b < p.B; b += step) {
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+    // (a bad range is the schedule's to report)
+    const int n = q0 >= 0 && q1 >= q0 && q1 <= p.T && q1 - q0 <= kTreeNodes ? q1 - q0 : 0;
+    if (tid < n) {
+      int up = p.parents[q0 + tid];
+      if (up < -1 || up >= tid) {  // as if it had none
+        bad = 1;
+        up = -1;
+      }
+      par[tid] = up;
+    }
+    __syncthreads();
+    if (tid < n) {
+      uint64_t w[kTreeWords] = {};
+      for (int at = tid; at >= 0; at = par[at]) {
+        const uint64_t bit = 1ull << (at & 63);
+#pragma unroll
+        for (int k = 0; k < kTreeWords; ++k) w[k] |= (at >> 6) == k ? bit : 0ull;
+      }
+      ulonglong2* dst = reinterpret_cast<ulonglong2*>(p.anc + static_cast<int64_t>(q0 + tid) * kTreeWords);
+#pragma unroll
+      for (int k = 0; k < kTreeWords; k += 2) dst[k / 2] = make_ulonglong2(w[k], w[k + 1]);
+    }
+    __syncthreads();
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) p.bad[first] = bad;
+}
+
+// The 64 bits of a node's ancestor set for the slots t0 .. t0 + 63, where the
+// tree begins in slot `base` < t0 + 64: slots before it are seen.
+__device__ __forceinline__ uint64_t tree_mask(const uint64_t* set, int t0, int base) {
+  const int k0 = t0 - base;
+  if (k0 <= 0) {
+    const int before = -k0;  // < 64
+    const uint64_t w = __ldcg(reinterpret_cast<const unsigned long long*>(set));
+    return (w << before) | ((1ull << before) - 1ull);
+  }
+  const int q = k0 >> 6, s = k0 & 63;
+  uint64_t m = 0ull;
+  if (q < kTreeWords) m = __ldcg(reinterpret_cast<const unsigned long long*>(set) + q) >> s;
+  if (s != 0 && q + 1 < kTreeWords) m |= __ldcg(reinterpret_cast<const unsigned long long*>(set) + q + 1) << (64 - s);
+  return m;
+}
+
+template <bool kSmall, bool kTree>
 __global__ void __launch_bounds__(kSmall ? kSchedSmall : kSchedThreads)
     mla_chunk_schedule_kernel(const __grid_constant__ Params p) {
   __shared__ int warp_tot[32];
@@ -215,6 +283,10 @@ __global__ void __launch_bounds__(kSmall ? kSchedSmall : kSchedThreads)
   __shared__ int2 s_rows[kKept];              // a block's first row, rows
   griddep_wait();
   griddep_launch_dependents();
+  if (kTree && blockIdx.x > 0) {
+    find_ancestors(p, static_cast<int>(blockIdx.x) - 1, p.tree_blocks);
+    return;
+  }
   const int tid = threadIdx.x;
   constexpr int nt = kSmall ? kSchedSmall : kSchedThreads;
   if (tid < 4) p.status[tid] = 0;
@@ -230,7 +302,10 @@ __global__ void __launch_bounds__(kSmall ? kSchedSmall : kSchedThreads)
     }
     q0 = p.cu_q[b];
     q1 = p.cu_q[b + 1];
-    if (q0 >= 0 && q1 >= q0 && q1 <= p.T && (b > 0 || q0 == 0)) return true;
+    if (q0 >= 0 && q1 >= q0 && q1 <= p.T && (b > 0 || q0 == 0)) {
+      if (kTree && q1 - q0 > kTreeNodes) q0 = q1 = 0;  // too many nodes: left out (reported below)
+      return true;
+    }
     q0 = q1 = 0;
     return false;
   };
@@ -242,6 +317,7 @@ __global__ void __launch_bounds__(kSmall ? kSchedSmall : kSchedThreads)
       const int L = p.seq_lens[b];
       int q0, q1;
       if (!range(b, q0, q1)) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
+      else if (kTree && p.cu_q[b + 1] - p.cu_q[b] > kTreeNodes) atomicOr(p.status, MLA_DEV_BAD_TREE);
       if (q1 > q0 && (L < q1 - q0 || L > p.max_pages * kPage)) atomicOr(p.status, MLA_DEV_BAD_SEQ_LEN);
       // (rows fit in 31 bits, rounded up in 32)
       nblk = static_cast<int>((static_cast<uint32_t>(q1 - q0) * static_cast<uint32_t>(p.H) + (p.BR - 1)) >>
@@ -302,7 +378,7 @@ __global__ void __launch_bounds__(kSmall ? kSchedSmall : kSchedThreads)
     k.pos0 = L - nq + static_cast<int>(i0);
     k.len = L;
     const int last = last_page(k, p.H);  // at least one page, all of it masked if nothing is seen
-    k.sp = last + 1;
+    k.sp = kTree ? L - nq : last + 1;
     k.skip = 0;
     if (p.window > 0) {
       const int wp = k.pos0 + 1 > p.window ? (k.pos0 + 1 - p.window) / kPage : 0;  // page of the first row's first key
@@ -489,7 +565,7 @@ __device__ __forceinline__ void drain_ring(Ctrl* ctrl, uint32_t i, uint64_t time
 // busy for ~940 cycles per 768 cycles of MMAs (2815 a tile instead of 2304).
 // So the slot of an entry is free once the tile of the page that it held is
 // scored (s_full), or once the query part that it held is in TMEM (q_part).
-template <bool kF8, int kCg>
+template <bool kF8, int kCg, bool kTree>
 __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUtensorMap* tm_s, const CUtensorMap* tm_pe,
                           const CUtensorMap* tm_qn, const CUtensorMap* tm_qp, int cid, int pr) {
   using C = Cfg<kF8, kCg>;
@@ -545,7 +621,7 @@ __device__ void produce_s(const Params& p, Ctrl* ctrl, uint8_t* ring, const CUte
       }
       if (e == 0) {
         ctrl->unit[un & 1][0] = make_int4(u.p0, u.p1, u.k.nrows, u.k.pos0);
-        ctrl->unit[un & 1][1] = make_int4(u.k.h0, u.k.sp, u.k.skip, 0);
+        ctrl->unit[un & 1][1] = make_int4(u.k.h0, u.k.sp, u.k.skip, kTree ? u.k.row0 : 0);
         mbar_expect_tx(qbar, static_cast<uint32_t>(C::kParts == 3 ? kRows * 1152 : qe * C::kQRows * 1152));
         qloaded = un + 1;
         if constexpr (C::kParts == 3)
@@ -772,7 +848,7 @@ __device__ __forceinline__ void store_row(const Params& p, const Unit& u, int br
 }
 
 // --------------------------------------------------------------- attention
-template <bool kF8, int kCg>
+template <bool kF8, int kCg, bool kTree>
 __global__ void __launch_bounds__(kThreads, 1)
     mla_chunk_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_s,
                      const __grid_constant__ CUtensorMap tm_o, const __grid_constant__ CUtensorMap tm_pe,
@@ -858,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================== S CTA ===========================
     uint8_t* ring = data;
     if (warp == 0) {
-      if (lane == 0) produce_s<kF8, kCg>(p, ctrl, ring, &tm_s, &tm_pe, &tm_qn, &tm_qp, cid, pr);
+      if (lane == 0) produce_s<kF8, kCg, kTree>(p, ctrl, ring, &tm_s, &tm_pe, &tm_qn, &tm_qp, cid, pr);
     } else if (warp == 1) {
       // The leader's warp issues QK for the pair (the whole warp runs the
       // loop, one elected lane issues); the other CTA's warp passes on that
@@ -1043,6 +1119,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int4 x = ctrl->unit[un & 1][0], y = ctrl->unit[un & 1][1];
           u.p0 = x.x; u.p1 = x.y; u.k.nrows = x.z; u.k.pos0 = x.w;
           u.k.h0 = y.x; u.k.sp = y.y; u.k.skip = y.z;
+          if (kTree) u.k.row0 = y.w;
         }
         if (kF8 && !mbar_wait_warp<false, true>(smem_u32(&ctrl->qs_full[un & 1]), (un >> 1) & 1, abort, p.timeout_ns)) {
           ok = false;
@@ -1092,12 +1169,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pos = u.k.pos0 + (u.k.h0 + (real ? br : u.k.nrows - 1)) / p.H;
         const int nvis = pos + 1;                                                     // sees t < nvis ...
         const int lo = p.window > 0 && nvis > p.window ? nvis - p.window : 0;         // ... and t >= lo or t < sinks
+        // a tree: keys before slot `base`, behind it those of the node's set
+        const int base = u.k.sp;
+        const uint64_t* set = nullptr;
+        if constexpr (kTree)
+          set = p.anc + static_cast<int64_t>(u.k.row0 / p.H + (u.k.h0 + (real ? br : u.k.nrows - 1)) / p.H) * kTreeWords;
         float m_run = kMinusBig, l = 0.f;
         for (int vt = u.p0; vt < u.p1; vt += kCg, ++jt) {
           if (kCg == 1 && (jt & 1u) != static_cast<uint32_t>(gg)) continue;
           const int vp = kCg == 1 ? vt : vt + gg;
           j = j0 + static_cast<uint32_t>(vp - u.p0);
           const int sb = static_cast<int>(jt % C::kNSB);
+          uint64_t seen = ~0ull;  // (asked for before the scores are awaited)
+          if (kTree && (vp + 1) * kPage > base) seen = tree_mask(set, vp * kPage, base);
           if (!mbar_wait_warp<false, true>(smem_u32(&ctrl->s_full[sb]), (jt / C::kNSB) & 1, abort, p.timeout_ns)) {
             ok = false;
             why = kWaitSFull;
@@ -1123,7 +1207,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else mbar_arrive(smem_u32(&ctrl->s_empty[sb]));
           }
           const int t0 = real_page(u.k, vp) * kPage;
-          const bool full = t0 + kPage <= nvis && (t0 >= lo || t0 + kPage <= p.sinks);
+          const bool full = kTree ? t0 + kPage <= base : t0 + kPage <= nvis && (t0 >= lo || t0 + kPage <= p.sinks);
           // the page's keys [a, z) and [0, s) are seen
           const int z = nvis - t0, a = lo - t0, s = p.sinks - t0;
 #define MLA_S(t) __uint_as_float(v[(t) >> 4][(t) & 15])
@@ -1134,7 +1218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             m4[0] = m4[1] = m4[2] = m4[3] = -INFINITY;
 #pragma unroll
             for (int t = 0; t < 64; ++t) {
-              const float x = (t < z && (t >= a || t < s)) ? MLA_S(t) : -INFINITY;
+              const bool see = kTree ? ((seen >> t) & 1ull) != 0ull : (t < z && (t >= a || t < s));
+              const float x = see ? MLA_S(t) : -INFINITY;
               v[t >> 4][t & 15] = __float_as_uint(x);
               m4[t & 3] = fmaxf(m4[t & 3], x);
             }
@@ -1230,6 +1315,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // =========================== O CTA ===========================
     uint8_t* vring = data + C::kVOff;
     uint8_t* raw = data + C::kRawOff;
+    if (kTree && warp == 3 && cid == 0 && leader) {  // the schedule block clears the status, so its siblings cannot
+      int bad = 0;
+      for (int i = lane; i < p.tree_blocks; i += 32) bad |= __ldcg(p.bad + i);
+      if (__any_sync(0xffffffffu, bad != 0) && lane == 0) atomicOr(p.status, MLA_DEV_BAD_TREE);
+    }
     if (warp == 0) {
       if (lane == 0) produce_o<kF8, kCg>(p, ctrl, kF8 ? raw : vring, &tm_o, cid, pr);
     } else if (warp == 1) {
@@ -1522,7 +1612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // kernel began, so it is read before waiting for the latter.
 constexpr int kCombineWarps = 4;
 
-template <int kParts>
+template <int kParts, bool kTree>
 __global__ void __launch_bounds__(kCombineWarps * 32) mla_chunk_combine_kernel(const __grid_constant__ Params p) {
   constexpr int kV = 4 / kParts;      // float4s of a row per lane
   constexpr int kFly = 2 * kParts;    // partial rows in flight

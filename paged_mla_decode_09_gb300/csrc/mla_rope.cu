@@ -1,0 +1,415 @@
+// mla_rope_pack (see include/mla_rope.h): a step's query and key parts rotated,
+// its rows written into the paged cache.
+//
+// Angles: a frequency is a 64-bit fraction F of a turn, so position * F modulo
+// 2^64 is the angle's fraction of a turn, with no range reduction and no loss at
+// far positions; as a signed number it is the angle in half turns, [-1, 1), for
+// sincospi in fp32 (2^-25 of a half turn from its conversion).  R / 2 of them a
+// token, once for all heads.
+//
+// Work: a block takes a few tokens.  A head's 64 values are four items of two
+// 16-byte chunks, chosen so that an item needs the same eight angles in both
+// layouts (interleaved: chunks 2 i and 2 i + 1; halves: chunk i and the one
+// R / 2 behind it), so a thread that walks over heads keeps its angles in
+// registers.  The loads of queries and rows do not depend on the request: they
+// are in flight while the block looks its tokens up (offsets, length, page:
+// three dependent reads) and forms the angles.
+//
+// What bounds it: HBM for prompts (each query value read and written once, each
+// row read and written once), the chain of dependent reads for a few tokens.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cmath>
+#include <cstdint>
+
+#include "mla_e4m3.cuh"
+#include "mla_host.h"
+#include "mla_rope.h"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace rope {
+
+constexpr int kPage = 64;
+constexpr int kRowVals = 576;
+constexpr int kLatChunks = 64;   // 16-byte chunks of c_kv
+constexpr int kThreads = 256;
+constexpr int kMaxTok = 16;      // tokens of a block
+constexpr int kAhead = 2;        // items and chunks a thread has in flight
+
+struct Params {
+  const uint8_t* q_pe;
+  const uint8_t* rows;
+  const int32_t* positions;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  uint8_t* q_out;
+  uint8_t* cache;
+  int32_t* status;
+  int64_t q_tok, q_head, row;  // strides in bytes
+  int32_t B, H, T, num_pages, max_pages, pt_stride, R, toks;
+  float amp;
+  e4m3::Scale sc;
+  uint64_t turn[32];
+};
+
+__device__ __forceinline__ uint4 ldg16(const uint8_t* p) { return *reinterpret_cast<const uint4*>(p); }
+
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[k]));
+    x[2 * k] = f.x;
+    x[2 * k + 1] = f.y;
+  }
+}
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * k], x[2 * k + 1]);
+    w[k] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The two chunks of item i of a head: rotating items first, then those that pass.
+__device__ __forceinline__ void chunks_of(int i, int R, bool inter, int& c0, int& c1) {
+  const bool halves = !inter && i < (R >> 4);
+  c0 = halves ? i : 2 * i;
+  c1 = halves ? i + (R >> 4) : 2 * i + 1;
+}
+
+// Rotates an item's two chunks by its eight angles.
+template <bool kInter>
+__device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const float (&co)[8], const float (&si)[8]) {
+  if constexpr (kInter) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float a0 = a[2 * k], a1 = a[2 * k + 1], b0 = b[2 * k], b1 = b[2 * k + 1];
+      a[2 * k] = a0 * co[k] - a1 * si[k];
+      a[2 * k + 1] = a0 * si[k] + a1 * co[k];
+      b[2 * k] = b0 * co[4 + k] - b1 * si[4 + k];
+      b[2 * k + 1] = b0 * si[4 + k] + b1 * co[4 + k];
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = a[k], y = b[k];
+      a[k] = x * co[k] - y * si[k];
+      b[k] = x * si[k] + y * co[k];
+    }
+  }
+}
+
+template <bool kF8, bool kInter>
+__global__ void __launch_bounds__(kThreads) mla_rope_pack_kernel(const __grid_constant__ Params p) {
+  __shared__ int s_req[kMaxTok];
+  __shared__ int64_t s_slot[kMaxTok];                        // cache row, -1: not written
+  __shared__ __align__(16) float s_cs[kMaxTok][4][16];       // per item: eight cosines, eight sines
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x;
+  const int t0 = blockIdx.x * p.toks;
+  const int nt = p.T - t0 < p.toks ? p.T - t0 : p.toks;
+  const int per = p.H * 4;                      // query items of a token
+  const int items = nt * per, lats = nt * kLatChunks;
+  // first loads: query items tid, tid + 256, ..; c_kv chunks likewise
+  auto q_at = [&](int it, int& c0, int& c1) -> const uint8_t* {
+    const int k = it / per, r = it - k * per;
+    chunks_of(r & 3, p.R, kInter, c0, c1);
+    return p.q_pe + (t0 + k) * p.q_tok + (r >> 2) * p.q_head;
+  };
+  uint4 qa[kAhead], qb[kAhead], lat[kAhead];
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int it = tid + u * kThreads;
+    if (it < items) {
+      int c0, c1;
+      const uint8_t* src = q_at(it, c0, c1);
+      qa[u] = ldg16(src + 16 * c0);
+      qb[u] = ldg16(src + 16 * c1);
+    }
+    if (it < lats) lat[u] = ldg16(p.rows + (t0 + (it >> 6)) * p.row + 16 * (it & 63));
+  }
+  // each token's request
+  if (tid < kMaxTok) s_req[tid] = -1;
+  __syncthreads();
+  for (int b = tid; b < p.B; b += kThreads) {
+    const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > p.T || (b == 0 && q0 != 0)) {
+      if (blockIdx.x == 0) atomicOr(p.status, MLA_DEV_BAD_QUERY_RANGE);
+      continue;
+    }
+    const int lo = q0 > t0 ? q0 : t0, hi = q1 < t0 + nt ? q1 : t0 + nt;
+    for (int t = lo; t < hi; ++t) s_req[t - t0] = b;
+  }
+  __syncthreads();
+  // its slot, and its angles
+  int fail = 0, mine = -1;
+  if (tid < nt) {
+    const int b = s_req[tid];
+    int64_t slot = -1;
+    if (b >= 0) {
+      const int q0 = p.cu_q[b], n = p.cu_q[b + 1] - q0, L = p.seq_lens[b];
+      if (L < n || L > p.max_pages * kPage) {
+        fail = MLA_DEV_BAD_SEQ_LEN;
+        mine = tid;
+      } else {
+        const int at = L - n + (t0 + tid - q0);
+        const int page = p.page_table[static_cast<int64_t>(b) * p.pt_stride + at / kPage];
+        if (page < 0 || page >= p.num_pages) fail = MLA_DEV_BAD_PAGE_ID;
+        else slot = static_cast<int64_t>(page) * kPage + at % kPage;
+      }
+    }
+    s_slot[tid] = slot;
+  }
+  const int half = p.R >> 1;
+  for (int x = tid; x < nt * 32; x += kThreads) {
+    const int k = x >> 5, i = x & 31, b = s_req[k];
+    if (i >= half || b < 0) continue;
+    int pos;
+    if (p.positions) pos = p.positions[t0 + k];
+    else pos = p.seq_lens[b] - p.cu_q[b + 1] + t0 + k;  // (used only if the length is right)
+    const int64_t phase = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * p.turn[i]);
+    float si, co;
+    sincospif(static_cast<float>(phase) * 0x1p-63f, &si, &co);
+    s_cs[k][i >> 3][i & 7] = co * p.amp;
+    s_cs[k][i >> 3][8 + (i & 7)] = si * p.amp;
+  }
+  if (fail != 0) atomicOr(p.status, fail);
+  __syncthreads();
+  if (mine >= 0) s_req[mine] = -1;  // a bad length: left out
+  __syncthreads();
+
+  // queries: a thread's items are all of one number i when 256 is a multiple of 4
+  const int i = tid & 3;
+  const bool turns = i < (p.R >> 4);
+  float co[8], si[8];
+  int have = -1;
+  auto put_q = [&](int it, const uint4& va, const uint4& vb) {
+    const int k = it / per, r = it - k * per;
+    if (s_req[k] < 0) return;
+    int c0, c1;
+    chunks_of(i, p.R, kInter, c0, c1);
+    uint8_t* dst = p.q_out + (static_cast<int64_t>(t0 + k) * p.H + (r >> 2)) * 128;
+    if (!turns) {
+      *reinterpret_cast<uint4*>(dst + 16 * c0) = va;
+      *reinterpret_cast<uint4*>(dst + 16 * c1) = vb;
+      return;
+    }
+    if (k != have) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        co[e] = s_cs[k][i][e];
+        si[e] = s_cs[k][i][8 + e];
+      }
+      have = k;
+    }
+    float a[8], b[8];
+    unpack(va, a);
+    unpack(vb, b);
+    turn8<kInter>(a, b, co, si);
+    *reinterpret_cast<uint4*>(dst + 16 * c0) = pack(a);
+    *reinterpret_cast<uint4*>(dst + 16 * c1) = pack(b);
+  };
+  auto put_lat = [&](int it, const uint4& v) {
+    const int64_t slot = s_slot[it >> 6];
+    if (slot < 0) return;
+    if constexpr (kF8) reinterpret_cast<uint2*>(p.cache + slot * kRowVals)[it & 63] = e4m3::e4m3x8(v, p.sc);
+    else reinterpret_cast<uint4*>(p.cache + slot * kRowVals * 2)[it & 63] = v;
+  };
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    const int it = tid + u * kThreads;
+    if (it < items) put_q(it, qa[u], qb[u]);
+    if (it < lats) put_lat(it, lat[u]);
+  }
+  for (int base = kAhead * kThreads; base < items; base += kAhead * kThreads) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int it = base + tid + u * kThreads;
+      if (it >= items) continue;
+      int c0, c1;
+      const uint8_t* src = q_at(it, c0, c1);
+      qa[u] = ldg16(src + 16 * c0);
+      qb[u] = ldg16(src + 16 * c1);
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int it = base + tid + u * kThreads;
+      if (it < items) put_q(it, qa[u], qb[u]);
+    }
+  }
+  for (int it = kAhead * kThreads + tid; it < lats; it += kThreads)
+    put_lat(it, ldg16(p.rows + (t0 + (it >> 6)) * p.row + 16 * (it & 63)));
+  // k_pe of each token: four items
+  for (int it = tid; it < nt * 4; it += kThreads) {
+    const int k = it >> 2;
+    const int64_t slot = s_slot[k];
+    if (slot < 0) continue;
+    int c0, c1;
+    chunks_of(i, p.R, kInter, c0, c1);
+    const uint8_t* src = p.rows + (t0 + k) * p.row + 1024;
+    const uint4 va = ldg16(src + 16 * c0), vb = ldg16(src + 16 * c1);
+    float a[8], b[8];
+    unpack(va, a);
+    unpack(vb, b);
+    if (turns) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        co[e] = s_cs[k][i][e];
+        si[e] = s_cs[k][i][8 + e];
+      }
+      turn8<kInter>(a, b, co, si);
+    }
+    if constexpr (kF8) {
+      uint2* dst = reinterpret_cast<uint2*>(p.cache + slot * kRowVals + 512);
+      dst[c0] = e4m3::e4m3x8(a, p.sc);
+      dst[c1] = e4m3::e4m3x8(b, p.sc);
+    } else {
+      uint4* dst = reinterpret_cast<uint4*>(p.cache + slot * kRowVals * 2 + 1024);
+      dst[c0] = turns ? pack(a) : va;
+      dst[c1] = turns ? pack(b) : vb;
+    }
+  }
+}
+
+}  // namespace rope
+}  // namespace mla
+
+namespace {
+
+using mla::host::aligned;
+
+bool rotary_ok(int32_t r) { return r >= 16 && r <= 64 && r % 16 == 0; }
+
+// Whether [a, a + an) and [b, b + bn) share a byte.
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
+}
+
+}  // namespace
+
+extern "C" {
+
+int mla_rope_frequencies(int32_t rotary_dim, double base, double factor, int32_t original_len, double fast,
+                         double slow, double* out) {
+  if (!out || !std::isfinite(base) || base < 1.0 || !std::isfinite(factor) || factor < 1.0 || original_len < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (original_len > 0 && (!std::isfinite(fast) || !std::isfinite(slow) || fast <= slow)) return MLA_ERR_INVALID_ARG;
+  if (!rotary_ok(rotary_dim)) return MLA_ERR_UNSUPPORTED;
+  const double two_pi = 6.283185307179586476925;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rotary_dim);
+    double g = 0.0;
+    if (original_len > 0) {
+      g = (original_len * f / two_pi - slow) / (fast - slow);
+      g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
+    }
+    out[i] = factor == 1.0 ? f : g * f + (1.0 - g) * f / factor;
+  }
+  return MLA_OK;
+}
+
+int mla_rope_plan_init(int32_t rotary_dim, int32_t interleaved, float amplitude, const double* frequencies,
+                       mla_rope_plan* plan) {
+  if (!frequencies || !plan || !std::isfinite(amplitude) || amplitude <= 0.f) return MLA_ERR_INVALID_ARG;
+  if (!rotary_ok(rotary_dim)) return MLA_ERR_UNSUPPORTED;
+  const double two_pi = 6.283185307179586476925;
+  mla_rope_plan r = {};
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    const double f = frequencies[i];
+    if (!(f >= 0.0) || f >= two_pi) return MLA_ERR_INVALID_ARG;
+    const double t = f / two_pi;  // < 1; a quotient that rounds to 1 is no turn at all
+    r.turn[i] = t < 1.0 ? static_cast<uint64_t>(t * 0x1p64) : 0;
+  }
+  r.rotary_dim = rotary_dim;
+  r.interleaved = interleaved != 0;
+  r.amplitude = amplitude;
+  *plan = r;
+  return MLA_OK;
+}
+
+int mla_rope_pack(const mla_rope_dims* d, const mla_rope_plan* plan, const void* q_pe, const void* rows,
+                  const int32_t* positions, const int32_t* page_table, const int32_t* seq_lens,
+                  const int32_t* cu_q_lens, float kv_scale, void* q_out, void* kv_cache, int32_t* status,
+                  void* stream_v) {
+  if (!d || !plan || !q_pe || !rows || !page_table || !seq_lens || !cu_q_lens || !q_out || !kv_cache || !status)
+    return MLA_ERR_INVALID_ARG;
+  if (d->batch < 1 || d->num_heads < 1 || d->total_q < 1 || d->num_pages < 1 || d->max_pages_per_req < 1 ||
+      d->page_table_stride < d->max_pages_per_req)
+    return MLA_ERR_INVALID_ARG;
+  const int64_t T = d->total_q, H = d->num_heads;
+  const int64_t q_head = H > 1 ? d->q_head_stride : 64, q_tok = T > 1 ? d->q_token_stride : 64;
+  const int64_t row = T > 1 ? d->row_stride : 576;
+  if (q_head < 64 || q_tok < 64 || row < 576) return MLA_ERR_INVALID_ARG;
+  if (d->kv_dtype != MLA_KV_BF16 && d->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_UNSUPPORTED;
+  if (!rotary_ok(plan->rotary_dim) || H > 65536 || T * H > INT_MAX || static_cast<int64_t>(d->max_pages_per_req) * 64 > INT_MAX ||
+      q_head > (1ll << 40) || q_tok > (1ll << 40) || row > (1ll << 40))
+    return MLA_ERR_UNSUPPORTED;
+  if (!std::isfinite(plan->amplitude) || plan->amplitude <= 0.f) return MLA_ERR_INVALID_ARG;
+  const bool f8 = d->kv_dtype == MLA_KV_FP8_E4M3;
+  if (f8 && !mla::e4m3::scale_ok(kv_scale)) return MLA_ERR_INVALID_ARG;
+  if (!aligned(q_pe, 16) || !aligned(rows, 16) || !aligned(q_out, 16) || !aligned(kv_cache, 16) || q_head % 8 != 0 ||
+      q_tok % 8 != 0 || row % 8 != 0 || !aligned(positions, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
+      !aligned(cu_q_lens, 4) || !aligned(status, 4))
+    return MLA_ERR_ALIGNMENT;
+  const bool same = q_pe == q_out && (H == 1 || q_head == 64) && (T == 1 || q_tok == H * 64);
+  if (!same && overlap(q_pe, 2 * ((T - 1) * q_tok + (H - 1) * q_head + 64), q_out, T * H * 128))
+    return MLA_ERR_INVALID_ARG;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  const int rc = mla::host::device_ok(dev);
+  if (rc != MLA_OK) return rc;
+  using namespace mla::rope;
+  Params p;
+  p.q_pe = static_cast<const uint8_t*>(q_pe);
+  p.rows = static_cast<const uint8_t*>(rows);
+  p.positions = positions;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.cu_q = cu_q_lens;
+  p.q_out = static_cast<uint8_t*>(q_out);
+  p.cache = static_cast<uint8_t*>(kv_cache);
+  p.status = status;
+  p.q_tok = 2 * q_tok;
+  p.q_head = 2 * q_head;
+  p.row = 2 * row;
+  p.B = d->batch;
+  p.H = d->num_heads;
+  p.T = d->total_q;
+  p.num_pages = d->num_pages;
+  p.max_pages = d->max_pages_per_req;
+  p.pt_stride = d->page_table_stride;
+  p.R = plan->rotary_dim;
+  p.amp = plan->amplitude;
+  p.sc = mla::e4m3::scale_of(f8 ? kv_scale : 1.0f);
+  for (int i = 0; i < 32; ++i) p.turn[i] = i < p.R / 2 ? plan->turn[i] : 0;
+  // as many tokens a block as give each thread an item or two, but blocks for
+  // every SM first
+  int64_t toks = (kAhead * kThreads) / (4 * H);
+  const int64_t spread = (T + 151) / 152;
+  toks = toks < spread ? toks : spread;
+  p.toks = static_cast<int32_t>(toks < 1 ? 1 : (toks > kMaxTok ? kMaxTok : toks));
+  const dim3 grid(static_cast<unsigned>((T + p.toks - 1) / p.toks)), block(kThreads);
+  cudaStream_t s = static_cast<cudaStream_t>(stream_v);
+  const bool inter = plan->interleaved != 0;
+  auto* kernel = f8 ? (inter ? &mla_rope_pack_kernel<true, true> : &mla_rope_pack_kernel<true, false>)
+                    : (inter ? &mla_rope_pack_kernel<false, true> : &mla_rope_pack_kernel<false, false>);
+  if (mla::host::launch_pdl(kernel, grid, block, 0, s, 0, p) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,467 @@
+// mla_verify (see include/mla_verify.h): which drafted tokens the target's
+// probabilities accept, and the token that follows.
+//
+// A cluster of eight blocks takes a request.  Every block walks the tree by
+// itself (a warp, from the nodes' entries of their parents' rows, all loaded
+// at once); parents come before children, so the walk is one pass over the
+// nodes.  What takes time is a pass over a whole row: the sum that a rejected
+// draft leaves (z), and the last token's.  Each block adds up its part of the
+// row in chunks of 256 entries, the blocks exchange their sums through
+// distributed shared memory, and the block that holds the token's place finds
+// the chunk by a scan of its sums and the entry by reading that chunk again.
+// So a chain whose draft is rejected reads one row of each kind once: the
+// sums for z are those that the token is chosen by.
+//
+// Sums are integers, units of 2^-60: exact in any order, so that the token is
+// the one that the formula names (fp32 sums over 100K entries are off by more
+// than an entry's width), without 64-bit floating point, which this chip has
+// little of.
+//
+// What bounds it: HBM for batches, for one request the chain of reads
+// (offsets, nodes, their entries, the row, the chunk) and the barriers.
+#include <cuda_runtime.h>
+
+#include <climits>
+#include <cstdint>
+
+#include "mla_host.h"
+#include "mla_sparse.h"
+#include "mla_verify.h"
+#include "sm100_ptx.cuh"
+
+namespace mla {
+namespace verify {
+
+constexpr int kCluster = 8;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 256;                       // entries that a warp adds up to one sum
+constexpr int kMaxVocab = 1 << 20;
+constexpr int kMaxChunks = kMaxVocab / kChunk / kCluster;  // of a block
+constexpr int kNodes = MLA_TREE_MAX_NODES;
+static_assert(kNodes <= kThreads && kNodes % 32 == 0 && kMaxChunks <= 2 * kThreads, "a thread per node, two chunks each");
+
+struct Params {
+  const float* target;
+  const float* draft;
+  const int32_t* tokens;
+  const int32_t* parents;
+  const int32_t* cu_q;
+  const float* accept;
+  const float* sample;
+  int32_t* path;
+  int32_t* tokens_out;
+  int32_t* num_out;
+  int32_t* status;
+  int64_t t_stride, d_stride;
+  int32_t B, T, V, cols;
+  int32_t t_vec, d_vec;  // rows are 16-byte aligned
+};
+
+// A probability in units of 2^-60 (NaN and below 0: 0, above 1: 1).
+__device__ __forceinline__ uint64_t fixed60(float x) {
+  return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 0x1p60f);
+}
+// a * b of such numbers, rounded down.
+__device__ __forceinline__ uint64_t mul60(uint64_t a, uint64_t b) {
+  return (__umul64hi(a, b) << 4) | ((a * b) >> 60);
+}
+
+struct State {
+  int cur, last, cnt;  // the walk's node, the last child tested, nodes on the path
+  int k;               // children rejected at cur
+  int todo;            // what the block does next
+};
+enum { kSum = 0, kFinish = 1 };
+
+struct Shared {
+  int par[kNodes];
+  int tok[kNodes];
+  float acc[kNodes], wp[kNodes], wq[kNodes];  // random number, entries of the parent's rows
+  int path[kNodes];
+  uint64_t z[kNodes];       // draft: the sums before each rejection at cur
+  int gone[kNodes];         // fixed proposals: nodes rejected at cur
+  uint64_t chunk[kMaxChunks];
+  uint64_t warp_sum[kWarps];
+  uint64_t total[2][kCluster];
+  State st;
+  int pick;
+  uint64_t left;
+};
+
+// The weight of an entry after k rejections with a draft.
+__device__ __forceinline__ uint64_t weight(uint64_t w, uint64_t q, const uint64_t* z, int k) {
+  if (k > 0) w = w > q ? w - q : 0;  // z = 1
+  for (int i = 1; i < k; ++i) {
+    const uint64_t t = mul60(z[i], q);
+    w = w > t ? w - t : 0;
+  }
+  return w;
+}
+
+__device__ __forceinline__ uint64_t warp_add(uint64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_scan(uint64_t v) {  // inclusive
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+
+// Four entries from e on (0 behind the row's end).
+__device__ __forceinline__ float4 load4(const float* row, int e, int V, bool vec) {
+  if (vec && e + 4 <= V) return *reinterpret_cast<const float4*>(row + e);
+  float4 v;
+  v.x = e + 0 < V ? row[e + 0] : 0.f;
+  v.y = e + 1 < V ? row[e + 1] : 0.f;
+  v.z = e + 2 < V ? row[e + 2] : 0.f;
+  v.w = e + 3 < V ? row[e + 3] : 0.f;
+  return v;
+}
+
+// Warp 0 of a block: on from s.st to the next sum over the row, or the end.
+// `sum` is the row's sum after the last rejection (draft), `summed` whether
+// the chunks hold the present weights.
+__device__ __forceinline__ void walk(Shared& s, int n, int cols, bool drafted, uint64_t sum, bool& summed) {
+  const int lane = threadIdx.x & 31;
+  State st = s.st;
+  int par[kNodes / 32];
+#pragma unroll
+  for (int g = 0; g < kNodes / 32; ++g) par[g] = g * 32 + lane < n ? s.par[g * 32 + lane] : -2;
+  double z = st.k == 0 ? 1.0 : static_cast<double>(sum) * 0x1p-60;  // (fixed proposals end in one go)
+  st.todo = kFinish;
+  while (st.cnt < cols) {
+    int j = -1;  // the next child of cur
+#pragma unroll
+    for (int g = 0; g < kNodes / 32; ++g) {
+      const unsigned m = __ballot_sync(0xffffffffu, par[g] == st.cur && g * 32 + lane > st.last);
+      if (j < 0 && m) j = g * 32 + __ffs(m) - 1;
+    }
+    if (j < 0) break;
+    st.last = j;
+    const int x = s.tok[j];
+    double w, qx = 1.0;
+    if (drafted) {
+      w = st.k == 0 ? static_cast<double>(fminf(fmaxf(s.wp[j], 0.f), 1.f))
+                    : static_cast<double>(weight(fixed60(s.wp[j]), fixed60(s.wq[j]), s.z, st.k)) * 0x1p-60;
+      qx = static_cast<double>(fminf(fmaxf(s.wq[j], 0.f), 1.f));
+    } else {
+      w = static_cast<double>(fminf(fmaxf(s.wp[j], 0.f), 1.f));
+      bool again = false;  // a token that was rejected already has no weight left
+      for (int i = lane; i < st.k; i += 32) again |= s.tok[s.gone[i]] == x;
+      if (__any_sync(0xffffffffu, again)) w = 0.0;
+    }
+    if (static_cast<double>(s.acc[j]) * z * qx < w) {
+      if (lane == 0) s.path[st.cnt] = j;
+      ++st.cnt;
+      st.cur = j;
+      st.k = 0;
+      z = 1.0;
+      summed = false;
+      continue;
+    }
+    if (drafted) {
+      if (lane == 0) s.z[st.k] = st.k == 0 ? 1ull << 60 : sum;
+      ++st.k;
+      summed = false;
+      st.todo = kSum;
+      break;
+    }
+    if (lane == 0) s.gone[st.k] = j;
+    __syncwarp();
+    ++st.k;
+    summed = false;
+    z = z > w ? z - w : 0.0;
+  }
+  __syncwarp();
+  if (lane == 0) s.st = st;
+}
+
+template <bool kDraft>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
+    mla_verify_kernel(const __grid_constant__ Params p) {
+  __shared__ Shared s;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int b = static_cast<int>(cluster_id_x());
+  int q0 = p.cu_q[b];
+  const int q1 = p.cu_q[b + 1];
+  int n = q1 - q0, flag = 0;
+  if (!(q0 >= 0 && q1 >= q0 && q1 <= p.T && (b > 0 || q0 == 0))) {
+    n = q0 = 0;
+    flag = MLA_DEV_BAD_QUERY_RANGE;
+  } else if (n > kNodes) {
+    n = q0 = 0;
+    flag = MLA_DEV_BAD_TREE;
+  }
+  int32_t* path = p.path + static_cast<int64_t>(b) * p.cols;
+  int32_t* next = p.tokens_out + static_cast<int64_t>(b) * p.cols;
+  if (n == 0) {  // (the same in every block of the cluster)
+    if (rank != 0) return;
+    for (int k = tid; k < p.cols; k += kThreads) path[k] = next[k] = -1;
+    if (tid == 0) {
+      p.num_out[b] = 0;
+      if (flag) atomicOr(p.status, flag);
+    }
+    return;
+  }
+  if (tid < n) {
+    int par = -2, tok = 0;
+    if (tid > 0) {
+      par = p.parents[q0 + tid];
+      tok = p.tokens[q0 + tid];
+      if (par < -1 || par >= tid) {
+        flag |= MLA_DEV_BAD_TREE;
+        par = -2;
+      }
+      if (tok < 0 || tok >= p.V) {
+        flag |= MLA_DEV_BAD_INDEX;
+        par = -2;
+      }
+    } else if (p.parents[q0] != -1) {
+      flag |= MLA_DEV_BAD_TREE;
+    }
+    s.par[tid] = par;
+    s.tok[tid] = tok;
+    if (par >= 0) {
+      s.acc[tid] = p.accept[q0 + tid];
+      s.wp[tid] = p.target[(q0 + par) * p.t_stride + tok];
+      if (kDraft) s.wq[tid] = p.draft[(q0 + par) * p.d_stride + tok];
+    }
+    if (flag && rank == 0) atomicOr(p.status, flag);
+  }
+  if (rank == 0)  // (the block that finds the last token writes it later)
+    for (int k = tid; k < p.cols; k += kThreads) next[k] = -1;
+  if (tid == 0) {
+    s.path[0] = 0;
+    s.st = {0, 0, 1, 0, kFinish};
+  }
+  cluster_sync();  // the blocks have all begun before one writes to another's shared memory
+  const int all = (p.V + kChunk - 1) / kChunk, per = (all + kCluster - 1) / kCluster;
+  const int c0 = rank * per < all ? rank * per : all, nc = (all - c0 < per ? all - c0 : per);
+  uint64_t sum = 0;      // of the row's weights, all blocks
+  bool summed = false;   // (warp 0 decides, then all know)
+  int pass = 0;
+  const float* tr = nullptr;
+  const float* dr = nullptr;
+  State st = {};
+
+  // adds up the weights of the row of st.cur after st.k rejections
+  auto add_up = [&]() {
+    tr = p.target + (q0 + st.cur) * p.t_stride;
+    if (kDraft) dr = p.draft + (q0 + st.cur) * p.d_stride;
+    const bool tv = p.t_vec != 0, dv = p.d_vec != 0, rest = kDraft && st.k > 0;
+    constexpr int kFly = 2;  // chunks of a warp in flight
+    for (int c = warp; c < nc; c += kWarps * kFly) {
+      float4 a[kFly][2], q[kFly][2];
+#pragma unroll
+      for (int f = 0; f < kFly; ++f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int e = (c0 + c + f * kWarps) * kChunk + h * 128 + lane * 4;
+          if (c + f * kWarps < nc) {
+            a[f][h] = load4(tr, e, p.V, tv);
+            if (rest) q[f][h] = load4(dr, e, p.V, dv);
+          }
+        }
+#pragma unroll
+      for (int f = 0; f < kFly; ++f) {
+        if (c + f * kWarps >= nc) break;
+        uint64_t v = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float x[4] = {a[f][h].x, a[f][h].y, a[f][h].z, a[f][h].w};
+          const float y[4] = {q[f][h].x, q[f][h].y, q[f][h].z, q[f][h].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint64_t w = fixed60(x[e]);
+            if (rest) w = weight(w, fixed60(y[e]), s.z, st.k);
+            v += w;
+          }
+        }
+        v = warp_add(v);
+        if (lane == 0) s.chunk[c + f * kWarps] = v;
+      }
+    }
+    __syncthreads();
+    if (!kDraft && tid < st.k) {  // tokens that were rejected have no weight left
+      const int x = s.tok[s.gone[tid]], c = x / kChunk - c0;
+      bool first = c >= 0 && c < nc;
+      for (int i = 0; first && i < tid; ++i) first = s.tok[s.gone[i]] != x;
+      if (first)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.chunk[c]), 0ull - fixed60(s.wp[s.gone[tid]]));
+    }
+    if (!kDraft) __syncthreads();
+    uint64_t v = 0;
+    for (int c = tid; c < nc; c += kThreads) v += s.chunk[c];
+    v = warp_add(v);
+    if (lane == 0) s.warp_sum[warp] = v;
+    __syncthreads();
+    if (warp == 0) {
+      v = warp_add(lane < kWarps ? s.warp_sum[lane] : 0ull);
+      if (lane < kCluster) {
+        const uint32_t dst = mapa(smem_u32(&s.total[pass & 1][rank]), static_cast<uint32_t>(lane));
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(v) : "memory");
+      }
+    }
+    cluster_sync();
+    sum = 0;
+#pragma unroll
+    for (int r = 0; r < kCluster; ++r) sum += s.total[pass & 1][r];
+    ++pass;
+  };
+
+  __shared__ int s_summed;
+  while (true) {
+    if (warp == 0) {
+      walk(s, n, p.cols, kDraft, sum, summed);
+      if (lane == 0) s_summed = summed;
+    }
+    __syncthreads();
+    st = s.st;
+    summed = s_summed != 0;
+    if (!summed) {
+      add_up();
+      summed = true;
+    }
+    if (st.todo == kFinish) break;
+    __syncthreads();
+  }
+  if (sum == 0) {  // rounding has left nothing: the node's own row
+    st.k = 0;
+    add_up();
+  }
+  // the outputs but the last token
+  if (rank == 0) {
+    for (int k = tid; k < p.cols; k += kThreads) {
+      path[k] = k < st.cnt ? s.path[k] : -1;
+      if (k < st.cnt - 1) next[k] = s.tok[s.path[k + 1]];
+    }
+    if (tid == 0) {
+      p.num_out[b] = st.cnt;
+      if (sum == 0) atomicOr(p.status, MLA_DEV_BAD_PROBS);
+    }
+  }
+  if (sum == 0) return;
+  const float u = fminf(fmaxf(p.sample[b], 0.f), 0x1.fffffep-1f);
+  uint64_t at = mul60(fixed60(u), sum);  // below sum
+  const int last_pass = (pass - 1) & 1;
+  bool here = true;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r)
+    if (r < rank) {
+      here = here && at >= s.total[last_pass][r];
+      at -= s.total[last_pass][r];
+    }
+  if (!here || at >= s.total[last_pass][rank]) return;  // (the same in the whole block)
+  // the chunk: each thread two, in order
+  const uint64_t x0 = 2 * tid < nc ? s.chunk[2 * tid] : 0, x1 = 2 * tid + 1 < nc ? s.chunk[2 * tid + 1] : 0;
+  uint64_t v = warp_scan(x0 + x1);
+  __syncthreads();
+  if (lane == 31) s.warp_sum[warp] = v;
+  __syncthreads();
+  v -= x0 + x1;
+  for (int w = 0; w < warp; ++w) v += s.warp_sum[w];
+  if (at >= v && at - v < x0 + x1) {
+    const bool second = at - v >= x0;
+    s.pick = c0 + 2 * tid + (second ? 1 : 0);
+    s.left = at - v - (second ? x0 : 0);
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  // the entry: each lane eight, in order
+  at = s.left;
+  uint64_t w[kChunk / 32], mine = 0;
+  const int e0 = s.pick * kChunk + lane * (kChunk / 32);
+#pragma unroll
+  for (int e = 0; e < kChunk / 32; ++e) {
+    w[e] = 0;
+    if (e0 + e < p.V) {
+      w[e] = fixed60(tr[e0 + e]);
+      if (kDraft) {
+        if (st.k > 0) w[e] = weight(w[e], fixed60(dr[e0 + e]), s.z, st.k);
+      } else {
+        for (int i = 0; i < st.k; ++i)
+          if (s.tok[s.gone[i]] == e0 + e) w[e] = 0;
+      }
+    }
+    mine += w[e];
+  }
+  uint64_t before = warp_scan(mine) - mine;
+  if (at >= before && at - before < mine) {
+    int y = e0;
+#pragma unroll
+    for (int e = 0; e < kChunk / 32; ++e) {
+      if (at >= before) y = e0 + e;
+      before += w[e];
+    }
+    next[st.cnt - 1] = y;
+  }
+}
+
+}  // namespace verify
+}  // namespace mla
+
+extern "C" int mla_verify(const mla_verify_dims* d, const float* target, const float* draft, const int32_t* tokens,
+                          const int32_t* parents, const int32_t* cu_q_lens, const float* accept, const float* sample,
+                          int32_t* path, int32_t* tokens_out, int32_t* num_out, int32_t* status, void* stream) {
+  using mla::host::aligned;
+  if (!d || !target || !tokens || !parents || !cu_q_lens || !accept || !sample || !path || !tokens_out || !num_out ||
+      !status)
+    return MLA_ERR_INVALID_ARG;
+  if (d->batch < 1 || d->total_q < 1 || d->vocab < 1 || d->path_cols < 1 || d->target_stride < d->vocab ||
+      (draft && d->draft_stride < d->vocab))
+    return MLA_ERR_INVALID_ARG;
+  if (d->batch > 1 << 27 || d->vocab > mla::verify::kMaxVocab || d->target_stride > (1ll << 40) ||
+      (draft && d->draft_stride > (1ll << 40)))
+    return MLA_ERR_UNSUPPORTED;
+  if (!aligned(target, 4) || !aligned(draft, 4) || !aligned(tokens, 4) || !aligned(parents, 4) ||
+      !aligned(cu_q_lens, 4) || !aligned(accept, 4) || !aligned(sample, 4) || !aligned(path, 4) ||
+      !aligned(tokens_out, 4) || !aligned(num_out, 4) || !aligned(status, 4))
+    return MLA_ERR_ALIGNMENT;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  const int rc = mla::host::device_ok(dev);
+  if (rc != MLA_OK) return rc;
+  using namespace mla::verify;
+  Params p;
+  p.target = target;
+  p.draft = draft;
+  p.tokens = tokens;
+  p.parents = parents;
+  p.cu_q = cu_q_lens;
+  p.accept = accept;
+  p.sample = sample;
+  p.path = path;
+  p.tokens_out = tokens_out;
+  p.num_out = num_out;
+  p.status = status;
+  p.t_stride = d->target_stride;
+  p.d_stride = draft ? d->draft_stride : 0;
+  p.B = d->batch;
+  p.T = d->total_q;
+  p.V = d->vocab;
+  p.cols = d->path_cols;
+  p.t_vec = aligned(target, 16) && p.t_stride % 4 == 0;
+  p.d_vec = draft && aligned(draft, 16) && p.d_stride % 4 == 0;
+  const dim3 grid(static_cast<unsigned>(p.B) * kCluster), block(kThreads);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = draft ? mla::host::launch_pdl(&mla_verify_kernel<true>, grid, block, 0, s, 0, p)
+                              : mla::host::launch_pdl(&mla_verify_kernel<false>, grid, block, 0, s, 0, p);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return MLA_ERR_CUDA;
+  }
+  return MLA_OK;
+}
