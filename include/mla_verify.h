@@ -20,7 +20,7 @@
  *
  * (Where w has become all zeros, by rounding, the last token comes from p[c].)
  * Sums run in integers, units of 2^-60, so that they are exact whatever their
- * order (an entry below 2^-36 loses what is under 2^-60), and the products of
+ * order (an entry below 2^-36 is rounded to them), and the products of
  * a test are formed in 64-bit floating point.
  *
  * Conventions as in mla_decode.h: caller-owned device buffers, asynchronous on

@@ -982,6 +982,23 @@ def _layers_of(kv_cache):
     return s[0], s[1], k[0] * kv_cache.element_size() if s[0] > 1 else 0
 
 
+def _vec(t, n, dtype, dev) -> bool:
+    """A contiguous vector of n elements."""
+    s = t.shape
+    return (len(s) == 1 and s[0] == n and t.dtype is dtype and t.get_device() == dev
+            and (n < 2 or t.stride(0) == 1))
+
+
+def _table_fits(t, rows, dev, i32) -> bool:
+    s = t.shape
+    return (len(s) == 2 and s[0] == rows and t.dtype is i32 and t.get_device() == dev and t.stride(1) == 1
+            and t.stride(0) >= s[1])
+
+
+def _status_fits(t, dev, i32) -> bool:
+    return t.dtype is i32 and t.get_device() == dev and t.numel() >= 1
+
+
 def _check_layers(kv_cache):
     if _layers_of(kv_cache) is None:
         raise ValueError("kv_cache must be bf16 or e4m3 [num_pages, 64, 576], or [num_layers, num_pages, 64, 576] "
@@ -1006,12 +1023,7 @@ def _check_status(status):
         raise ValueError("status must be an int32 tensor of at least one element")
 
 
-def mla_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status, stream=None) -> None:
-    """Enqueue the move of the accepted nodes' rows (see include/mla_tree.h).
-
-    kv_cache: [num_pages, 64, 576], or one such cache per layer as
-    [num_layers, num_pages, 64, 576]; path int32 [B, cols], num_path and
-    new_lens int32 [B] (new_lens not seq_lens itself); status int32 [1]."""
+def _explain_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status):
     _check_cuda(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status)
     _check_layers(kv_cache)
     B = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
@@ -1023,13 +1035,29 @@ def mla_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, n
     _check_table("page_table", page_table, B)
     _check_status(status)
     _check_devices(dev, page_table, status)
-    _check_current_device(dev.index)
-    layers, pages, step = _layers_of(kv_cache)
-    dims = MlaTreeCommitDims(B, layers, path.shape[1], pages, page_table.shape[1], page_table.stride(0),
-                             _t().cache_codes[kv_cache.dtype], 0, step)
+
+
+def mla_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status, stream=None) -> None:
+    """Enqueue the move of the accepted nodes' rows (see include/mla_tree.h).
+
+    kv_cache: [num_pages, 64, 576], or one such cache per layer as
+    [num_layers, num_pages, 64, 576]; path int32 [B, cols], num_path and
+    new_lens int32 [B] (new_lens not seq_lens itself); status int32 [1]."""
+    t, dev = _t(), kv_cache.get_device()
+    B, i32, ps = seq_lens.shape[0] if seq_lens.dim() == 1 else -1, t.i32, path.shape
+    layers = _layers_of(kv_cache)
+    if not (dev >= 0 and layers is not None and len(ps) == 2 and _vec(seq_lens, B, i32, dev)
+            and _vec(cu_q_lens, B + 1, i32, dev) and _vec(num_path, B, i32, dev) and _vec(new_lens, B, i32, dev)
+            and _fits(path, (B, ps[1]), i32, dev) and _table_fits(page_table, B, dev, i32)
+            and _status_fits(status, dev, i32)):
+        _explain_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status)
+        raise ValueError("commit tensors do not have the shapes, types and layouts the library expects")
+    _check_current_device(dev)
+    dims = MlaTreeCommitDims(B, layers[0], ps[1], layers[1], page_table.shape[1], _stride_of(page_table),
+                             t.cache_codes[kv_cache.dtype], 0, layers[2])
     rc = load_library().mla_tree_commit(
         ctypes.byref(dims), kv_cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), cu_q_lens.data_ptr(),
-        path.data_ptr(), num_path.data_ptr(), new_lens.data_ptr(), status.data_ptr(), _stream_int(stream, dev.index))
+        path.data_ptr(), num_path.data_ptr(), new_lens.data_ptr(), status.data_ptr(), _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_tree_commit")
 
@@ -1040,13 +1068,7 @@ def _check_probs(name, t, rows, vocab):
         raise ValueError(f"{name} must be an fp32 [total_q, vocab] tensor with unit column stride")
 
 
-def mla_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status,
-               stream=None) -> None:
-    """Enqueue the verification of drafted tokens (see include/mla_verify.h).
-
-    target and draft (None: fixed proposals) fp32 [total_q, vocab]; tokens,
-    parents int32 and accept fp32 [total_q]; sample fp32 [B]; path and
-    tokens_out int32 [B, cols], num_out int32 [B]; status int32 [1]."""
+def _explain_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status):
     _check_cuda(target, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status)
     if target.dim() != 2:
         raise ValueError("target must be [total_q, vocab]")
@@ -1067,13 +1089,35 @@ def mla_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, 
                    path=(path, shape), tokens_out=(tokens_out, shape), num_out=(num_out, (B,)))
     _check_status(status)
     _check_devices(dev, accept, sample, status)
-    _check_current_device(dev.index)
-    dims = MlaVerifyDims(B, T, V, path.shape[1], target.stride(0) if T > 1 else V,
+
+
+def mla_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status,
+               stream=None) -> None:
+    """Enqueue the verification of drafted tokens (see include/mla_verify.h).
+
+    target and draft (None: fixed proposals) fp32 [total_q, vocab]; tokens,
+    parents int32 and accept fp32 [total_q]; sample fp32 [B]; path and
+    tokens_out int32 [B, cols], num_out int32 [B]; status int32 [1]."""
+    t, dev, ts = _t(), target.get_device(), target.shape
+    T, V = ts if len(ts) == 2 else (-1, -1)
+    B, f32, i32, ps = sample.shape[0] if sample.dim() == 1 else -1, t.f32, t.i32, path.shape
+    if not (dev >= 0 and len(ts) == 2 and target.dtype is f32 and target.stride(1) == 1
+            and (T < 2 or target.stride(0) >= V)
+            and (draft is None or (draft.dtype is f32 and draft.shape == ts and draft.get_device() == dev
+                                   and draft.stride(1) == 1 and (T < 2 or draft.stride(0) >= V)))
+            and _vec(tokens, T, i32, dev) and _vec(parents, T, i32, dev) and _vec(accept, T, f32, dev)
+            and _vec(sample, B, f32, dev) and _vec(cu_q_lens, B + 1, i32, dev) and len(ps) == 2
+            and _fits(path, (B, ps[1]), i32, dev) and _fits(tokens_out, ps, i32, dev) and _vec(num_out, B, i32, dev)
+            and _status_fits(status, dev, i32)):
+        _explain_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status)
+        raise ValueError("verify tensors do not have the shapes, types and layouts the library expects")
+    _check_current_device(dev)
+    dims = MlaVerifyDims(B, T, V, ps[1], target.stride(0) if T > 1 else V,
                          (draft.stride(0) if T > 1 else V) if draft is not None else 0)
     rc = load_library().mla_verify(
         ctypes.byref(dims), target.data_ptr(), None if draft is None else draft.data_ptr(), tokens.data_ptr(),
         parents.data_ptr(), cu_q_lens.data_ptr(), accept.data_ptr(), sample.data_ptr(), path.data_ptr(),
-        tokens_out.data_ptr(), num_out.data_ptr(), status.data_ptr(), _stream_int(stream, dev.index))
+        tokens_out.data_ptr(), num_out.data_ptr(), status.data_ptr(), _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_verify")
 
@@ -1092,9 +1136,7 @@ def _stride_of(table):
     return table.stride(0) if table.shape[0] > 1 else max(table.stride(0), table.shape[1])
 
 
-def mla_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace, stream=None) -> None:
-    """Enqueue handing out and freeing pages for the requests' new lengths (see
-    include/mla_pages.h); page_table_out and page_refs_out may be the inputs."""
+def _explain_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace):
     _check_cuda(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace)
     B = new_lens.shape[0] if new_lens.dim() == 1 else -1
     dev = new_lens.device
@@ -1109,13 +1151,25 @@ def mla_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_o
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _check_devices(dev, page_table, page_table_out, workspace)
-    _check_current_device(dev.index)
-    dims = MlaPageResizeDims(B, page_refs.shape[0], page_table.shape[1], _stride_of(page_table),
+
+
+def mla_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace, stream=None) -> None:
+    """Enqueue handing out and freeing pages for the requests' new lengths (see
+    include/mla_pages.h); page_table_out and page_refs_out may be the inputs."""
+    t, dev, cols = _t(), new_lens.get_device(), page_table.shape
+    i32, B, P = t.i32, new_lens.shape[0] if new_lens.dim() == 1 else -1, page_refs.shape[0] if page_refs.dim() == 1 else -1
+    if not (dev >= 0 and _vec(new_lens, B, i32, dev) and _vec(page_refs, P, i32, dev) and _vec(page_refs_out, P, i32, dev)
+            and _table_fits(page_table, B, dev, i32) and _table_fits(page_table_out, B, dev, i32)
+            and page_table_out.shape == cols and workspace.is_contiguous() and workspace.get_device() == dev):
+        _explain_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace)
+        raise ValueError("resize tensors do not have the shapes, types and layouts the library expects")
+    _check_current_device(dev)
+    dims = MlaPageResizeDims(B, P, cols[1], _stride_of(page_table),
                              _stride_of(page_table_out))
     rc = load_library().mla_page_resize(
         ctypes.byref(dims), new_lens.data_ptr(), page_table.data_ptr(), page_refs.data_ptr(),
         page_table_out.data_ptr(), page_refs_out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-        _stream_int(stream, dev.index))
+        _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_page_resize")
 
@@ -1129,11 +1183,7 @@ def mla_page_fork_workspace_size(sources: int, children: int, max_pages: int, nu
     return int(n)
 
 
-def mla_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace,
-                  stream=None) -> None:
-    """Enqueue the fork of requests (see include/mla_pages.h): child c continues
-    request src[c] (int32 [children], -1 = an empty row); kv_cache as for
-    mla_tree_commit; page_refs_out may be page_refs."""
+def _explain_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace):
     _check_cuda(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace)
     _check_layers(kv_cache)
     S = seq_lens.shape[0] if seq_lens.dim() == 1 else -1
@@ -1149,13 +1199,29 @@ def mla_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out
     if not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
     _check_devices(dev, page_table, page_table_out, workspace)
-    _check_current_device(dev.index)
-    dims = MlaPageForkDims(S, C, layers, pages, page_table.shape[1], _stride_of(page_table),
-                           _stride_of(page_table_out), _t().cache_codes[kv_cache.dtype], step)
+
+
+def mla_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace,
+                  stream=None) -> None:
+    """Enqueue the fork of requests (see include/mla_pages.h): child c continues
+    request src[c] (int32 [children], -1 = an empty row); kv_cache as for
+    mla_tree_commit; page_refs_out may be page_refs."""
+    t, dev, cols = _t(), kv_cache.get_device(), page_table.shape
+    i32, S, C = t.i32, seq_lens.shape[0] if seq_lens.dim() == 1 else -1, src.shape[0] if src.dim() == 1 else -1
+    layers = _layers_of(kv_cache)
+    if not (dev >= 0 and layers is not None and _vec(src, C, i32, dev) and _vec(seq_lens, S, i32, dev)
+            and _vec(page_refs, layers[1], i32, dev) and _vec(page_refs_out, layers[1], i32, dev)
+            and _table_fits(page_table, S, dev, i32) and _table_fits(page_table_out, C, dev, i32)
+            and page_table_out.shape[1] == cols[1] and workspace.is_contiguous() and workspace.get_device() == dev):
+        _explain_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace)
+        raise ValueError("fork tensors do not have the shapes, types and layouts the library expects")
+    _check_current_device(dev)
+    dims = MlaPageForkDims(S, C, layers[0], layers[1], cols[1], _stride_of(page_table), _stride_of(page_table_out),
+                           t.cache_codes[kv_cache.dtype], layers[2])
     rc = load_library().mla_page_fork(
         ctypes.byref(dims), src.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), page_refs.data_ptr(),
         kv_cache.data_ptr(), page_table_out.data_ptr(), page_refs_out.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _stream_int(stream, dev.index))
+        workspace.nbytes, _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_page_fork")
 
@@ -1189,14 +1255,7 @@ def mla_rope_plan(rotary_dim, base=10000.0, factor=1.0, original_len=0, fast=32.
     return plan
 
 
-def mla_rope_pack(plan, q_pe, rows, positions, page_table, seq_lens, cu_q_lens, kv_scale, q_out, kv_cache, status,
-                  stream=None) -> None:
-    """Enqueue the rotation of a step's q_pe and k_pe and the cache write of its
-    rows (see include/mla_rope.h).
-
-    q_pe bf16 [total_q, H, 64] and rows bf16 [total_q, 576], with unit stride in
-    the last dimension; positions int32 [total_q], or None: the tokens' slots;
-    q_out bf16 [total_q, H, 64], contiguous (q_pe itself if that is)."""
+def _explain_rope(q_pe, rows, positions, page_table, seq_lens, cu_q_lens, q_out, kv_cache, status):
     t = _t()
     _check_cuda(q_pe, rows, page_table, seq_lens, cu_q_lens, q_out, kv_cache, status)
     if q_pe.dim() != 3 or q_pe.shape[2] != 64 or q_pe.dtype != t.bf16 or q_pe.stride(2) != 1:
@@ -1216,14 +1275,33 @@ def mla_rope_pack(plan, q_pe, rows, positions, page_table, seq_lens, cu_q_lens, 
         _check_vectors(dev, positions=(positions, (T,)))
     _check_status(status)
     _check_devices(dev, rows, q_out, kv_cache, page_table, seq_lens, status)
-    _check_current_device(dev.index)
-    dims = MlaRopeDims(B, H, T, kv_cache.shape[0], page_table.shape[1], page_table.stride(0),
+
+
+def mla_rope_pack(plan, q_pe, rows, positions, page_table, seq_lens, cu_q_lens, kv_scale, q_out, kv_cache, status,
+                  stream=None) -> None:
+    """Enqueue the rotation of a step's q_pe and k_pe and the cache write of its
+    rows (see include/mla_rope.h).
+
+    q_pe bf16 [total_q, H, 64] and rows bf16 [total_q, 576], with unit stride in
+    the last dimension; positions int32 [total_q], or None: the tokens' slots;
+    q_out bf16 [total_q, H, 64], contiguous (q_pe itself if that is)."""
+    t, dev, qs = _t(), q_pe.get_device(), q_pe.shape
+    B, i32, bf16 = seq_lens.shape[0] if seq_lens.dim() == 1 else -1, t.i32, t.bf16
+    if not (dev >= 0 and len(qs) == 3 and qs[2] == 64 and q_pe.dtype is bf16 and q_pe.stride(2) == 1
+            and rows.dtype is bf16 and rows.shape == (qs[0], 576) and rows.stride(1) == 1 and rows.get_device() == dev
+            and _fits(q_out, qs, bf16, dev) and _cache_fits(kv_cache, page_table, seq_lens, B, dev, t)
+            and kv_cache.shape[1] == 64 and _vec(cu_q_lens, B + 1, i32, dev)
+            and (positions is None or _vec(positions, qs[0], i32, dev)) and _status_fits(status, dev, i32)):
+        _explain_rope(q_pe, rows, positions, page_table, seq_lens, cu_q_lens, q_out, kv_cache, status)
+        raise ValueError("rope tensors do not have the shapes, types and layouts the library expects")
+    _check_current_device(dev)
+    dims = MlaRopeDims(B, qs[1], qs[0], kv_cache.shape[0], page_table.shape[1], page_table.stride(0),
                        t.cache_codes[kv_cache.dtype], 0, q_pe.stride(0), q_pe.stride(1), rows.stride(0))
     rc = load_library().mla_rope_pack(
         ctypes.byref(dims), ctypes.byref(plan), q_pe.data_ptr(), rows.data_ptr(),
         None if positions is None else positions.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
         cu_q_lens.data_ptr(), float(kv_scale), q_out.data_ptr(), kv_cache.data_ptr(), status.data_ptr(),
-        _stream_int(stream, dev.index))
+        _stream_int(stream, dev))
     if rc != MLA_OK:
         raise MlaError(rc, "mla_rope_pack")
 

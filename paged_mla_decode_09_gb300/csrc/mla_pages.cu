@@ -2,14 +2,16 @@
 // include/mla_tree.h).
 //
 // Handing out (mla_page_resize, mla_page_fork): one cluster of eight blocks
-// does a call, in steps that a cluster barrier separates: counts copied; pages
-// given back or shared (atomic additions: the counts do not depend on their
-// order) and missing entries counted; free pages counted; as many free ids as
-// entries are missing written to a list, lowest first; the k-th missing entry
-// takes the k-th id.  Every block holds a contiguous part of the tables' and of
-// the counts' order, so ranks are a block's scan plus the sums of the blocks
-// before it.  A free list kept between calls would spare the walk over the
-// counts (4 bytes a page), but its order would depend on the calls before.
+// does a call, in steps that a cluster barrier separates: counts copied and
+// their zeros counted; pages given back or shared (atomic additions: the counts
+// do not depend on their order; what becomes free is added to its block's
+// zeros) and each row's missing entries counted; as many free ids as entries
+// are missing written to a list, lowest first; the k-th missing entry takes the
+// k-th id.  Every block holds a contiguous part of the rows and of the counts,
+// so ranks are a block's scan plus the sums of the blocks before it, and blocks
+// behind the last id that is wanted have nothing to list.  A free list kept
+// between calls would spare the walk over the counts (4 bytes a page), but its
+// order would depend on the calls before.
 // What bounds it: the latency of the steps, about four reads and barriers, then
 // what eight SMs read.
 //
@@ -39,7 +41,7 @@ constexpr int kPage = 64;
 constexpr int kCluster = 8;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
-constexpr int kTile = 4 * kThreads;  // entries of a step: four in a row per thread
+constexpr int kTile = 4 * kThreads;  // pages of a step: four in a row per thread
 
 struct Params {
   const int32_t* table;
@@ -49,6 +51,7 @@ struct Params {
   int32_t* table_out;
   int32_t* refs_out;
   int32_t* status;
+  int32_t* missing;      // [B] entries of each row that receive a free page
   int32_t* list;         // free ids, as many as entries are missing at most
   int4* copies;          // fork: [B] page, new page (-1: none), rows, -
   int64_t t_stride, o_stride;
@@ -79,142 +82,204 @@ __device__ __forceinline__ int block_before(int v, int (&warps)[kWarps], int& al
   return base + incl - v;
 }
 
-// What an entry of the tables is to become.
-struct Entry {
-  int32_t out;      // kept or shared id, else -1
-  bool missing;     // receives a free page
-  int32_t change;   // of the count of page `id`
-  int32_t id;
-  int flag;
-  int32_t from, rows;  // fork: the started page and its rows
+__device__ __forceinline__ void red_cluster_add(uint32_t addr, int v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.add.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// What a row of the output is made of: `row` of the input, its first `keep`
+// entries as they are (fork: shared), the entries below `need` present, those
+// from there on not.  fork: need - keep is 1 where a page has been started.
+struct Row {
+  const int32_t* row;
+  int keep, need, tail, flag;
 };
 
 template <bool kFork>
-__device__ __forceinline__ Entry entry_at(const Params& p, const int32_t* table, int b, int c) {
-  Entry e = {-1, false, 0, 0, 0, -1, 0};
+__device__ __forceinline__ Row row_of(const Params& p, int b) {
+  Row r = {p.table, 0, 0, 0, 0};
   int s = b;
   if (kFork) {
     s = p.src[b];
     if (s < 0 || s >= p.S) {
-      if (s != -1 && c == 0) e.flag = MLA_DEV_BAD_INDEX;
-      return e;
+      if (s != -1) r.flag = MLA_DEV_BAD_INDEX;
+      return r;
     }
   }
   int L = p.lens[s];
   if (L < 0 || L > p.cols * kPage) {
-    if (c == 0) e.flag = MLA_DEV_BAD_SEQ_LEN;
+    r.flag = MLA_DEV_BAD_SEQ_LEN;
     L = L < 0 ? 0 : p.cols * kPage;
   }
-  const int need = (L >> 6) + ((L & 63) != 0);
-  if (kFork && c >= need) return e;
-  const int32_t id = table[static_cast<int64_t>(s) * p.t_stride + c];
-  if (kFork) {
-    if (id < 0 || id >= p.P) {
-      e.flag |= MLA_DEV_BAD_PAGE_ID;
-    } else if (c < (L >> 6)) {
-      e.out = e.id = id;
-      e.change = 1;
-    } else {
-      e.missing = true;
-      e.from = id;
-      e.rows = L & 63;
-    }
-    return e;
-  }
-  if (id >= p.P) {
-    e.flag |= MLA_DEV_BAD_PAGE_ID;
-    e.out = c < need ? id : -1;
-  } else if (id < 0) {
-    e.missing = c < need;
-  } else if (c < need) {
-    e.out = id;
-  } else {
-    e.id = id;
-    e.change = -1;
-  }
-  return e;
+  r.row = p.table + s * p.t_stride;
+  r.keep = L >> 6;
+  r.tail = L & 63;
+  r.need = r.keep + (r.tail != 0);
+  if (!kFork) r.keep = r.need;
+  return r;
 }
 
 template <bool kFork>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     mla_pages_kernel(const __grid_constant__ Params p) {
   __shared__ int warps[kWarps];
-  __shared__ int missing_of[kCluster], free_of[kCluster];  // every block's, written by the blocks themselves
+  __shared__ int missing_of[kCluster];  // every block's, written by the blocks themselves
+  __shared__ int free_of[kCluster];
+  __shared__ int free_pages;            // of this block's part of the counts
+  __shared__ int lacks[kThreads], begins[kThreads];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, rank = static_cast<int>(cluster_ctarank());
-  auto tell = [&](int (&dst)[kCluster], int v) {  // v of this block to all
-    if (tid < kCluster) st_cluster_u32(mapa(smem_u32(&dst[rank]), static_cast<uint32_t>(tid)), static_cast<uint32_t>(v));
-  };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = static_cast<int>(cluster_ctarank());
   if (rank == 0 && tid == 0) *p.status = 0;
-  if (p.refs_out != p.refs) {
-    const bool vec = ((reinterpret_cast<uintptr_t>(p.refs) | reinterpret_cast<uintptr_t>(p.refs_out)) & 15) == 0;
-    const int quads = vec ? p.P / 4 : 0, at = rank * kThreads + tid;
-    for (int i = at; i < quads; i += kCluster * kThreads)
-      reinterpret_cast<int4*>(p.refs_out)[i] = reinterpret_cast<const int4*>(p.refs)[i];
-    for (int i = 4 * quads + at; i < p.P; i += kCluster * kThreads) p.refs_out[i] = p.refs[i];
+  // rows of the tables: a contiguous part of them per block
+  const int rpart = static_cast<int>((static_cast<int64_t>(p.B) + kCluster - 1) / kCluster);
+  const int rlo = static_cast<int>(min(static_cast<int64_t>(p.B), static_cast<int64_t>(rank) * rpart));
+  const int rhi = p.B - rlo < rpart ? p.B : rlo + rpart;
+  for (int b = rlo + tid; b < rhi; b += kThreads) p.missing[b] = 0;
+  // this block's part of the counts: copied, at least 0, free pages counted
+  const int ppart = (p.P / kCluster + 4) & ~3;
+  const int plo = static_cast<int>(min(static_cast<int64_t>(p.P), static_cast<int64_t>(rank) * ppart));
+  const int phi = p.P - plo < ppart ? p.P : plo + ppart;
+  const bool vec = ((reinterpret_cast<uintptr_t>(p.refs) | reinterpret_cast<uintptr_t>(p.refs_out)) & 15) == 0;
+  int zeros = 0, below = 0, all;
+  {
+    const bool copy = p.refs_out != p.refs;
+    const int quads = vec ? (phi - plo) / 4 : 0;
+    const int4* src = reinterpret_cast<const int4*>(p.refs + plo);
+    int4* dst = reinterpret_cast<int4*>(p.refs_out + plo);
+#pragma unroll 4
+    for (int i = tid; i < quads; i += kThreads) {
+      int4 v = src[i];
+      const bool neg = (v.x | v.y | v.z | v.w) < 0;
+      if (neg) {
+        v = make_int4(max(v.x, 0), max(v.y, 0), max(v.z, 0), max(v.w, 0));
+        below = 1;
+      }
+      zeros += (v.x == 0) + (v.y == 0) + (v.z == 0) + (v.w == 0);
+      if (copy || neg) dst[i] = v;
+    }
+    for (int i = plo + 4 * quads + tid; i < phi; i += kThreads) {
+      const int v = p.refs[i];
+      if (copy || v < 0) p.refs_out[i] = max(v, 0);
+      below |= v < 0;
+      zeros += v <= 0;
+    }
   }
-  cluster_sync();  // (also: every block has begun)
-  // the tables' entries of this block: [lo, hi) of the rows in one sequence
-  const int total = p.B * p.cols;
-  const int part = total / kCluster + 1;
-  const int lo = static_cast<int>(min(static_cast<int64_t>(total), static_cast<int64_t>(rank) * part));
-  const int hi = total - lo < part ? total : lo + part;
-  int missing = 0, flag = 0;
-  for (int64_t i0 = lo; i0 < hi; i0 += kTile) {
+  block_before(zeros, warps, all);
+  if (tid == 0) free_pages = all;
+  cluster_sync();  // every block has begun, the counts are in place, the status is clear
+  if (below) atomicOr(p.status, MLA_DEV_BAD_REFS);
+  // entries, four of a row a time: kFly times four of them in flight
+  auto owner = [&](int id) { return mapa(smem_u32(&free_pages), static_cast<uint32_t>(id / ppart)); };
+  constexpr int kFly = 2;
+  const uint32_t per_row = static_cast<uint32_t>(p.cols + 3) / 4, quads = static_cast<uint32_t>(rhi - rlo) * per_row;
+  const bool tvec = ((reinterpret_cast<uintptr_t>(p.table) | 4 * p.t_stride) & 15) == 0;
+  const bool ovec = ((reinterpret_cast<uintptr_t>(p.table_out) | 4 * p.o_stride) & 15) == 0;
+  int lacking = 0, flag = 0;
+  for (uint32_t i0 = tid; i0 < quads; i0 += kFly * kThreads) {
+    Row r[kFly];
+    int b[kFly], c[kFly];
+    int32_t id[kFly][4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + u * kThreads + tid;
-      if (i >= hi) break;
-      const int b = static_cast<int>(i) / p.cols, c = static_cast<int>(i) - b * p.cols;
-      const Entry e = entry_at<kFork>(p, p.table, b, c);
-      if (kFork && c == 0) p.copies[b] = make_int4(0, -1, 0, 0);
-      if (e.change) atomicAdd(p.refs_out + e.id, e.change);
-      p.table_out[b * p.o_stride + c] = e.out;
-      missing += e.missing;
-      flag |= e.flag;
+    for (int f = 0; f < kFly; ++f) {
+      const uint32_t i = i0 + f * kThreads, row = i < quads ? i / per_row : 0;
+      b[f] = rlo + static_cast<int>(row);
+      c[f] = i < quads ? 4 * static_cast<int>(i - row * per_row) : p.cols;
+      if (!kFork && c[f] < p.cols) {  // (does not wait for the length)
+        const int32_t* at = p.table + b[f] * p.t_stride + c[f];
+        if (tvec && c[f] + 4 <= p.cols) {
+          const int4 v = *reinterpret_cast<const int4*>(at);
+          id[f][0] = v.x; id[f][1] = v.y; id[f][2] = v.z; id[f][3] = v.w;
+        } else {
+#pragma unroll
+          for (int u = 0; u < 4; ++u) id[f][u] = c[f] + u < p.cols ? at[u] : -1;
+        }
+      }
+      if (c[f] < p.cols) r[f] = row_of<kFork>(p, b[f]);
+    }
+    if (kFork)
+#pragma unroll
+      for (int f = 0; f < kFly; ++f)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c[f] < p.cols) id[f][u] = c[f] + u < r[f].need ? r[f].row[c[f] + u] : -1;
+#pragma unroll
+    for (int f = 0; f < kFly; ++f) {
+      if (c[f] >= p.cols) break;
+      int32_t o[4];
+      int missing = 0, old[4];
+      unsigned did = 0;  // entries whose page's count changed
+      flag |= r[f].flag;
+      if (kFork && c[f] == 0) p.copies[b[f]] = make_int4(0, -1, r[f].tail, r[f].keep);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int col = c[f] + u, e = id[f][u];
+        o[u] = -1;
+        if (kFork) {
+          if (col >= r[f].need) continue;
+          if (e < 0 || e >= p.P) {
+            flag |= MLA_DEV_BAD_PAGE_ID;
+          } else if (col < r[f].keep) {
+            o[u] = e;
+            old[u] = atomicAdd(p.refs_out + e, 1);
+            did |= 1u << u;
+          } else {
+            ++missing;
+          }
+        } else {
+          if (e >= p.P) flag |= MLA_DEV_BAD_PAGE_ID;
+          if (col >= p.cols) continue;
+          if (col < r[f].need) {
+            o[u] = e < 0 ? -1 : e;
+            missing += e < 0;
+          } else if (e >= 0 && e < p.P) {  // given back
+            old[u] = atomicSub(p.refs_out + e, 1);
+            did |= 1u << u;
+          }
+        }
+      }
+      int32_t* out = p.table_out + b[f] * p.o_stride + c[f];
+      if (ovec && c[f] + 4 <= p.cols) {
+        *reinterpret_cast<int4*>(out) = make_int4(o[0], o[1], o[2], o[3]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (c[f] + u < p.cols) out[u] = o[u];
+      }
+      if (missing) atomicAdd(p.missing + b[f], missing);
+      lacking += missing;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int e = id[f][u];
+        if (!(did >> u & 1u)) continue;
+        if (kFork) {
+          if (old[u] == 0) red_cluster_add(owner(e), -1);  // (a count that was wrong)
+        } else if (old[u] == 1) {  // free now
+          red_cluster_add(owner(e), 1);
+        } else if (old[u] <= 0) {  // given back more often than it was named: the count stays 0
+          atomicAdd(p.refs_out + e, 1);
+          flag |= MLA_DEV_BAD_REFS;
+        }
+      }
     }
   }
   if (flag) atomicOr(p.status, flag);
-  int mine;
-  block_before(missing, warps, mine);
-  tell(missing_of, mine);
+  block_before(lacking, warps, all);
+  if (tid < kCluster)
+    st_cluster_u32(mapa(smem_u32(&missing_of[rank]), static_cast<uint32_t>(tid)), static_cast<uint32_t>(all));
   cluster_sync();
-  int wanted = 0, before = 0;  // missing entries in all, and of the blocks before this one
+  // free pages of all blocks, read where they are counted (no block ends before the next barrier)
+  if (tid < kCluster)
+    free_of[tid] = static_cast<int>(ld_cluster_u32(mapa(smem_u32(&free_pages), static_cast<uint32_t>(tid))));
+  __syncthreads();
+  int wanted = 0, before = 0, have = 0, fbefore = 0;  // in all, and of the blocks before this one
 #pragma unroll
   for (int r = 0; r < kCluster; ++r) {
     wanted += missing_of[r];
     before += r < rank ? missing_of[r] : 0;
-  }
-  // free pages of this block's part of the counts
-  const int ppart = ((p.P + kCluster - 1) / kCluster + 3) & ~3;
-  const int plo = static_cast<int>(min(static_cast<int64_t>(p.P), static_cast<int64_t>(rank) * ppart));
-  const int phi = p.P - plo < ppart ? p.P : plo + ppart;
-  int zeros = 0, below = 0;
-  for (int i0 = plo + tid; i0 < phi; i0 += kTile) {
-    int v[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) v[u] = i0 + u * kThreads < phi ? __ldcg(p.refs_out + i0 + u * kThreads) : 1;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (v[u] < 0) {
-        p.refs_out[i0 + u * kThreads] = 0;
-        below = 1;
-      }
-      zeros += v[u] <= 0;
-    }
-  }
-  if (below) atomicOr(p.status, MLA_DEV_BAD_REFS);
-  if (wanted == 0) return;  // (the same in every block; no block writes to another from here on)
-  block_before(zeros, warps, mine);
-  tell(free_of, mine);
-  cluster_sync();
-  int have = 0, fbefore = 0;
-#pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
     have += free_of[r];
     fbefore += r < rank ? free_of[r] : 0;
   }
+  // the lowest free ids
   for (int i0 = plo; i0 < phi && fbefore < wanted; i0 += kTile) {
     int v[4];
     const int i = i0 + 4 * tid;
@@ -224,7 +289,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       v[u] = i + u < phi ? __ldcg(p.refs_out + i + u) : 1;
       n += v[u] <= 0;
     }
-    int all;
     int k = fbefore + block_before(n, warps, all);
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -241,40 +305,38 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   // the k-th missing entry takes the k-th free id
   if (wanted > have && rank == 0 && tid == 0) atomicOr(p.status, MLA_DEV_NO_PAGES);
   if (missing_of[rank] == 0) return;
-  for (int64_t i0 = lo; i0 < hi; i0 += kTile) {
-    unsigned mask = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t i = i0 + 4 * tid + u;
-      if (i >= hi) break;
-      const int b = static_cast<int>(i) / p.cols, c = static_cast<int>(i) - b * p.cols;
-      // resize: the entry as the first walk left it, which may have been in place
-      if (kFork) {
-        mask |= entry_at<kFork>(p, p.table, b, c).missing ? 1u << u : 0u;
-      } else {
-        int L = p.lens[b];
-        L = L < 0 ? 0 : (L > p.cols * kPage ? p.cols * kPage : L);
-        if (c < (L >> 6) + ((L & 63) != 0) && p.table_out[b * p.o_stride + c] < 0) mask |= 1u << u;
+  for (int b0 = rlo; b0 < rhi; b0 += kThreads) {
+    const int b = b0 + tid, n = b < rhi ? __ldcg(p.missing + b) : 0;
+    const int at = before + block_before(n, warps, all);  // where the row's entries begin in the list
+    before += all;
+    if (kFork) {  // the one entry behind the shared ones
+      if (n > 0 && at < have) {
+        const int4 c = __ldcg(p.copies + b);
+        const int32_t id = __ldcg(p.list + at);
+        p.copies[b] = make_int4(p.table[p.src[b] * p.t_stride + c.w], id, c.z, 0);
+        p.table_out[b * p.o_stride + c.w] = id;
+      }
+      continue;
+    }
+    lacks[tid] = n;
+    begins[tid] = at;
+    __syncthreads();
+    for (int j = warp; j < kThreads && b0 + j < rhi; j += kWarps) {  // a warp per row, from its end, where requests grow
+      if (lacks[j] == 0) continue;
+      int L = p.lens[b0 + j];
+      L = L > p.cols * kPage ? p.cols * kPage : L;
+      const int need = (L >> 6) + ((L & 63) != 0), k = begins[j];
+      int32_t* out = p.table_out + (b0 + j) * p.o_stride;
+      int upto = k + lacks[j];
+      for (int c0 = (need - 1) / 32 * 32; c0 >= 0 && upto > k; c0 -= 32) {
+        const int c = c0 + lane;
+        const unsigned lack = __ballot_sync(0xffffffffu, c < need && out[c] < 0);
+        upto -= __popc(lack);
+        const int place = upto + __popc(lack & ((1u << lane) - 1u));
+        if ((lack >> lane & 1u) && place < have) out[c] = __ldcg(p.list + place);
       }
     }
-    int all;
-    int k = before + block_before(__popc(mask), warps, all);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (mask >> u & 1u) {
-        if (k < have) {
-          const int64_t i = i0 + 4 * tid + u;
-          const int b = static_cast<int>(i) / p.cols, c = static_cast<int>(i) - b * p.cols;
-          const int32_t id = __ldcg(p.list + k);
-          p.table_out[b * p.o_stride + c] = id;
-          if (kFork) {
-            const Entry e = entry_at<kFork>(p, p.table, b, c);
-            p.copies[b] = make_int4(e.from, id, e.rows, 0);
-          }
-        }
-        ++k;
-      }
-    before += all;
+    __syncthreads();
   }
 }
 
@@ -404,10 +466,11 @@ bool sizes_ok(int64_t rows, int64_t cols, int64_t pages) {
   return cols * 64 <= INT_MAX && rows * cols <= INT_MAX && pages <= 1 << 30;
 }
 
-// [status | free ids | copies]
+// [status | missing entries of each row | free ids | copies]
 size_t list_bytes(int64_t rows, int64_t cols, int64_t pages) {
   return align256(4 * static_cast<size_t>(rows * cols < pages ? rows * cols : pages));
 }
+size_t row_bytes(int64_t rows) { return align256(4 * static_cast<size_t>(rows)); }
 int64_t cache_bytes(int64_t num_pages, bool f8) { return num_pages * 64 * (f8 ? 576 : 1152); }
 
 template <bool kFork>
@@ -422,7 +485,7 @@ extern "C" {
 
 size_t mla_page_resize_workspace_size(int32_t batch, int32_t max_pages_per_req, int32_t num_pages) {
   if (batch < 1 || max_pages_per_req < 1 || num_pages < 1 || !sizes_ok(batch, max_pages_per_req, num_pages)) return 0;
-  return 256 + list_bytes(batch, max_pages_per_req, num_pages);
+  return 256 + row_bytes(batch) + list_bytes(batch, max_pages_per_req, num_pages);
 }
 
 int mla_page_resize(const mla_page_resize_dims* d, const int32_t* new_lens, const int32_t* page_table,
@@ -452,7 +515,8 @@ int mla_page_resize(const mla_page_resize_dims* d, const int32_t* new_lens, cons
   p.table_out = page_table_out;
   p.refs_out = page_refs_out;
   p.status = reinterpret_cast<int32_t*>(ws);
-  p.list = reinterpret_cast<int32_t*>(ws + 256);
+  p.missing = reinterpret_cast<int32_t*>(ws + 256);
+  p.list = reinterpret_cast<int32_t*>(ws + 256 + row_bytes(B));
   p.t_stride = d->table_stride;
   p.o_stride = d->out_stride;
   p.B = p.S = d->batch;
@@ -469,7 +533,7 @@ size_t mla_page_fork_workspace_size(int32_t sources, int32_t children, int32_t m
   if (sources < 1 || children < 1 || max_pages_per_req < 1 || num_pages < 1 ||
       !sizes_ok(children, max_pages_per_req, num_pages))
     return 0;
-  return 256 + list_bytes(children, 1, num_pages) + align256(static_cast<size_t>(children) * 16);
+  return 256 + row_bytes(children) + list_bytes(children, 1, num_pages) + align256(static_cast<size_t>(children) * 16);
 }
 
 int mla_page_fork(const mla_page_fork_dims* d, const int32_t* src, const int32_t* seq_lens, const int32_t* page_table,
@@ -504,8 +568,9 @@ int mla_page_fork(const mla_page_fork_dims* d, const int32_t* src, const int32_t
   p.table_out = page_table_out;
   p.refs_out = page_refs_out;
   p.status = reinterpret_cast<int32_t*>(ws);
-  p.list = reinterpret_cast<int32_t*>(ws + 256);
-  p.copies = reinterpret_cast<int4*>(ws + 256 + list_bytes(B, 1, P));
+  p.missing = reinterpret_cast<int32_t*>(ws + 256);
+  p.list = reinterpret_cast<int32_t*>(ws + 256 + row_bytes(B));
+  p.copies = reinterpret_cast<int4*>(ws + 256 + row_bytes(B) + list_bytes(B, 1, P));
   p.t_stride = d->table_stride;
   p.o_stride = d->out_stride;
   p.B = d->children;

@@ -10,8 +10,7 @@
 // Work: a block takes a few tokens.  A head's 64 values are four items of two
 // 16-byte chunks, chosen so that an item needs the same eight angles in both
 // layouts (interleaved: chunks 2 i and 2 i + 1; halves: chunk i and the one
-// R / 2 behind it), so a thread that walks over heads keeps its angles in
-// registers.  The loads of queries and rows do not depend on the request: they
+// R / 2 behind it); a thread's items are all of one i.  The loads of queries and rows do not depend on the request: they
 // are in flight while the block looks its tokens up (offsets, length, page:
 // three dependent reads) and forms the angles.
 //
@@ -50,7 +49,7 @@ struct Params {
   uint8_t* cache;
   int32_t* status;
   int64_t q_tok, q_head, row;  // strides in bytes
-  int32_t B, H, T, num_pages, max_pages, pt_stride, R, toks;
+  int32_t B, H, T, num_pages, max_pages, pt_stride, R, toks, more;
   float amp;
   e4m3::Scale sc;
   uint64_t turn[32];
@@ -84,9 +83,16 @@ __device__ __forceinline__ void chunks_of(int i, int R, bool inter, int& c0, int
   c1 = halves ? i + (R >> 4) : 2 * i + 1;
 }
 
-// Rotates an item's two chunks by its eight angles.
+// Rotates an item's two chunks by its eight angles (cosines, then sines).
 template <bool kInter>
-__device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const float (&co)[8], const float (&si)[8]) {
+__device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const float (&cs)[16]) {
+  float co[8], si[8];
+#pragma unroll
+  for (int k = 0; k < 8; k += 4) {
+    const float4 c = *reinterpret_cast<const float4*>(cs + k), s = *reinterpret_cast<const float4*>(cs + 8 + k);
+    co[k] = c.x; co[k + 1] = c.y; co[k + 2] = c.z; co[k + 3] = c.w;
+    si[k] = s.x; si[k + 1] = s.y; si[k + 2] = s.z; si[k + 3] = s.w;
+  }
   if constexpr (kInter) {
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -107,15 +113,16 @@ __device__ __forceinline__ void turn8(float (&a)[8], float (&b)[8], const float 
 }
 
 template <bool kF8, bool kInter>
-__global__ void __launch_bounds__(kThreads) mla_rope_pack_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 5) mla_rope_pack_kernel(const __grid_constant__ Params p) {
   __shared__ int s_req[kMaxTok];
   __shared__ int64_t s_slot[kMaxTok];                        // cache row, -1: not written
   __shared__ __align__(16) float s_cs[kMaxTok][4][16];       // per item: eight cosines, eight sines
   griddep_wait();
   griddep_launch_dependents();
   const int tid = threadIdx.x;
-  const int t0 = blockIdx.x * p.toks;
-  const int nt = p.T - t0 < p.toks ? p.T - t0 : p.toks;
+  // the tokens in equal parts (the first p.more blocks take one more)
+  const int bx = static_cast<int>(blockIdx.x), nt = p.toks + (bx < p.more ? 1 : 0);
+  const int t0 = bx * p.toks + (bx < p.more ? bx : p.more);
   const int per = p.H * 4;                      // query items of a token
   const int items = nt * per, lats = nt * kLatChunks;
   // first loads: query items tid, tid + 256, ..; c_kv chunks likewise
@@ -189,8 +196,6 @@ __global__ void __launch_bounds__(kThreads) mla_rope_pack_kernel(const __grid_co
   // queries: a thread's items are all of one number i when 256 is a multiple of 4
   const int i = tid & 3;
   const bool turns = i < (p.R >> 4);
-  float co[8], si[8];
-  int have = -1;
   auto put_q = [&](int it, const uint4& va, const uint4& vb) {
     const int k = it / per, r = it - k * per;
     if (s_req[k] < 0) return;
@@ -202,18 +207,10 @@ __global__ void __launch_bounds__(kThreads) mla_rope_pack_kernel(const __grid_co
       *reinterpret_cast<uint4*>(dst + 16 * c1) = vb;
       return;
     }
-    if (k != have) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        co[e] = s_cs[k][i][e];
-        si[e] = s_cs[k][i][8 + e];
-      }
-      have = k;
-    }
     float a[8], b[8];
     unpack(va, a);
     unpack(vb, b);
-    turn8<kInter>(a, b, co, si);
+    turn8<kInter>(a, b, s_cs[k][i]);
     *reinterpret_cast<uint4*>(dst + 16 * c0) = pack(a);
     *reinterpret_cast<uint4*>(dst + 16 * c1) = pack(b);
   };
@@ -259,14 +256,7 @@ __global__ void __launch_bounds__(kThreads) mla_rope_pack_kernel(const __grid_co
     float a[8], b[8];
     unpack(va, a);
     unpack(vb, b);
-    if (turns) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        co[e] = s_cs[k][i][e];
-        si[e] = s_cs[k][i][8 + e];
-      }
-      turn8<kInter>(a, b, co, si);
-    }
+    if (turns) turn8<kInter>(a, b, s_cs[k][i]);
     if constexpr (kF8) {
       uint2* dst = reinterpret_cast<uint2*>(p.cache + slot * kRowVals + 512);
       dst[c0] = e4m3::e4m3x8(a, p.sc);
@@ -394,13 +384,20 @@ int mla_rope_pack(const mla_rope_dims* d, const mla_rope_plan* plan, const void*
   p.amp = plan->amplitude;
   p.sc = mla::e4m3::scale_of(f8 ? kv_scale : 1.0f);
   for (int i = 0; i < 32; ++i) p.turn[i] = i < p.R / 2 ? plan->turn[i] : 0;
-  // as many tokens a block as give each thread an item or two, but blocks for
-  // every SM first
+  // blocks: their tokens give each thread an item or two, but there is one for
+  // every SM first; where more would run than fit at once, whole rounds of them
+  // with about eight tokens each, whose look-ups are one chain (6K tokens of 128
+  // heads: 45 us at a token a block, 36 at eight, 45 in one round and a third)
+  constexpr int64_t kAtOnce = 152 * 5;
   int64_t toks = (kAhead * kThreads) / (4 * H);
-  const int64_t spread = (T + 151) / 152;
+  toks = toks < 1 ? 1 : (toks > kMaxTok - 1 ? kMaxTok - 1 : toks);
+  const int64_t spread = (T + 151) / 152, most = toks > 9 ? toks : 9;
   toks = toks < spread ? toks : spread;
-  p.toks = static_cast<int32_t>(toks < 1 ? 1 : (toks > kMaxTok ? kMaxTok : toks));
-  const dim3 grid(static_cast<unsigned>((T + p.toks - 1) / p.toks)), block(kThreads);
+  int64_t blocks = (T + toks - 1) / toks;
+  if (blocks > kAtOnce) blocks = kAtOnce * ((T + kAtOnce * most - 1) / (kAtOnce * most));
+  p.toks = static_cast<int32_t>(T / blocks);
+  p.more = static_cast<int32_t>(T % blocks);
+  const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
   cudaStream_t s = static_cast<cudaStream_t>(stream_v);
   const bool inter = plan->interleaved != 0;
   auto* kernel = f8 ? (inter ? &mla_rope_pack_kernel<true, true> : &mla_rope_pack_kernel<true, false>)

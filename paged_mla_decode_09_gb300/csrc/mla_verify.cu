@@ -58,9 +58,43 @@ struct Params {
   int32_t t_vec, d_vec;  // rows are 16-byte aligned
 };
 
-// A probability in units of 2^-60 (NaN and below 0: 0, above 1: 1).
+// A value of [0, 1] in units of 2^-60, as h 2^38 + m 2^18 + l: adding a constant
+// whose last place is 2^-22, 2^-42 or 2^-60 rounds to that place, and leaves the
+// rounded value's integer in the sum's low bits; what was rounded off is exact.
+// Integers of the bits add up in 32 bits over a few entries (the constants' own
+// bits are taken off at the end).  (A conversion to 64-bit integers runs at a
+// rate of two a cycle and SM: 64 rows of 131072 entries took 42 us with it.)
+constexpr float kPlace1 = 2.f, kPlace2 = 0x1.8p-19f, kPlace3 = 0x1.8p-37f;
+constexpr uint32_t kBits1 = 0x40000000u, kBits2 = 0x36400000u, kBits3 = 0x2d400000u;  // of these constants
+struct Split {
+  uint32_t h, m, l;
+};
+template <int kSign>
+__device__ __forceinline__ void add_split(Split& s, float x) {
+  const float t1 = __fadd_rn(x, kPlace1), r1 = __fsub_rn(x, __fsub_rn(t1, kPlace1));
+  const float t2 = __fadd_rn(r1, kPlace2), r2 = __fsub_rn(r1, __fsub_rn(t2, kPlace2));
+  const float t3 = __fadd_rn(r2, kPlace3);
+  if (kSign > 0) {
+    s.h += __float_as_uint(t1);
+    s.m += __float_as_uint(t2);
+    s.l += __float_as_uint(t3);
+  } else {
+    s.h -= __float_as_uint(t1);
+    s.m -= __float_as_uint(t2);
+    s.l -= __float_as_uint(t3);
+  }
+}
+// the sum of what was added less what was subtracted; n: entries added less entries subtracted
+__device__ __forceinline__ uint64_t joined(const Split& s, int n) {
+  const int32_t h = static_cast<int32_t>(s.h - n * kBits1), m = static_cast<int32_t>(s.m - n * kBits2),
+                l = static_cast<int32_t>(s.l - n * kBits3);
+  return static_cast<uint64_t>((static_cast<int64_t>(h) << 38) + (static_cast<int64_t>(m) << 18) + l);
+}
+// A probability in units of 2^-60, rounded (NaN and below 0: 0, above 1: 1).
 __device__ __forceinline__ uint64_t fixed60(float x) {
-  return __float2ull_rz(fminf(fmaxf(x, 0.f), 1.f) * 0x1p60f);
+  Split s = {0u, 0u, 0u};
+  add_split<1>(s, __saturatef(x));
+  return joined(s, 1);
 }
 // a * b of such numbers, rounded down.
 __device__ __forceinline__ uint64_t mul60(uint64_t a, uint64_t b) {
@@ -148,11 +182,11 @@ __device__ __forceinline__ void walk(Shared& s, int n, int cols, bool drafted, u
     const int x = s.tok[j];
     double w, qx = 1.0;
     if (drafted) {
-      w = st.k == 0 ? static_cast<double>(fminf(fmaxf(s.wp[j], 0.f), 1.f))
+      w = st.k == 0 ? static_cast<double>(__saturatef(s.wp[j]))
                     : static_cast<double>(weight(fixed60(s.wp[j]), fixed60(s.wq[j]), s.z, st.k)) * 0x1p-60;
-      qx = static_cast<double>(fminf(fmaxf(s.wq[j], 0.f), 1.f));
+      qx = static_cast<double>(__saturatef(s.wq[j]));
     } else {
-      w = static_cast<double>(fminf(fmaxf(s.wp[j], 0.f), 1.f));
+      w = static_cast<double>(__saturatef(s.wp[j]));
       bool again = false;  // a token that was rejected already has no weight left
       for (int i = lane; i < st.k; i += 32) again |= s.tok[s.gone[i]] == x;
       if (__any_sync(0xffffffffu, again)) w = 0.0;
@@ -192,6 +226,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = static_cast<int>(cluster_ctarank());
   const int b = static_cast<int>(cluster_id_x());
+  cluster_arrive();  // waited for before a block writes to another's shared memory
   int q0 = p.cu_q[b];
   const int q1 = p.cu_q[b + 1];
   int n = q1 - q0, flag = 0;
@@ -205,6 +240,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
   int32_t* path = p.path + static_cast<int64_t>(b) * p.cols;
   int32_t* next = p.tokens_out + static_cast<int64_t>(b) * p.cols;
   if (n == 0) {  // (the same in every block of the cluster)
+    cluster_wait();
     if (rank != 0) return;
     for (int k = tid; k < p.cols; k += kThreads) path[k] = next[k] = -1;
     if (tid == 0) {
@@ -244,7 +280,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     s.path[0] = 0;
     s.st = {0, 0, 1, 0, kFinish};
   }
-  cluster_sync();  // the blocks have all begun before one writes to another's shared memory
+  __syncthreads();
   const int all = (p.V + kChunk - 1) / kChunk, per = (all + kCluster - 1) / kCluster;
   const int c0 = rank * per < all ? rank * per : all, nc = (all - c0 < per ? all - c0 : per);
   uint64_t sum = 0;      // of the row's weights, all blocks
@@ -276,17 +312,27 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
       for (int f = 0; f < kFly; ++f) {
         if (c + f * kWarps >= nc) break;
         uint64_t v = 0;
+        Split sp = {0u, 0u, 0u};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const float x[4] = {a[f][h].x, a[f][h].y, a[f][h].z, a[f][h].w};
           const float y[4] = {q[f][h].x, q[f][h].y, q[f][h].z, q[f][h].w};
+          if (!rest) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint64_t w = fixed60(x[e]);
-            if (rest) w = weight(w, fixed60(y[e]), s.z, st.k);
-            v += w;
+            for (int e = 0; e < 4; ++e) add_split<1>(sp, __saturatef(x[e]));
+          } else if (st.k == 1) {  // p - q where that is above 0
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float c = __saturatef(x[e]), d = __saturatef(y[e]);
+              add_split<1>(sp, c > d ? c : 0.f);
+              add_split<-1>(sp, c > d ? d : 0.f);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v += weight(fixed60(x[e]), fixed60(y[e]), s.z, st.k);
           }
         }
+        if (!rest || st.k == 1) v = joined(sp, rest ? 0 : 8);
         v = warp_add(v);
         if (lane == 0) s.chunk[c + f * kWarps] = v;
       }
@@ -307,11 +353,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     __syncthreads();
     if (warp == 0) {
       v = warp_add(lane < kWarps ? s.warp_sum[lane] : 0ull);
+      if (pass == 0) cluster_wait();  // every block has begun
       if (lane < kCluster) {
         const uint32_t dst = mapa(smem_u32(&s.total[pass & 1][rank]), static_cast<uint32_t>(lane));
         asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(v) : "memory");
       }
     }
+    if (pass == 0 && warp != 0) cluster_wait();
     cluster_sync();
     sum = 0;
 #pragma unroll

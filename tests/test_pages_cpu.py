@@ -58,9 +58,9 @@ def test_resize_refusals(lib):
     assert lib.mla_page_resize(None, *ptrs(6), 1 << 40, None) == -1
     for args in ((0, 5, 16), (2, 0, 16), (2, 5, 0), (2, 1 << 25, 16), (1 << 16, 1 << 16, 16)):
         assert lib.mla_page_resize_workspace_size(*args) == 0
-    assert lib.mla_page_resize_workspace_size(2, 5, 16) == 512
-    assert lib.mla_page_resize_workspace_size(2, 5, 1 << 20) == 512
-    assert lib.mla_page_resize_workspace_size(200, 5, 100) == 256 + 512
+    # no more ids are listed than there are pages, or entries
+    assert lib.mla_page_resize_workspace_size(2, 5, 16) == lib.mla_page_resize_workspace_size(2, 5, 1 << 20)
+    assert lib.mla_page_resize_workspace_size(200, 500, 100) == lib.mla_page_resize_workspace_size(200, 5000, 100)
 
 
 def test_fork_refusals(lib):
