@@ -93,7 +93,8 @@ typedef struct {
  *   cu_q_lens   int32 [B + 1], non-decreasing from >= 0
  *   path        int32 [B][path_cols]: nodes, ascending, in [0, n_b)
  *   num_path    int32 [B]; in [0, min(n_b, path_cols)]; 0 drops all nodes
- *   new_lens    int32 [B]; must not overlap seq_lens, which every block reads
+ *   new_lens    int32 [B]; must not overlap seq_lens, cu_q_lens or num_path, which
+ *               every block reads
  *   status      int32 [1]; OR-ed in: MLA_DEV_BAD_SEQ_LEN, MLA_DEV_BAD_QUERY_RANGE,
  *               MLA_DEV_BAD_INDEX (path or num_path): the request is left out
  *               and new_lens[b] = seq_lens[b]; MLA_DEV_BAD_PAGE_ID: a move that

@@ -20,8 +20,9 @@
  *
  * (Where w has become all zeros, by rounding, the last token comes from p[c].)
  * Sums run in integers, units of 2^-60, so that they are exact whatever their
- * order (an entry below 2^-36 is rounded to them), and the products of
- * a test are formed in 64-bit floating point.
+ * order (an entry below 2^-36 is rounded to them).  The product of a test is
+ * compared exactly, but for drafts after a rejection, where it is formed in
+ * 64-bit floating point.
  *
  * Conventions as in mla_decode.h: caller-owned device buffers, asynchronous on
  * `stream`, no allocation, no synchronisation, an mla_status return.  One
@@ -75,6 +76,9 @@ typedef struct {
  *               token, then -1
  *   num_out     int32 [B]: entries of both; 0 for a request without nodes
  *   status      int32 [1], OR-ed into; the caller clears it
+ * The outputs overlap neither one another nor tokens .. sample
+ * (MLA_ERR_INVALID_ARG).  Rows of target and draft that the walk does not come
+ * to are read in single entries only, and may hold anything where no node is.
  */
 int mla_verify(const mla_verify_dims* d, const float* target, const float* draft, const int32_t* tokens,
                const int32_t* parents, const int32_t* cu_q_lens, const float* accept, const float* sample,

@@ -457,8 +457,7 @@ int current_device_ok() {
 
 // Whether two int32 tables share an element, counted from first to last.
 bool overlap(const int32_t* a, int64_t an, const int32_t* b, int64_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + 4 * static_cast<uintptr_t>(bn) && y < x + 4 * static_cast<uintptr_t>(an);
+  return mla::host::overlap(a, 4 * an, b, 4 * bn);
 }
 int64_t extent(int64_t rows, int64_t stride, int64_t cols) { return (rows - 1) * stride + cols; }
 
@@ -612,7 +611,9 @@ int mla_tree_commit(const mla_tree_commit_dims* d, void* kv_cache, const int32_t
       !aligned(path, 4) || !aligned(num_path, 4) || !aligned(new_lens, 4) || !aligned(status, 4) ||
       (d->num_layers > 1 && d->layer_stride % 16 != 0))
     return MLA_ERR_ALIGNMENT;
-  if (overlap(seq_lens, d->batch, new_lens, d->batch)) return MLA_ERR_INVALID_ARG;
+  if (overlap(seq_lens, d->batch, new_lens, d->batch) || overlap(num_path, d->batch, new_lens, d->batch) ||
+      overlap(cu_q_lens, d->batch + 1ll, new_lens, d->batch))
+    return MLA_ERR_INVALID_ARG;
   const int rc = current_device_ok();
   if (rc != MLA_OK) return rc;
   using namespace mla::pages;

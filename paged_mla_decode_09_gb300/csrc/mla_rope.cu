@@ -275,14 +275,9 @@ __global__ void __launch_bounds__(kThreads, 5) mla_rope_pack_kernel(const __grid
 namespace {
 
 using mla::host::aligned;
+using mla::host::overlap;
 
 bool rotary_ok(int32_t r) { return r >= 16 && r <= 64 && r % 16 == 0; }
-
-// Whether [a, a + an) and [b, b + bn) share a byte.
-bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
-}
 
 }  // namespace
 

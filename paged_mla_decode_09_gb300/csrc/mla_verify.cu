@@ -159,48 +159,69 @@ __device__ __forceinline__ float4 load4(const float* row, int e, int V, bool vec
   return v;
 }
 
+// Whether u q < w, exactly: the product's rounding never passes w, and decides
+// where it is w itself.  (Scaled, so that no product is subnormal.)
+__device__ __forceinline__ bool below(float u, float q, float w) {
+  const float big = q * 0x1p64f, prod = __fmul_rn(u, big), err = __fmaf_rn(u, big, -prod), lim = w * 0x1p64f;
+  return prod < lim || (prod == lim && err < 0.f);
+}
+// Whether a b < w, all in units of 2^-60.
+__device__ __forceinline__ bool below60(uint64_t a, uint64_t b, uint64_t w) {
+  const uint64_t hi = __umul64hi(a, b), lim = w >> 4;
+  return hi < lim || (hi == lim && a * b < w << 60);
+}
+
 // Warp 0 of a block: on from s.st to the next sum over the row, or the end.
 // `sum` is the row's sum after the last rejection (draft), `summed` whether
-// the chunks hold the present weights.
-__device__ __forceinline__ void walk(Shared& s, int n, int cols, bool drafted, uint64_t sum, bool& summed) {
-  const int lane = threadIdx.x & 31;
+// the chunks hold the present weights.  64-bit floating point, at about half a
+// microsecond a test, only where a draft follows a rejection.
+template <bool kDraft>
+__device__ __forceinline__ void walk(Shared& s, int n, int cols, uint64_t sum, bool& summed) {
+  const int lane = threadIdx.x & 31, groups = (n + 31) >> 5;
   State st = s.st;
   int par[kNodes / 32];
 #pragma unroll
   for (int g = 0; g < kNodes / 32; ++g) par[g] = g * 32 + lane < n ? s.par[g * 32 + lane] : -2;
-  double z = st.k == 0 ? 1.0 : static_cast<double>(sum) * 0x1p-60;  // (fixed proposals end in one go)
+  uint64_t z = 1ull << 60;  // fixed proposals (which end in one go)
   st.todo = kFinish;
   while (st.cnt < cols) {
     int j = -1;  // the next child of cur
 #pragma unroll
-    for (int g = 0; g < kNodes / 32; ++g) {
-      const unsigned m = __ballot_sync(0xffffffffu, par[g] == st.cur && g * 32 + lane > st.last);
-      if (j < 0 && m) j = g * 32 + __ffs(m) - 1;
-    }
+    for (int g = 0; g < kNodes / 32; ++g)
+      if (g < groups) {
+        const unsigned m = __ballot_sync(0xffffffffu, par[g] == st.cur && g * 32 + lane > st.last);
+        if (j < 0 && m) j = g * 32 + __ffs(m) - 1;
+      }
     if (j < 0) break;
     st.last = j;
-    const int x = s.tok[j];
-    double w, qx = 1.0;
-    if (drafted) {
-      w = st.k == 0 ? static_cast<double>(__saturatef(s.wp[j]))
-                    : static_cast<double>(weight(fixed60(s.wp[j]), fixed60(s.wq[j]), s.z, st.k)) * 0x1p-60;
-      qx = static_cast<double>(__saturatef(s.wq[j]));
+    const float u = s.acc[j], w = __saturatef(s.wp[j]);
+    bool yes;
+    if (kDraft) {
+      const float q = __saturatef(s.wq[j]);
+      if (st.k == 0) {
+        yes = below(u, q, w);
+      } else {
+        const double left = static_cast<double>(weight(fixed60(w), fixed60(q), s.z, st.k)) * 0x1p-60;
+        yes = static_cast<double>(u) * (static_cast<double>(sum) * 0x1p-60) * static_cast<double>(q) < left;
+      }
     } else {
-      w = static_cast<double>(__saturatef(s.wp[j]));
+      const int x = s.tok[j];
       bool again = false;  // a token that was rejected already has no weight left
       for (int i = lane; i < st.k; i += 32) again |= s.tok[s.gone[i]] == x;
-      if (__any_sync(0xffffffffu, again)) w = 0.0;
+      const uint64_t left = __any_sync(0xffffffffu, again) ? 0ull : fixed60(w);
+      yes = st.k == 0 ? u < w : below60(fixed60(u), z, left);
+      if (!yes) z = z > left ? z - left : 0ull;
     }
-    if (static_cast<double>(s.acc[j]) * z * qx < w) {
+    if (yes) {
       if (lane == 0) s.path[st.cnt] = j;
       ++st.cnt;
       st.cur = j;
       st.k = 0;
-      z = 1.0;
+      z = 1ull << 60;
       summed = false;
       continue;
     }
-    if (drafted) {
+    if (kDraft) {
       if (lane == 0) s.z[st.k] = st.k == 0 ? 1ull << 60 : sum;
       ++st.k;
       summed = false;
@@ -211,7 +232,6 @@ __device__ __forceinline__ void walk(Shared& s, int n, int cols, bool drafted, u
     __syncwarp();
     ++st.k;
     summed = false;
-    z = z > w ? z - w : 0.0;
   }
   __syncwarp();
   if (lane == 0) s.st = st;
@@ -370,7 +390,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
   __shared__ int s_summed;
   while (true) {
     if (warp == 0) {
-      walk(s, n, p.cols, kDraft, sum, summed);
+      walk<kDraft>(s, n, p.cols, sum, summed);
       if (lane == 0) s_summed = summed;
     }
     __syncthreads();
@@ -429,17 +449,23 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
   at = s.left;
   uint64_t w[kChunk / 32], mine = 0;
   const int e0 = s.pick * kChunk + lane * (kChunk / 32);
+  static_assert(kChunk == 256, "two quads a lane");
+  const float4 a0 = load4(tr, e0, p.V, p.t_vec), a1 = load4(tr, e0 + 4, p.V, p.t_vec);
+  const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+  float4 d0 = make_float4(0.f, 0.f, 0.f, 0.f), d1 = d0;
+  if (kDraft && st.k > 0) {
+    d0 = load4(dr, e0, p.V, p.d_vec);
+    d1 = load4(dr, e0 + 4, p.V, p.d_vec);
+  }
+  const float d[8] = {d0.x, d0.y, d0.z, d0.w, d1.x, d1.y, d1.z, d1.w};
 #pragma unroll
   for (int e = 0; e < kChunk / 32; ++e) {
-    w[e] = 0;
-    if (e0 + e < p.V) {
-      w[e] = fixed60(tr[e0 + e]);
-      if (kDraft) {
-        if (st.k > 0) w[e] = weight(w[e], fixed60(dr[e0 + e]), s.z, st.k);
-      } else {
-        for (int i = 0; i < st.k; ++i)
-          if (s.tok[s.gone[i]] == e0 + e) w[e] = 0;
-      }
+    w[e] = fixed60(a[e]);
+    if (kDraft) {
+      if (st.k > 0) w[e] = weight(w[e], fixed60(d[e]), s.z, st.k);
+    } else {
+      for (int i = 0; i < st.k; ++i)
+        if (s.tok[s.gone[i]] == e0 + e) w[e] = 0;
     }
     mine += w[e];
   }
@@ -475,6 +501,21 @@ extern "C" int mla_verify(const mla_verify_dims* d, const float* target, const f
       !aligned(cu_q_lens, 4) || !aligned(accept, 4) || !aligned(sample, 4) || !aligned(path, 4) ||
       !aligned(tokens_out, 4) || !aligned(num_out, 4) || !aligned(status, 4))
     return MLA_ERR_ALIGNMENT;
+  // every block of a request reads its inputs, one writes the outputs
+  {
+    const int64_t T = d->total_q, B = d->batch, cells = B * d->path_cols;
+    const struct {
+      const void* at;
+      int64_t bytes;
+    } outs[] = {{path, 4 * cells}, {tokens_out, 4 * cells}, {num_out, 4 * B}, {status, 4}},
+      ins[] = {{tokens, 4 * T}, {parents, 4 * T}, {cu_q_lens, 4 * B + 4}, {accept, 4 * T}, {sample, 4 * B}};
+    for (int i = 0; i < 4; ++i) {
+      for (int j = 0; j < i; ++j)
+        if (mla::host::overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return MLA_ERR_INVALID_ARG;
+      for (const auto& in : ins)
+        if (mla::host::overlap(outs[i].at, outs[i].bytes, in.at, in.bytes)) return MLA_ERR_INVALID_ARG;
+    }
+  }
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();

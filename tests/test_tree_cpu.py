@@ -84,16 +84,20 @@ def test_commit_refusals(lib):
         assert _commit(lib, good[:k] + [None] + good[k + 1:]) == -1, k
         off = ctypes.c_void_p(((k + 1) << 20) + (8 if k == 0 else 2))
         assert _commit(lib, good[:k] + [off] + good[k + 1:]) == -3, k
-    # new lengths over the lengths that every block reads
-    assert _commit(lib, good[:6] + [good[2]] + good[7:]) == -1
+    # new lengths over what every block reads
+    for k in (2, 3, 5):
+        assert _commit(lib, good[:6] + [good[k]] + good[7:]) == -1
     assert _commit(lib, good[:6] + [ctypes.c_void_p(good[2].value + 4)] + good[7:]) == -1
     assert lib.mla_tree_commit(None, *good, None) == -1
+
+
+V = [ctypes.c_void_p((k + 1) << 20) for k in range(11)]
 
 
 def _verify(lib, ptrs=None, **kw):
     d = dict(batch=2, total_q=6, vocab=100, path_cols=4, target_stride=100, draft_stride=100)
     d.update(kw)
-    a = [P] * 11 if ptrs is None else ptrs
+    a = V if ptrs is None else ptrs
     return lib.mla_verify(ctypes.byref(mla.MlaVerifyDims(**d)), *a, None)
 
 
@@ -104,13 +108,20 @@ def test_verify_refusals(lib):
     for bad in (dict(vocab=(1 << 20) + 1, target_stride=1 << 21, draft_stride=1 << 21), dict(batch=(1 << 27) + 1),
                 dict(target_stride=1 << 41)):
         assert _verify(lib, **bad) == -2, bad
+    def but(k, p):
+        return V[:k] + [p] + V[k + 1:]
+
     for k in range(11):
         if k != 1:  # no draft: fixed proposals
-            assert _verify(lib, [P] * k + [None] + [P] * (10 - k)) == -1, k
-        assert _verify(lib, [P] * k + [ctypes.c_void_p((1 << 20) + 2)] + [P] * (10 - k)) == -3, k
+            assert _verify(lib, but(k, None)) == -1, k
+        assert _verify(lib, but(k, ctypes.c_void_p(V[k].value + 2))) == -3, k
     # without a draft its stride is not looked at: what is refused is the next thing
-    assert _verify(lib, [P, None] + [ctypes.c_void_p((1 << 20) + 2)] + [P] * 8, draft_stride=0) == -3
-    assert lib.mla_verify(None, *[P] * 11, None) == -1
+    assert _verify(lib, [V[0], None, ctypes.c_void_p(V[2].value + 2)] + V[3:], draft_stride=0) == -3
+    assert lib.mla_verify(None, *V, None) == -1
+    # outputs over inputs or one another
+    for out in range(7, 11):
+        for other in [2, 3, 4, 5, 6] + [k for k in range(7, 11) if k != out]:
+            assert _verify(lib, but(out, V[other])) == -1, (out, other)
 
 
 def test_binding_refuses_what_the_library_cannot_see(lib):
