@@ -1,8 +1,8 @@
 // Page operations (see include/mla_pages.h and mla_tree_commit in
 // include/mla_tree.h).
 //
-// Handing out (mla_page_resize, mla_page_fork): one cluster of eight blocks
-// does a call, in steps that a cluster barrier separates: counts copied and
+// Handing out (mla_page_resize, mla_page_fork): one block or a cluster of up
+// to 16 does a call, in steps that a cluster barrier separates: counts copied and
 // their zeros counted; pages given back or shared (atomic additions: the counts
 // do not depend on their order; what becomes free is added to its block's
 // zeros) and each row's missing entries counted; as many free ids as entries
@@ -13,7 +13,7 @@
 // between calls would spare the walk over the counts (4 bytes a page), but its
 // order would depend on the calls before.
 // What bounds it: the latency of the steps, about four reads and barriers, then
-// what eight SMs read.
+// what 16 SMs read.
 //
 // Rows (mla_tree_commit, mla_page_fork's second kernel): copies of 16-byte
 // columns.  A committed path is ascending, so that slot k is read (if at all)
@@ -24,6 +24,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <mutex>
 
 #include "mla_host.h"
 #include "mla_pages.h"
@@ -38,7 +39,7 @@ namespace pages {
 constexpr int kPage = 64;
 
 // ------------------------------------------------------------ handing out
-constexpr int kCluster = 8;
+constexpr int kOneBlock = 16384;  // entries and pages up to which one block does a call
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 4 * kThreads;  // pages of a step: four in a row per thread
@@ -118,9 +119,14 @@ __device__ __forceinline__ Row row_of(const Params& p, int b) {
   return r;
 }
 
-template <bool kFork>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
-    mla_pages_kernel(const __grid_constant__ Params p) {
+template <int kCluster>
+__device__ __forceinline__ void sync_all() {
+  if constexpr (kCluster == 1) __syncthreads();
+  else cluster_sync();
+}
+
+template <bool kFork, int kCluster>
+__global__ void __launch_bounds__(kThreads, 1) mla_pages_kernel(const __grid_constant__ Params p) {
   __shared__ int warps[kWarps];
   __shared__ int missing_of[kCluster];  // every block's, written by the blocks themselves
   __shared__ int free_of[kCluster];
@@ -128,7 +134,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   __shared__ int lacks[kThreads], begins[kThreads];
   griddep_wait();
   griddep_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = static_cast<int>(cluster_ctarank());
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = kCluster == 1 ? 0 : static_cast<int>(cluster_ctarank());
   if (rank == 0 && tid == 0) *p.status = 0;
   // rows of the tables: a contiguous part of them per block
   const int rpart = static_cast<int>((static_cast<int64_t>(p.B) + kCluster - 1) / kCluster);
@@ -166,7 +172,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   }
   block_before(zeros, warps, all);
   if (tid == 0) free_pages = all;
-  cluster_sync();  // every block has begun, the counts are in place, the status is clear
+  sync_all<kCluster>();  // every block has begun, the counts are in place, the status is clear
   if (below) atomicOr(p.status, MLA_DEV_BAD_REFS);
   // entries, four of a row a time: kFly times four of them in flight
   auto owner = [&](int id) { return mapa(smem_u32(&free_pages), static_cast<uint32_t>(id / ppart)); };
@@ -209,7 +215,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       int missing = 0, old[4];
       unsigned did = 0;  // entries whose page's count changed
       flag |= r[f].flag;
-      if (kFork && c[f] == 0) p.copies[b[f]] = make_int4(0, -1, r[f].tail, r[f].keep);
+      // (the page that has been started, if any: the new one is added below)
+      const int started = r[f].keep - c[f];
+      if (kFork && (r[f].tail == 0 ? c[f] == 0 : started >= 0 && started < 4)) {
+        int e = 0;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) e = u == started ? id[f][u] : e;
+        p.copies[b[f]] = make_int4(e, -1, r[f].tail, r[f].keep);
+      }
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int col = c[f] + u, e = id[f][u];
@@ -266,7 +279,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
   block_before(lacking, warps, all);
   if (tid < kCluster)
     st_cluster_u32(mapa(smem_u32(&missing_of[rank]), static_cast<uint32_t>(tid)), static_cast<uint32_t>(all));
-  cluster_sync();
+  sync_all<kCluster>();
   // free pages of all blocks, read where they are counted (no block ends before the next barrier)
   if (tid < kCluster)
     free_of[tid] = static_cast<int>(ld_cluster_u32(mapa(smem_u32(&free_pages), static_cast<uint32_t>(tid))));
@@ -301,7 +314,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
       }
     fbefore += all;
   }
-  cluster_sync();
+  sync_all<kCluster>();
   // the k-th missing entry takes the k-th free id
   if (wanted > have && rank == 0 && tid == 0) atomicOr(p.status, MLA_DEV_NO_PAGES);
   if (missing_of[rank] == 0) return;
@@ -311,9 +324,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
     before += all;
     if (kFork) {  // the one entry behind the shared ones
       if (n > 0 && at < have) {
-        const int4 c = __ldcg(p.copies + b);
+        const int4 c = p.copies[b];
         const int32_t id = __ldcg(p.list + at);
-        p.copies[b] = make_int4(p.table[p.src[b] * p.t_stride + c.w], id, c.z, 0);
+        p.copies[b] = make_int4(c.x, id, c.z, 0);
         p.table_out[b * p.o_stride + c.w] = id;
       }
       continue;
@@ -472,10 +485,49 @@ size_t list_bytes(int64_t rows, int64_t cols, int64_t pages) {
 size_t row_bytes(int64_t rows) { return align256(4 * static_cast<size_t>(rows)); }
 int64_t cache_bytes(int64_t num_pages, bool f8) { return num_pages * 64 * (f8 ? 576 : 1152); }
 
+// Whether clusters of 16 blocks (beyond the portable 8) fit on the device.
+template <bool kFork>
+bool sixteen_fit(int device) {
+  static std::mutex mu;
+  static int8_t known[64] = {};  // 1: they do, 2: they do not
+  if (device < 0 || device >= 64) return false;
+  std::lock_guard<std::mutex> lk(mu);
+  if (!known[device]) {
+    const void* fn = reinterpret_cast<const void*>(&mla::pages::mla_pages_kernel<kFork, 16>);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(16);
+    cfg.blockDim = dim3(mla::pages::kThreads);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 16;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    const bool ok = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+                    cudaOccupancyMaxActiveClusters(&n, fn, &cfg) == cudaSuccess && n >= 1;
+    if (!ok) cudaGetLastError();
+    known[device] = ok ? 1 : 2;
+  }
+  return known[device] == 1;
+}
+
+// One block for small calls (its barriers are cheaper), else a cluster of 16
+// where that fits.  Measured, one block, a cluster of 8, of 16: 4 requests of 32
+// columns over 512 pages 3.1, 4.3, - us; 256 of 512 columns over 131072 pages
+// 46.9, 14.1, 11.7; 64 forks of 25 columns over 800 pages (with the copies)
+// 11.3, 13.5, -.  The limit is where lines through these meet, not measured
+// there.
 template <bool kFork>
 cudaError_t launch(const mla::pages::Params& p, cudaStream_t s) {
-  return launch_pdl(&mla::pages::mla_pages_kernel<kFork>, dim3(mla::pages::kCluster), dim3(mla::pages::kThreads), 0, s, 0,
-                    p);
+  using namespace mla::pages;
+  const dim3 block(kThreads);
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (static_cast<int64_t>(p.B) * p.cols + p.P > kOneBlock && sixteen_fit<kFork>(dev))
+    return launch_pdl(&mla_pages_kernel<kFork, 16>, dim3(16), block, 0, s, 16, p);
+  return launch_pdl(&mla_pages_kernel<kFork, 1>, dim3(1), block, 0, s, 0, p);
 }
 
 }  // namespace
