@@ -14,7 +14,7 @@ import ctypes
 import os
 from dataclasses import dataclass
 
-from .build import LIB_PATH, build_library
+from .build import BINDING_PATH, LIB_PATH, build_library
 
 MLA_OK = 0
 MLA_KV_BF16 = 0
@@ -299,6 +299,37 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     if path is None:
         _lib = lib
     return lib
+
+
+_fast = None
+
+
+def _binding():
+    """The compiled fast path of the calls of a speculative step
+    (csrc/binding.cpp): each of its functions makes the C call, or returns
+    None where a tensor is not what the call takes."""
+    global _fast
+    if _fast is None:
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries are loaded first)
+
+        load_library()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with __graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
+        loader.exec_module(module)
+        _fast = module
+    return _fast
+
+
+def _refuse(call, explain, device, *tensors):
+    """The binding found a tensor that the call does not take: say which."""
+    explain(*tensors)
+    _check_current_device(device)
+    raise ValueError(f"{call}: the arguments do not have the shapes, types and layouts the library expects")
 
 
 def status_string(code: int) -> str:
@@ -944,21 +975,19 @@ def mla_decode_tree(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, par
     """Enqueue the attention of trees of drafted tokens (see
     include/mla_tree.h): tensors as for mla_prefill; parents int32 [total_q],
     each node's parent within its request, -1 = none."""
-    if not (_prefill_fits(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
-            and _fits(parents, q_nope.shape[:1], _t().i32, q_nope.get_device())):
-        _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, parents, out, lse, workspace)
-        _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
-        _check_vectors(q_nope.device, parents=(parents, q_nope.shape[:1]))
-        raise ValueError("tree tensors do not have the shapes, types and layouts the library expects")
-    dev = q_nope.get_device()
-    _check_current_device(dev)
-    dims = make_prefill_dims(q_nope, kv_cache, page_table, seq_lens)
-    rc = load_library().mla_decode_tree(
-        ctypes.byref(dims), q_nope.data_ptr(), q_pe.data_ptr(), kv_cache.data_ptr(), page_table.data_ptr(),
-        seq_lens.data_ptr(), cu_q_lens.data_ptr(), parents.data_ptr(), float(scale), float(kv_scale), out.data_ptr(),
-        lse.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream_int(stream, dev))
+    rc = _binding().decode_tree(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, parents, scale, kv_scale, out,
+                                lse, workspace, stream)
+    if rc is None:
+        _refuse("mla_decode_tree", _explain_decode_tree, q_nope.get_device(), q_nope, q_pe, kv_cache, page_table,
+                seq_lens, cu_q_lens, parents, out, lse, workspace)
     if rc != MLA_OK:
         raise MlaError(rc, "mla_decode_tree")
+
+
+def _explain_decode_tree(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, parents, out, lse, workspace):
+    _check_cuda(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, parents, out, lse, workspace)
+    _check_prefill_tensors(q_nope, q_pe, kv_cache, page_table, seq_lens, cu_q_lens, out, lse, workspace)
+    _check_vectors(q_nope.device, parents=(parents, q_nope.shape[:1]))
 
 
 def _check_vectors(device, **named):
@@ -980,23 +1009,6 @@ def _layers_of(kv_cache):
     if len(s) == 3:
         return 1, s[0], 0
     return s[0], s[1], k[0] * kv_cache.element_size() if s[0] > 1 else 0
-
-
-def _vec(t, n, dtype, dev) -> bool:
-    """A contiguous vector of n elements."""
-    s = t.shape
-    return (len(s) == 1 and s[0] == n and t.dtype is dtype and t.get_device() == dev
-            and (n < 2 or t.stride(0) == 1))
-
-
-def _table_fits(t, rows, dev, i32) -> bool:
-    s = t.shape
-    return (len(s) == 2 and s[0] == rows and t.dtype is i32 and t.get_device() == dev and t.stride(1) == 1
-            and t.stride(0) >= s[1])
-
-
-def _status_fits(t, dev, i32) -> bool:
-    return t.dtype is i32 and t.get_device() == dev and t.numel() >= 1
 
 
 def _check_layers(kv_cache):
@@ -1043,21 +1055,10 @@ def mla_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, n
     kv_cache: [num_pages, 64, 576], or one such cache per layer as
     [num_layers, num_pages, 64, 576]; path int32 [B, cols], num_path and
     new_lens int32 [B] (new_lens not seq_lens itself); status int32 [1]."""
-    t, dev = _t(), kv_cache.get_device()
-    B, i32, ps = seq_lens.shape[0] if seq_lens.dim() == 1 else -1, t.i32, path.shape
-    layers = _layers_of(kv_cache)
-    if not (dev >= 0 and layers is not None and len(ps) == 2 and _vec(seq_lens, B, i32, dev)
-            and _vec(cu_q_lens, B + 1, i32, dev) and _vec(num_path, B, i32, dev) and _vec(new_lens, B, i32, dev)
-            and _fits(path, (B, ps[1]), i32, dev) and _table_fits(page_table, B, dev, i32)
-            and _status_fits(status, dev, i32)):
-        _explain_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status)
-        raise ValueError("commit tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(dev)
-    dims = MlaTreeCommitDims(B, layers[0], ps[1], layers[1], page_table.shape[1], _stride_of(page_table),
-                             t.cache_codes[kv_cache.dtype], 0, layers[2])
-    rc = load_library().mla_tree_commit(
-        ctypes.byref(dims), kv_cache.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), cu_q_lens.data_ptr(),
-        path.data_ptr(), num_path.data_ptr(), new_lens.data_ptr(), status.data_ptr(), _stream_int(stream, dev))
+    tensors = kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status
+    rc = _binding().tree_commit(*tensors, stream)
+    if rc is None:
+        _refuse("mla_tree_commit", _explain_tree_commit, kv_cache.get_device(), *tensors)
     if rc != MLA_OK:
         raise MlaError(rc, "mla_tree_commit")
 
@@ -1098,26 +1099,10 @@ def mla_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, 
     target and draft (None: fixed proposals) fp32 [total_q, vocab]; tokens,
     parents int32 and accept fp32 [total_q]; sample fp32 [B]; path and
     tokens_out int32 [B, cols], num_out int32 [B]; status int32 [1]."""
-    t, dev, ts = _t(), target.get_device(), target.shape
-    T, V = ts if len(ts) == 2 else (-1, -1)
-    B, f32, i32, ps = sample.shape[0] if sample.dim() == 1 else -1, t.f32, t.i32, path.shape
-    if not (dev >= 0 and len(ts) == 2 and target.dtype is f32 and target.stride(1) == 1
-            and (T < 2 or target.stride(0) >= V)
-            and (draft is None or (draft.dtype is f32 and draft.shape == ts and draft.get_device() == dev
-                                   and draft.stride(1) == 1 and (T < 2 or draft.stride(0) >= V)))
-            and _vec(tokens, T, i32, dev) and _vec(parents, T, i32, dev) and _vec(accept, T, f32, dev)
-            and _vec(sample, B, f32, dev) and _vec(cu_q_lens, B + 1, i32, dev) and len(ps) == 2
-            and _fits(path, (B, ps[1]), i32, dev) and _fits(tokens_out, ps, i32, dev) and _vec(num_out, B, i32, dev)
-            and _status_fits(status, dev, i32)):
-        _explain_verify(target, draft, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status)
-        raise ValueError("verify tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(dev)
-    dims = MlaVerifyDims(B, T, V, ps[1], target.stride(0) if T > 1 else V,
-                         (draft.stride(0) if T > 1 else V) if draft is not None else 0)
-    rc = load_library().mla_verify(
-        ctypes.byref(dims), target.data_ptr(), None if draft is None else draft.data_ptr(), tokens.data_ptr(),
-        parents.data_ptr(), cu_q_lens.data_ptr(), accept.data_ptr(), sample.data_ptr(), path.data_ptr(),
-        tokens_out.data_ptr(), num_out.data_ptr(), status.data_ptr(), _stream_int(stream, dev))
+    tensors = target, draft, tokens, parents, cu_q_lens, accept, sample, path, tokens_out, num_out, status
+    rc = _binding().verify(*tensors, stream)
+    if rc is None:
+        _refuse("mla_verify", _explain_verify, target.get_device(), *tensors)
     if rc != MLA_OK:
         raise MlaError(rc, "mla_verify")
 
@@ -1130,10 +1115,6 @@ def mla_page_resize_workspace_size(batch: int, max_pages: int, num_pages: int) -
     if n == 0:
         raise MlaError(-1, "mla_page_resize_workspace_size")
     return int(n)
-
-
-def _stride_of(table):
-    return table.stride(0) if table.shape[0] > 1 else max(table.stride(0), table.shape[1])
 
 
 def _explain_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace):
@@ -1156,20 +1137,10 @@ def _explain_page_resize(new_lens, page_table, page_refs, page_table_out, page_r
 def mla_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace, stream=None) -> None:
     """Enqueue handing out and freeing pages for the requests' new lengths (see
     include/mla_pages.h); page_table_out and page_refs_out may be the inputs."""
-    t, dev, cols = _t(), new_lens.get_device(), page_table.shape
-    i32, B, P = t.i32, new_lens.shape[0] if new_lens.dim() == 1 else -1, page_refs.shape[0] if page_refs.dim() == 1 else -1
-    if not (dev >= 0 and _vec(new_lens, B, i32, dev) and _vec(page_refs, P, i32, dev) and _vec(page_refs_out, P, i32, dev)
-            and _table_fits(page_table, B, dev, i32) and _table_fits(page_table_out, B, dev, i32)
-            and page_table_out.shape == cols and workspace.is_contiguous() and workspace.get_device() == dev):
-        _explain_page_resize(new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace)
-        raise ValueError("resize tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(dev)
-    dims = MlaPageResizeDims(B, P, cols[1], _stride_of(page_table),
-                             _stride_of(page_table_out))
-    rc = load_library().mla_page_resize(
-        ctypes.byref(dims), new_lens.data_ptr(), page_table.data_ptr(), page_refs.data_ptr(),
-        page_table_out.data_ptr(), page_refs_out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
-        _stream_int(stream, dev))
+    tensors = new_lens, page_table, page_refs, page_table_out, page_refs_out, workspace
+    rc = _binding().page_resize(*tensors, stream)
+    if rc is None:
+        _refuse("mla_page_resize", _explain_page_resize, new_lens.get_device(), *tensors)
     if rc != MLA_OK:
         raise MlaError(rc, "mla_page_resize")
 
@@ -1206,22 +1177,10 @@ def mla_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out
     """Enqueue the fork of requests (see include/mla_pages.h): child c continues
     request src[c] (int32 [children], -1 = an empty row); kv_cache as for
     mla_tree_commit; page_refs_out may be page_refs."""
-    t, dev, cols = _t(), kv_cache.get_device(), page_table.shape
-    i32, S, C = t.i32, seq_lens.shape[0] if seq_lens.dim() == 1 else -1, src.shape[0] if src.dim() == 1 else -1
-    layers = _layers_of(kv_cache)
-    if not (dev >= 0 and layers is not None and _vec(src, C, i32, dev) and _vec(seq_lens, S, i32, dev)
-            and _vec(page_refs, layers[1], i32, dev) and _vec(page_refs_out, layers[1], i32, dev)
-            and _table_fits(page_table, S, dev, i32) and _table_fits(page_table_out, C, dev, i32)
-            and page_table_out.shape[1] == cols[1] and workspace.is_contiguous() and workspace.get_device() == dev):
-        _explain_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace)
-        raise ValueError("fork tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(dev)
-    dims = MlaPageForkDims(S, C, layers[0], layers[1], cols[1], _stride_of(page_table), _stride_of(page_table_out),
-                           t.cache_codes[kv_cache.dtype], layers[2])
-    rc = load_library().mla_page_fork(
-        ctypes.byref(dims), src.data_ptr(), seq_lens.data_ptr(), page_table.data_ptr(), page_refs.data_ptr(),
-        kv_cache.data_ptr(), page_table_out.data_ptr(), page_refs_out.data_ptr(), workspace.data_ptr(),
-        workspace.nbytes, _stream_int(stream, dev))
+    tensors = src, seq_lens, page_table, page_refs, kv_cache, page_table_out, page_refs_out, workspace
+    rc = _binding().page_fork(*tensors, stream)
+    if rc is None:
+        _refuse("mla_page_fork", _explain_page_fork, kv_cache.get_device(), *tensors)
     if rc != MLA_OK:
         raise MlaError(rc, "mla_page_fork")
 
@@ -1285,23 +1244,13 @@ def mla_rope_pack(plan, q_pe, rows, positions, page_table, seq_lens, cu_q_lens, 
     q_pe bf16 [total_q, H, 64] and rows bf16 [total_q, 576], with unit stride in
     the last dimension; positions int32 [total_q], or None: the tokens' slots;
     q_out bf16 [total_q, H, 64], contiguous (q_pe itself if that is)."""
-    t, dev, qs = _t(), q_pe.get_device(), q_pe.shape
-    B, i32, bf16 = seq_lens.shape[0] if seq_lens.dim() == 1 else -1, t.i32, t.bf16
-    if not (dev >= 0 and len(qs) == 3 and qs[2] == 64 and q_pe.dtype is bf16 and q_pe.stride(2) == 1
-            and rows.dtype is bf16 and rows.shape == (qs[0], 576) and rows.stride(1) == 1 and rows.get_device() == dev
-            and _fits(q_out, qs, bf16, dev) and _cache_fits(kv_cache, page_table, seq_lens, B, dev, t)
-            and kv_cache.shape[1] == 64 and _vec(cu_q_lens, B + 1, i32, dev)
-            and (positions is None or _vec(positions, qs[0], i32, dev)) and _status_fits(status, dev, i32)):
-        _explain_rope(q_pe, rows, positions, page_table, seq_lens, cu_q_lens, q_out, kv_cache, status)
-        raise ValueError("rope tensors do not have the shapes, types and layouts the library expects")
-    _check_current_device(dev)
-    dims = MlaRopeDims(B, qs[1], qs[0], kv_cache.shape[0], page_table.shape[1], page_table.stride(0),
-                       t.cache_codes[kv_cache.dtype], 0, q_pe.stride(0), q_pe.stride(1), rows.stride(0))
-    rc = load_library().mla_rope_pack(
-        ctypes.byref(dims), ctypes.byref(plan), q_pe.data_ptr(), rows.data_ptr(),
-        None if positions is None else positions.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(),
-        cu_q_lens.data_ptr(), float(kv_scale), q_out.data_ptr(), kv_cache.data_ptr(), status.data_ptr(),
-        _stream_int(stream, dev))
+    rc = _binding().rope_pack(plan, q_pe, rows, positions, page_table, seq_lens, cu_q_lens, kv_scale, q_out, kv_cache,
+                              status, stream)
+    if rc is None:
+        if not isinstance(plan, MlaRopePlan):
+            raise TypeError("plan must come from mla_rope_plan")
+        _refuse("mla_rope_pack", _explain_rope, q_pe.get_device(), q_pe, rows, positions, page_table, seq_lens,
+                cu_q_lens, q_out, kv_cache, status)
     if rc != MLA_OK:
         raise MlaError(rc, "mla_rope_pack")
 
