@@ -39,7 +39,7 @@ constexpr int kChunk = 256;                       // entries that a warp adds up
 constexpr int kMaxVocab = 1 << 20;
 constexpr int kMaxChunks = kMaxVocab / kChunk / kCluster;  // of a block
 constexpr int kNodes = MLA_TREE_MAX_NODES;
-static_assert(kNodes <= kThreads && kNodes % 32 == 0 && kMaxChunks <= 2 * kThreads, "a thread per node, two chunks each");
+static_assert(kNodes <= kThreads && kNodes % 32 == 0, "a thread per node");
 
 struct Params {
   const float* target;
@@ -119,8 +119,6 @@ struct Shared {
   uint64_t warp_sum[kWarps];
   uint64_t total[2][kCluster];
   State st;
-  int pick;
-  uint64_t left;
 };
 
 // The weight of an entry after k rejections with a draft.
@@ -316,6 +314,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     if (kDraft) dr = p.draft + (q0 + st.cur) * p.d_stride;
     const bool tv = p.t_vec != 0, dv = p.d_vec != 0, rest = kDraft && st.k > 0;
     constexpr int kFly = 2;  // chunks of a warp in flight
+    uint64_t mine = 0;       // of this warp's chunks
+#pragma unroll 1
     for (int c = warp; c < nc; c += kWarps * kFly) {
       float4 a[kFly][2], q[kFly][2];
 #pragma unroll
@@ -355,24 +355,26 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
         if (!rest || st.k == 1) v = joined(sp, rest ? 0 : 8);
         v = warp_add(v);
         if (lane == 0) s.chunk[c + f * kWarps] = v;
+        mine += v;
       }
     }
+    if (lane == 0) s.warp_sum[warp] = mine;
     __syncthreads();
-    if (!kDraft && tid < st.k) {  // tokens that were rejected have no weight left
-      const int x = s.tok[s.gone[tid]], c = x / kChunk - c0;
-      bool first = c >= 0 && c < nc;
-      for (int i = 0; first && i < tid; ++i) first = s.tok[s.gone[i]] != x;
-      if (first)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s.chunk[c]), 0ull - fixed60(s.wp[s.gone[tid]]));
+    if (!kDraft && st.k > 0) {  // tokens that were rejected have no weight left
+      if (tid < st.k) {
+        const int x = s.tok[s.gone[tid]], c = x / kChunk - c0;
+        bool first = c >= 0 && c < nc;
+        for (int i = 0; first && i < tid; ++i) first = s.tok[s.gone[i]] != x;
+        if (first) {
+          const unsigned long long less = 0ull - fixed60(s.wp[s.gone[tid]]);
+          atomicAdd(reinterpret_cast<unsigned long long*>(&s.chunk[c]), less);
+          atomicAdd(reinterpret_cast<unsigned long long*>(&s.warp_sum[0]), less);
+        }
+      }
+      __syncthreads();
     }
-    if (!kDraft) __syncthreads();
-    uint64_t v = 0;
-    for (int c = tid; c < nc; c += kThreads) v += s.chunk[c];
-    v = warp_add(v);
-    if (lane == 0) s.warp_sum[warp] = v;
-    __syncthreads();
     if (warp == 0) {
-      v = warp_add(lane < kWarps ? s.warp_sum[lane] : 0ull);
+      const uint64_t v = warp_add(lane < kWarps ? s.warp_sum[lane] : 0ull);
       if (pass == 0) cluster_wait();  // every block has begun
       if (lane < kCluster) {
         const uint32_t dst = mapa(smem_u32(&s.total[pass & 1][rank]), static_cast<uint32_t>(lane));
@@ -407,16 +409,17 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     st.k = 0;
     add_up();
   }
-  // the outputs but the last token
-  if (rank == 0) {
-    for (int k = tid; k < p.cols; k += kThreads) {
+  if (warp > 0) {  // the outputs but the last token
+    if (rank != 0) return;
+    for (int k = tid - 32; k < p.cols; k += kThreads - 32) {
       path[k] = k < st.cnt ? s.path[k] : -1;
       if (k < st.cnt - 1) next[k] = s.tok[s.path[k + 1]];
     }
-    if (tid == 0) {
+    if (tid == 32) {
       p.num_out[b] = st.cnt;
       if (sum == 0) atomicOr(p.status, MLA_DEV_BAD_PROBS);
     }
+    return;
   }
   if (sum == 0) return;
   const float u = fminf(fmaxf(p.sample[b], 0.f), 0x1.fffffep-1f);
@@ -429,26 +432,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
       here = here && at >= s.total[last_pass][r];
       at -= s.total[last_pass][r];
     }
-  if (!here || at >= s.total[last_pass][rank]) return;  // (the same in the whole block)
-  // the chunk: each thread two, in order
-  const uint64_t x0 = 2 * tid < nc ? s.chunk[2 * tid] : 0, x1 = 2 * tid + 1 < nc ? s.chunk[2 * tid + 1] : 0;
-  uint64_t v = warp_scan(x0 + x1);
-  __syncthreads();
-  if (lane == 31) s.warp_sum[warp] = v;
-  __syncthreads();
-  v -= x0 + x1;
-  for (int w = 0; w < warp; ++w) v += s.warp_sum[w];
-  if (at >= v && at - v < x0 + x1) {
-    const bool second = at - v >= x0;
-    s.pick = c0 + 2 * tid + (second ? 1 : 0);
-    s.left = at - v - (second ? x0 : 0);
-  }
-  __syncthreads();
-  if (warp != 0) return;
+  if (!here || at >= s.total[last_pass][rank]) return;
+  // the chunk: each lane some, in order
+  const int each = (nc + 31) / 32, first = lane * each;
+  uint64_t mine = 0, before;
+#pragma unroll 1
+  for (int c = first; c < first + each && c < nc; ++c) mine += s.chunk[c];
+  before = warp_scan(mine) - mine;
+  const unsigned who = __ballot_sync(0xffffffffu, at >= before && at - before < mine);
+  if (who == 0) return;
+  int pick = first;
+  uint64_t left = at - before;
+  if (lane == __ffs(who) - 1)
+    while (left >= s.chunk[pick]) left -= s.chunk[pick++];
+  pick = c0 + __shfl_sync(0xffffffffu, pick, __ffs(who) - 1);
+  at = __shfl_sync(0xffffffffu, left, __ffs(who) - 1);
   // the entry: each lane eight, in order
-  at = s.left;
-  uint64_t w[kChunk / 32], mine = 0;
-  const int e0 = s.pick * kChunk + lane * (kChunk / 32);
+  uint64_t w[kChunk / 32];
+  mine = 0;
+  const int e0 = pick * kChunk + lane * (kChunk / 32);
   static_assert(kChunk == 256, "two quads a lane");
   const float4 a0 = load4(tr, e0, p.V, p.t_vec), a1 = load4(tr, e0 + 4, p.V, p.t_vec);
   const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
@@ -469,7 +471,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     }
     mine += w[e];
   }
-  uint64_t before = warp_scan(mine) - mine;
+  before = warp_scan(mine) - mine;
   if (at >= before && at - before < mine) {
     int y = e0;
 #pragma unroll
