@@ -96,6 +96,7 @@ typedef struct {
  *   new_lens    int32 [B]; must not overlap seq_lens, cu_q_lens or num_path, which
  *               every block reads
  *   status      int32 [1]; OR-ed in: MLA_DEV_BAD_SEQ_LEN, MLA_DEV_BAD_QUERY_RANGE,
+ *               MLA_DEV_BAD_TREE (more than MLA_TREE_MAX_NODES nodes),
  *               MLA_DEV_BAD_INDEX (path or num_path): the request is left out
  *               and new_lens[b] = seq_lens[b]; MLA_DEV_BAD_PAGE_ID: a move that
  *               meets a bad page id is skipped.  The caller clears it
