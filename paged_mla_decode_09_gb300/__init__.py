@@ -4,7 +4,8 @@ include/mla_prefill.h, include/mla_evict.h, include/mla_tree.h,
 include/mla_verify.h, include/mla_pages.h and include/mla_rope.h.
 
 The functions here only marshal arguments (torch tensors -> device
-pointers, shapes -> ``mla_dims``); every step of the decode runs in the
+pointers, shapes -> ``mla_dims``), those of a speculative step through a
+compiled module (csrc/binding.cpp); every step of the decode runs in the
 CUDA library.  There is no CPU fallback: if the library is missing or the
 device is not sm_103a, calls raise.
 """

@@ -13,13 +13,17 @@
 // between calls would spare the walk over the counts (4 bytes a page), but its
 // order would depend on the calls before.
 // What bounds it: the latency of the steps, about four reads and barriers, then
-// what 16 SMs read.
+// what 16 SMs read: 4 requests over 512 pages 3.2 us, 256 requests of 512 columns
+// over 131072 pages 11.7 (counts 1.3, their barrier 0.9, entries and the slowest
+// block's atomics 4.4, sums 0.9, the list 1.6, the entries' pages 1.6).
 //
 // Rows (mla_tree_commit, mla_page_fork's second kernel): copies of 16-byte
 // columns.  A committed path is ascending, so that slot k is read (if at all)
 // by a move that is not behind the one that writes it; a thread takes one
 // column of the row through all moves in order, eight loads before their
-// stores, and needs no barrier.
+// stores, and needs no barrier.  64 requests in 24 layers 3.6 us (4.6 MB, 1.3
+// TB/s: the launch and three dependent reads), 64 forks in 16 layers 13.3 with
+// the handing out (35 MB).
 #include <cuda_runtime.h>
 
 #include <climits>
