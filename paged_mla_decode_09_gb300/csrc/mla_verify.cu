@@ -20,8 +20,8 @@
 // What bounds it: HBM for batches (64 chains over 131072 tokens 19.6 us: 3 us
 // until the walks end, 67 MB at 5-6 TB/s, 2 us for the tokens), for one request
 // the chain of reads (offsets, nodes, their entries, the row, the chunk) and the
-// barriers (32000 tokens 6.8 us).  A rejected sibling costs another pass over
-// the rows, from L2: about 4 us at 65536 tokens.
+// barriers (32000 tokens 6.4 us).  A rejected sibling costs another pass over
+// the rows, from L2: about 3 us at 65536 tokens.
 #include <cuda_runtime.h>
 
 #include <climits>
@@ -107,9 +107,10 @@ __device__ __forceinline__ uint64_t mul60(uint64_t a, uint64_t b) {
 struct State {
   int cur, last, cnt;  // the walk's node, the last child tested, nodes on the path
   int k;               // children rejected at cur
-  int todo;            // what the block does next
+  int todo;            // what comes after the row's sum
+  int row;             // cur's row of the probabilities; -1: a request without nodes
 };
-enum { kSum = 0, kFinish = 1 };
+enum { kWalk = 0, kFinish = 1 };
 
 struct Shared {
   int par[kNodes];
@@ -120,7 +121,7 @@ struct Shared {
   int gone[kNodes];         // fixed proposals: nodes rejected at cur
   uint64_t chunk[kMaxChunks];
   uint64_t warp_sum[kWarps];
-  uint64_t total[2][kCluster];
+  ulonglong2 told[2][kCluster];  // every block's sum, and where its walk is
   State st;
 };
 
@@ -172,27 +173,28 @@ __device__ __forceinline__ bool below60(uint64_t a, uint64_t b, uint64_t w) {
   return hi < lim || (hi == lim && a * b < w << 60);
 }
 
-// Warp 0 of a block: on from s.st to the next sum over the row, or the end.
-// `sum` is the row's sum after the last rejection (draft), `summed` whether
-// the chunks hold the present weights.  64-bit floating point, at about half a
-// microsecond a test, only where a draft follows a rejection.
+// Warp 0 of a block: on from s.st to the next sum over a row.  (Every walk
+// ends before one that has not been formed: a child is left to be tested where
+// a walk goes on.)  `sum` is the row's sum after the last rejection (draft).
+// 64-bit floating point, at about half a microsecond a test, only where a draft
+// follows a rejection.
 template <bool kDraft>
-__device__ __forceinline__ void walk(Shared& s, int n, int cols, uint64_t sum, bool& summed) {
+__device__ __forceinline__ void walk(Shared& s, int n, int q0, int cols, uint64_t sum) {
   const int lane = threadIdx.x & 31, groups = (n + 31) >> 5;
   State st = s.st;
-  int par[kNodes / 32];
-#pragma unroll
-  for (int g = 0; g < kNodes / 32; ++g) par[g] = g * 32 + lane < n ? s.par[g * 32 + lane] : -2;
   uint64_t z = 1ull << 60;  // fixed proposals (which end in one go)
+  auto next_child = [&]() {  // of cur; -1: none
+#pragma unroll 1
+    for (int g = (st.last + 1) >> 5; g < groups; ++g) {
+      const int i = g * 32 + lane;
+      const unsigned m = __ballot_sync(0xffffffffu, i > st.last && i < n && s.par[i] == st.cur);
+      if (m) return g * 32 + __ffs(m) - 1;
+    }
+    return -1;
+  };
   st.todo = kFinish;
   while (st.cnt < cols) {
-    int j = -1;  // the next child of cur
-#pragma unroll
-    for (int g = 0; g < kNodes / 32; ++g)
-      if (g < groups) {
-        const unsigned m = __ballot_sync(0xffffffffu, par[g] == st.cur && g * 32 + lane > st.last);
-        if (j < 0 && m) j = g * 32 + __ffs(m) - 1;
-      }
+    const int j = next_child();
     if (j < 0) break;
     st.last = j;
     const float u = s.acc[j], w = __saturatef(s.wp[j]);
@@ -217,22 +219,20 @@ __device__ __forceinline__ void walk(Shared& s, int n, int cols, uint64_t sum, b
       if (lane == 0) s.path[st.cnt] = j;
       ++st.cnt;
       st.cur = j;
+      st.row = q0 + j;
       st.k = 0;
       z = 1ull << 60;
-      summed = false;
       continue;
     }
     if (kDraft) {
       if (lane == 0) s.z[st.k] = st.k == 0 ? 1ull << 60 : sum;
       ++st.k;
-      summed = false;
-      st.todo = kSum;
+      st.todo = next_child() < 0 ? kFinish : kWalk;
       break;
     }
     if (lane == 0) s.gone[st.k] = j;
     __syncwarp();
     ++st.k;
-    summed = false;
   }
   __syncwarp();
   if (lane == 0) s.st = st;
@@ -260,16 +260,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
   }
   int32_t* path = p.path + static_cast<int64_t>(b) * p.cols;
   int32_t* next = p.tokens_out + static_cast<int64_t>(b) * p.cols;
-  if (n == 0) {  // (the same in every block of the cluster)
-    cluster_wait();
-    if (rank != 0) return;
-    for (int k = tid; k < p.cols; k += kThreads) path[k] = next[k] = -1;
-    if (tid == 0) {
-      p.num_out[b] = 0;
-      if (flag) atomicOr(p.status, flag);
-    }
-    return;
-  }
+  if (flag && rank == 0 && tid == 0) atomicOr(p.status, flag);
+  flag = 0;
   if (tid < n) {
     int par = -2, tok = 0;
     if (tid > 0) {
@@ -299,25 +291,46 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     for (int k = tid; k < p.cols; k += kThreads) next[k] = -1;
   if (tid == 0) {
     s.path[0] = 0;
-    s.st = {0, 0, 1, 0, kFinish};
+    s.st = {0, 0, n > 0 ? 1 : 0, 0, kFinish, n > 0 ? q0 : -1};
   }
   __syncthreads();
   const int all = (p.V + kChunk - 1) / kChunk, per = (all + kCluster - 1) / kCluster;
-  const int c0 = rank * per < all ? rank * per : all, nc = (all - c0 < per ? all - c0 : per);
+  const int c0 = rank * per < all ? rank * per : all, chunks = (all - c0 < per ? all - c0 : per);
   uint64_t sum = 0;      // of the row's weights, all blocks
-  bool summed = false;   // (warp 0 decides, then all know)
   int pass = 0;
   const float* tr = nullptr;
   const float* dr = nullptr;
   State st = {};
+  auto gone = [&](int i) { return s.gone[i] & (kNodes - 1); };  // (a state taken over may count more than this block has)
 
-  // adds up the weights of the row of st.cur after st.k rejections
+  // adds up the weights of st.row after st.k rejections.  The blocks walk by
+  // themselves, on the same inputs; the first one's state goes with its sum and
+  // is taken over by all, so that they use the same barriers, and stay within
+  // the rows, even if another stream changes the inputs meanwhile
   auto add_up = [&]() {
-    tr = p.target + (q0 + st.cur) * p.t_stride;
-    if (kDraft) dr = p.draft + (q0 + st.cur) * p.d_stride;
-    const bool tv = p.t_vec != 0, dv = p.d_vec != 0, rest = kDraft && st.k > 0;
+    const int nc = st.row < 0 ? 0 : chunks;
+    tr = p.target + (st.row < 0 ? 0 : st.row) * p.t_stride;
+    if (kDraft) dr = p.draft + (st.row < 0 ? 0 : st.row) * p.d_stride;
+    const bool tv = p.t_vec != 0, dv = p.d_vec != 0, rest = kDraft && st.k == 1;
     constexpr int kFly = 2;  // chunks of a warp in flight
     uint64_t mine = 0;       // of this warp's chunks
+    if (kDraft && st.k > 1) {  // behind rejected siblings: entry by entry
+#pragma unroll 1
+      for (int c = warp; c < nc; c += kWarps) {
+        const int e = (c0 + c) * kChunk + lane * 4;
+        const float4 a[2] = {load4(tr, e, p.V, tv), load4(tr, e + 128, p.V, tv)};
+        const float4 q[2] = {load4(dr, e, p.V, dv), load4(dr, e + 128, p.V, dv)};
+        uint64_t v = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          v += weight(fixed60(a[h].x), fixed60(q[h].x), s.z, st.k) + weight(fixed60(a[h].y), fixed60(q[h].y), s.z, st.k);
+          v += weight(fixed60(a[h].z), fixed60(q[h].z), s.z, st.k) + weight(fixed60(a[h].w), fixed60(q[h].w), s.z, st.k);
+        }
+        v = warp_add(v);
+        if (lane == 0) s.chunk[c] = v;
+        mine += v;
+      }
+    } else
 #pragma unroll 1
     for (int c = warp; c < nc; c += kWarps * kFly) {
       float4 a[kFly][2], q[kFly][2];
@@ -334,7 +347,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
 #pragma unroll
       for (int f = 0; f < kFly; ++f) {
         if (c + f * kWarps >= nc) break;
-        uint64_t v = 0;
         Split sp = {0u, 0u, 0u};
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -343,20 +355,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
           if (!rest) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) add_split<1>(sp, __saturatef(x[e]));
-          } else if (st.k == 1) {  // p - q where that is above 0
+          } else {  // p - q where that is above 0
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const float c = __saturatef(x[e]), d = __saturatef(y[e]);
               add_split<1>(sp, c > d ? c : 0.f);
               add_split<-1>(sp, c > d ? d : 0.f);
             }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v += weight(fixed60(x[e]), fixed60(y[e]), s.z, st.k);
           }
         }
-        if (!rest || st.k == 1) v = joined(sp, rest ? 0 : 8);
-        v = warp_add(v);
+        const uint64_t v = warp_add(joined(sp, rest ? 0 : 8));
         if (lane == 0) s.chunk[c + f * kWarps] = v;
         mine += v;
       }
@@ -365,11 +373,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     __syncthreads();
     if (!kDraft && st.k > 0) {  // tokens that were rejected have no weight left
       if (tid < st.k) {
-        const int x = s.tok[s.gone[tid]], c = x / kChunk - c0;
+        const int x = s.tok[gone(tid)], c = x / kChunk - c0;
         bool first = c >= 0 && c < nc;
-        for (int i = 0; first && i < tid; ++i) first = s.tok[s.gone[i]] != x;
+        for (int i = 0; first && i < tid; ++i) first = s.tok[gone(i)] != x;
         if (first) {
-          const unsigned long long less = 0ull - fixed60(s.wp[s.gone[tid]]);
+          const unsigned long long less = 0ull - fixed60(s.wp[gone(tid)]);
           atomicAdd(reinterpret_cast<unsigned long long*>(&s.chunk[c]), less);
           atomicAdd(reinterpret_cast<unsigned long long*>(&s.warp_sum[0]), less);
         }
@@ -380,35 +388,41 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
       const uint64_t v = warp_add(lane < kWarps ? s.warp_sum[lane] : 0ull);
       if (pass == 0) cluster_wait();  // every block has begun
       if (lane < kCluster) {
-        const uint32_t dst = mapa(smem_u32(&s.total[pass & 1][rank]), static_cast<uint32_t>(lane));
-        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(dst), "l"(v) : "memory");
+        const uint32_t dst = mapa(smem_u32(&s.told[pass & 1][rank]), static_cast<uint32_t>(lane));
+        // (cur, last, k and cnt - 1 are below 256; rows below 2^31 - 1, which stands for none)
+        const uint32_t lo = static_cast<uint32_t>(st.cur | st.last << 8 | (st.k & 255) << 16) |
+                            static_cast<uint32_t>(st.cnt - 1) << 24;
+        const uint32_t hi = (st.row < 0 ? 0x7fffffffu : static_cast<uint32_t>(st.row)) |
+                            static_cast<uint32_t>(st.todo) << 31;
+        st_cluster_v4(dst, make_uint4(static_cast<uint32_t>(v), static_cast<uint32_t>(v >> 32), lo, hi));
       }
     }
     if (pass == 0 && warp != 0) cluster_wait();
     cluster_sync();
     sum = 0;
 #pragma unroll
-    for (int r = 0; r < kCluster; ++r) sum += s.total[pass & 1][r];
+    for (int r = 0; r < kCluster; ++r) sum += s.told[pass & 1][r].x;
+    const uint32_t lo = static_cast<uint32_t>(s.told[pass & 1][0].y), hi = static_cast<uint32_t>(s.told[pass & 1][0].y >> 32);
+    const bool some = (hi & 0x7fffffffu) != 0x7fffffffu;
+    st.cur = static_cast<int>(lo & 255u);
+    st.last = static_cast<int>(lo >> 8 & 255u);
+    st.k = static_cast<int>(lo >> 16 & 255u);
+    st.cnt = some ? static_cast<int>(lo >> 24) + 1 : 0;
+    st.todo = static_cast<int>(hi >> 31);
+    st.row = some ? static_cast<int>(hi & 0x7fffffffu) : -1;
     ++pass;
   };
 
-  __shared__ int s_summed;
   while (true) {
-    if (warp == 0) {
-      walk<kDraft>(s, n, p.cols, sum, summed);
-      if (lane == 0) s_summed = summed;
-    }
+    if (warp == 0) walk<kDraft>(s, n, q0, p.cols, sum);
     __syncthreads();
     st = s.st;
-    summed = s_summed != 0;
-    if (!summed) {
-      add_up();
-      summed = true;
-    }
+    add_up();
     if (st.todo == kFinish) break;
-    __syncthreads();
+    if (tid == 0) s.st = st;
+    __syncwarp();
   }
-  if (sum == 0) {  // rounding has left nothing: the node's own row
+  if (sum == 0 && st.row >= 0) {  // rounding has left nothing: the node's own row
     st.k = 0;
     add_up();
   }
@@ -420,7 +434,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     }
     if (tid == 32) {
       p.num_out[b] = st.cnt;
-      if (sum == 0) atomicOr(p.status, MLA_DEV_BAD_PROBS);
+      if (sum == 0 && st.row >= 0) atomicOr(p.status, MLA_DEV_BAD_PROBS);
     }
     return;
   }
@@ -432,15 +446,15 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
 #pragma unroll
   for (int r = 0; r < kCluster; ++r)
     if (r < rank) {
-      here = here && at >= s.total[last_pass][r];
-      at -= s.total[last_pass][r];
+      here = here && at >= s.told[last_pass][r].x;
+      at -= s.told[last_pass][r].x;
     }
-  if (!here || at >= s.total[last_pass][rank]) return;
+  if (!here || at >= s.told[last_pass][rank].x) return;
   // the chunk: each lane some, in order
-  const int each = (nc + 31) / 32, first = lane * each;
+  const int each = (chunks + 31) / 32, first = lane * each;
   uint64_t mine = 0, before;
 #pragma unroll 1
-  for (int c = first; c < first + each && c < nc; ++c) mine += s.chunk[c];
+  for (int c = first; c < first + each && c < chunks; ++c) mine += s.chunk[c];
   before = warp_scan(mine) - mine;
   const unsigned who = __ballot_sync(0xffffffffu, at >= before && at - before < mine);
   if (who == 0) return;
@@ -470,7 +484,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
       if (st.k > 0) w[e] = weight(w[e], fixed60(d[e]), s.z, st.k);
     } else {
       for (int i = 0; i < st.k; ++i)
-        if (s.tok[s.gone[i]] == e0 + e) w[e] = 0;
+        if (s.tok[gone(i)] == e0 + e) w[e] = 0;
     }
     mine += w[e];
   }
