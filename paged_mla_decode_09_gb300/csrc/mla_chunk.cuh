@@ -227,8 +227,8 @@ __device__ __forceinline__ void find_ancestors(const Params& p, int first, int s
     const int q0 = p.cu_q[b], q1 = p.cu_q[b + 1];
     // (a bad range is the schedule's to report)
     const int n = q0 >= 0 && q1 >= q0 && q1 <= p.T && q1 - q0 <= kTreeNodes ? q1 - q0 : 0;
-    if (tid < n) {
-      int up = p.parents[q0 + tid];
+    if (tid < kTreeNodes) {
+      int up = tid < n ? p.parents[q0 + tid] : -1;
       if (up < -1 || up >= tid) {  // as if it had none
         bad = 1;
         up = -1;

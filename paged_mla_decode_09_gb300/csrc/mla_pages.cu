@@ -411,11 +411,11 @@ __global__ void __launch_bounds__(kCommitThreads) mla_tree_commit_kernel(const _
   else if (a < 0 || a > nodes || a > p.cols) flag |= MLA_DEV_BAD_INDEX;
   const int n = static_cast<int>(nodes), base = L - n;
   int bad = 0, page_bad = 0;
+  int64_t f = -1, t = -1;
   if (flag == 0 && tid < a) {
     const int32_t* path = p.path + static_cast<int64_t>(b) * p.cols;
     const int j = path[tid], prev = tid > 0 ? path[tid - 1] : -1;
     bad = j <= prev || j >= n || j < tid;
-    int64_t f = -1, t = -1;
     if (!bad && j != tid) {
       const int32_t* row = p.table + static_cast<int64_t>(b) * p.pt_stride;
       const int sf = base + j, st = base + tid;
@@ -427,6 +427,8 @@ __global__ void __launch_bounds__(kCommitThreads) mla_tree_commit_kernel(const _
         t = (static_cast<int64_t>(pt) * kPage + st % kPage) * p.row_bytes;
       }
     }
+  }
+  if (tid < MLA_TREE_MAX_NODES) {
     from[tid] = f;
     to[tid] = t;
   }

@@ -169,8 +169,9 @@ __global__ void __launch_bounds__(kThreads, 5) mla_rope_pack_kernel(const __grid
         fail = MLA_DEV_BAD_SEQ_LEN;
         mine = tid;
       } else {
-        const int at = L - n + (t0 + tid - q0);
-        const int page = p.page_table[static_cast<int64_t>(b) * p.pt_stride + at / kPage];
+        const int at = L - n + (t0 + tid - q0);  // (in the table, unless offsets change under the call)
+        const bool in = at >= 0 && at < p.max_pages * kPage;
+        const int page = in ? p.page_table[static_cast<int64_t>(b) * p.pt_stride + at / kPage] : -1;
         if (page < 0 || page >= p.num_pages) fail = MLA_DEV_BAD_PAGE_ID;
         else slot = static_cast<int64_t>(page) * kPage + at % kPage;
       }
