@@ -1346,6 +1346,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int vs = static_cast<int>(j % C::kNV);
           const int ps = static_cast<int>(j % C::kNP);
           const bool first = vp == u.p0;
+          uint8_t* slot = vring + vs * C::kSlotV;
+          // V rows that this page has from ordinary stores: a pair's leader
+          // and the other CTA order them at cluster scope
+          const int valid = u.k.len - real_page(u.k, vp) * kPage;
+          const bool stored = kF8 || valid < kPage;
+          if constexpr (!kF8) {
+            if (valid < kPage) {  // before the page's weights are awaited
+              if (!mbar_wait_warp(smem_u32(&ctrl->kv_full[vs]), (j / C::kNV) & 1, abort, p.timeout_ns)) {
+                ok = false;
+                why = kWaitPage;
+                break;
+              }
+              const int v0 = valid > 0 ? valid : 0;
+              for (int row = v0 + (lane >> 3); row < kPage; row += 4)
+#pragma unroll
+                for (int box = 0; box < C::kVBoxes; ++box)
+                  *reinterpret_cast<uint4*>(slot + box * C::kVBox + row * 128 + (lane & 7) * 16) =
+                      make_uint4(0, 0, 0, 0);
+              __syncwarp();
+            }
+          }
           {
             const uint32_t vbar = kF8 ? smem_u32(&ctrl->v_full[vs & 3]) : smem_u32(&ctrl->kv_full[vs]);
             const uint32_t pph = (j / C::kNP) & 1;
@@ -1374,22 +1395,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           // this phase is done: arm the slot for page j + kNP, whose bytes
           // come only after PV(j)
           if (lane == 0) mbar_expect_tx(smem_u32(&ctrl->p_full[ps]), C::kPTx);
-          uint8_t* slot = vring + vs * C::kSlotV;
-          // V rows that this page has from ordinary stores: a pair's leader
-          // and the other CTA order them at cluster scope
-          const int valid = u.k.len - real_page(u.k, vp) * kPage;
-          const bool stored = kF8 || valid < kPage;
-          if constexpr (!kF8) {
-            if (valid < kPage) {
-              const int v0 = valid > 0 ? valid : 0;
-              for (int row = v0 + (lane >> 3); row < kPage; row += 4)
-#pragma unroll
-                for (int box = 0; box < C::kVBoxes; ++box)
-                  *reinterpret_cast<uint4*>(slot + box * C::kVBox + row * 128 + (lane & 7) * 16) =
-                      make_uint4(0, 0, 0, 0);
-              __syncwarp();
-            }
-          }
           fence_proxy_async_cta();
           tc_fence_after();
           if (kCg == 2 && !leader) {
