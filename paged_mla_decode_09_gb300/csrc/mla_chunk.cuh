@@ -745,8 +745,9 @@ __device__ __forceinline__ float store_lse(const Params& p, const Unit& u, int b
 // shared memory: boxes of 32 rows x 64 bytes (64-byte swizzle), kBufs in turn,
 // that TMA writes.  (A lane's own stores to its row take a line each: a block's
 // bf16 outputs took 4.9 us that way, 2.5 this way, and O is not free for the
-// next block before that.)  A single form's partial rows of 4 KB took 5 us, 4
-// this way (a tree of 128 rows over 700 tokens, cut: 21.0 -> 20.0 us in all).
+// next block before that.)  The single form's last block likewise: a tree of
+// 128 rows over 700 tokens, cut, 21.0 -> 19.6 us in all; 64 of them over 60, uncut,
+// 18.4 -> 16.8.
 constexpr int kLastBufs = 8;
 template <bool kF8, int kCg, int kBufs>
 __device__ __forceinline__ void store_staged(const Params& p, const Unit& u, int br0, int c0, uint32_t taddr, float f,
@@ -1580,10 +1581,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int br0 = br - lane;  // the warp's first row
         bool staged = false;
         if constexpr (C::kStage > 0) staged = u.slot >= 0 ? u.slot < 2 * p.C : br0 + 32 <= u.k.nrows;
-        // a single form's slice ends with a piece: its page rings are idle, and
-        // stage the partial rows of blocks with more than 64 (calls of 128 rows
-        // 1.0-2.6 us shorter, of 64 up to 0.5 longer, of 16 and 32 2.2 and 1.6)
-        else staged = it.n > it.nlast && u.slot >= 0 && u.slot < 2 * p.C && u.k.nrows > 64 && br0 + 16 <= u.k.nrows;
+        // a single form's last unit of a slice finds the page rings idle and
+        // stages there, for blocks of more than 64 rows (calls of 128 rows 1.0-2.6
+        // us shorter, of 64 up to 0.5 longer, of 16 and 32 2.2 and 1.6)
+        else staged = it.n > it.nlast && u.slot < 2 * p.C && u.k.nrows > 64 && br0 + (u.slot >= 0 ? 16 : 32) <= u.k.nrows;
         if (!staged && lane == 0) mbar_arrive_cluster(mlempty_remote);
         const float f = store_lse<kF8>(p, u, br, c0 == 0, m_log2, l);
         if (staged) {
@@ -1593,7 +1594,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             static_assert(8 * kLastBufs * 2048 <= C::kStageOff - C::kVOff, "the rings hold the staging");
             store_staged<kF8, kCg, kLastBufs>(p, u, br0, c0, tmem + lane_base, f, vring + (warp - 4) * kLastBufs * 2048,
-                                              &tm_part);
+                                              u.slot < 0 ? &tm_out : &tm_part);
           }
         } else {
           store_row<kF8, kCg>(p, u, br, c0, c0 + kCols, tmem + lane_base, f);
