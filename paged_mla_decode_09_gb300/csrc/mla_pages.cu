@@ -284,15 +284,20 @@ __global__ void __launch_bounds__(kThreads, 1) mla_pages_kernel(const __grid_con
   if (tid < kCluster)
     st_cluster_u32(mapa(smem_u32(&missing_of[rank]), static_cast<uint32_t>(tid)), static_cast<uint32_t>(all));
   sync_all<kCluster>();
-  // free pages of all blocks, read where they are counted (no block ends before the next barrier)
-  if (tid < kCluster)
-    free_of[tid] = static_cast<int>(ld_cluster_u32(mapa(smem_u32(&free_pages), static_cast<uint32_t>(tid))));
-  __syncthreads();
-  int wanted = 0, before = 0, have = 0, fbefore = 0;  // in all, and of the blocks before this one
+  int wanted = 0, before = 0;  // missing entries in all, and of the blocks before this one
 #pragma unroll
   for (int r = 0; r < kCluster; ++r) {
     wanted += missing_of[r];
     before += r < rank ? missing_of[r] : 0;
+  }
+  if (wanted == 0) return;  // (the same in every block, before any reads another's shared memory)
+  // free pages of all blocks, read where they are counted: no block ends before the next barrier
+  if (tid < kCluster)
+    free_of[tid] = static_cast<int>(ld_cluster_u32(mapa(smem_u32(&free_pages), static_cast<uint32_t>(tid))));
+  __syncthreads();
+  int have = 0, fbefore = 0;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) {
     have += free_of[r];
     fbefore += r < rank ? free_of[r] : 0;
   }

@@ -83,6 +83,17 @@ def test_resize_grows_from_nothing_and_frees_all():
     assert np.all(t == -1) and np.all(r == 0)
 
 
+def test_large_pools_that_only_free():
+    """Nothing is handed out: the blocks of a cluster end early."""
+    rng = np.random.default_rng(11)
+    lens = rng.integers(1, 700 * 64, 40) // 2
+    table, refs = pool(rng, lens, 700, 40000)
+    for new in (np.zeros(40, np.int64), lens // 3, lens):
+        for _ in range(3):
+            want = check_resize(new, table, refs)
+        assert want[2] == 0
+
+
 def test_resize_hands_out_what_it_gets_back():
     table, refs = np.arange(8, dtype=np.int32).reshape(2, 4), np.ones(8, np.int32)
     t, r, status = check_resize([64, 256], table, refs)
