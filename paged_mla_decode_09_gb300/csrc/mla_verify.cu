@@ -20,7 +20,7 @@
 // What bounds it: HBM for batches (64 chains over 131072 tokens 19.6 us: 3 us
 // until the walks end, 67 MB at 5-6 TB/s, 2 us for the tokens), for one request
 // the chain of reads (offsets, nodes, their entries, the row, the chunk) and the
-// barriers (32000 tokens 6.4 us).  A rejected sibling costs another pass over
+// barriers (32000 tokens 6 us).  A rejected sibling costs another pass over
 // the rows, from L2: about 3 us at 65536 tokens.
 #include <cuda_runtime.h>
 
