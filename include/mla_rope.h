@@ -97,8 +97,9 @@ typedef struct {
  *               MLA_DEV_BAD_SEQ_LEN and the request is left out: neither its
  *               queries nor its rows are written)
  *   cu_q_lens   int32 [B + 1] as for mla_prefill (else MLA_DEV_BAD_QUERY_RANGE and
- *               the request is left out); tokens from cu_q_lens[B] on are not
- *               touched
+ *               the request is left out; a token that two others name where the
+ *               offsets decrease is the last one's, and the first's slot keeps
+ *               its row); tokens from cu_q_lens[B] on are not touched
  *   kv_scale    e4m3 cache: a normal, finite number with a finite reciprocal;
  *               bf16 cache: ignored
  *   q_out       bf16 [total_q][H][64], contiguous, 16-byte aligned: the rotated

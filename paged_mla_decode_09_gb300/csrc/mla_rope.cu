@@ -157,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 5) mla_rope_pack_kernel(const __grid
       continue;
     }
     const int lo = q0 > t0 ? q0 : t0, hi = q1 < t0 + nt ? q1 : t0 + nt;
-    for (int t = lo; t < hi; ++t) s_req[t - t0] = b;
+    for (int t = lo; t < hi; ++t) atomicMax(&s_req[t - t0], b);  // (offsets that decrease: the last that names it)
   }
   __syncthreads();
   // its slot, and its angles

@@ -238,6 +238,36 @@ def test_flags(slots):
         c.run(plan, status=mla.MLA_DEV_BAD_QUERY_RANGE)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("slots", [True, False])
+@pytest.mark.parametrize("cu,owners", [([0, 3, 2, 10], [0, 0, 2, 2, 2, 2, 2, 2, 2, 2]), ([0, 9, 1, 4], [0, 2, 2, 2] + [0] * 5 + [None]),
+                                       ([0, 3, 8, 11], [0, 0, 0, 1, 1, 1, 1, 1, None, None]),
+                                       ([1, 3, 8, 10], [None] * 3 + [1] * 5 + [2] * 2), ([0, -5, 8, 10], [None] * 8 + [2, 2])])
+def test_bad_offsets_leave_the_other_requests_right(cu, owners, slots, kv):
+    """A token that two requests name is the last one's; a request with a bad
+    offset is left out; everything else is as it would be without them."""
+    import paged_mla_decode_09_gb300 as mla
+
+    plan, freq = plan_of(64, True)
+    c = Case([3, 5, 2], [100, 200, 90], 4, kv=kv, seed=6)
+    c.table = np.arange(12, dtype=np.int32).reshape(3, 4)
+    c.cache = np.random.default_rng(8).integers(0, 120, (12, 64, 576)).astype(c.cache.dtype)
+    c.cu, c.slots = np.asarray(cu, np.int32), slots
+    out, cache = c.run(plan, status=mla.MLA_DEV_BAD_QUERY_RANGE)
+    # the same with a request for each token, whose length puts it where its owner does
+    one = Case([3, 5, 2], [100, 200, 90], 4, kv=kv, seed=6)
+    one.cache, one.slots = c.cache, slots
+    kept = [t for t in range(10) if owners[t] is not None]
+    one.table = np.stack([c.table[owners[t]] for t in kept])
+    one.lens = np.asarray([c.lens[owners[t]] - c.cu[owners[t] + 1] + t + 1 for t in kept], np.int32)
+    one.cu = np.arange(len(kept) + 1, dtype=np.int32)
+    one.q, one.rows, one.T, one.positions = c.q[kept], c.rows[kept], len(kept), c.positions[kept]
+    want, rows = one.run(plan)
+    assert np.array_equal(out[kept], want) and np.array_equal(cache, rows)
+    gone = [t for t in range(10) if owners[t] is None]
+    assert np.all(oracle.bf16_bits_to_f64(out[gone]) == 7.0)
+
+
 def _without(c, cache, b):
     """The cache, after checking that request b's rows are as they were."""
     n = int(c.cu[b + 1] - c.cu[b])
