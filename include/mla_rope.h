@@ -45,22 +45,40 @@ typedef struct {
 } mla_rope_plan;
 
 /*
- * Frequencies in radians a position, out[i] for i < rotary_dim / 2:
- * f_i = base^(-2 i / rotary_dim), and for contexts `factor` times longer than
- * trained for
+ * Frequencies in radians a position, out[i] for i < R / 2, R = rotary_dim:
+ * f_i = base^(-2 i / R), and for contexts `factor` times longer than trained
+ * for
  *
  *     original_len == 0:  f_i / factor
- *     original_len > 0:   g f_i + (1 - g) f_i / factor with
- *                         g = (r - slow) / (fast - slow), limited to [0, 1],
- *                         r = original_len f_i / (2 pi) turns in that length:
- *                         pairs that turn often stay, the slow ones stretch.
+ *     original_len > 0:   g_i f_i + (1 - g_i) f_i / factor, g_i in [0, 1]:
+ *                         pairs that turn often in original_len positions
+ *                         stay, the slow ones stretch.
+ *
+ * The two functions differ in g between the pairs that turn `fast` and `slow`
+ * times, which are whole other frequencies (R = 64, base 10000, factor 40,
+ * original_len 4096, fast 32, slow 1: pairs 11 to 22, pair 20 by a factor of
+ * 4.3).  Take the one that the weights were trained with:
+ *
+ *   mla_rope_frequencies           linear in the turns, as the method was
+ *       published: g_i = (r_i - slow) / (fast - slow), limited to [0, 1], with
+ *       r_i = original_len f_i / (2 pi) turns;
+ *   mla_rope_frequencies_by_index  linear in the pair's index, between whole
+ *       indices: what DeepSeek-V3's configuration means by these parameters
+ *       (factor, original_len, fast and slow = beta_fast and beta_slow).
+ *       g_i = 1 - (i - lo) / (hi - lo), limited to [0, 1], with
+ *       lo = max(floor(I(fast)), 0), hi = min(ceil(I(slow)), R - 1) and
+ *       I(n) = R ln(original_len / (2 pi n)) / (2 ln base), the index that turns
+ *       n times.  Where hi <= lo, pairs up to lo stay and the others stretch.
  *
  * Host only.  MLA_ERR_INVALID_ARG for a null pointer, base < 1, factor < 1,
- * original_len < 0 or fast <= slow (looked at where original_len > 0), or
- * values that are not finite; MLA_ERR_UNSUPPORTED for another rotary_dim.
+ * original_len < 0 or fast <= slow (looked at where original_len > 0; by
+ * index, there, also for base == 1 or slow <= 0), or values that are not
+ * finite; MLA_ERR_UNSUPPORTED for another rotary_dim.
  */
 int mla_rope_frequencies(int32_t rotary_dim, double base, double factor, int32_t original_len, double fast,
                          double slow, double* out);
+int mla_rope_frequencies_by_index(int32_t rotary_dim, double base, double factor, int32_t original_len, double fast,
+                                  double slow, double* out);
 
 /* A plan of any frequencies, each in [0, 2 pi) (else MLA_ERR_INVALID_ARG, as
  * for an amplitude that is not finite and above 0).  Host only. */

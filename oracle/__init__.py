@@ -14,7 +14,7 @@ from .e4m3 import e4m3_decode_table, e4m3_encode, e4m3_to_f64
 from .evict import attn_mass_ref, evict_ref
 from .kv_pack import kv_pack_ref
 from .pages import page_fork_ref, page_resize_ref
-from .rope import new_slots, rope_frequencies_ref, rotate_ref
+from .rope import new_slots, rope_frequencies_by_index_ref, rope_frequencies_ref, rotate_ref
 from .sparse import mla_decode_sparse_ref
 from .tree import ancestors, mla_tree_ref, tree_commit_ref, tree_keys, verify_ref
 from .mla_oracle import (
@@ -50,6 +50,7 @@ __all__ = [
     "new_slots",
     "page_fork_ref",
     "page_resize_ref",
+    "rope_frequencies_by_index_ref",
     "rope_frequencies_ref",
     "rotate_ref",
     "seen_keys",

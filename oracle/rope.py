@@ -24,6 +24,21 @@ def rope_frequencies_ref(rotary_dim, base, factor=1.0, original_len=0, fast=32.0
     return out
 
 
+def rope_frequencies_by_index_ref(rotary_dim, base, factor, original_len, fast=32.0, slow=1.0):
+    """Between the indices that turn `fast` and `slow` times (rounded outwards),
+    the share that is kept falls linearly with the pair's index."""
+    def index_of(turns):
+        return rotary_dim * math.log(original_len / (2.0 * math.pi * turns)) / (2.0 * math.log(base))
+
+    lo, hi = max(math.floor(index_of(fast)), 0), min(math.ceil(index_of(slow)), rotary_dim - 1)
+    out = []
+    for i in range(rotary_dim // 2):
+        f = base ** (-2.0 * i / rotary_dim)
+        keep = min(1.0, max(0.0, (hi - i) / (hi - lo))) if hi > lo else float(i <= lo)
+        out.append(f * (keep + (1.0 - keep) / factor))
+    return out
+
+
 def rotate_ref(x, positions, frequencies, interleaved, amplitude=1.0):
     """x float64 [T, ..., n] with its first 2 len(frequencies) values rotated.
     The angle is reduced exactly: its turns are formed as integers over 2^60."""

@@ -67,6 +67,7 @@ ENTRY_POINTS = (
     "mla_page_fork_workspace_size",
     "mla_page_fork",
     "mla_rope_frequencies",
+    "mla_rope_frequencies_by_index",
     "mla_rope_plan_init",
     "mla_rope_pack",
 )
@@ -291,8 +292,9 @@ def load_library(path: str | None = None, build: bool = False) -> ctypes.CDLL:
     lib.mla_page_fork.argtypes = [ctypes.POINTER(MlaPageForkDims), P, P, P, P, P, P, P, P, SZ, P]
     lib.mla_page_fork.restype = ctypes.c_int
     DP, R = ctypes.POINTER(ctypes.c_double), ctypes.POINTER(MlaRopePlan)
-    lib.mla_rope_frequencies.argtypes = [I32, ctypes.c_double, ctypes.c_double, I32, ctypes.c_double, ctypes.c_double, DP]
-    lib.mla_rope_frequencies.restype = ctypes.c_int
+    for f in (lib.mla_rope_frequencies, lib.mla_rope_frequencies_by_index):
+        f.argtypes = [I32, ctypes.c_double, ctypes.c_double, I32, ctypes.c_double, ctypes.c_double, DP]
+        f.restype = ctypes.c_int
     lib.mla_rope_plan_init.argtypes = [I32, I32, F, DP, R]
     lib.mla_rope_plan_init.restype = ctypes.c_int
     lib.mla_rope_pack.argtypes = [ctypes.POINTER(MlaRopeDims), R, P, P, P, P, P, P, F, P, P, P, P]
@@ -1188,22 +1190,33 @@ def mla_page_fork(src, seq_lens, page_table, page_refs, kv_cache, page_table_out
 
 # ---- rotary positions (include/mla_rope.h) ----
 
-def mla_rope_frequencies(rotary_dim, base=10000.0, factor=1.0, original_len=0, fast=32.0, slow=1.0) -> list:
-    """Radians a position of every rotated pair (see include/mla_rope.h)."""
+def mla_rope_frequencies(rotary_dim, base=10000.0, factor=1.0, original_len=0, fast=32.0, slow=1.0,
+                         ramp="turns") -> list:
+    """Radians a position of every rotated pair (see include/mla_rope.h).
+
+    With a factor and an original_len, ramp says how the pairs between `fast`
+    and `slow` turns pass from kept to stretched: "turns" (as published) or
+    "index" (what DeepSeek-V3's configuration means by these parameters)."""
+    lib = load_library()
+    try:
+        name = {"turns": "mla_rope_frequencies", "index": "mla_rope_frequencies_by_index"}[ramp]
+    except (KeyError, TypeError):
+        raise ValueError(f"ramp must be 'turns' or 'index', got {ramp!r}") from None
     out = (ctypes.c_double * 32)()
-    rc = load_library().mla_rope_frequencies(_int32_arg("rotary_dim", rotary_dim), float(base), float(factor),
-                                             _int32_arg("original_len", original_len), float(fast), float(slow), out)
+    rc = getattr(lib, name)(_int32_arg("rotary_dim", rotary_dim), float(base), float(factor),
+                            _int32_arg("original_len", original_len), float(fast), float(slow), out)
     if rc != MLA_OK:
-        raise MlaError(rc, "mla_rope_frequencies")
+        raise MlaError(rc, name)
     return list(out)[:rotary_dim // 2]
 
 
 def mla_rope_plan(rotary_dim, base=10000.0, factor=1.0, original_len=0, fast=32.0, slow=1.0, interleaved=True,
-                  amplitude=1.0, frequencies=None) -> MlaRopePlan:
-    """The plan of a rotation: from base and scaling, or from the frequencies
-    themselves (rotary_dim / 2 of them)."""
+                  amplitude=1.0, frequencies=None, ramp="turns") -> MlaRopePlan:
+    """The plan of a rotation: from base and scaling (see mla_rope_frequencies;
+    the ramp has to be the one that the weights were trained with), or from the
+    frequencies themselves (rotary_dim / 2 of them)."""
     if frequencies is None:
-        frequencies = mla_rope_frequencies(rotary_dim, base, factor, original_len, fast, slow)
+        frequencies = mla_rope_frequencies(rotary_dim, base, factor, original_len, fast, slow, ramp)
     elif len(frequencies) != rotary_dim // 2:
         raise ValueError(f"rotary_dim {rotary_dim} needs {rotary_dim // 2} frequencies, got {len(frequencies)}")
     plan = MlaRopePlan()

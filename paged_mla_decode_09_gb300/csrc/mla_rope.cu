@@ -284,25 +284,55 @@ using mla::host::overlap;
 
 bool rotary_ok(int32_t r) { return r >= 16 && r <= 64 && r % 16 == 0; }
 
+constexpr double kTwoPi = 6.283185307179586476925;
+
+// What both frequency functions refuse.
+int frequencies_ok(int32_t rotary_dim, double base, double factor, int32_t original_len, double fast, double slow,
+                   const double* out) {
+  if (!out || !std::isfinite(base) || base < 1.0 || !std::isfinite(factor) || factor < 1.0 || original_len < 0)
+    return MLA_ERR_INVALID_ARG;
+  if (original_len > 0 && (!std::isfinite(fast) || !std::isfinite(slow) || fast <= slow)) return MLA_ERR_INVALID_ARG;
+  return rotary_ok(rotary_dim) ? MLA_OK : MLA_ERR_UNSUPPORTED;
+}
+
+// A frequency of which a share `keep`, limited to [0, 1], stays and the rest is divided by the factor.
+double scaled(double f, double factor, double keep) {
+  const double g = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+  return factor == 1.0 ? f : g * f + (1.0 - g) * f / factor;
+}
+
 }  // namespace
 
 extern "C" {
 
 int mla_rope_frequencies(int32_t rotary_dim, double base, double factor, int32_t original_len, double fast,
                          double slow, double* out) {
-  if (!out || !std::isfinite(base) || base < 1.0 || !std::isfinite(factor) || factor < 1.0 || original_len < 0)
-    return MLA_ERR_INVALID_ARG;
-  if (original_len > 0 && (!std::isfinite(fast) || !std::isfinite(slow) || fast <= slow)) return MLA_ERR_INVALID_ARG;
-  if (!rotary_ok(rotary_dim)) return MLA_ERR_UNSUPPORTED;
-  const double two_pi = 6.283185307179586476925;
+  const int rc = frequencies_ok(rotary_dim, base, factor, original_len, fast, slow, out);
+  if (rc != MLA_OK) return rc;
   for (int i = 0; i < rotary_dim / 2; ++i) {
     const double f = std::pow(base, -2.0 * i / rotary_dim);
-    double g = 0.0;
-    if (original_len > 0) {
-      g = (original_len * f / two_pi - slow) / (fast - slow);
-      g = g < 0.0 ? 0.0 : (g > 1.0 ? 1.0 : g);
-    }
-    out[i] = factor == 1.0 ? f : g * f + (1.0 - g) * f / factor;
+    out[i] = scaled(f, factor, original_len > 0 ? (original_len * f / kTwoPi - slow) / (fast - slow) : 0.0);
+  }
+  return MLA_OK;
+}
+
+int mla_rope_frequencies_by_index(int32_t rotary_dim, double base, double factor, int32_t original_len, double fast,
+                                  double slow, double* out) {
+  const int rc = frequencies_ok(rotary_dim, base, factor, original_len, fast, slow, out);
+  if (rc != MLA_OK) return rc;
+  double lo = 0.0, hi = 0.0;
+  if (original_len > 0) {
+    if (base <= 1.0 || slow <= 0.0) return MLA_ERR_INVALID_ARG;
+    auto index_of = [&](double turns) {
+      return rotary_dim * std::log(original_len / (kTwoPi * turns)) / (2.0 * std::log(base));
+    };
+    lo = std::fmax(std::floor(index_of(fast)), 0.0);
+    hi = std::fmin(std::ceil(index_of(slow)), rotary_dim - 1.0);
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double keep = 0.0;
+    if (original_len > 0) keep = hi > lo ? 1.0 - (i - lo) / (hi - lo) : (i <= lo ? 1.0 : 0.0);
+    out[i] = scaled(std::pow(base, -2.0 * i / rotary_dim), factor, keep);
   }
   return MLA_OK;
 }
@@ -311,12 +341,11 @@ int mla_rope_plan_init(int32_t rotary_dim, int32_t interleaved, float amplitude,
                        mla_rope_plan* plan) {
   if (!frequencies || !plan || !std::isfinite(amplitude) || amplitude <= 0.f) return MLA_ERR_INVALID_ARG;
   if (!rotary_ok(rotary_dim)) return MLA_ERR_UNSUPPORTED;
-  const double two_pi = 6.283185307179586476925;
   mla_rope_plan r = {};
   for (int i = 0; i < rotary_dim / 2; ++i) {
     const double f = frequencies[i];
-    if (!(f >= 0.0) || f >= two_pi) return MLA_ERR_INVALID_ARG;
-    const double t = f / two_pi;  // < 1; a quotient that rounds to 1 is no turn at all
+    if (!(f >= 0.0) || f >= kTwoPi) return MLA_ERR_INVALID_ARG;
+    const double t = f / kTwoPi;  // < 1; a quotient that rounds to 1 is no turn at all
     r.turn[i] = t < 1.0 ? static_cast<uint64_t>(t * 0x1p64) : 0;
   }
   r.rotary_dim = rotary_dim;

@@ -28,6 +28,56 @@ def test_frequencies(lib, dim, kw):
     assert got[0] == 1.0 if kw.get("factor", 1.0) == 1.0 or kw.get("original_len") else got[0] == 1.0 / kw["factor"]
 
 
+def test_frequencies_by_index_by_hand(lib):
+    """R = 64, base 10000, 4096 positions: index 10.5 turns 32 times and 22.5
+    once, so pairs up to 10 stay, pairs from 23 on are divided by 40."""
+    assert 10 < 32 * math.log(4096 / (2 * math.pi * 32)) / math.log(10000) < 11
+    assert 22 < 32 * math.log(4096 / (2 * math.pi)) / math.log(10000) < 23
+    f = [10000.0 ** (-i / 32) for i in range(32)]
+    got = mla.mla_rope_frequencies(64, factor=40.0, original_len=4096, ramp="index")
+    assert np.allclose(got[:11], f[:11], rtol=1e-14, atol=0) and np.allclose(got[23:], np.asarray(f[23:]) / 40, rtol=1e-14, atol=0)
+    for i in range(11, 23):
+        assert abs(got[i] / f[i] - ((23 - i) + (i - 10) / 40) / 13) < 1e-14
+    assert abs(got[16] / f[16] - 0.55) < 1e-14
+    # the ramp over turns is another one in just these twelve pairs
+    turns = mla.mla_rope_frequencies(64, factor=40.0, original_len=4096)
+    assert turns == mla.mla_rope_frequencies(64, factor=40.0, original_len=4096, ramp="turns")
+    assert [i for i in range(32) if abs(turns[i] / got[i] - 1) > 1e-12] == list(range(11, 23))
+    # without a length, or a factor, there is no ramp
+    assert mla.mla_rope_frequencies(64, factor=40.0, ramp="index") == mla.mla_rope_frequencies(64, factor=40.0)
+    assert mla.mla_rope_frequencies(64, original_len=4096, ramp="index") == mla.mla_rope_frequencies(64)
+    plan = mla.mla_rope_plan(64, factor=40.0, original_len=4096, ramp="index")
+    assert list(plan.turn) == list(mla.mla_rope_plan(64, frequencies=got).turn)
+
+
+@pytest.mark.parametrize("kw", [dict(factor=40.0, original_len=4096), dict(factor=4.0, original_len=32768, base=1e6),
+                                dict(factor=8.0, original_len=8192, fast=4.0, slow=0.5, base=1e6),
+                                dict(factor=2.0, original_len=3), dict(factor=2.0, original_len=2**31 - 1),
+                                dict(factor=2.0, original_len=2**31 - 1, base=2.0),
+                                dict(factor=3.0, original_len=1000, fast=1.01, slow=1.0)])
+@pytest.mark.parametrize("dim", [16, 32, 48, 64])
+def test_frequencies_by_index(lib, dim, kw):
+    got = mla.mla_rope_frequencies(dim, ramp="index", **kw)
+    assert np.allclose(got, oracle.rope_frequencies_by_index_ref(dim, **{"base": 10000.0, **kw}), rtol=1e-13, atol=0)
+    assert all(a >= b for a, b in zip(got, got[1:]))  # never faster than the pair before
+
+
+def test_frequencies_by_index_refusals(lib):
+    for kw in (dict(base=0.5), dict(base=float("nan")), dict(factor=0.9), dict(original_len=-1),
+               dict(original_len=10, fast=1.0, slow=1.0), dict(original_len=10, fast=float("nan")),
+               dict(original_len=10, slow=0.0), dict(original_len=10, slow=-1.0), dict(original_len=10, base=1.0)):
+        with pytest.raises((mla.MlaError, ValueError)):
+            mla.mla_rope_frequencies(64, **{"factor": 2.0, **kw}, ramp="index")
+    with pytest.raises(mla.MlaError):
+        mla.mla_rope_frequencies(40, ramp="index")
+    for ramp in ("linear", None, 1, []):
+        with pytest.raises(ValueError):
+            mla.mla_rope_frequencies(64, ramp=ramp)
+        with pytest.raises(ValueError):
+            mla.mla_rope_plan(64, ramp=ramp)
+    assert lib.mla_rope_frequencies_by_index(16, 10.0, 1.0, 0, 1.0, 1.0, None) == -1
+
+
 def test_plan_holds_turns(lib):
     plan = mla.mla_rope_plan(32, interleaved=False, amplitude=1.25)
     assert plan.rotary_dim == 32 and plan.interleaved == 0 and plan.amplitude == 1.25
