@@ -64,6 +64,8 @@ size_t mla_page_resize_workspace_size(int32_t batch, int32_t max_pages_per_req, 
  *   page_table_out, page_refs_out: int32; each may be its input itself (with the
  *               same stride), and must not overlap it otherwise
  *   workspace   256-byte aligned
+ * Outputs and workspace overlap nothing else (MLA_ERR_INVALID_ARG; a table is
+ * its rows' columns, what lies between them is free).
  * One kernel.
  */
 int mla_page_resize(const mla_page_resize_dims* d, const int32_t* new_lens, const int32_t* page_table,

@@ -26,6 +26,16 @@ inline bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return x < y + static_cast<uintptr_t>(bn) && y < x + static_cast<uintptr_t>(an);
 }
 
+// Whether `n` elements of 4 bytes at v share one with the rows of a table,
+// `cols` of them every `stride` elements (a vector may lie in a row's gap).
+inline bool overlap_rows(const void* table, int64_t rows, int64_t stride, int64_t cols, const void* v, int64_t n) {
+  if (!overlap(table, 4 * ((rows - 1) * stride + cols), v, 4 * n)) return false;
+  const intptr_t off = static_cast<intptr_t>(reinterpret_cast<uintptr_t>(v) - reinterpret_cast<uintptr_t>(table)) / 4;
+  if (off < 0) return true;  // begins before the table and reaches it
+  const int64_t c = off % stride;
+  return c < cols || c + n > stride;  // (behind the last row nothing is shared, see above)
+}
+
 inline int device_ok(int device) {
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, device) != cudaSuccess ||

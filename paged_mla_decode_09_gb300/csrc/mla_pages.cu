@@ -480,7 +480,7 @@ int current_device_ok() {
 }
 
 // Whether two int32 tables share an element, counted from first to last.
-bool overlap(const int32_t* a, int64_t an, const int32_t* b, int64_t bn) {
+bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
   return mla::host::overlap(a, 4 * an, b, 4 * bn);
 }
 int64_t extent(int64_t rows, int64_t stride, int64_t cols) { return (rows - 1) * stride + cols; }
@@ -565,8 +565,21 @@ int mla_page_resize(const mla_page_resize_dims* d, const int32_t* new_lens, cons
   if (!in_place && overlap(page_table, extent(B, d->table_stride, cols), page_table_out, extent(B, d->out_stride, cols)))
     return MLA_ERR_INVALID_ARG;
   if (page_refs != page_refs_out && overlap(page_refs, P, page_refs_out, P)) return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes < mla_page_resize_workspace_size(d->batch, d->max_pages_per_req, d->num_pages))
-    return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = mla_page_resize_workspace_size(d->batch, d->max_pages_per_req, d->num_pages);
+  {  // blocks read the inputs and what other blocks have written in every step
+    using mla::host::overlap_rows;
+    const int64_t words = static_cast<int64_t>(need / 4);
+    if (overlap_rows(page_table_out, B, d->out_stride, cols, new_lens, B) ||
+        overlap_rows(page_table_out, B, d->out_stride, cols, page_refs, P) ||
+        overlap_rows(page_table_out, B, d->out_stride, cols, page_refs_out, P) ||
+        overlap_rows(page_table, B, d->table_stride, cols, page_refs_out, P) ||
+        overlap(page_refs_out, P, new_lens, B) ||
+        overlap_rows(page_table_out, B, d->out_stride, cols, workspace, words) ||
+        overlap_rows(page_table, B, d->table_stride, cols, workspace, words) || overlap(workspace, words, page_refs, P) ||
+        overlap(workspace, words, page_refs_out, P) || overlap(workspace, words, new_lens, B))
+      return MLA_ERR_INVALID_ARG;
+  }
+  if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const int rc = current_device_ok();
   if (rc != MLA_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -63,6 +63,33 @@ def test_resize_refusals(lib):
     assert lib.mla_page_resize_workspace_size(200, 500, 100) == lib.mla_page_resize_workspace_size(200, 5000, 100)
 
 
+def test_resize_refuses_overlaps(lib):
+    """Each output and the workspace over each other buffer, from its first and
+    over its last element; a vector in the gaps of a table's rows is none."""
+    words = [2, 2 * 5, 16, 2 * 5, 16, 4 * 64]  # new_lens, table, counts, table_out, counts_out, workspace (256 B pieces)
+    assert lib.mla_page_resize_workspace_size(2, 5, 16) == 768
+    for out in (3, 4, 5):
+        for other in range(6):
+            if other == out or (out, other) in ((3, 1), (4, 2)):  # (in place)
+                continue
+            a = ptrs(6)
+            a[out] = a[other]
+            assert _resize(lib, a) == -1, (out, other)
+            if other != 5 and out != 5:
+                a[out] = ctypes.c_void_p(a[other].value + 4 * words[other] - 4)
+                assert _resize(lib, a) == -1, (out, other)
+                a[out] = ctypes.c_void_p(a[other].value + 4 * words[other])  # right behind it
+                assert _resize(lib, a, ws=256) == -4, (out, other)
+    a = ptrs(6)
+    a[5] = ctypes.c_void_p(a[1].value - 512)  # its third piece reaches into the table
+    assert _resize(lib, a) == -1
+    # rows of 5 entries, 9 apart: lengths in the gap, at its end, and one further
+    for at, rc in ((4, -1), (5, -4), (7, -4), (8, -1), (9, -1), (14, -4)):
+        a = ptrs(6)
+        a[0] = ctypes.c_void_p(a[3].value + 4 * at)
+        assert _resize(lib, a, ws=256, out_stride=9) == rc, at
+
+
 def test_fork_refusals(lib):
     for bad in (dict(sources=0), dict(children=0), dict(num_layers=0), dict(num_pages=0), dict(max_pages_per_req=0),
                 dict(table_stride=4), dict(out_stride=4), dict(num_layers=2, layer_stride=16 * 64 * 1152 - 16)):
