@@ -106,6 +106,8 @@ size_t mla_page_fork_workspace_size(int32_t sources, int32_t children, int32_t m
  *   page_table_out: int32 [children][out_stride]; the two tables must not
  *               overlap, counted from their first to their last element
  *   workspace   256-byte aligned
+ * Outputs and workspace overlap nothing else (as for mla_page_resize; no buffer
+ * lies in the caches, which is not looked at).
  * Two kernels.
  */
 int mla_page_fork(const mla_page_fork_dims* d, const int32_t* src, const int32_t* seq_lens, const int32_t* page_table,

@@ -28,6 +28,7 @@
 
 #include <climits>
 #include <cstdint>
+#include <initializer_list>
 #include <mutex>
 
 #include "mla_host.h"
@@ -485,6 +486,30 @@ bool overlap(const void* a, int64_t an, const void* b, int64_t bn) {
 }
 int64_t extent(int64_t rows, int64_t stride, int64_t cols) { return (rows - 1) * stride + cols; }
 
+struct Table {
+  const int32_t* at;
+  int64_t rows, stride;
+};
+struct Vec {
+  const int32_t* at;
+  int64_t n;
+};
+// Whether an output of a page call (table, counts) or its workspace shares
+// memory with another buffer; table over table and counts over counts apart,
+// which have rules of their own.  Blocks read all of them in every step.
+bool outputs_overlap(const Table& table, const Table& out, int64_t cols, const int32_t* refs, const int32_t* refs_out,
+                     int64_t pages, const void* workspace, size_t bytes, std::initializer_list<Vec> inputs) {
+  const int64_t words = static_cast<int64_t>(bytes / 4);
+  auto in_table = [&](const Table& t, const void* v, int64_t n) {
+    return mla::host::overlap_rows(t.at, t.rows, t.stride, cols, v, n);
+  };
+  for (const Vec& v : inputs)
+    if (in_table(out, v.at, v.n) || overlap(refs_out, pages, v.at, v.n) || overlap(workspace, words, v.at, v.n)) return true;
+  return in_table(out, refs, pages) || in_table(out, refs_out, pages) || in_table(table, refs_out, pages) ||
+         in_table(out, workspace, words) || in_table(table, workspace, words) ||
+         overlap(workspace, words, refs, pages) || overlap(workspace, words, refs_out, pages);
+}
+
 bool sizes_ok(int64_t rows, int64_t cols, int64_t pages) {
   return cols * 64 <= INT_MAX && rows * cols <= INT_MAX && pages <= 1 << 30;
 }
@@ -566,19 +591,9 @@ int mla_page_resize(const mla_page_resize_dims* d, const int32_t* new_lens, cons
     return MLA_ERR_INVALID_ARG;
   if (page_refs != page_refs_out && overlap(page_refs, P, page_refs_out, P)) return MLA_ERR_INVALID_ARG;
   const size_t need = mla_page_resize_workspace_size(d->batch, d->max_pages_per_req, d->num_pages);
-  {  // blocks read the inputs and what other blocks have written in every step
-    using mla::host::overlap_rows;
-    const int64_t words = static_cast<int64_t>(need / 4);
-    if (overlap_rows(page_table_out, B, d->out_stride, cols, new_lens, B) ||
-        overlap_rows(page_table_out, B, d->out_stride, cols, page_refs, P) ||
-        overlap_rows(page_table_out, B, d->out_stride, cols, page_refs_out, P) ||
-        overlap_rows(page_table, B, d->table_stride, cols, page_refs_out, P) ||
-        overlap(page_refs_out, P, new_lens, B) ||
-        overlap_rows(page_table_out, B, d->out_stride, cols, workspace, words) ||
-        overlap_rows(page_table, B, d->table_stride, cols, workspace, words) || overlap(workspace, words, page_refs, P) ||
-        overlap(workspace, words, page_refs_out, P) || overlap(workspace, words, new_lens, B))
-      return MLA_ERR_INVALID_ARG;
-  }
+  if (outputs_overlap({page_table, B, d->table_stride}, {page_table_out, B, d->out_stride}, cols, page_refs, page_refs_out,
+                      P, workspace, need, {{new_lens, B}}))
+    return MLA_ERR_INVALID_ARG;
   if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const int rc = current_device_ok();
   if (rc != MLA_OK) return rc;
@@ -630,8 +645,11 @@ int mla_page_fork(const mla_page_fork_dims* d, const int32_t* src, const int32_t
   if (overlap(page_table, extent(S, d->table_stride, cols), page_table_out, extent(B, d->out_stride, cols)))
     return MLA_ERR_INVALID_ARG;
   if (page_refs != page_refs_out && overlap(page_refs, P, page_refs_out, P)) return MLA_ERR_INVALID_ARG;
-  if (workspace_bytes < mla_page_fork_workspace_size(d->sources, d->children, d->max_pages_per_req, d->num_pages))
-    return MLA_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = mla_page_fork_workspace_size(d->sources, d->children, d->max_pages_per_req, d->num_pages);
+  if (outputs_overlap({page_table, S, d->table_stride}, {page_table_out, B, d->out_stride}, cols, page_refs, page_refs_out,
+                      P, workspace, need, {{src, B}, {seq_lens, S}}))
+    return MLA_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return MLA_ERR_WORKSPACE_TOO_SMALL;
   const int rc = current_device_ok();
   if (rc != MLA_OK) return rc;
   uint8_t* ws = static_cast<uint8_t*>(workspace);

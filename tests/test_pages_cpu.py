@@ -117,6 +117,32 @@ def test_fork_refusals(lib):
     assert lib.mla_page_fork_workspace_size(2, 0, 5, 16) == 0
 
 
+def test_fork_refuses_overlaps(lib):
+    """As for resize; 2 sources, 3 children, 5 columns, 16 pages."""
+    words = {0: 3, 1: 2, 2: 10, 3: 16, 5: 15, 6: 16, 7: 256}
+    assert lib.mla_page_fork_workspace_size(2, 3, 5, 16) == 1024
+    for out in (5, 6, 7):
+        for other in words:
+            if other == out or (out, other) == (6, 3):  # (in place)
+                continue
+            a = ptrs(8)
+            a[out] = a[other]
+            assert _fork(lib, a) == -1, (out, other)
+            if out == 7:
+                a[7] = ctypes.c_void_p(a[other].value - 768)  # its fourth piece reaches into the other
+                assert _fork(lib, a) == -1, other
+                continue
+            a[out] = ctypes.c_void_p(a[other].value + 4 * words[other] - 4)
+            assert _fork(lib, a) == -1, (out, other)
+            a[out] = ctypes.c_void_p(a[other].value + 4 * words[other])  # right behind it
+            assert _fork(lib, a, ws=256) == -4, (out, other)
+    # rows of 5 entries, 9 apart: sources in the gap, at its end, and one further
+    for at, rc in ((4, -1), (5, -4), (6, -4), (7, -1), (9, -1), (23, -4)):
+        a = ptrs(8)
+        a[0] = ctypes.c_void_p(a[5].value + 4 * at)
+        assert _fork(lib, a, ws=256, out_stride=9) == rc, at
+
+
 def test_binding_refuses_what_the_library_cannot_see(lib):
     torch = pytest.importorskip("torch")
     z = torch.zeros(4, dtype=torch.int32)
