@@ -93,8 +93,9 @@ typedef struct {
  *   cu_q_lens   int32 [B + 1], non-decreasing from >= 0
  *   path        int32 [B][path_cols]: nodes, ascending, in [0, n_b)
  *   num_path    int32 [B]; in [0, min(n_b, path_cols)]; 0 drops all nodes
- *   new_lens    int32 [B]; must not overlap seq_lens, cu_q_lens or num_path, which
- *               every block reads
+ *   new_lens    int32 [B]; like status, must not overlap the inputs, which every
+ *               block reads (MLA_ERR_INVALID_ARG; of a table's row what is behind
+ *               max_pages_per_req is free.  The cache is not looked at)
  *   status      int32 [1]; OR-ed in: MLA_DEV_BAD_SEQ_LEN, MLA_DEV_BAD_QUERY_RANGE,
  *               MLA_DEV_BAD_TREE (more than MLA_TREE_MAX_NODES nodes),
  *               MLA_DEV_BAD_INDEX (path or num_path): the request is left out

@@ -1057,7 +1057,7 @@ def mla_tree_commit(kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, n
 
     kv_cache: [num_pages, 64, 576], or one such cache per layer as
     [num_layers, num_pages, 64, 576]; path int32 [B, cols], num_path and
-    new_lens int32 [B] (new_lens not seq_lens itself); status int32 [1]."""
+    new_lens int32 [B] (new_lens and status apart from the inputs); status int32 [1]."""
     tensors = kv_cache, page_table, seq_lens, cu_q_lens, path, num_path, new_lens, status
     rc = _binding().tree_commit(*tensors, stream)
     if rc is None:

@@ -701,13 +701,19 @@ int mla_tree_commit(const mla_tree_commit_dims* d, void* kv_cache, const int32_t
       static_cast<int64_t>(d->num_pages) * 64 > INT_MAX)
     return MLA_ERR_UNSUPPORTED;
   if (d->num_layers > 1 && d->layer_stride < cache_bytes(d->num_pages, f8)) return MLA_ERR_INVALID_ARG;
+  // every layer's block of a request reads the inputs, the first one writes the outputs
+  const int64_t B = d->batch;
+  for (const Vec& out : {Vec{new_lens, B}, Vec{status, 1}}) {
+    for (const Vec& in : {Vec{seq_lens, B}, Vec{cu_q_lens, B + 1}, Vec{num_path, B}, Vec{path, B * d->path_cols}})
+      if (overlap(in.at, in.n, out.at, out.n)) return MLA_ERR_INVALID_ARG;
+    if (mla::host::overlap_rows(page_table, B, d->page_table_stride, d->max_pages_per_req, out.at, out.n))
+      return MLA_ERR_INVALID_ARG;
+  }
+  if (overlap(new_lens, B, status, 1)) return MLA_ERR_INVALID_ARG;
   if (!aligned(kv_cache, 16) || !aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q_lens, 4) ||
       !aligned(path, 4) || !aligned(num_path, 4) || !aligned(new_lens, 4) || !aligned(status, 4) ||
       (d->num_layers > 1 && d->layer_stride % 16 != 0))
     return MLA_ERR_ALIGNMENT;
-  if (overlap(seq_lens, d->batch, new_lens, d->batch) || overlap(num_path, d->batch, new_lens, d->batch) ||
-      overlap(cu_q_lens, d->batch + 1ll, new_lens, d->batch))
-    return MLA_ERR_INVALID_ARG;
   const int rc = current_device_ok();
   if (rc != MLA_OK) return rc;
   using namespace mla::pages;

@@ -91,6 +91,29 @@ def test_commit_refusals(lib):
     assert lib.mla_tree_commit(None, *good, None) == -1
 
 
+def test_commit_refuses_outputs_over_inputs(lib):
+    """New lengths and the status word over each buffer that every block reads,
+    from its first and over its last element; 2 requests, 4 path columns, 5 pages."""
+    # (the cache is off its alignment, which is looked at next: no call gets further)
+    good = [ctypes.c_void_p((1 << 20) + 8)] + [ctypes.c_void_p((k + 1) << 20) for k in range(1, 8)]
+    assert _commit(lib, good) == -3
+    words = {1: 2 * 5, 2: 2, 3: 3, 4: 2 * 4, 5: 2, 6: 2, 7: 1}
+    for out in (6, 7):
+        for other in words:
+            if other != out:
+                for at in (0, words[other] - 1):
+                    a = list(good)
+                    a[out] = ctypes.c_void_p(a[other].value + 4 * at)
+                    assert _commit(lib, a) == -1, (out, other, at)
+                a[out] = ctypes.c_void_p(a[other].value + 4 * words[other])  # right behind it
+                assert _commit(lib, a) == -3, (out, other)
+    # rows of 5 entries, 9 apart: in the gap, at its end, one further, behind the last row
+    for at, rc in ((4, -1), (5, -3), (7, -3), (8, -1), (9, -1), (14, -3)):
+        a = list(good)
+        a[6] = ctypes.c_void_p(a[1].value + 4 * at)
+        assert _commit(lib, a, page_table_stride=9) == rc, at
+
+
 V = [ctypes.c_void_p((k + 1) << 20) for k in range(11)]
 
 
