@@ -130,6 +130,11 @@ typedef struct {
  *               is not written (MLA_DEV_BAD_PAGE_ID)
  *   status      int32 [1] (device), OR-ed into; the caller clears it
  *
+ * q_out and status overlap neither one another nor rows, positions, page_table,
+ * seq_lens and cu_q_lens (MLA_ERR_INVALID_ARG; what lies between the rows of a
+ * strided buffer is free).  Rows of the cache that the call writes are not
+ * among its inputs (which is not looked at).
+ *
  * One kernel, asynchronous on `stream`; it can be captured into a CUDA graph.
  */
 int mla_rope_pack(const mla_rope_dims* d, const mla_rope_plan* plan, const void* q_pe, const void* rows,

@@ -281,6 +281,7 @@ namespace {
 
 using mla::host::aligned;
 using mla::host::overlap;
+using mla::host::overlap_rows;
 
 bool rotary_ok(int32_t r) { return r >= 16 && r <= 64 && r % 16 == 0; }
 
@@ -375,6 +376,21 @@ int mla_rope_pack(const mla_rope_dims* d, const mla_rope_plan* plan, const void*
   if (!std::isfinite(plan->amplitude) || plan->amplitude <= 0.f) return MLA_ERR_INVALID_ARG;
   const bool f8 = d->kv_dtype == MLA_KV_FP8_E4M3;
   if (f8 && !mla::e4m3::scale_ok(kv_scale)) return MLA_ERR_INVALID_ARG;
+  {  // blocks look up their tokens, and read their rows, after others have written
+    const int64_t B = d->batch, words = T * H * 32;  // of q_out
+    const struct {
+      const int32_t* at;
+      int64_t n;
+    } ins[] = {{positions, T}, {seq_lens, B}, {cu_q_lens, B + 1}};
+    for (const auto& in : ins)
+      if (in.at && (overlap(q_out, 4 * words, in.at, 4 * in.n) || overlap(status, 4, in.at, 4 * in.n)))
+        return MLA_ERR_INVALID_ARG;
+    if (overlap_rows(page_table, B, d->page_table_stride, d->max_pages_per_req, q_out, words) ||
+        overlap_rows(page_table, B, d->page_table_stride, d->max_pages_per_req, status, 1) ||
+        overlap_rows(rows, T, row / 2, 288, q_out, words) || overlap_rows(rows, T, row / 2, 288, status, 1) ||
+        overlap(q_out, 4 * words, status, 4))
+      return MLA_ERR_INVALID_ARG;
+  }
   if (!aligned(q_pe, 16) || !aligned(rows, 16) || !aligned(q_out, 16) || !aligned(kv_cache, 16) || q_head % 8 != 0 ||
       q_tok % 8 != 0 || row % 8 != 0 || !aligned(positions, 4) || !aligned(page_table, 4) || !aligned(seq_lens, 4) ||
       !aligned(cu_q_lens, 4) || !aligned(status, 4))

@@ -148,6 +148,35 @@ def test_pack_refusals(lib):
     assert _pack(lib, plan=plan) == -1
 
 
+def test_pack_refuses_outputs_over_inputs(lib):
+    """The rotated queries and the status word over what blocks read while others
+    write; 6 tokens, 16 heads, 2 requests, 5 pages.  (q_pe is off its alignment,
+    which is looked at next: no call gets further.)"""
+    good = [ctypes.c_void_p((k + 1) << 24) for k in range(9)]
+    good[0] = ctypes.c_void_p((1 << 24) + 8)
+    assert _pack(lib, good) == -3
+    words = {1: 6 * 288, 2: 6, 3: 2 * 5, 4: 2, 5: 3, 6: 6 * 16 * 32, 8: 1}
+    for out in (6, 8):
+        for other in words:
+            if other != out:
+                for at in (0, words[other] - 1):
+                    a = list(good)
+                    a[out] = ctypes.c_void_p(a[other].value + 4 * at)
+                    assert _pack(lib, a) == -1, (out, other, at)
+                a[out] = ctypes.c_void_p(a[other].value + 4 * words[other])  # right behind it
+                assert _pack(lib, a) == -3, (out, other)
+    # a status word between the rows, and between the table's
+    for k, wide, n in ((1, dict(row_stride=584), 288), (3, dict(page_table_stride=9), 5)):
+        for at, rc in ((n - 1, -1), (n, -3), (n + 3, -3), (n + 4, -1)):
+            a = list(good)
+            a[8] = ctypes.c_void_p(a[k].value + 4 * at)
+            assert _pack(lib, a, **wide) == rc, (k, at)
+    # without positions there is nothing to overlap
+    a = list(good)
+    a[2] = None
+    assert _pack(lib, a) == -3
+
+
 def test_binding_refuses_cpu_tensors(lib):
     torch = pytest.importorskip("torch")
     z = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
