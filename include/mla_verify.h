@@ -76,8 +76,8 @@ typedef struct {
  *               token, then -1
  *   num_out     int32 [B]: entries of both; 0 for a request without nodes
  *   status      int32 [1], OR-ed into; the caller clears it
- * The outputs overlap neither one another nor tokens .. sample
- * (MLA_ERR_INVALID_ARG).  Rows of target and draft that the walk does not come
+ * The outputs and status overlap neither one another nor the inputs
+ * (MLA_ERR_INVALID_ARG; what lies between the rows of target or draft is free).  Rows of target and draft that the walk does not come
  * to are read in single entries only, and may hold anything where no node is.
  */
 int mla_verify(const mla_verify_dims* d, const float* target, const float* draft, const int32_t* tokens,

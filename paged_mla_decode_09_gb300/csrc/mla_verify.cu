@@ -516,10 +516,6 @@ extern "C" int mla_verify(const mla_verify_dims* d, const float* target, const f
   if (d->batch > 1 << 27 || d->vocab > mla::verify::kMaxVocab || d->target_stride > (1ll << 40) ||
       (draft && d->draft_stride > (1ll << 40)))
     return MLA_ERR_UNSUPPORTED;
-  if (!aligned(target, 4) || !aligned(draft, 4) || !aligned(tokens, 4) || !aligned(parents, 4) ||
-      !aligned(cu_q_lens, 4) || !aligned(accept, 4) || !aligned(sample, 4) || !aligned(path, 4) ||
-      !aligned(tokens_out, 4) || !aligned(num_out, 4) || !aligned(status, 4))
-    return MLA_ERR_ALIGNMENT;
   // every block of a request reads its inputs, one writes the outputs
   {
     const int64_t T = d->total_q, B = d->batch, cells = B * d->path_cols;
@@ -533,8 +529,16 @@ extern "C" int mla_verify(const mla_verify_dims* d, const float* target, const f
         if (mla::host::overlap(outs[i].at, outs[i].bytes, outs[j].at, outs[j].bytes)) return MLA_ERR_INVALID_ARG;
       for (const auto& in : ins)
         if (mla::host::overlap(outs[i].at, outs[i].bytes, in.at, in.bytes)) return MLA_ERR_INVALID_ARG;
+      const int64_t words = outs[i].bytes / 4;
+      if (mla::host::overlap_rows(target, T, d->target_stride, d->vocab, outs[i].at, words) ||
+          (draft && mla::host::overlap_rows(draft, T, d->draft_stride, d->vocab, outs[i].at, words)))
+        return MLA_ERR_INVALID_ARG;
     }
   }
+  if (!aligned(target, 4) || !aligned(draft, 4) || !aligned(tokens, 4) || !aligned(parents, 4) ||
+      !aligned(cu_q_lens, 4) || !aligned(accept, 4) || !aligned(sample, 4) || !aligned(path, 4) ||
+      !aligned(tokens_out, 4) || !aligned(num_out, 4) || !aligned(status, 4))
+    return MLA_ERR_ALIGNMENT;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();

@@ -147,6 +147,24 @@ def test_verify_refusals(lib):
             assert _verify(lib, but(out, V[other])) == -1, (out, other)
 
 
+def test_verify_refuses_outputs_over_probabilities(lib):
+    """6 rows of 100 entries, 104 apart.  (tokens is off its alignment, which is
+    looked at next: no call gets further.)"""
+    good = V[:2] + [ctypes.c_void_p(V[2].value + 2)] + V[3:]
+    wide = dict(target_stride=104, draft_stride=104)
+    assert _verify(lib, good, **wide) == -3
+    for out, n in ((7, 8), (8, 8), (9, 2), (10, 1)):
+        for rows in (0, 1):
+            for at, rc in ((0, -1), (100 - n, -1), (99, -1), (5 * 104 + 99, -1), (5 * 104 + 100, -3),
+                           (100, -3 if n <= 4 else -1), (104 - n, -3 if n <= 4 else -1), (105 - n, -1)):
+                a = list(good)
+                a[out] = ctypes.c_void_p(a[rows].value + 4 * at)
+                assert _verify(lib, a, **wide) == rc, (out, rows, at)
+    a = list(good)  # no draft: its place is free
+    a[1], a[7] = None, V[1]
+    assert _verify(lib, a, **wide) == -3
+
+
 def test_binding_refuses_what_the_library_cannot_see(lib):
     torch = pytest.importorskip("torch")
     z = torch.zeros
