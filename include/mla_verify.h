@@ -68,8 +68,8 @@ typedef struct {
  *               nodes a request (else MLA_DEV_BAD_QUERY_RANGE, MLA_DEV_BAD_TREE: the
  *               request is treated as one without nodes)
  *   accept      fp32 [total_q]: a random number in [0, 1) per node
- *   sample      fp32 [B]: a random number in [0, 1) per request (others are taken
- *               as the nearest of these, a NaN as 0)
+ *   sample      fp32 [B]: a random number in [0, 1) per request (in both, others
+ *               are taken as the nearest of these, a NaN as 0)
  *   path        int32 [B][path_cols]: node 0 and the accepted nodes, then -1: what
  *               mla_tree_commit takes.  The walk ends where the row is full
  *   tokens_out  int32 [B][path_cols]: the accepted nodes' tokens and the last

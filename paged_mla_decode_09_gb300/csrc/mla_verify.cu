@@ -61,6 +61,9 @@ struct Params {
   int32_t t_vec, d_vec;  // rows are 16-byte aligned
 };
 
+// The number of [0, 1) nearest to a random number (NaN: 0).
+__device__ __forceinline__ float unit(float u) { return fminf(fmaxf(u, 0.f), 0x1.fffffep-1f); }
+
 // A value of [0, 1] in units of 2^-60, as h 2^38 + m 2^18 + l: adding a constant
 // whose last place is 2^-22, 2^-42 or 2^-60 rounds to that place, and leaves the
 // rounded value's integer in the sum's low bits; what was rounded off is exact.
@@ -281,7 +284,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     s.par[tid] = par;
     s.tok[tid] = tok;
     if (par >= 0) {
-      s.acc[tid] = p.accept[q0 + tid];
+      s.acc[tid] = unit(p.accept[q0 + tid]);
       s.wp[tid] = p.target[(q0 + par) * p.t_stride + tok];
       if (kDraft) s.wq[tid] = p.draft[(q0 + par) * p.d_stride + tok];
     }
@@ -439,7 +442,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 4)
     return;
   }
   if (sum == 0) return;
-  const float u = fminf(fmaxf(p.sample[b], 0.f), 0x1.fffffep-1f);
+  const float u = unit(p.sample[b]);
   uint64_t at = mul60(fixed60(u), sum);  // below sum
   const int last_pass = (pass - 1) & 1;
   bool here = true;

@@ -151,6 +151,35 @@ def test_random_numbers_at_their_ends():
     assert all(np.array_equal(x, y) for x, y in zip(got[:3], want[:3])) and got[3] == 0
 
 
+@pytest.mark.parametrize("drafted", [True, False])
+@pytest.mark.parametrize("kind", ["chain", "star"])
+def test_acceptance_numbers_outside_their_range(kind, drafted):
+    """Taken as the nearest inside, a NaN as 0, at a node's first child and at
+    later ones; above all a token that the target gives nothing is not accepted."""
+    c = make([6] * 40, 50, drafted, kind, seed=14, noise=2.0)
+    rng = np.random.default_rng(15)
+    odd = np.asarray([-1.0, -np.inf, np.nan, 1.0, 7.0, np.inf, -0.0, -1e-30], np.float32)
+    inside = np.asarray([0, 0, 0, *[np.nextafter(np.float32(1), np.float32(0))] * 3, 0, 0], np.float32)
+    pick = rng.integers(0, 8, len(c["accept"]))
+    c["target"][np.arange(1, 240), c["tokens"][1:]] = 0.0  # some rows lose a token's weight
+    c["target"][0::2, :25] = 0.0
+    clean = dict(c, accept=inside[pick])
+    want = oracle.verify_ref(clean["target"], clean["draft"], clean["tokens"], clean["parents"], clean["cu"],
+                             clean["accept"], clean["sample"], 6)
+    path, out, num, status = Run(dict(c, accept=odd[pick]), 6).launch().result()
+    assert status == 0
+    assert np.array_equal(path, want[0]) and np.array_equal(num, want[2]) and np.array_equal(out, want[1])
+    # one request whose draft has no weight at all: rejected whatever its number
+    p = np.zeros((2, 8), np.float32)
+    p[:, 3] = 1.0
+    q = np.full((2, 8), 0.125, np.float32)
+    one = dict(target=p, draft=q if drafted else None, tokens=np.array([0, 5], np.int32),
+               parents=np.array([-1, 0], np.int32), cu=np.array([0, 2], np.int32), sample=np.array([0.5], np.float32))
+    for u in odd:
+        path, out, num, status = Run(dict(one, accept=np.asarray([0, u], np.float32)), 2).launch().result()
+        assert status == 0 and num.tolist() == [1] and out.tolist() == [[3, -1]], u
+
+
 def test_odd_values_in_rows():
     """NaN and negative entries count as nothing, entries above 1 as 1; a row
     with nothing in it raises a flag."""
