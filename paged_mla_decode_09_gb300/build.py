@@ -10,7 +10,7 @@ windows), ``csrc/mla_mass.cu`` (attention mass), ``csrc/mla_evict.cu``
 ``csrc/mla_rope.cu`` (rotary cache write) with nvcc into
 ``libmla_decode.so`` next to this file.  One ``-gencode``, the files in
 parallel; a few seconds.  Beside it g++ compiles ``csrc/binding.cpp``, the
-Python binding's fast path, into ``_binding.so``.
+Python binding's fast path, into ``_binding.so``, where torch is installed.
 """
 from __future__ import annotations
 
@@ -33,11 +33,8 @@ SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "mla_kv_pack.cu", "m
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
-def depends():
-    files = [*SOURCES, BINDING_SOURCE]
-    for d in (CSRC, INCLUDE):
-        files += [os.path.join(d, f) for f in os.listdir(d) if f.endswith((".cuh", ".h"))]
-    return files
+def _headers():
+    return [os.path.join(d, f) for d in (CSRC, INCLUDE) for f in os.listdir(d) if f.endswith((".cuh", ".h"))]
 
 
 def nvcc_path() -> str:
@@ -47,69 +44,102 @@ def nvcc_path() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is needed to build the library")
 
 
-def up_to_date() -> bool:
-    if not (os.path.exists(LIB_PATH) and os.path.exists(BINDING_PATH)):
+def _newer(path: str, sources) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(p) <= os.path.getmtime(path) for p in sources)
+
+
+def _have_torch() -> bool:
+    try:
+        import torch  # noqa: F401
+    except ImportError:
         return False
-    t = min(os.path.getmtime(LIB_PATH), os.path.getmtime(BINDING_PATH))
-    return all(os.path.getmtime(p) <= t for p in depends())
+    return True
 
 
-def _failed(what, cmd, out):
-    return RuntimeError(f"{what} failed:\n" + " ".join(cmd) + "\n" + out)
+def up_to_date() -> bool:
+    """The library and, where there is a torch to load it, the binding."""
+    return _newer(LIB_PATH, [*SOURCES, *_headers()]) and (_binding_up_to_date() or not _have_torch())
 
 
-def _compile_binding(obj: str):
-    """g++ on the binding's source, started; returns (process, command)."""
-    import sysconfig
-
-    import torch
-
-    inc = os.path.join(os.path.dirname(torch.__file__), "include")
-    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
-    cmd = ["g++", "-c", "-O2", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
-           "-I", inc, "-I", sysconfig.get_paths()["include"], "-I", cuda, "-I", INCLUDE, BINDING_SOURCE, "-o", obj]
-    return subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True), cmd
+def _binding_up_to_date() -> bool:
+    return _newer(BINDING_PATH, [BINDING_SOURCE, *_headers()])
 
 
-def _link_binding(obj: str, tmp: str):
-    import torch
-
-    cmd = ["g++", "-shared", obj, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
-           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
+def _run(what, cmd):
+    try:
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:
+        raise RuntimeError(f"{what} failed: {e}") from e
     if res.returncode != 0:
-        raise _failed("linking the binding", cmd, res.stdout + res.stderr)
-    os.replace(tmp, BINDING_PATH)
+        raise RuntimeError(f"{what} failed:\n" + " ".join(cmd) + "\n" + res.stdout + res.stderr)
+    return res.stdout + res.stderr
 
 
-def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compile the shared library and the binding in place; returns the library's path."""
-    if not force and up_to_date():
-        return LIB_PATH
+def _build_library(verbose: bool) -> None:
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    obj = BINDING_PATH + f".tmp{os.getpid()}.o"
     cmd = [
         nvcc_path(), "-shared", "-Xcompiler", "-fPIC", *ARCH_FLAGS, "-O3", "-lineinfo", "-std=c++17",
         "-I", INCLUDE, "-I", CSRC, "-cudart", "shared", "--threads", "0", "-o", tmp, *SOURCES,
     ]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
-    binding, binding_cmd = _compile_binding(obj)
     try:
-        res = subprocess.run(cmd, capture_output=True, text=True)
-        out, _ = binding.communicate()
-        if res.returncode != 0:
-            raise _failed("nvcc", cmd, res.stdout + res.stderr)
+        out = _run("nvcc", cmd)
         if verbose:
-            sys.stderr.write(res.stdout + res.stderr)
-        if binding.returncode != 0:
-            raise _failed("compiling the binding", binding_cmd, out)
+            sys.stderr.write(out)
         os.replace(tmp, LIB_PATH)
-        _link_binding(obj, BINDING_PATH + f".tmp{os.getpid()}")
     finally:
-        for f in (tmp, obj):
-            if os.path.exists(f):
-                os.remove(f)
+        if os.path.exists(tmp):
+            os.remove(tmp)
+
+
+def _compile_binding(obj: str) -> None:
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc_path())), "include")
+    _run("compiling the binding",
+         ["g++", "-c", "-O2", "-fPIC", "-std=c++17", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", inc, "-I", sysconfig.get_paths()["include"], "-I", cuda, "-I", INCLUDE, BINDING_SOURCE, "-o", obj])
+
+
+def _link_binding(obj: str, tmp: str) -> None:
+    import torch
+
+    _run("linking the binding",
+         ["g++", "-shared", obj, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
+          "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING_PATH)
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compile the shared library and the binding in place; returns the
+    library's path.  The library needs nvcc alone and is there whatever becomes
+    of the binding, which needs torch and its headers: without torch it is left
+    out, and an error in it is raised once the library is in place."""
+    if not force and up_to_date():
+        return LIB_PATH
+    from concurrent.futures import ThreadPoolExecutor
+
+    obj, tmp = (BINDING_PATH + f".tmp{os.getpid()}" + end for end in (".o", ""))
+    with ThreadPoolExecutor(1) as beside:
+        binding = beside.submit(_compile_binding, obj) if _have_torch() else None
+        try:
+            if force or not _newer(LIB_PATH, [*SOURCES, *_headers()]):
+                _build_library(verbose)
+            if binding is None:
+                sys.stderr.write("torch is not importable: the library is built, its Python binding is not\n")
+            else:
+                binding.result()
+                _link_binding(obj, tmp)
+        finally:
+            if binding is not None:
+                binding.exception()  # (ends before its output is removed)
+            for f in (obj, tmp):
+                if os.path.exists(f):
+                    os.remove(f)
     return LIB_PATH
 
 

@@ -1,0 +1,84 @@
+"""The in-tree build without a GPU: what of the library and the binding is there
+when one of the two cannot be built.  (Compilers are stand-ins that write a
+file, in a folder of the test's.)"""
+import os
+import subprocess
+import sys
+
+import pytest
+
+from paged_mla_decode_09_gb300 import build
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def tool(path, body):
+    path.write_text("#!/bin/sh\n" + body)
+    path.chmod(0o755)
+    return str(path)
+
+
+WRITES = 'while [ "$1" != -o ]; do shift; done; echo built > "$2"\n'
+
+
+@pytest.fixture
+def tree(tmp_path, monkeypatch):
+    """build.py with outputs in tmp_path, an nvcc that works, and the given g++."""
+    (tmp_path / "bin").mkdir()
+    monkeypatch.setenv("NVCC", tool(tmp_path / "bin" / "nvcc", WRITES))
+    monkeypatch.setenv("PATH", f"{tmp_path}/bin:/usr/bin:/bin")
+    monkeypatch.setattr(build, "LIB_PATH", str(tmp_path / "libmla_decode.so"))
+    monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "_binding.so"))
+    tool(tmp_path / "bin" / "g++", WRITES)
+    return tmp_path
+
+
+def left(tree):
+    return sorted(f for f in os.listdir(tree) if f != "bin")
+
+
+def test_both(tree):
+    pytest.importorskip("torch")
+    assert not build.up_to_date()
+    assert build.build_library() == build.LIB_PATH
+    assert left(tree) == ["_binding.so", "libmla_decode.so"] and build.up_to_date()
+
+
+@pytest.mark.parametrize("gxx", ["echo no such header; exit 1\n", None])
+def test_a_binding_that_does_not_compile_leaves_the_library(tree, monkeypatch, gxx):
+    pytest.importorskip("torch")
+    if gxx is None:
+        os.remove(tree / "bin" / "g++")
+        monkeypatch.setenv("PATH", f"{tree}/bin")
+    else:
+        tool(tree / "bin" / "g++", gxx)
+    with pytest.raises(RuntimeError, match="binding"):
+        build.build_library()
+    assert left(tree) == ["libmla_decode.so"]
+    before = os.stat(build.LIB_PATH).st_mtime_ns
+    tool(tree / "bin" / "g++", WRITES)  # mended: the library is not built again
+    monkeypatch.setenv("PATH", f"{tree}/bin:/usr/bin:/bin")
+    build.build_library()
+    assert left(tree) == ["_binding.so", "libmla_decode.so"] and os.stat(build.LIB_PATH).st_mtime_ns == before
+
+
+def test_a_library_that_does_not_compile_leaves_nothing(tree):
+    tool(tree / "bin" / "nvcc", "echo no; exit 2\n")
+    with pytest.raises(RuntimeError, match="nvcc"):
+        build.build_library()
+    assert left(tree) == []
+
+
+def test_without_torch_there_is_the_library(tree):
+    code = f"""
+import sys
+sys.path.insert(0, {ROOT!r})
+sys.modules["torch"] = None  # an import raises
+from paged_mla_decode_09_gb300 import build
+build.LIB_PATH, build.BINDING_PATH = {build.LIB_PATH!r}, {build.BINDING_PATH!r}
+assert not build.up_to_date()
+assert build.build_library() == build.LIB_PATH and build.up_to_date()
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    assert "binding is not" in r.stderr and left(tree) == ["libmla_decode.so"]
