@@ -15,7 +15,7 @@ import ctypes
 import os
 from dataclasses import dataclass
 
-from .build import BINDING_PATH, LIB_PATH, build_library
+from .build import LIB_PATH, binding_path, build_library
 
 MLA_OK = 0
 MLA_KV_BF16 = 0
@@ -319,9 +319,11 @@ def _binding():
         import torch  # noqa: F401  (its libraries are loaded first)
 
         load_library()
-        if not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"{BINDING_PATH} is missing: build it with __graft_entry__.build()")
-        loader = importlib.machinery.ExtensionFileLoader("_binding", BINDING_PATH)
+        path = binding_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"{path}, the binding for this Python and torch, is missing: build it with "
+                               "__graft_entry__.build()")
+        loader = importlib.machinery.ExtensionFileLoader("_binding", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_binding", loader))
         loader.exec_module(module)
         _fast = module

@@ -10,7 +10,8 @@ windows), ``csrc/mla_mass.cu`` (attention mass), ``csrc/mla_evict.cu``
 ``csrc/mla_rope.cu`` (rotary cache write) with nvcc into
 ``libmla_decode.so`` next to this file.  One ``-gencode``, the files in
 parallel; a few seconds.  Beside it g++ compiles ``csrc/binding.cpp``, the
-Python binding's fast path, into ``_binding.so``, where torch is installed.
+Python binding's fast path, where torch is installed: into ``_binding.*.so``,
+whose name holds the versions that it fits.
 """
 from __future__ import annotations
 
@@ -26,7 +27,6 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB_NAME = "libmla_decode.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 BINDING_SOURCE = os.path.join(CSRC, "binding.cpp")
-BINDING_PATH = os.path.join(PKG, "_binding.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("mla_decode.cu", "mla_kv_pack.cu", "mla_sparse.cu", "mla_cascade.cu",
                                                "mla_chunk.cu", "mla_mass.cu", "mla_evict.cu", "mla_tree.cu", "mla_verify.cu",
                                                "mla_pages.cu", "mla_rope.cu")]
@@ -58,11 +58,23 @@ def _have_torch() -> bool:
 
 def up_to_date() -> bool:
     """The library and, where there is a torch to load it, the binding."""
-    return _newer(LIB_PATH, [*SOURCES, *_headers()]) and (_binding_up_to_date() or not _have_torch())
+    return _newer(LIB_PATH, [*SOURCES, *_headers()]) and (not _have_torch() or _binding_up_to_date())
+
+
+def binding_path() -> str:
+    """Where the binding for this interpreter and this torch is.  It reads
+    their objects' layouts, which differ between releases, so the name holds
+    both: a module built for others is not this one."""
+    import sysconfig
+
+    import torch
+
+    cxx11 = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(PKG, f"_binding.torch-{torch.__version__}-abi{cxx11}{sysconfig.get_config_var('EXT_SUFFIX')}")
 
 
 def _binding_up_to_date() -> bool:
-    return _newer(BINDING_PATH, [BINDING_SOURCE, *_headers()])
+    return _newer(binding_path(), [BINDING_SOURCE, *_headers()])
 
 
 def _run(what, cmd):
@@ -111,7 +123,7 @@ def _link_binding(obj: str, tmp: str) -> None:
     _run("linking the binding",
          ["g++", "-shared", obj, "-o", tmp, "-L", os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python",
           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L", PKG, f"-l:{LIB_NAME}", "-Wl,-rpath,$ORIGIN"])
-    os.replace(tmp, BINDING_PATH)
+    os.replace(tmp, binding_path())
 
 
 def build_library(force: bool = False, verbose: bool = False) -> str:
@@ -123,7 +135,7 @@ def build_library(force: bool = False, verbose: bool = False) -> str:
         return LIB_PATH
     from concurrent.futures import ThreadPoolExecutor
 
-    obj, tmp = (BINDING_PATH + f".tmp{os.getpid()}" + end for end in (".o", ""))
+    obj, tmp = (os.path.join(PKG, f"_binding.tmp{os.getpid()}{end}") for end in (".o", ".so"))
     with ThreadPoolExecutor(1) as beside:
         binding = beside.submit(_compile_binding, obj) if _have_torch() else None
         try:

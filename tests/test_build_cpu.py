@@ -28,7 +28,7 @@ def tree(tmp_path, monkeypatch):
     monkeypatch.setenv("NVCC", tool(tmp_path / "bin" / "nvcc", WRITES))
     monkeypatch.setenv("PATH", f"{tmp_path}/bin:/usr/bin:/bin")
     monkeypatch.setattr(build, "LIB_PATH", str(tmp_path / "libmla_decode.so"))
-    monkeypatch.setattr(build, "BINDING_PATH", str(tmp_path / "_binding.so"))
+    monkeypatch.setattr(build, "binding_path", lambda: str(tmp_path / "_binding.so"))
     tool(tmp_path / "bin" / "g++", WRITES)
     return tmp_path
 
@@ -75,10 +75,35 @@ import sys
 sys.path.insert(0, {ROOT!r})
 sys.modules["torch"] = None  # an import raises
 from paged_mla_decode_09_gb300 import build
-build.LIB_PATH, build.BINDING_PATH = {build.LIB_PATH!r}, {build.BINDING_PATH!r}
+build.LIB_PATH = {build.LIB_PATH!r}
 assert not build.up_to_date()
 assert build.build_library() == build.LIB_PATH and build.up_to_date()
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
     assert "binding is not" in r.stderr and left(tree) == ["libmla_decode.so"]
+
+
+def test_a_binding_of_another_torch_or_python_is_another_file(monkeypatch):
+    """It would read tensors by the wrong layout: it is neither up to date nor loaded."""
+    import sysconfig
+
+    torch = pytest.importorskip("torch")
+    import paged_mla_decode_09_gb300 as mla
+
+    build.build_library()
+    here = build.binding_path()
+    assert os.path.exists(here) and build.up_to_date()
+    monkeypatch.setattr(mla, "_fast", None)
+    assert mla._binding() is mla._binding()
+    suffix = sysconfig.get_config_var("EXT_SUFFIX")
+    real = sysconfig.get_config_var
+    for patch in ((torch, "__version__", "9.9.9+cu999"), (torch._C, "_GLIBCXX_USE_CXX11_ABI", not torch._C._GLIBCXX_USE_CXX11_ABI),
+                  (sysconfig, "get_config_var", lambda k: suffix.replace("cpython-3", "cpython-9") if k == "EXT_SUFFIX" else real(k))):
+        with monkeypatch.context() as m:
+            m.setattr(*patch)
+            m.setattr(mla, "_fast", None)
+            assert build.binding_path() != here and not build.up_to_date()
+            with pytest.raises(RuntimeError, match="missing"):
+                mla._binding()
+    assert build.binding_path() == here and build.up_to_date()
