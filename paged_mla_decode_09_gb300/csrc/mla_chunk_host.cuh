@@ -205,7 +205,7 @@ int run_chunk(const Shape& s, int page_size, int kv_dtype, const void* q_nope, c
   if ((rc = clusters_of<kTree>(dev, s.f8, cg, &C)) != MLA_OK) return rc;
   const Layout lay = layout_of<kTree>(s, C);
   if (ws_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
-  if (!encode_fn()) return MLA_ERR_CUDA;
+  if (!encode_fn() || !mla::host::bind_context(dev)) return MLA_ERR_CUDA;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   Params p;
   p.q_nope = static_cast<const uint8_t*>(q_nope);

@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "mla_decode.h"
+#include "mla_host.h"
 #include "mla_internal.h"
 #include "mla_kernels.cuh"
 
@@ -326,6 +327,7 @@ int decode_impl(const mla_dims* d, const void* q_nope, const void* q_pe, const v
   }
   const Layout lay = workspace_layout(d->batch, C, G, terms);
   if (ws_bytes < lay.total) return MLA_ERR_WORKSPACE_TOO_SMALL;
+  if (!mla::host::bind_context(dev)) return MLA_ERR_CUDA;
   Maps maps;
   if ((rc = make_maps(kv_cache, d->num_pages, f8, &maps)) != MLA_OK) return rc;
   if ((rc = make_qmaps(q_nope, q_pe, terms ? ws + lay.qterms : nullptr, static_cast<int64_t>(d->batch) * R, &maps)) !=
@@ -539,6 +541,7 @@ int mla_gather_rows(const mla_dims* d, const void* kv_cache, const int32_t* page
   if ((rc = current_device(&dev)) != MLA_OK) return rc;
   if ((rc = device_ok(dev)) != MLA_OK) return rc;
   const bool f8 = d->kv_dtype == MLA_KV_FP8_E4M3;
+  if (!mla::host::bind_context(dev)) return MLA_ERR_CUDA;
   Maps maps;
   if ((rc = make_maps(kv_cache, d->num_pages, f8, &maps)) != MLA_OK) return rc;
   mla::GatherParams gp;

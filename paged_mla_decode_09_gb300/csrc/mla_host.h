@@ -59,6 +59,27 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+// Makes a context current for this thread where none is, as in a thread whose
+// first call of CUDA this is: the runtime would at a launch, but tensor maps
+// are encoded before that, and by the driver, which asks for one.  A context
+// that the caller has made current stays.
+inline bool bind_context(int device) {
+  static PFN_cuCtxGetCurrent_v4000 get = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuCtxGetCurrent", &f, 4000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      get = reinterpret_cast<PFN_cuCtxGetCurrent_v4000>(f);
+  });
+  CUcontext ctx = nullptr;
+  if (get && get(&ctx) == CUDA_SUCCESS && ctx) return true;
+  if (cudaSetDevice(device) == cudaSuccess) return true;
+  cudaGetLastError();
+  return false;
+}
+
 // A 3-D map over rows of `row_bytes`: (128 bytes of a row, rows, 128-byte
 // columns), read in boxes of 128 bytes x box_rows x box_cols that land as
 // [column][row][128 bytes] with the 128-byte swizzle.

@@ -988,7 +988,7 @@ int mla_attn_mass(const mla_dims* d, const void* q_nope, const void* q_pe, const
   }
   if ((rc = device_ok(dev)) != MLA_OK) return rc;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return MLA_ERR_CUDA;
-  if (!encode_fn()) return MLA_ERR_CUDA;
+  if (!encode_fn() || !mla::host::bind_context(dev)) return MLA_ERR_CUDA;
   const int64_t R = static_cast<int64_t>(d->num_heads) * d->q_len;
   const int64_t krows = static_cast<int64_t>(d->num_pages) * 64, qrows = d->batch * R;
   // more than 128 rows per request: the keys stay and the rows stream (64 at
