@@ -149,6 +149,18 @@ struct Call {
   }
 };
 
+// The C call, with the interpreter's lock given up meanwhile: a launch waits
+// where the stream's queue is full, and what it waits for may need the lock (a
+// callback, another thread).  The caller's arguments keep the tensors alive.
+template <typename F>
+int unlocked(F call) {
+  struct Released {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Released() { PyEval_RestoreThread(state); }
+  } released;
+  return call();
+}
+
 template <typename F>
 PyObject* guarded(F f) {
   try {
@@ -183,7 +195,9 @@ PyObject* decode_tree(PyObject*, PyObject* const* args, Py_ssize_t n) {
     const mla_prefill_dims d = {c.i32(B),    c.i32(H),      c.i32(T),      c.i32(kv.page_size), c.i32(kv.pages),
                                 c.i32(cols), c.i32(stride), kv.dtype};
     if (!c.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(mla_decode_tree(&d, qn, qp, kv.at, table, lens, cu, parents, scale, kv_scale, out, lse, ws, bytes, s));
+    return PyLong_FromLong(unlocked([&] {
+      return mla_decode_tree(&d, qn, qp, kv.at, table, lens, cu, parents, scale, kv_scale, out, lse, ws, bytes, s);
+    }));
   });
 }
 
@@ -208,7 +222,8 @@ PyObject* tree_commit(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                     c.i32(cols), c.i32(stride),    kv.dtype,         0,
                                     kv.step};
     if (!c.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(mla_tree_commit(&d, kv.at, table, lens, cu, path, num, new_lens, status, s));
+    return PyLong_FromLong(
+        unlocked([&] { return mla_tree_commit(&d, kv.at, table, lens, cu, path, num, new_lens, status, s); }));
   });
 }
 
@@ -245,8 +260,9 @@ PyObject* verify(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* s = c.stream(11);
     const mla_verify_dims d = {c.i32(B), c.i32(T), c.i32(V), c.i32(cols), ts, ds};
     if (!c.ok) Py_RETURN_NONE;
-    return PyLong_FromLong(
-        mla_verify(&d, target, draft, tokens, parents, cu, accept, sample, path, out, num, status, s));
+    return PyLong_FromLong(unlocked([&] {
+      return mla_verify(&d, target, draft, tokens, parents, cu, accept, sample, path, out, num, status, s);
+    }));
   });
 }
 
@@ -266,7 +282,8 @@ PyObject* page_resize(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* s = c.stream(6);
     const mla_page_resize_dims d = {c.i32(B), c.i32(P), c.i32(cols), c.i32(stride), c.i32(out_stride)};
     if (!c.ok || cols != out_cols) Py_RETURN_NONE;
-    return PyLong_FromLong(mla_page_resize(&d, lens, table, refs, table_out, refs_out, ws, bytes, s));
+    return PyLong_FromLong(
+        unlocked([&] { return mla_page_resize(&d, lens, table, refs, table_out, refs_out, ws, bytes, s); }));
   });
 }
 
@@ -290,7 +307,9 @@ PyObject* page_fork(PyObject*, PyObject* const* args, Py_ssize_t n) {
                                   c.i32(cols), c.i32(stride), c.i32(out_stride), kv.dtype,
                                   kv.step};
     if (!c.ok || cols != out_cols || kv.page_size != 64) Py_RETURN_NONE;
-    return PyLong_FromLong(mla_page_fork(&d, src, lens, table, refs, kv.at, table_out, refs_out, ws, bytes, s));
+    return PyLong_FromLong(unlocked([&] {
+      return mla_page_fork(&d, src, lens, table, refs, kv.at, table_out, refs_out, ws, bytes, s);
+    }));
   });
 }
 
@@ -311,6 +330,7 @@ PyObject* rope_pack(PyObject*, PyObject* const* args, Py_ssize_t n) {
     int32_t* lens = c.ints(5, B);
     int32_t* cu = c.ints(6, B + 1);
     const float kv_scale = c.number(7);
+    const void *qp = q->data_ptr(), *rows = r->data_ptr();
     void* out = c.full(8, bf16, {T, H, 64});
     const Call::Cache kv = c.cache(9, false);
     int32_t* status = c.status(10);
@@ -326,8 +346,10 @@ PyObject* rope_pack(PyObject*, PyObject* const* args, Py_ssize_t n) {
     }
     int rc = 1;
     if (plan.len == static_cast<Py_ssize_t>(sizeof(mla_rope_plan)))
-      rc = mla_rope_pack(&d, static_cast<const mla_rope_plan*>(plan.buf), q->data_ptr(), r->data_ptr(), positions, table,
-                         lens, cu, kv_scale, out, kv.at, status, s);
+      rc = unlocked([&] {
+        return mla_rope_pack(&d, static_cast<const mla_rope_plan*>(plan.buf), qp, rows, positions, table, lens, cu,
+                             kv_scale, out, kv.at, status, s);
+      });
     PyBuffer_Release(&plan);
     if (rc == 1) Py_RETURN_NONE;
     return PyLong_FromLong(rc);

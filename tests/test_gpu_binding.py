@@ -116,3 +116,35 @@ def test_rope_takes_a_plan_only():
     for plan in (None, 3, b"x" * 271, b"x" * 16, object()):
         with pytest.raises(TypeError):
             call(plan, *args[1:])
+
+
+@pytest.mark.parametrize("name", ["tree", "commit", "verify", "resize", "fork", "rope"])
+def test_other_threads_run_while_a_launch_waits(name):
+    """Calls behind a kernel of a good half second: the stream's queue fills up
+    and launches wait for it, and meanwhile this thread has to get on."""
+    import threading
+    import time
+
+    call, args, _, _ = calls()[name]
+    call(*args)
+    torch.cuda.synchronize()
+    took = []
+
+    def enqueue():
+        begin = time.perf_counter()
+        for _ in range(4000):
+            call(*args)
+        took.append(time.perf_counter() - begin)
+
+    torch.cuda._sleep(1_500_000_000)  # cycles, at 2 GHz or less
+    other = threading.Thread(target=enqueue)
+    longest, last = 0.0, time.perf_counter()
+    other.start()
+    while other.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        longest, last = max(longest, now - last), now
+    other.join()
+    torch.cuda.synchronize()
+    assert took[0] > 0.5  # the queue was full
+    assert longest < 0.2
