@@ -114,3 +114,36 @@ def error_bounds(c, b, i):
     lse = s.max(axis=1) + np.log(np.exp(s - s.max(axis=1, keepdims=True)).sum(axis=1))
     lse_tol = d + acc + 8 * 2.0**-23 * (np.abs(lse) + 1)
     return out_tol, lse_tol
+
+
+def takes_single_form(c):
+    """Whether the call's blocks are of 128 rows (mean rows of a request up to 128)."""
+    return c.q_nope.shape[0] * c.q_nope.shape[1] <= 128 * len(c.seq_lens)
+
+
+def may_be_cut(c):
+    """Whether the call's blocks may be cut into pieces that a combine joins (the
+    table is longer than what one cluster takes whole, and the combine's worth)."""
+    T, H, _ = c.q_nope.shape
+    rows = T * H // len(c.seq_lens)
+    return c.page_table.shape[1] > 5 + min(rows, 128) // 40 + T * H // 600 + 3
+
+
+# Blocks of more than 64 rows in the single form, cut into pieces: a cluster's
+# last outputs go by way of shared memory in boxes of 32 rows, of which a piece's
+# may reach into the rows behind the block (80 to 95, 112 to 127 rows).
+WIDE_SINGLE = {
+    "128_rows": dict(new=[1], total=[20000], heads=128),
+    "80_rows": dict(new=[1], total=[9000], heads=80),
+    "81_rows": dict(new=[1], total=[9001], heads=81),
+    "95_rows": dict(new=[1], total=[9002], heads=95),
+    "96_rows": dict(new=[1], total=[9003], heads=96),
+    "112_rows": dict(new=[1], total=[9023], heads=112),
+    "120_rows": dict(new=[1], total=[9024], heads=120),
+    "65_rows": dict(new=[1], total=[9025], heads=65),
+    "8_tokens": dict(new=[8], total=[9000], heads=16),
+    "6_tokens_of_20": dict(new=[6], total=[3000], heads=20),
+    "several": dict(new=[1, 1, 1], total=[9000, 300, 5000], heads=128),
+    "some_short": dict(new=[1] * 9, total=[9000, 1, 64, 65, 5000, 2, 700, 130, 12], heads=120),
+    "more_blocks_than_clusters": dict(new=[1] * 90, total=[300 + 13 * k for k in range(90)], heads=66),
+}

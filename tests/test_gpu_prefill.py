@@ -112,6 +112,31 @@ def test_prefill_parity(name, kv_dtype):
     run_and_check(K.make(seed=len(name), kv_dtype=kv_dtype, **CASES[name]))
 
 
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("name", list(K.WIDE_SINGLE))
+def test_wide_blocks_of_the_single_form(name, kv_dtype):
+    c = K.make(seed=len(name), kv_dtype=kv_dtype, **K.WIDE_SINGLE[name])
+    assert K.takes_single_form(c) and K.may_be_cut(c)
+    run_and_check(c)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("heads", [80, 96, 112, 127, 128])
+def test_wide_blocks_of_the_single_form_uncut(heads, kv_dtype):
+    c = K.make([1, 1], [500, 90], heads=heads, kv_dtype=kv_dtype, seed=heads)
+    assert K.takes_single_form(c) and not K.may_be_cut(c)
+    run_and_check(c)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("window,sinks", [(5000, 100), (70, 0)])
+@pytest.mark.parametrize("heads", [80, 112, 128])
+def test_wide_blocks_of_the_single_form_over_windows(heads, window, sinks, kv_dtype):
+    c = K.make([1, 1, 1], [9000, 300, 6000], heads=heads, window=window, sinks=sinks, kv_dtype=kv_dtype, seed=heads)
+    assert K.takes_single_form(c)
+    run_and_check(c)
+
+
 WINDOWS = [(1, 0), (1, 3), (33, 4), (64, 64), (100, 70), (129, 0), (500, 1), (2000, 130), (5000, 10000)]
 
 

@@ -128,6 +128,31 @@ def test_a_chain_is_a_prompt_chunk_bit_for_bit(heads, kv_dtype):
 
 
 @pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("name", list(K.WIDE_SINGLE))
+def test_wide_blocks_of_the_single_form(name, kv_dtype):
+    c, parents = TC.make(seed=len(name), kv_dtype=kv_dtype, **K.WIDE_SINGLE[name])
+    assert K.takes_single_form(c) and K.may_be_cut(c)
+    run_and_check(c, parents)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
+@pytest.mark.parametrize("new,total,heads", [([8], [9000], 16), ([1, 1], [9000, 5000], 120), ([6, 5, 0], [3000, 700, 5], 20),
+                                             ([5, 3], [60, 130], 16)])
+def test_a_chain_is_a_prompt_chunk_in_the_single_form(new, total, heads, kv_dtype):
+    import paged_mla_decode_09_gb300 as mla
+
+    c, parents = TC.make(new, total, heads=heads, kind="chain", kv_dtype=kv_dtype, seed=heads)
+    assert K.takes_single_form(c)
+    r = run_and_check(c, parents)
+    out, lse = torch.full_like(r.out, SENTINEL), torch.full_like(r.lse, SENTINEL)
+    ws = torch.empty(mla.mla_prefill_workspace_size(mla.make_prefill_dims(r.qn, r.cache, r.table, r.lens)),
+                     dtype=torch.uint8, device="cuda")
+    mla.mla_prefill(r.qn, r.qp, r.cache, r.table, r.lens, r.cu, 0, 0, c.scale, c.kv_scale, out, lse, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(out, r.out) and torch.equal(lse, r.lse)
+
+
+@pytest.mark.parametrize("kv_dtype", ["bf16", "fp8_e4m3"])
 def test_peaked_scores(kv_dtype):
     run_and_check(*TC.make([20, 3], [1500, 900], heads=32, kv_dtype=kv_dtype, seed=5, q_gain=10.0))
 
