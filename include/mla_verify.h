@@ -63,7 +63,7 @@ typedef struct {
  *               (MLA_DEV_BAD_INDEX)
  *   parents     int32 [total_q] as for mla_decode_tree; a node that is not below
  *               node 0 is never reached.  A bad parent: MLA_DEV_BAD_TREE, and the
- *               node is as if it were not there
+ *               node is as if it were not there (node 0 stays: it has none)
  *   cu_q_lens   int32 [B + 1] as for mla_prefill, with at most MLA_TREE_MAX_NODES
  *               nodes a request (else MLA_DEV_BAD_QUERY_RANGE, MLA_DEV_BAD_TREE: the
  *               request is treated as one without nodes)

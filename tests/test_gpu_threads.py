@@ -1,6 +1,10 @@
 """Entry points as the first CUDA call of a thread, where the runtime has no
-context current yet: they give what they give in the main thread."""
+context current yet: they give what they give in the main thread.  And as the
+process's first call, captured."""
 import ctypes
+import os
+import subprocess
+import sys
 import threading
 
 import pytest
@@ -134,3 +138,9 @@ def test_threads_at_once():
     assert not failed, failed
     for (_, outs), ref in zip(jobs, want):
         assert all(torch.equal(a, b) for a, b in zip(outs, ref))
+
+
+def test_first_calls_of_a_process_can_be_captured():
+    child = os.path.join(os.path.dirname(os.path.abspath(__file__)), "first_capture_speculative_child.py")
+    r = subprocess.run([sys.executable, child], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr

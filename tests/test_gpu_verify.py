@@ -239,6 +239,19 @@ def test_bad_nodes_and_offsets():
     assert status == mla.MLA_DEV_BAD_TREE and num[0] == 0 and np.all(out[0] == -1) and num[1] >= 1
 
 
+def test_node_0_stays_whatever_its_parent():
+    import paged_mla_decode_09_gb300 as mla
+
+    c = make([4, 6, 3], 500, True, "tree", seed=12)
+    want = check(c, 6)
+    for value in (0, 3, -2, 2**31 - 1):
+        d = dict(c, parents=c["parents"].copy())
+        d["parents"][4] = value
+        path, out, num, status = Run(d, 6).launch().result()
+        assert status == mla.MLA_DEV_BAD_TREE
+        assert np.array_equal(path, want[0]) and np.array_equal(out, want[1]) and np.array_equal(num, want[2])
+
+
 @pytest.mark.parametrize("pad", [1, 2, 3, 4, 7])
 def test_strides_and_alignment(pad):
     """Rows of a wider tensor, at any offset of four bytes."""
