@@ -746,10 +746,11 @@ __device__ __forceinline__ float store_lse(const Params& p, const Unit& u, int b
 // shared memory: boxes of 32 rows x 64 bytes (64-byte swizzle), kBufs in turn,
 // that TMA writes.  (A lane's own stores to its row take a line each: a block's
 // bf16 outputs took 4.9 us that way, 2.5 this way, and O is not free for the
-// next block before that.)  The single form's last block likewise: a tree of
-// 128 rows over 700 tokens, cut, 21.0 -> 19.6 us in all; 64 of them over 60, uncut,
-// 18.4 -> 16.8.
+// next block before that.)  The single form's last block likewise: 128 rows over
+// 700 tokens, cut, 20.5 -> 19.9 us for the call; 64 such requests of 60 tokens,
+// uncut, 16.2 -> 14.8 (bf16 cache, calls of a graph).
 constexpr int kLastBufs = 8;
+constexpr int kStageRows = 80;  // of a block, from which on the single form's last one is staged
 template <bool kF8, int kCg, int kBufs>
 __device__ __forceinline__ void store_staged(const Params& p, const Unit& u, int br0, int c0, uint32_t taddr, float f,
                                              uint8_t* stage, const CUtensorMap* map) {
@@ -1583,9 +1584,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool staged = false;
         if constexpr (C::kStage > 0) staged = u.slot >= 0 ? u.slot < 2 * p.C : br0 + 32 <= u.k.nrows;
         // a single form's last unit of a slice finds the page rings idle and
-        // stages there, for blocks of more than 64 rows (calls of 128 rows 1.0-2.6
-        // us shorter, of 64 up to 0.5 longer, of 16 and 32 2.2 and 1.6)
-        else staged = it.n > it.nlast && u.slot < 2 * p.C && u.k.nrows > 64 && br0 + (u.slot >= 0 ? 16 : 32) <= u.k.nrows;
+        // stages there, for blocks of at least 80 rows: less than that takes up to
+        // 0.6 us longer than the lanes' own stores (72 rows: 0.5 longer to 0.3 shorter;
+        // 65: 0.2-0.6 longer; 16 to 48: 0.3-2.2), 80 rows 0.5 us shorter to equal, 96
+        // rows 0.6-1.1 shorter, 112 0.3-1.2, 128 0.5-1.5 (requests of 60 to 20000
+        // tokens, 1 to 64 of them, both caches)
+        else staged = it.n > it.nlast && u.slot < 2 * p.C && u.k.nrows >= kStageRows &&
+                      br0 + (u.slot >= 0 ? 16 : 32) <= u.k.nrows;
         if (!staged && lane == 0) mbar_arrive_cluster(mlempty_remote);
         const float f = store_lse<kF8>(p, u, br, c0 == 0, m_log2, l);
         if (staged) {

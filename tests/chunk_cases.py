@@ -129,11 +129,12 @@ def may_be_cut(c):
     return c.page_table.shape[1] > 5 + min(rows, 128) // 40 + T * H // 600 + 3
 
 
-# Blocks of more than 64 rows in the single form, cut into pieces: a cluster's
-# last outputs go by way of shared memory in boxes of 32 rows, of which a piece's
-# may reach into the rows behind the block (80 to 95, 112 to 127 rows).
+# Blocks of more than 64 rows in the single form, cut into pieces: from 80 rows on
+# a cluster's last outputs go by way of shared memory in boxes of 32 rows, of which
+# a piece's may reach into the rows behind the block (80 to 95, 112 to 127 rows).
 WIDE_SINGLE = {
     "128_rows": dict(new=[1], total=[20000], heads=128),
+    "79_rows": dict(new=[1], total=[9000], heads=79),
     "80_rows": dict(new=[1], total=[9000], heads=80),
     "81_rows": dict(new=[1], total=[9001], heads=81),
     "95_rows": dict(new=[1], total=[9002], heads=95),
