@@ -13,16 +13,17 @@
 // between calls would spare the walk over the counts (4 bytes a page), but its
 // order would depend on the calls before.
 // What bounds it: the latency of the steps, about four reads and barriers, then
-// what 16 SMs read: 4 requests over 512 pages 3.2 us, 256 requests of 512 columns
-// over 131072 pages 11.7 (counts 1.3, their barrier 0.9, entries and the slowest
-// block's atomics 4.4, sums 0.9, the list 1.6, the entries' pages 1.6).
+// what 16 SMs read: 4 requests over 512 pages 3.0 us, 256 requests of 512 columns
+// over 131072 pages 12.0 (counts 1.3, their barrier 0.9, entries and the slowest
+// block's atomics 4.4, sums 0.9, the list 1.6, the entries' pages 1.6).  Times
+// in this file: a call of a graph of calls.
 //
 // Rows (mla_tree_commit, mla_page_fork's second kernel): copies of 16-byte
 // columns.  A committed path is ascending, so that slot k is read (if at all)
 // by a move that is not behind the one that writes it; a thread takes one
 // column of the row through all moves in order, eight loads before their
-// stores, and needs no barrier.  64 requests in 24 layers 3.6 us (4.6 MB, 1.3
-// TB/s: the launch and three dependent reads), 64 forks in 16 layers 13.3 with
+// stores, and needs no barrier.  64 requests in 24 layers 3.3 us (4.6 MB, 1.4
+// TB/s: the launch and three dependent reads), 64 forks in 16 layers 11.6 with
 // the handing out (35 MB).
 #include <cuda_runtime.h>
 
@@ -44,7 +45,8 @@ namespace pages {
 constexpr int kPage = 64;
 
 // ------------------------------------------------------------ handing out
-constexpr int kOneBlock = 16384;  // entries and pages up to which one block does a call
+template <bool kFork>
+constexpr int kOneBlock = kFork ? 10240 : 16384;  // entries and pages up to which one block does a call (see launch)
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 4 * kThreads;  // pages of a step: four in a row per thread
@@ -549,11 +551,13 @@ bool sixteen_fit(int device) {
 }
 
 // One block for small calls (its barriers are cheaper), else a cluster of 16
-// where that fits.  Measured, one block, a cluster of 8, of 16: 4 requests of 32
-// columns over 512 pages 3.1, 4.3, - us; 256 of 512 columns over 131072 pages
-// 46.9, 14.1, 11.7; 64 forks of 25 columns over 800 pages (with the copies)
-// 11.3, 13.5, -.  The limit is where lines through these meet, not measured
-// there.
+// where that fits.  Measured, one block and a cluster, us a call of a graph:
+//   resize, entries and pages  6.1K 5.4, 7.3   12.3K 6.0, 8.0   16.4K 7.2, 8.3
+//                              32.8K 11.0, 8.9   65.5K 17.2, 9.3   262K 46.5, 12.7
+//     with 8 entries only      6K 3.3, 3.7   12K 3.7, 3.7   16K 4.0, 3.7   40K 5.9, 3.9
+//   fork (with its copies)     4.9K 8.5, 11.1   8.2K 11.0, 11.9   12.5K 12.6, 11.5
+//                              25.7K 19.4, 11.9
+// (a cluster of 8 took 14.1 where 16 blocks took 11.7).
 template <bool kFork>
 cudaError_t launch(const mla::pages::Params& p, cudaStream_t s) {
   using namespace mla::pages;
@@ -561,7 +565,7 @@ cudaError_t launch(const mla::pages::Params& p, cudaStream_t s) {
   int dev = 0;
   const cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (static_cast<int64_t>(p.B) * p.cols + p.P > kOneBlock && sixteen_fit<kFork>(dev))
+  if (static_cast<int64_t>(p.B) * p.cols + p.P > kOneBlock<kFork> && sixteen_fit<kFork>(dev))
     return launch_pdl(&mla_pages_kernel<kFork, 16>, dim3(16), block, 0, s, 16, p);
   return launch_pdl(&mla_pages_kernel<kFork, 1>, dim3(1), block, 0, s, 0, p);
 }

@@ -200,6 +200,21 @@ def test_fork_over_many_rows():
     check_fork(*fork_case(rng, lens, rng.integers(0, 700, 900), 40, 1, np.uint8))
 
 
+@pytest.mark.parametrize("spare", [10239 - 72 - 4, 10240 - 72 - 4, 10241 - 72 - 4, 16400])
+def test_fork_around_the_size_from_which_a_cluster_does_it(spare):
+    rng = np.random.default_rng(spare)
+    check_fork(*fork_case(rng, [70, 130], rng.integers(0, 2, 24), 3, 1, np.uint8, spare=spare))
+
+
+@pytest.mark.parametrize("pages", [16383 - 72, 16384 - 72, 16385 - 72])
+def test_resize_around_the_size_from_which_a_cluster_does_it(pages):
+    rng = np.random.default_rng(pages)
+    lens = rng.integers(0, 193, 24)
+    table, refs = pool(rng, lens, 3, pages)
+    for _ in range(2):
+        check_resize(np.clip(lens + rng.integers(-100, 100, 24), 0, 192), table, refs)
+
+
 def test_fork_runs_out_of_pages():
     import paged_mla_decode_09_gb300 as mla
 
