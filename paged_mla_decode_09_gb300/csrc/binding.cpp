@@ -2,7 +2,7 @@
 // the tensors' shapes, types, strides and addresses and makes the C call.  Each
 // function returns the mla_status, or None where an argument is not what the
 // call takes, which Python then explains.  (A small call's kernels take 2 to 4
-// us; the same tests and the call through ctypes take 10, here 3 to 4.)
+// us; the same tests and the call through ctypes take 10, here 2 to 4.)
 #include <Python.h>
 
 #include <c10/cuda/CUDAFunctions.h>

@@ -17,7 +17,7 @@
 // What bounds it: HBM for prompts (each query value read and written once, each
 // row read and written once: 6.1K tokens of 128 heads into an e4m3 cache 36 us,
 // 5.5 TB/s of the 6.8 that a copy reaches), the chain of dependent reads for a
-// few tokens (4 tokens of 16 heads 3.2 us).  Swept: two items in flight and five
+// few tokens (4 tokens of 16 heads 3.2 us a call of a graph).  Swept: two items in flight and five
 // blocks an SM; three and five 38.2 us, three and four 35.3 (64 trees of 16
 // tokens 7.5 us instead of 6.7), two and six 37.5; streaming hints 36.3-36.5.
 #include <cuda_bf16.h>

@@ -17,11 +17,15 @@
 // than an entry's width), without 64-bit floating point, which this chip has
 // little of.
 //
-// What bounds it: HBM for batches (64 chains over 131072 tokens 19.6 us: 3 us
-// until the walks end, 67 MB at 5-6 TB/s, 2 us for the tokens), for one request
-// the chain of reads (offsets, nodes, their entries, the row, the chunk) and the
-// barriers (32000 tokens 6 us).  A rejected sibling costs another pass over
-// the rows, from L2: about 3 us at 65536 tokens.
+// What bounds it: HBM for batches (64 chains over 131072 tokens 18.0 us a call of
+// a graph, 20.2 in a loop on changing inputs: 3 us until the walks end, 67 MB at
+// 5-6 TB/s, 2 us for the tokens), for one request the chain of reads (offsets,
+// nodes, their entries, the row, the chunk) and the barriers (32000 tokens 6.1
+// in the loop).  Each rejected sibling of sampled drafts costs another pass over
+// both rows, from L2, and the pass after k of them forms k - 1 products in 64 bits
+// per entry, whose weight it finds anew from p and q: one request over 65536
+// tokens takes 5.4 us, 7.4 with one rejected, then 17.7, 28, 52, 100, 277 and 1275
+// with 2, 3, 5, 8, 16 and 40.  Fixed proposals take one pass whatever is rejected.
 #include <cuda_runtime.h>
 
 #include <climits>
