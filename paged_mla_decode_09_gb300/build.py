@@ -51,7 +51,7 @@ def _newer(path: str, sources) -> bool:
 def _have_torch() -> bool:
     try:
         import torch  # noqa: F401
-    except ImportError:
+    except Exception:  # not there, or its libraries do not load
         return False
     return True
 

@@ -69,11 +69,15 @@ def test_a_library_that_does_not_compile_leaves_nothing(tree):
     assert left(tree) == []
 
 
-def test_without_torch_there_is_the_library(tree):
+@pytest.mark.parametrize("torch", ["", "raise OSError('libcudart.so: cannot open shared object file')"])
+def test_without_torch_there_is_the_library(tree, torch):
+    (tree / "bin" / "torch").mkdir()
+    (tree / "bin" / "torch" / "__init__.py").write_text(torch)
     code = f"""
 import sys
-sys.path.insert(0, {ROOT!r})
-sys.modules["torch"] = None  # an import raises
+sys.path[:0] = [{ROOT!r}, {str(tree / "bin")!r}]
+if not {torch!r}:
+    sys.modules["torch"] = None  # not there: an import raises ImportError
 from paged_mla_decode_09_gb300 import build
 build.LIB_PATH = {build.LIB_PATH!r}
 assert not build.up_to_date()
