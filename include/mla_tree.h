@@ -53,7 +53,8 @@ size_t mla_decode_tree_workspace_size(const mla_prefill_dims* d, int device);
  * window, and
  *
  *   cu_q_lens   as for mla_prefill, with at most MLA_TREE_MAX_NODES nodes a
- *               request
+ *               request.  (Where offsets decrease, which is flagged, a token that two
+ *               requests name gets either's outputs, seeing either's ancestors)
  *   parents     int32 [total_q]: each node's parent within its request, < its
  *               own index, or -1.  Entries from cu_q_lens[B] on are not read
  *
